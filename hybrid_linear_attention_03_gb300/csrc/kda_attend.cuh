@@ -1,0 +1,148 @@
+// kda_attend.cuh -- what the attention kernels share: how the keys of a call
+// are shared out over the CTAs, the records of the shares and their layout in
+// the workspace.
+//
+// An item is one row tile: the query heads of one cache head (the group, G of
+// them) for TT consecutive tokens of one sequence, rows r = t * G + g.  Its
+// keys are positions [0, ctx + last token + 1).  All items of a call, ordered
+// by sequence, cache head and tile, form one line whose length is the sum of
+// their key counts, and CTA c of C takes the c-th of C equal pieces of that
+// line (cut points rounded down to whole key steps inside an item).  So any
+// mix of lengths loads every CTA alike, with no table built on the host and
+// no launch per sequence.  An item cut by one or more cut points is computed
+// in parts: every part leaves its unnormalised output, row maxima and row sums
+// in the workspace, and the combine kernel joins them in order, so results do
+// not depend on timing.
+#pragma once
+
+#include "kda_kv.cuh"
+
+namespace kda {
+namespace kv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Part {
+    int32_t n, h, tile;  // item
+    int32_t state;       // 0 none, 1 there, 2 there and the item's last
+};
+
+struct AttendParams {
+    BatchView b;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;
+    const void *pk, *pv;
+    const uint8_t *sk, *sv;
+    int32_t hq, hkv, group;
+    int32_t tile_tokens;  // TT
+    int32_t key_step;     // keys per step; cut points are multiples of it
+    int32_t min_keys;     // a CTA's piece is at least this long (fewer CTAs take part in a small call)
+    float scale_log2;     // scale * log2(e)
+    Part *parts;          // [C][2]: the CTA's first part (of an item begun before) and its last
+    float *part_data;     // [C][2][BM * (D + 2)]: out [BM][D], then row maxima [BM], then row sums [BM]
+};
+
+// Keys of tile i's last row: how far the item reaches.
+__device__ __forceinline__ int tile_keys(int ctx, int T, int tt, int i) { return ctx + min(T, (i + 1) * tt); }
+
+// Sum of tile_keys over the first m tiles of a sequence (m <= ceil(T / tt)).
+__device__ __forceinline__ long long tile_prefix(int ctx, int T, int tt, int m) {
+    const int full = min(m, T / tt);
+    long long s = static_cast<long long>(full) * ctx + static_cast<long long>(tt) * full * (full + 1) / 2;
+    if (m > full) s += ctx + T;
+    return s;
+}
+
+struct Cursor {  // a place on the line: key `key` of item (n, h, tile)
+    int n, h, tile, key;
+};
+
+// The whole warp finds this CTA's piece [from, to) of the line; false if it
+// has none.  Lane i sums the sequences [i * per, (i + 1) * per), so the tables
+// are read twice: once for the sums, once inside the piece's sequence.
+__device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n_cta, int lane, Cursor &from,
+                                           Cursor &to) {
+    const int N = p.b.n_seqs, per = (N + 31) / 32, tt = p.tile_tokens;
+    const int n0 = min(lane * per, N), n1 = min(n0 + per, N);
+    long long sum = 0;
+    for (int n = n0; n < n1; ++n) {
+        Seq s;
+        if (load_seq(p.b, n, s, cta == 0) && s.T > 0)
+            sum += tile_prefix(s.L - s.T, s.T, tt, (s.T + tt - 1) / tt) * p.hkv;
+    }
+    long long before = sum;  // inclusive scan over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
+    }
+    const long long total = __shfl_sync(0xffffffffu, before, 31);
+    before -= sum;
+    const long long want = (total + p.min_keys - 1) / p.min_keys;
+    const int active = int(min(static_cast<long long>(n_cta), want));
+    if (cta >= active) return false;
+    Cursor c[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const long long x = total / active * (cta + e) + total % active * (cta + e) / active;
+        c[e] = Cursor{N, 0, 0, 0};
+        if (x < total) {  // the lane whose sequences hold x walks them
+            const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + sum);
+            const int src = __ffs(owner) - 1;
+            if (lane == src) {
+                long long rest = x - before;
+                for (int n = n0; n < n1; ++n) {
+                    Seq s;
+                    if (!load_seq(p.b, n, s, false) || s.T == 0) continue;
+                    const int ctx = s.L - s.T, tiles = (s.T + tt - 1) / tt;
+                    const long long head = tile_prefix(ctx, s.T, tt, tiles);
+                    if (rest >= head * p.hkv) {
+                        rest -= head * p.hkv;
+                        continue;
+                    }
+                    c[e].n = n;
+                    c[e].h = int(rest / head);
+                    rest -= head * c[e].h;
+                    int lo = 0, hi = tiles - 1;  // last tile whose prefix is at most rest
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) / 2;
+                        if (tile_prefix(ctx, s.T, tt, mid) <= rest) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    c[e].tile = lo;
+                    const int key = int(rest - tile_prefix(ctx, s.T, tt, lo));
+                    c[e].key = key / p.key_step * p.key_step;
+                    break;
+                }
+            }
+            c[e].n = __shfl_sync(0xffffffffu, c[e].n, src);
+            c[e].h = __shfl_sync(0xffffffffu, c[e].h, src);
+            c[e].tile = __shfl_sync(0xffffffffu, c[e].tile, src);
+            c[e].key = __shfl_sync(0xffffffffu, c[e].key, src);
+        }
+    }
+    from = c[0];
+    to = c[1];
+    return true;
+}
+
+// Workspace: the part records of every CTA, then their data, 256-aligned.
+__host__ __device__ __forceinline__ size_t parts_bytes(int n_cta) {
+    return (sizeof(Part) * 2 * size_t(n_cta) + 255) / 256 * 256;
+}
+inline size_t share_bytes(int n_cta, int bm, int D) {
+    return parts_bytes(n_cta) + sizeof(float) * size_t(n_cta) * 2 * size_t(bm) * size_t(D + 2);
+}
+
+// What a kernel of this family needs from the host: its row tile, its grid
+// and its workspace.  supports() is decided on sizes and types alone.
+struct AttendPlan {
+    int bm;     // rows of a tile
+    int n_cta;  // grid
+};
+bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
+kda_status generic_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+
+}  // namespace kv
+}  // namespace kda

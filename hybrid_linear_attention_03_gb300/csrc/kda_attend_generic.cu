@@ -1,0 +1,297 @@
+// kda_attend_generic.cu -- kda_kv_attend in 32-bit arithmetic on the CUDA
+// cores, for every activation type, cache format and head size.
+//
+// One pass over the keys with the running row maximum m and sum l of a
+// softmax (in powers of two, x = scale * log2(e) * q . k):
+//   m' = max(m, max_j x_j),  l <- l 2^(m - m') + sum_j 2^(x_j - m'),
+//   o <- o 2^(m - m') + sum_j 2^(x_j - m') v_j,   out = o / l.
+// A CTA holds a tile of BM rows (query heads of one cache head, consecutive
+// tokens) and walks 64 keys a step through shared memory, each of its 256
+// threads keeping BM / 16 rows x 4 keys of the scores and BM / 16 rows x D / 16
+// channels of the output in registers.  FFMA issue bounds the 64-row tile.
+#include "kda_attend.cuh"
+
+namespace kda {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int KS = 64;  // keys a step
+
+template <typename Kv> __device__ __forceinline__ void load4(const Kv *src, float (&x)[4]);
+template <> __device__ __forceinline__ void load4<float>(const float *src, float (&x)[4]) {
+    const float4 t = *reinterpret_cast<const float4 *>(src);
+    x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+}
+template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16 *src, float (&x)[4]) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(src);
+    x[0] = __uint_as_float(t.x << 16), x[1] = __uint_as_float(t.x & 0xffff0000u);
+    x[2] = __uint_as_float(t.y << 16), x[3] = __uint_as_float(t.y & 0xffff0000u);
+}
+template <> __device__ __forceinline__ void load4<uint8_t>(const uint8_t *src, float (&x)[4]) {
+    const uint32_t t = *reinterpret_cast<const uint32_t *>(src);
+    const float2 a = unpack_e4m3(uint16_t(t)), b = unpack_e4m3(uint16_t(t >> 16));
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+
+template <int BM, int D> struct Smem {
+    float q[D][BM];      // channel-major
+    float k[D][KS + 4];  // channel-major
+    float v[KS][D];
+    float p[KS][BM + 4];
+    int64_t line[KS];  // vector index of each key's line, -1 where there is none
+    Cursor piece[2];
+    int has;
+};
+
+template <typename Act, typename Kv, int BM, int D>
+__global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_constant__ AttendParams p) {
+    constexpr int RT = BM / 16, CT = D / 16;  // rows and channels of a thread
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem<BM, D> &s = *reinterpret_cast<Smem<BM, D> *>(smem_raw);
+    const int tid = int(threadIdx.x), ty = tid >> 4, tx = tid & 15;
+    const int cta = int(blockIdx.x);
+    wait_prior_kernel();
+    allow_next_kernel();
+    Part *my_parts = p.parts + 2 * cta;
+    if (tid < 2) my_parts[tid].state = 0;
+    if (tid < 32) {
+        Cursor a, z;
+        const bool has = find_piece(p, cta, int(gridDim.x), tid, a, z);
+        if (tid == 0) s.piece[0] = a, s.piece[1] = z, s.has = has;
+    }
+    __syncthreads();
+    if (!s.has) return;
+    Cursor at = s.piece[0];
+    const Cursor end = s.piece[1];
+    const int page_mask = (1 << p.b.page_shift) - 1;
+
+    for (; at.n < p.b.n_seqs; ++at.n, at.h = 0, at.tile = 0, at.key = 0) {
+        Seq sq;
+        if (!load_seq(p.b, at.n, sq, false) || sq.T == 0) {
+            if (at.n >= end.n) return;
+            continue;
+        }
+        const int tiles = (sq.T + p.tile_tokens - 1) / p.tile_tokens, ctx = sq.L - sq.T;
+        for (; at.h < p.hkv; ++at.h, at.tile = 0, at.key = 0) {
+            for (; at.tile < tiles; ++at.tile, at.key = 0) {
+                const bool last = at.n == end.n && at.h == end.h && at.tile == end.tile;
+                const int keys = tile_keys(ctx, sq.T, p.tile_tokens, at.tile);
+                const int k0 = at.key, k1 = last ? end.key : keys;
+                if (k0 >= k1) {
+                    if (last) return;
+                    continue;
+                }
+                const int tok0 = at.tile * p.tile_tokens, rows = min(p.tile_tokens, sq.T - tok0) * p.group;
+                __syncthreads();
+                for (int i = tid; i < BM * D / 4; i += kThreads) {
+                    const int r = i % BM, c = i / BM * 4;
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (r < rows)
+                        load4<Act>(static_cast<const Act *>(p.q) +
+                                       size_t(sq.row0 + tok0 + r / p.group) * size_t(p.q_stride) +
+                                       size_t(at.h * p.group + r % p.group) * D + c, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s.q[c + e][r] = x[e] * p.scale_log2;
+                }
+                float o[RT][CT], m[RT], l[RT];
+#pragma unroll
+                for (int a = 0; a < RT; ++a) {
+                    m[a] = -INFINITY, l[a] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) o[a][c] = 0.f;
+                }
+                int lim[RT];  // last key a row sees
+#pragma unroll
+                for (int a = 0; a < RT; ++a) {
+                    const int r = ty * RT + a;
+                    lim[a] = r < rows ? ctx + tok0 + r / p.group : -1;
+                }
+                for (int kb = k0; kb < k1; kb += KS) {
+                    __syncthreads();  // the previous step's keys and values are done with
+                    bool hidden = false;  // this thread's key is absent, or behind some row's position
+                    if (tid < KS) {
+                        const int j = kb + tid;
+                        int64_t line = -1;
+                        if (j < k1) {
+                            const int page = load_page(p.b, at.n, j);
+                            if (page >= 0)
+                                line = ((int64_t(page) * p.hkv + at.h) << p.b.page_shift) + (j & page_mask);
+                        }
+                        s.line[tid] = line;
+                        hidden = line < 0 || j > ctx + tok0;
+                    }
+                    const bool masked = __syncthreads_or(hidden);
+                    for (int i = tid; i < KS * D / 4; i += kThreads) {
+                        const int j = i / (D / 4), c = i % (D / 4) * 4;
+                        float xk[4] = {0.f, 0.f, 0.f, 0.f}, xv[4] = {0.f, 0.f, 0.f, 0.f};
+                        const int64_t line = s.line[j];
+                        if (line >= 0) {
+                            load4<Kv>(static_cast<const Kv *>(p.pk) + line * D + c, xk);
+                            load4<Kv>(static_cast<const Kv *>(p.pv) + line * D + c, xv);
+                            if constexpr (sizeof(Kv) == 1) {
+                                const float fk = exp2_biased(p.sk[line]), fv = exp2_biased(p.sv[line]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) xk[e] *= fk, xv[e] *= fv;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s.k[c + e][j] = xk[e];
+                        *reinterpret_cast<float4 *>(&s.v[j][c]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
+                    }
+                    __syncthreads();
+                    float x[RT][4];
+#pragma unroll
+                    for (int a = 0; a < RT; ++a)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[a][e] = 0.f;
+#pragma unroll 8
+                    for (int c = 0; c < D; ++c) {
+                        const float4 kk = *reinterpret_cast<const float4 *>(&s.k[c][tx * 4]);
+                        float qq[RT];
+                        if constexpr (RT == 4) {
+                            const float4 t = *reinterpret_cast<const float4 *>(&s.q[c][ty * 4]);
+                            qq[0] = t.x, qq[1] = t.y, qq[2] = t.z, qq[3] = t.w;
+                        } else {
+#pragma unroll
+                            for (int a = 0; a < RT; ++a) qq[a] = s.q[c][ty * RT + a];
+                        }
+#pragma unroll
+                        for (int a = 0; a < RT; ++a) {
+                            x[a][0] = fmaf(qq[a], kk.x, x[a][0]);
+                            x[a][1] = fmaf(qq[a], kk.y, x[a][1]);
+                            x[a][2] = fmaf(qq[a], kk.z, x[a][2]);
+                            x[a][3] = fmaf(qq[a], kk.w, x[a][3]);
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bool there = s.line[tx * 4 + e] >= 0;
+#pragma unroll
+                            for (int a = 0; a < RT; ++a)
+                                if (!there || kb + tx * 4 + e > lim[a]) x[a][e] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int a = 0; a < RT; ++a) {
+                        float mx = fmaxf(fmaxf(x[a][0], x[a][1]), fmaxf(x[a][2], x[a][3]));
+#pragma unroll
+                        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        const float mn = fmaxf(m[a], mx), ref = mn == -INFINITY ? 0.f : mn;
+                        const float f = exp2f(m[a] - ref);
+                        float sum = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[a][e] = exp2f(x[a][e] - ref);
+                            sum += x[a][e];
+                            s.p[tx * 4 + e][ty * RT + a] = x[a][e];
+                        }
+#pragma unroll
+                        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                        l[a] = l[a] * f + sum;
+                        m[a] = mn;
+#pragma unroll
+                        for (int c = 0; c < CT; ++c) o[a][c] *= f;
+                    }
+                    __syncwarp();  // a row's weights are written and read by the same half warp
+                    // channels of a thread: groups of four (or the D / 16 there are) 16 groups apart
+                    constexpr int CV = CT >= 4 ? 4 : CT;
+#pragma unroll 4
+                    for (int j = 0; j < KS; ++j) {
+                        float w[RT], vv[CT];
+#pragma unroll
+                        for (int a = 0; a < RT; ++a) w[a] = s.p[j][ty * RT + a];
+#pragma unroll
+                        for (int g = 0; g < CT / CV; ++g)
+#pragma unroll
+                            for (int e = 0; e < CV; ++e) vv[g * CV + e] = s.v[j][g * 16 * CV + tx * CV + e];
+                        if (!masked) {
+#pragma unroll
+                            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                                for (int c = 0; c < CT; ++c) o[a][c] = fmaf(w[a], vv[c], o[a][c]);
+                        } else {  // a value of a key that the row does not see may be anything
+#pragma unroll
+                            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                                for (int c = 0; c < CT; ++c) o[a][c] = w[a] != 0.f ? fmaf(w[a], vv[c], o[a][c]) : o[a][c];
+                        }
+                    }
+                }
+                constexpr int CV = CT >= 4 ? 4 : CT;
+                const bool whole = k0 == 0 && k1 == keys;
+                const int which = k0 == 0 ? 1 : 0;
+                float *data = p.part_data + (size_t(cta) * 2 + which) * size_t(BM) * (D + 2);
+                if (!whole && tid == 0) my_parts[which] = Part{at.n, at.h, at.tile, k1 == keys ? 2 : 1};
+#pragma unroll
+                for (int a = 0; a < RT; ++a) {
+                    const int r = ty * RT + a;
+                    if (r >= rows) continue;
+                    const float inv = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
+                    Act *dst = static_cast<Act *>(p.out) + size_t(sq.row0 + tok0 + r / p.group) * size_t(p.out_stride) +
+                               size_t(at.h * p.group + r % p.group) * D;
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        const int ch = c / CV * 16 * CV + tx * CV + c % CV;
+                        if (whole) dst[ch] = from_f32<Act>(o[a][c] * inv);
+                        else data[size_t(r) * D + ch] = o[a][c];
+                    }
+                    if (!whole && tx == 0) data[BM * D + r] = m[a], data[BM * D + BM + r] = l[a];
+                }
+                if (last) return;
+            }
+        }
+        if (at.n >= end.n) return;
+    }
+}
+
+template <typename Act, typename Kv, int BM, int D>
+kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    auto kern = attend_generic_kernel<Act, Kv, BM, D>;
+    const int smem = int(sizeof(Smem<BM, D>));
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    p.key_step = KS;
+    p.min_keys = 2 * KS;
+    const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
+    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), kThreads, size_t(smem), stream, p);
+}
+
+template <typename Act, typename Kv>
+kda_status by_size(int D, AttendParams &p, const AttendPlan &plan, cudaStream_t s) {
+    switch (D * 100 + plan.bm) {
+        case 1616: return launch<Act, Kv, 16, 16>(p, plan, s);
+        case 1664: return launch<Act, Kv, 64, 16>(p, plan, s);
+        case 3216: return launch<Act, Kv, 16, 32>(p, plan, s);
+        case 3264: return launch<Act, Kv, 64, 32>(p, plan, s);
+        case 6416: return launch<Act, Kv, 16, 64>(p, plan, s);
+        case 6464: return launch<Act, Kv, 64, 64>(p, plan, s);
+        case 12816: return launch<Act, Kv, 16, 128>(p, plan, s);
+        case 12864: return launch<Act, Kv, 64, 128>(p, plan, s);
+    }
+    return KDA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
+    const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
+    plan->bm = rows <= 16 ? 16 : 64;
+    plan->n_cta = 2 * sm_count();
+    return true;
+}
+
+kda_status generic_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    const int D = c->head_dim;
+    const bool e4 = c->format == KDA_KV_E4M3;
+    if (c->act == KDA_BF16)
+        return e4 ? by_size<__nv_bfloat16, uint8_t>(D, p, plan, stream)
+                  : by_size<__nv_bfloat16, __nv_bfloat16>(D, p, plan, stream);
+    return e4 ? by_size<float, uint8_t>(D, p, plan, stream) : by_size<float, float>(D, p, plan, stream);
+}
+
+}  // namespace kv
+}  // namespace kda

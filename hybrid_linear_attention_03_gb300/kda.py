@@ -32,6 +32,9 @@ KDA_BF16 = 1
 KDA_DEVERR_SLOT_RANGE = 0x1
 KDA_DEVERR_META = 0x2
 KDA_DEVERR_TIMEOUT = 0x4
+KDA_DEVERR_PAGE_RANGE = 0x8
+KDA_KV_ACT = 0
+KDA_KV_E4M3 = 1
 KDA_POOL_OVERLAP_INPUTS = 0x1
 
 # Every symbol include/kda.h declares.
@@ -41,11 +44,13 @@ EXPORTS = ("kda_state_pool_bytes", "kda_state_pool_create", "kda_state_pool_dest
            "kda_state_slot_bytes", "kda_state_export", "kda_state_import", "kda_prefill_workspace_bytes_bound",
            "kda_prefill_chunked_dev", "kda_prefix_cache_create", "kda_prefix_cache_destroy", "kda_prefix_cache_plan",
            "kda_prefix_cache_forget", "kda_prefix_cache_get_stats", "kda_prefix_cache_saved", "kda_stream_wait",
-           "kda_state_pool_set_flags", "kda_profile_start", "kda_profile_stop", "kda_state_prefetch")
+           "kda_state_pool_set_flags", "kda_profile_start", "kda_profile_stop", "kda_state_prefetch",
+           "kda_kv_append", "kda_kv_read", "kda_kv_attend_workspace_bytes", "kda_kv_attend",
+           "kda_kv_poll_device_error")
 
 # kda_kernel_kind
 KERNEL_KINDS = ("step", "slot_copy", "prefill_meta", "prefill_intra", "prefill_chain", "prefill_out", "prefill_tails",
-                "state_prefetch", "prefill_intra_exact")
+                "state_prefetch", "prefill_intra_exact", "kv_append", "kv_read", "kv_attend", "kv_combine")
 
 KDA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -88,6 +93,36 @@ class kda_prefix_cache_stats(ctypes.Structure):
 class kda_profile(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_int64 * len(KERNEL_KINDS)), ("ms", ctypes.c_double * len(KERNEL_KINDS)),
                 ("dropped", ctypes.c_int64)]
+
+
+class kda_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("err", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("act", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class kda_kv_batch(ctypes.Structure):
+    _fields_ = [("cu_seqlens", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_new", ctypes.c_int32)]
+
+
+class kda_qk_params(ctypes.Structure):
+    _fields_ = [("q_norm_w", ctypes.c_void_p), ("k_norm_w", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class kda_kv_io(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64)]
+
+
+class kda_attn_io(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
 class KdaError(RuntimeError):
@@ -168,6 +203,16 @@ def lib() -> ctypes.CDLL:
         L.kda_profile_start.restype = i32
         L.kda_profile_stop.argtypes = [P(kda_profile)]
         L.kda_profile_stop.restype = i32
+        L.kda_kv_append.argtypes = [P(kda_kv_cache), P(kda_qk_params), P(kda_kv_io), P(kda_kv_batch), vp]
+        L.kda_kv_append.restype = i32
+        L.kda_kv_read.argtypes = [P(kda_kv_cache), P(kda_kv_batch), vp, vp, vp]
+        L.kda_kv_read.restype = i32
+        L.kda_kv_attend_workspace_bytes.argtypes = [P(kda_kv_cache), P(kda_kv_batch)]
+        L.kda_kv_attend_workspace_bytes.restype = sz
+        L.kda_kv_attend.argtypes = [P(kda_kv_cache), P(kda_attn_io), P(kda_kv_batch), vp, sz, vp]
+        L.kda_kv_attend.restype = i32
+        L.kda_kv_poll_device_error.argtypes = [P(kda_kv_cache), vp, P(ctypes.c_uint32)]
+        L.kda_kv_poll_device_error.restype = i32
         L.kda_status_string.argtypes = [i32]
         L.kda_status_string.restype = ctypes.c_char_p
         _LIB = L
@@ -517,3 +562,185 @@ class PrefixCache:
 
     def saved(self) -> dict:
         return kda_prefix_cache_saved(self.handle)
+
+
+# ---- full attention over a paged cache ------------------------------------------------
+
+
+class PagedKV:
+    """A paged key / value cache of one layer (a kda_kv_cache record and the
+    tensors behind it).  k and v are [num_pages, num_kv_heads, page_size,
+    head_dim] in ``act`` (kv_format "act") or float8_e4m3fn ("e4m3", with
+    k_scale and v_scale uint8 [num_pages, num_kv_heads, page_size]); those not
+    given are allocated, zero-filled, on ``device``."""
+
+    def __init__(self, num_pages, page_size, num_heads, num_kv_heads, head_dim, act: torch.dtype = torch.bfloat16,
+                 kv_format: str = "act", k=None, v=None, k_scale=None, v_scale=None, device="cuda"):
+        if kv_format not in ("act", "e4m3"):
+            raise ValueError(f"kv_format must be \"act\" or \"e4m3\", not {kv_format!r}")
+        e4m3 = kv_format == "e4m3"
+        dtype = torch.float8_e4m3fn if e4m3 else act
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        for t in (k, v, k_scale, v_scale):
+            if t is not None:
+                device = t.device
+                break
+
+        def pages(t, name):
+            if t is None:
+                return torch.zeros(shape, dtype=torch.uint8 if e4m3 else act, device=device).view(dtype)
+            return _kv_tensor(t, name, dtype, shape, device)
+
+        def scales(t, name):
+            if not e4m3:
+                if t is not None:
+                    raise ValueError(f"{name} is for kv_format \"e4m3\"")
+                return None
+            if t is None:
+                return torch.zeros(shape[:3], dtype=torch.uint8, device=device)
+            return _kv_tensor(t, name, torch.uint8, shape[:3], device)
+
+        self.k, self.v = pages(k, "k"), pages(v, "v")
+        self.k_scale, self.v_scale = scales(k_scale, "k_scale"), scales(v_scale, "v_scale")
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device, self.act, self.kv_format = self.k.device, act, kv_format
+        self.num_pages, self.page_size, self.num_heads = num_pages, page_size, num_heads
+        self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
+        self.desc = kda_kv_cache(self.k.data_ptr(), self.v.data_ptr(), _addr(self.k_scale), _addr(self.v_scale),
+                                 self.err.data_ptr(), num_pages, page_size, num_heads, num_kv_heads, head_dim,
+                                 act_code(act), KDA_KV_E4M3 if e4m3 else KDA_KV_ACT)
+
+    def error_word(self) -> torch.Tensor:
+        return self.err
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _kv_tensor(t, name, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != torch.device(device) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _row_stride(t, name):
+    """[rows][heads][head_dim] with the heads of a row back to back; the row stride in elements."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with each row's heads back to back")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def make_kv_batch(cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, max_rows: int,
+                  max_new: int) -> kda_kv_batch:
+    """The batch's device tables (int32: cu_seqlens [n + 1], kv_lens [n],
+    page_table [n, pages]) and host bounds; the record keeps the tensors alive."""
+    n = kv_lens.numel()
+    for name, t, shape in (("cu_seqlens", cu_seqlens, (n + 1,)), ("kv_lens", kv_lens, (n,)),
+                           ("page_table", page_table, (n,) + tuple(page_table.shape[1:]))):
+        if not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {shape}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, pages]")
+    b = kda_kv_batch(cu_seqlens.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), n, page_table.shape[1],
+                     int(max_rows), int(max_new))
+    b._tensors = (cu_seqlens, kv_lens, page_table)
+    return b
+
+
+def make_qk_params(q_norm_w: torch.Tensor | None = None, k_norm_w: torch.Tensor | None = None, eps: float = 1e-5,
+                   inv_freq=(), interleaved: bool = False) -> kda_qk_params:
+    """Norm weights (or None) and the rotation: inv_freq holds one frequency
+    (radians per position) per rotated pair, so 2 * len(inv_freq) channels turn."""
+    freq = [float(f) for f in inv_freq]
+    arr = (ctypes.c_double * max(1, len(freq)))(*freq)
+    p = kda_qk_params(_addr(q_norm_w), _addr(k_norm_w), float(eps), 2 * len(freq), int(bool(interleaved)),
+                      ctypes.cast(arr, ctypes.POINTER(ctypes.c_double)) if freq else None)
+    p._tensors = (q_norm_w, k_norm_w, arr)
+    return p
+
+
+def make_kv_io(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, q_out: torch.Tensor | None) -> kda_kv_io:
+    """Row tensors [rows, heads, head_dim] (rows may be strided); q and q_out
+    may both be None (keys and values only)."""
+    io = kda_kv_io(_addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), _row_stride(q, "q") if q is not None else 0,
+                   _row_stride(k, "k"), _row_stride(v, "v"), _row_stride(q_out, "q_out") if q_out is not None else 0)
+    io._tensors = (q, k, v, q_out)
+    return io
+
+
+def make_attn_io(q: torch.Tensor, out: torch.Tensor, scale: float | None = None) -> kda_attn_io:
+    """q and out [rows, num_heads, head_dim]; scale defaults to head_dim^-0.5."""
+    s = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
+    io = kda_attn_io(q.data_ptr(), out.data_ptr(), _row_stride(q, "q"), _row_stride(out, "out"), s)
+    io._tensors = (q, out)
+    return io
+
+
+def _check_rows(kv: PagedKV, batch: kda_kv_batch, where: str, **tensors) -> None:
+    """The row tensors hold max_rows rows of the cache's heads, type and device."""
+    for name, (t, heads) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != kv.act or t.device != kv.device or t.shape[0] < batch.max_rows or t.shape[1] != heads \
+                or t.shape[2] != kv.head_dim:
+            raise ValueError(f"{where}: {name} must be a {kv.act} tensor on {kv.device} of shape "
+                             f"[>= {batch.max_rows}, {heads}, {kv.head_dim}]")
+
+
+def _kv_stream(kv: PagedKV, batch: kda_kv_batch, stream, where: str) -> ctypes.c_void_p:
+    """The call's stream; it, the cache, the batch and the current device must be on one GPU."""
+    if stream is None:
+        stream = torch.cuda.current_stream(kv.device)
+    if stream.device != kv.device or torch.cuda.current_device() != kv.device.index:
+        raise ValueError(f"{where}: the cache is on {kv.device}: make it the current device and use its stream")
+    if batch is not None and batch._tensors[0].device != kv.device:
+        raise ValueError(f"{where}: the batch's tables are not on {kv.device}")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def kda_kv_append(kv: PagedKV, params: kda_qk_params | None, io: kda_kv_io, batch: kda_kv_batch, stream=None) -> None:
+    """Norm and rotation of q and k per head, q to q_out, k and v to their pages."""
+    q, k, v, q_out = io._tensors
+    _check_rows(kv, batch, "kda_kv_append", q=(q, kv.num_heads), k=(k, kv.num_kv_heads), v=(v, kv.num_kv_heads),
+                q_out=(q_out, kv.num_heads))
+    if params is not None:
+        for name, w in (("q_norm_w", params._tensors[0]), ("k_norm_w", params._tensors[1])):
+            if w is not None and (w.dtype != kv.act or w.device != kv.device or tuple(w.shape) != (kv.head_dim,)
+                                  or not w.is_contiguous()):
+                raise ValueError(f"kda_kv_append: {name} must be a contiguous {kv.act} tensor [{kv.head_dim}]")
+    st = lib().kda_kv_append(ctypes.byref(kv.desc), ctypes.byref(params) if params is not None else None,
+                             ctypes.byref(io), ctypes.byref(batch), _kv_stream(kv, batch, stream, "kda_kv_append"))
+    _check(st, "kda_kv_append")
+
+
+def kda_kv_read(kv: PagedKV, batch: kda_kv_batch, k_out: torch.Tensor, v_out: torch.Tensor, stream=None) -> None:
+    """The batch's tokens read back from their pages into contiguous rows."""
+    _check_rows(kv, batch, "kda_kv_read", k_out=(k_out, kv.num_kv_heads), v_out=(v_out, kv.num_kv_heads))
+    if not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError("kda_kv_read: k_out and v_out must be contiguous")
+    _check(lib().kda_kv_read(ctypes.byref(kv.desc), ctypes.byref(batch), k_out.data_ptr(), v_out.data_ptr(),
+                             _kv_stream(kv, batch, stream, "kda_kv_read")), "kda_kv_read")
+
+
+def kda_kv_attend_workspace_bytes(kv: PagedKV, batch: kda_kv_batch) -> int:
+    return int(lib().kda_kv_attend_workspace_bytes(ctypes.byref(kv.desc), ctypes.byref(batch)))
+
+
+def kda_kv_attend(kv: PagedKV, io: kda_attn_io, batch: kda_kv_batch, workspace: torch.Tensor, stream=None) -> None:
+    """Causal attention of the batch's tokens over their sequences' pages."""
+    q, out = io._tensors
+    _check_rows(kv, batch, "kda_kv_attend", q=(q, kv.num_heads), out=(out, kv.num_heads))
+    if workspace is not None and workspace.device != kv.device:
+        raise ValueError(f"kda_kv_attend: the workspace is not on {kv.device}")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kda_kv_attend(ctypes.byref(kv.desc), ctypes.byref(io), ctypes.byref(batch), _dptr(workspace), ws_bytes,
+                               _kv_stream(kv, batch, stream, "kda_kv_attend")), "kda_kv_attend")
+
+
+def kda_kv_poll_device_error(kv: PagedKV, stream=None) -> tuple[int, int]:
+    """Returns (status, flags) of the cache's error word; reading clears it."""
+    flags = ctypes.c_uint32(0)
+    st = int(lib().kda_kv_poll_device_error(ctypes.byref(kv.desc), _kv_stream(kv, None, stream, "kda_kv_poll_device_error"),
+                                            ctypes.byref(flags)))
+    return st, int(flags.value)

@@ -404,6 +404,135 @@ KDA_API int32_t kda_prefix_cache_saved(const kda_prefix_cache *cache, int32_t *l
  * and clears it.  Returns KDA_ERR_DEVICE if any bit was set, else KDA_OK. */
 KDA_API kda_status kda_poll_device_error(kda_pool *pool, kda_stream_t stream, uint32_t *flags);
 
+/* ---- Full attention over a paged cache ----------------------------------
+ * The other half of a hybrid layer stack: its full-attention layers keep keys
+ * and values in pages beside the KDA state slots.  Source: "vLLM Kimi K3
+ * 지원", section "Kimi K3 아키텍처 개요" (KDA layers interleaved with full
+ * attention) and section "하이브리드 KV-Cache 관리" (paged KV blocks next to
+ * the KDA state blocks).  The pages print no formulas for them; these are
+ *   norm    x <- x * w / sqrt(mean(x^2) + eps)           per q and k head
+ *   rotate  (a, b) <- (a cos - b sin, a sin + b cos), angle p * inv_freq[i],
+ *           on pair i of the first rot_dim channels       per q and k head
+ *   attend  o = sum_j softmax_j(scale * q . k_j) v_j over the keys j <= p
+ * for the token at position p; query head h reads cache head
+ * h / (num_heads / num_kv_heads).
+ *
+ * A cache is plain device memory described by kda_kv_cache, one per layer:
+ *   k, v              [num_pages][num_kv_heads][page_size][head_dim], in the
+ *                     activation dtype (KDA_KV_ACT) or in e4m3 (KDA_KV_E4M3)
+ *   k_scale, v_scale  KDA_KV_E4M3 only: [num_pages][num_kv_heads][page_size]
+ *                     bytes; a vector stands for e4m3 * 2^(byte - 127).  The
+ *                     exponent is the smallest that brings the vector's
+ *                     largest finite magnitude to at most 448 (byte 0 for a
+ *                     vector of zeros); an infinity or NaN is stored as NaN.
+ *   err               one device uint32, the cache's error word
+ * Position p of a sequence is line p % page_size of page
+ * page_table[seq][p / page_size].  Sequences may share pages that no call
+ * writes; a call must not write the same line twice.
+ *
+ * A batch (kda_kv_batch) names the tokens a call works on: sequence n owns
+ * the rows [cu_seqlens[n], cu_seqlens[n+1]), T_n of them, and row
+ * cu_seqlens[n] + t is its token at position kv_lens[n] - T_n + t, so kv_lens
+ * counts the call's own tokens.  T_n may be 0.  All three tables are DEVICE
+ * arrays, read when the call runs, so the calls can sit in a CUDA graph.
+ * Rows past cu_seqlens[n_seqs] are neither read nor written.
+ * Device errors: a sequence whose tables are inconsistent (cu_seqlens
+ * decreasing or past max_rows, more than max_new tokens, kv_lens below T_n or
+ * past page_table's width) sets KDA_DEVERR_META and its rows are left as they
+ * were; a page outside the cache sets KDA_DEVERR_PAGE_RANGE, and its tokens
+ * are not written, read back as zeros, and are absent from the attention.
+ * The work may start while the preceding kernel on its stream finishes
+ * (programmatic dependent launch); it reads nothing until that kernel has
+ * completed. */
+#define KDA_DEVERR_PAGE_RANGE 0x8u /* a page index was outside the cache */
+
+typedef enum { KDA_KV_ACT = 0, KDA_KV_E4M3 = 1 } kda_kv_format;
+
+typedef struct {
+    void *k, *v;                /* 16-byte aligned */
+    uint8_t *k_scale, *v_scale; /* NULL for KDA_KV_ACT */
+    uint32_t *err;
+    int32_t num_pages;    /* > 0 */
+    int32_t page_size;    /* 16, 32, 64 or 128 */
+    int32_t num_heads;    /* query heads, a multiple of num_kv_heads, at most 64 times it */
+    int32_t num_kv_heads; /* > 0 */
+    int32_t head_dim;     /* 16, 32, 64 or 128 */
+    int32_t act;          /* kda_dtype of q, k, v, outputs and norm weights */
+    int32_t format;       /* kda_kv_format */
+} kda_kv_cache;
+
+typedef struct {
+    const int32_t *cu_seqlens; /* [n_seqs + 1], from 0 */
+    const int32_t *kv_lens;    /* [n_seqs] */
+    const int32_t *page_table; /* [n_seqs][table_stride] */
+    int32_t n_seqs;
+    int32_t table_stride; /* pages a sequence may have */
+    int32_t max_rows;     /* host bound on cu_seqlens[n_seqs]: the row tensors have this many rows */
+    int32_t max_new;      /* host bound on the tokens of one sequence (1 for a decode step) */
+} kda_kv_batch;
+
+/* The norm and rotation of kda_kv_append. */
+typedef struct {
+    const void *q_norm_w, *k_norm_w; /* [head_dim] act, 16-byte aligned; NULL: no norm */
+    float eps;
+    int32_t rot_dim;        /* 0 (no rotation) .. head_dim, a multiple of 8 */
+    int32_t interleaved;    /* 0: pair i is channels (i, i + rot_dim/2); 1: (2i, 2i + 1) */
+    const double *inv_freq; /* HOST [rot_dim / 2]: radians per position (read during the call) */
+} kda_qk_params;
+
+/* Row tensors of kda_kv_append: a row holds its heads back to back; the next
+ * row starts *_stride elements later (a multiple of 16 bytes, so the rows may
+ * be slices of one fused projection). */
+typedef struct {
+    const void *q; /* [rows][num_heads][head_dim], or NULL with q_out: keys and values only */
+    const void *k; /* [rows][num_kv_heads][head_dim] */
+    const void *v;
+    void *q_out;   /* may be q itself (with the same stride) */
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+} kda_kv_io;
+
+typedef struct {
+    const void *q; /* [rows][num_heads][head_dim] act, normalised and rotated */
+    void *out;     /* [rows][num_heads][head_dim] act; must not overlap q */
+    int64_t q_stride, out_stride;
+    float scale; /* finite; usually 1 / sqrt(head_dim) */
+} kda_attn_io;
+
+/* Normalises and rotates q and k per head, writes q to q_out and k and v to
+ * their pages (quantised once, from 32-bit values).  One launch.  p may be
+ * NULL: no norm, no rotation.  Angles are exact to 32 bits at any position:
+ * they are reduced in 64-bit fixed point.
+ * Errors: KDA_ERR_INVALID_ARG (null or misaligned pointers, bad sizes or
+ * strides, only one of q and q_out), KDA_ERR_UNSUPPORTED (sizes outside the
+ * lists above), KDA_ERR_CUDA.  n_seqs = 0 or max_rows = 0 is a no-op. */
+KDA_API kda_status kda_kv_append(const kda_kv_cache *cache, const kda_qk_params *p, const kda_kv_io *io,
+                                 const kda_kv_batch *batch, kda_stream_t stream);
+
+/* Reads the batch's tokens back from their pages: k_out and v_out
+ * [max_rows][num_kv_heads][head_dim] act, contiguous, 16-byte aligned.
+ * KDA_KV_ACT lines come back bit for bit; e4m3 lines as value * 2^exponent
+ * (exact in bf16 and fp32).  Errors as kda_kv_append's. */
+KDA_API kda_status kda_kv_read(const kda_kv_cache *cache, const kda_kv_batch *batch, void *k_out, void *v_out,
+                               kda_stream_t stream);
+
+/* Causal attention of the batch's tokens over their sequences' pages (the
+ * tokens' own lines included, so kda_kv_append comes first).  One call serves
+ * a decode step (max_new = 1), a speculative verify (a few) and a chunk of a
+ * prompt; keys behind a row's position are never weighed, whatever they hold.
+ * A row whose keys are all absent or score -inf gets zeros.
+ * workspace: device, 256-byte aligned, at least
+ * kda_kv_attend_workspace_bytes(cache, batch) bytes (the host fields of batch
+ * set it; 0 on invalid input); its contents mean nothing between calls, and
+ * calls that share one must be ordered.  Results do not depend on it.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE,
+ * KDA_ERR_CUDA. */
+KDA_API size_t kda_kv_attend_workspace_bytes(const kda_kv_cache *cache, const kda_kv_batch *batch);
+KDA_API kda_status kda_kv_attend(const kda_kv_cache *cache, const kda_attn_io *io, const kda_kv_batch *batch,
+                                 void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* kda_poll_device_error for a cache's error word. */
+KDA_API kda_status kda_kv_poll_device_error(const kda_kv_cache *cache, kda_stream_t stream, uint32_t *flags);
+
 /* Host watchdog: waits for the work enqueued on `stream` (NULL: the legacy
  * default stream) by polling it, for at most timeout_s seconds, instead of
  * blocking without limit.  KDA_OK once it has finished; KDA_ERR_TIMEOUT if it
@@ -442,6 +571,10 @@ typedef enum {
     KDA_KERNEL_PREFILL_INTRA_EXACT, /* intra-chunk prefill kernel with per-pair decay exponents (bf16
                                   inputs: the chunk-heads the factored kernel hands over; fp32 inputs:
                                   every chunk-head) */
+    KDA_KERNEL_KV_APPEND,      /* kda_kv_append */
+    KDA_KERNEL_KV_READ,        /* kda_kv_read */
+    KDA_KERNEL_KV_ATTEND,      /* kda_kv_attend: scores, softmax and values over each CTA's share of the keys */
+    KDA_KERNEL_KV_COMBINE,     /* kda_kv_attend: the shares of one row tile joined */
     KDA_KERNEL_COUNT
 } kda_kernel_kind;
 typedef struct {
