@@ -127,6 +127,56 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
     return true;
 }
 
+// One item's share of a CTA's piece.
+struct Item {
+    int n, h, tile;
+    int k0, k1, keys;  // this CTA's keys [k0, k1) of the item's [0, keys)
+    int row0;          // row of the sequence's first token
+    int ctx;           // position of that token
+    int tok0, rows;    // the tile's first token and its rows
+    __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == keys; }
+    // where a part goes: the CTA's first part slot, or its last one for a part that begins its item
+    __device__ __forceinline__ int slot() const { return k0 == 0 ? 1 : 0; }
+    __device__ __forceinline__ Part part() const { return Part{n, h, tile, k1 == keys ? 2 : 1}; }
+    // element offset of row r's channels in a row tensor
+    __device__ __forceinline__ size_t at(int r, int group, long long stride, int D) const {
+        return size_t(row0 + tok0 + r / group) * size_t(stride) + size_t(h * group + r % group) * size_t(D);
+    }
+};
+
+// Walks a piece item by item; every role of a kernel runs its own copy.
+struct ItemWalk {
+    Cursor at, end;
+    Seq sq;
+    int tiles = -1;  // of sequence at.n; -1: not read yet
+    __device__ __forceinline__ ItemWalk(const Cursor &a, const Cursor &z) : at(a), end(z) {}
+    __device__ __forceinline__ bool next(const AttendParams &p, Item &it) {
+        while (at.n < p.b.n_seqs && at.n <= end.n) {
+            if (tiles < 0) tiles = load_seq(p.b, at.n, sq, false) ? (sq.T + p.tile_tokens - 1) / p.tile_tokens : 0;
+            if (tiles == 0 || at.h >= p.hkv) {
+                at = Cursor{at.n + 1, 0, 0, 0};
+                tiles = -1;
+                continue;
+            }
+            if (at.tile >= tiles) {
+                at = Cursor{at.n, at.h + 1, 0, 0};
+                continue;
+            }
+            const bool last = at.n == end.n && at.h == end.h && at.tile == end.tile;
+            it.n = at.n, it.h = at.h, it.tile = at.tile;
+            it.row0 = sq.row0, it.ctx = sq.L - sq.T;
+            it.tok0 = at.tile * p.tile_tokens;
+            it.rows = min(p.tile_tokens, sq.T - it.tok0) * p.group;
+            it.keys = tile_keys(it.ctx, sq.T, p.tile_tokens, at.tile);
+            it.k0 = at.key, it.k1 = last ? end.key : it.keys;
+            if (last) at.n = p.b.n_seqs;  // done
+            else ++at.tile, at.key = 0;
+            if (it.k0 < it.k1) return true;
+        }
+        return false;
+    }
+};
+
 // Workspace: the part records of every CTA, then their data, 256-aligned.
 __host__ __device__ __forceinline__ size_t parts_bytes(int n_cta) {
     return (sizeof(Part) * 2 * size_t(n_cta) + 255) / 256 * 256;
@@ -141,6 +191,8 @@ struct AttendPlan {
     int bm;     // rows of a tile
     int n_cta;  // grid
 };
+bool tile_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
+kda_status tile_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
 kda_status generic_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 

@@ -62,187 +62,162 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
     }
     __syncthreads();
     if (!s.has) return;
-    Cursor at = s.piece[0];
-    const Cursor end = s.piece[1];
+    ItemWalk walk(s.piece[0], s.piece[1]);
+    Item it;
     const int page_mask = (1 << p.b.page_shift) - 1;
 
-    for (; at.n < p.b.n_seqs; ++at.n, at.h = 0, at.tile = 0, at.key = 0) {
-        Seq sq;
-        if (!load_seq(p.b, at.n, sq, false) || sq.T == 0) {
-            if (at.n >= end.n) return;
-            continue;
+    while (walk.next(p, it)) {
+        __syncthreads();
+        for (int i = tid; i < BM * D / 4; i += kThreads) {
+            const int r = i % BM, c = i / BM * 4;
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            if (r < it.rows) load4<Act>(static_cast<const Act *>(p.q) + it.at(r, p.group, p.q_stride, D) + c, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s.q[c + e][r] = x[e] * p.scale_log2;
         }
-        const int tiles = (sq.T + p.tile_tokens - 1) / p.tile_tokens, ctx = sq.L - sq.T;
-        for (; at.h < p.hkv; ++at.h, at.tile = 0, at.key = 0) {
-            for (; at.tile < tiles; ++at.tile, at.key = 0) {
-                const bool last = at.n == end.n && at.h == end.h && at.tile == end.tile;
-                const int keys = tile_keys(ctx, sq.T, p.tile_tokens, at.tile);
-                const int k0 = at.key, k1 = last ? end.key : keys;
-                if (k0 >= k1) {
-                    if (last) return;
-                    continue;
-                }
-                const int tok0 = at.tile * p.tile_tokens, rows = min(p.tile_tokens, sq.T - tok0) * p.group;
-                __syncthreads();
-                for (int i = tid; i < BM * D / 4; i += kThreads) {
-                    const int r = i % BM, c = i / BM * 4;
-                    float x[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (r < rows)
-                        load4<Act>(static_cast<const Act *>(p.q) +
-                                       size_t(sq.row0 + tok0 + r / p.group) * size_t(p.q_stride) +
-                                       size_t(at.h * p.group + r % p.group) * D + c, x);
+        float o[RT][CT], m[RT], l[RT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s.q[c + e][r] = x[e] * p.scale_log2;
+        for (int a = 0; a < RT; ++a) {
+            m[a] = -INFINITY, l[a] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) o[a][c] = 0.f;
+        }
+        int lim[RT];  // last key a row sees
+#pragma unroll
+        for (int a = 0; a < RT; ++a) {
+            const int r = ty * RT + a;
+            lim[a] = r < it.rows ? it.ctx + it.tok0 + r / p.group : -1;
+        }
+        for (int kb = it.k0; kb < it.k1; kb += KS) {
+            __syncthreads();  // the previous step's keys and values are done with
+            bool hidden = false;  // this thread's key is absent, or behind some row's position
+            if (tid < KS) {
+                const int j = kb + tid;
+                int64_t line = -1;
+                if (j < it.k1) {
+                    const int page = load_page(p.b, it.n, j);
+                    if (page >= 0)
+                        line = ((int64_t(page) * p.hkv + it.h) << p.b.page_shift) + (j & page_mask);
                 }
-                float o[RT][CT], m[RT], l[RT];
+                s.line[tid] = line;
+                hidden = line < 0 || j > it.ctx + it.tok0;
+            }
+            const bool masked = __syncthreads_or(hidden);
+            for (int i = tid; i < KS * D / 4; i += kThreads) {
+                const int j = i / (D / 4), c = i % (D / 4) * 4;
+                float xk[4] = {0.f, 0.f, 0.f, 0.f}, xv[4] = {0.f, 0.f, 0.f, 0.f};
+                const int64_t line = s.line[j];
+                if (line >= 0) {
+                    load4<Kv>(static_cast<const Kv *>(p.pk) + line * D + c, xk);
+                    load4<Kv>(static_cast<const Kv *>(p.pv) + line * D + c, xv);
+                    if constexpr (sizeof(Kv) == 1) {
+                        const float fk = exp2_biased(p.sk[line]), fv = exp2_biased(p.sv[line]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) xk[e] *= fk, xv[e] *= fv;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s.k[c + e][j] = xk[e];
+                *reinterpret_cast<float4 *>(&s.v[j][c]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
+            }
+            __syncthreads();
+            float x[RT][4];
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[a][e] = 0.f;
+#pragma unroll 8
+            for (int c = 0; c < D; ++c) {
+                const float4 kk = *reinterpret_cast<const float4 *>(&s.k[c][tx * 4]);
+                float qq[RT];
+                if constexpr (RT == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(&s.q[c][ty * 4]);
+                    qq[0] = t.x, qq[1] = t.y, qq[2] = t.z, qq[3] = t.w;
+                } else {
+#pragma unroll
+                    for (int a = 0; a < RT; ++a) qq[a] = s.q[c][ty * RT + a];
+                }
 #pragma unroll
                 for (int a = 0; a < RT; ++a) {
-                    m[a] = -INFINITY, l[a] = 0.f;
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) o[a][c] = 0.f;
+                    x[a][0] = fmaf(qq[a], kk.x, x[a][0]);
+                    x[a][1] = fmaf(qq[a], kk.y, x[a][1]);
+                    x[a][2] = fmaf(qq[a], kk.z, x[a][2]);
+                    x[a][3] = fmaf(qq[a], kk.w, x[a][3]);
                 }
-                int lim[RT];  // last key a row sees
+            }
+            if (masked) {
 #pragma unroll
-                for (int a = 0; a < RT; ++a) {
-                    const int r = ty * RT + a;
-                    lim[a] = r < rows ? ctx + tok0 + r / p.group : -1;
+                for (int e = 0; e < 4; ++e) {
+                    const bool there = s.line[tx * 4 + e] >= 0;
+#pragma unroll
+                    for (int a = 0; a < RT; ++a)
+                        if (!there || kb + tx * 4 + e > lim[a]) x[a][e] = -INFINITY;
                 }
-                for (int kb = k0; kb < k1; kb += KS) {
-                    __syncthreads();  // the previous step's keys and values are done with
-                    bool hidden = false;  // this thread's key is absent, or behind some row's position
-                    if (tid < KS) {
-                        const int j = kb + tid;
-                        int64_t line = -1;
-                        if (j < k1) {
-                            const int page = load_page(p.b, at.n, j);
-                            if (page >= 0)
-                                line = ((int64_t(page) * p.hkv + at.h) << p.b.page_shift) + (j & page_mask);
-                        }
-                        s.line[tid] = line;
-                        hidden = line < 0 || j > ctx + tok0;
-                    }
-                    const bool masked = __syncthreads_or(hidden);
-                    for (int i = tid; i < KS * D / 4; i += kThreads) {
-                        const int j = i / (D / 4), c = i % (D / 4) * 4;
-                        float xk[4] = {0.f, 0.f, 0.f, 0.f}, xv[4] = {0.f, 0.f, 0.f, 0.f};
-                        const int64_t line = s.line[j];
-                        if (line >= 0) {
-                            load4<Kv>(static_cast<const Kv *>(p.pk) + line * D + c, xk);
-                            load4<Kv>(static_cast<const Kv *>(p.pv) + line * D + c, xv);
-                            if constexpr (sizeof(Kv) == 1) {
-                                const float fk = exp2_biased(p.sk[line]), fv = exp2_biased(p.sv[line]);
+            }
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) xk[e] *= fk, xv[e] *= fv;
-                            }
-                        }
+            for (int a = 0; a < RT; ++a) {
+                float mx = fmaxf(fmaxf(x[a][0], x[a][1]), fmaxf(x[a][2], x[a][3]));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s.k[c + e][j] = xk[e];
-                        *reinterpret_cast<float4 *>(&s.v[j][c]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
-                    }
-                    __syncthreads();
-                    float x[RT][4];
+                for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const float mn = fmaxf(m[a], mx), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[a] - ref);
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[a][e] = exp2f(x[a][e] - ref);
+                    sum += x[a][e];
+                    s.p[tx * 4 + e][ty * RT + a] = x[a][e];
+                }
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                l[a] = l[a] * f + sum;
+                m[a] = mn;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) o[a][c] *= f;
+            }
+            __syncwarp();  // a row's weights are written and read by the same half warp
+            // channels of a thread: groups of four (or the D / 16 there are) 16 groups apart
+            constexpr int CV = CT >= 4 ? 4 : CT;
+#pragma unroll 4
+            for (int j = 0; j < KS; ++j) {
+                float w[RT], vv[CT];
+#pragma unroll
+                for (int a = 0; a < RT; ++a) w[a] = s.p[j][ty * RT + a];
+#pragma unroll
+                for (int g = 0; g < CT / CV; ++g)
+#pragma unroll
+                    for (int e = 0; e < CV; ++e) vv[g * CV + e] = s.v[j][g * 16 * CV + tx * CV + e];
+                if (!masked) {
 #pragma unroll
                     for (int a = 0; a < RT; ++a)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[a][e] = 0.f;
-#pragma unroll 8
-                    for (int c = 0; c < D; ++c) {
-                        const float4 kk = *reinterpret_cast<const float4 *>(&s.k[c][tx * 4]);
-                        float qq[RT];
-                        if constexpr (RT == 4) {
-                            const float4 t = *reinterpret_cast<const float4 *>(&s.q[c][ty * 4]);
-                            qq[0] = t.x, qq[1] = t.y, qq[2] = t.z, qq[3] = t.w;
-                        } else {
+                        for (int c = 0; c < CT; ++c) o[a][c] = fmaf(w[a], vv[c], o[a][c]);
+                } else {  // a value of a key that the row does not see may be anything
 #pragma unroll
-                            for (int a = 0; a < RT; ++a) qq[a] = s.q[c][ty * RT + a];
-                        }
+                    for (int a = 0; a < RT; ++a)
 #pragma unroll
-                        for (int a = 0; a < RT; ++a) {
-                            x[a][0] = fmaf(qq[a], kk.x, x[a][0]);
-                            x[a][1] = fmaf(qq[a], kk.y, x[a][1]);
-                            x[a][2] = fmaf(qq[a], kk.z, x[a][2]);
-                            x[a][3] = fmaf(qq[a], kk.w, x[a][3]);
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool there = s.line[tx * 4 + e] >= 0;
-#pragma unroll
-                            for (int a = 0; a < RT; ++a)
-                                if (!there || kb + tx * 4 + e > lim[a]) x[a][e] = -INFINITY;
-                        }
-                    }
-#pragma unroll
-                    for (int a = 0; a < RT; ++a) {
-                        float mx = fmaxf(fmaxf(x[a][0], x[a][1]), fmaxf(x[a][2], x[a][3]));
-#pragma unroll
-                        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        const float mn = fmaxf(m[a], mx), ref = mn == -INFINITY ? 0.f : mn;
-                        const float f = exp2f(m[a] - ref);
-                        float sum = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[a][e] = exp2f(x[a][e] - ref);
-                            sum += x[a][e];
-                            s.p[tx * 4 + e][ty * RT + a] = x[a][e];
-                        }
-#pragma unroll
-                        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                        l[a] = l[a] * f + sum;
-                        m[a] = mn;
-#pragma unroll
-                        for (int c = 0; c < CT; ++c) o[a][c] *= f;
-                    }
-                    __syncwarp();  // a row's weights are written and read by the same half warp
-                    // channels of a thread: groups of four (or the D / 16 there are) 16 groups apart
-                    constexpr int CV = CT >= 4 ? 4 : CT;
-#pragma unroll 4
-                    for (int j = 0; j < KS; ++j) {
-                        float w[RT], vv[CT];
-#pragma unroll
-                        for (int a = 0; a < RT; ++a) w[a] = s.p[j][ty * RT + a];
-#pragma unroll
-                        for (int g = 0; g < CT / CV; ++g)
-#pragma unroll
-                            for (int e = 0; e < CV; ++e) vv[g * CV + e] = s.v[j][g * 16 * CV + tx * CV + e];
-                        if (!masked) {
-#pragma unroll
-                            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                                for (int c = 0; c < CT; ++c) o[a][c] = fmaf(w[a], vv[c], o[a][c]);
-                        } else {  // a value of a key that the row does not see may be anything
-#pragma unroll
-                            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                                for (int c = 0; c < CT; ++c) o[a][c] = w[a] != 0.f ? fmaf(w[a], vv[c], o[a][c]) : o[a][c];
-                        }
-                    }
+                        for (int c = 0; c < CT; ++c) o[a][c] = w[a] != 0.f ? fmaf(w[a], vv[c], o[a][c]) : o[a][c];
                 }
-                constexpr int CV = CT >= 4 ? 4 : CT;
-                const bool whole = k0 == 0 && k1 == keys;
-                const int which = k0 == 0 ? 1 : 0;
-                float *data = p.part_data + (size_t(cta) * 2 + which) * size_t(BM) * (D + 2);
-                if (!whole && tid == 0) my_parts[which] = Part{at.n, at.h, at.tile, k1 == keys ? 2 : 1};
-#pragma unroll
-                for (int a = 0; a < RT; ++a) {
-                    const int r = ty * RT + a;
-                    if (r >= rows) continue;
-                    const float inv = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
-                    Act *dst = static_cast<Act *>(p.out) + size_t(sq.row0 + tok0 + r / p.group) * size_t(p.out_stride) +
-                               size_t(at.h * p.group + r % p.group) * D;
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        const int ch = c / CV * 16 * CV + tx * CV + c % CV;
-                        if (whole) dst[ch] = from_f32<Act>(o[a][c] * inv);
-                        else data[size_t(r) * D + ch] = o[a][c];
-                    }
-                    if (!whole && tx == 0) data[BM * D + r] = m[a], data[BM * D + BM + r] = l[a];
-                }
-                if (last) return;
             }
         }
-        if (at.n >= end.n) return;
+        constexpr int CV = CT >= 4 ? 4 : CT;
+        const bool whole = it.whole();
+        float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * (D + 2);
+        if (!whole && tid == 0) my_parts[it.slot()] = it.part();
+#pragma unroll
+        for (int a = 0; a < RT; ++a) {
+            const int r = ty * RT + a;
+            if (r >= it.rows) continue;
+            const float inv = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
+            Act *dst = static_cast<Act *>(p.out) + it.at(r, p.group, p.out_stride, D);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const int ch = c / CV * 16 * CV + tx * CV + c % CV;
+                if (whole) dst[ch] = from_f32<Act>(o[a][c] * inv);
+                else data[size_t(r) * D + ch] = o[a][c];
+            }
+            if (!whole && tx == 0) data[BM * D + r] = m[a], data[BM * D + BM + r] = l[a];
+        }
     }
 }
 

@@ -107,7 +107,7 @@ kda_status kda_kv_attend(const kda_kv_cache *cache, const kda_attn_io *io, const
     const CallRange range("kda_kv_attend");
     kda_status st = check_cache(cache);
     if (st != KDA_OK || (st = check_batch(batch)) != KDA_OK) return st;
-    if (!io || !std::isfinite(io->scale)) return KDA_ERR_INVALID_ARG;
+    if (!io || !(io->scale > 0.f) || !std::isfinite(io->scale * 1.4426950f)) return KDA_ERR_INVALID_ARG;
     if (empty(batch)) return KDA_OK;
     if (!good_rows(io->q, io->q_stride, cache->num_heads, cache) ||
         !good_rows(io->out, io->out_stride, cache->num_heads, cache) || io->q == io->out)

@@ -495,7 +495,7 @@ typedef struct {
     const void *q; /* [rows][num_heads][head_dim] act, normalised and rotated */
     void *out;     /* [rows][num_heads][head_dim] act; must not overlap q */
     int64_t q_stride, out_stride;
-    float scale; /* finite; usually 1 / sqrt(head_dim) */
+    float scale; /* > 0, finite; usually 1 / sqrt(head_dim) */
 } kda_attn_io;
 
 /* Normalises and rotates q and k per head, writes q to q_out and k and v to

@@ -98,7 +98,7 @@ def test_bad_norm_and_rotation(lib):
 def test_bad_attend_arguments(lib):
     c, b = cache(), batch()
     for kw in (dict(q=None), dict(out=A), dict(out=2 * A + 2), dict(q_stride=8), dict(out_stride=513),
-               dict(scale=float("inf"))):
+               dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(scale=float("nan"))):
         assert lib.kda_kv_attend(ref(c), ref(attn_io(**kw)), ref(b), A, 1 << 40, None) == BAD, kw
     need = lib.kda_kv_attend_workspace_bytes(ref(c), ref(b))
     assert need > 0
