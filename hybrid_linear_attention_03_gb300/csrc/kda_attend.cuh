@@ -5,9 +5,10 @@
 // An item is one row tile: the query heads of one cache head (the group, G of
 // them) for TT consecutive tokens of one sequence, rows r = t * G + g.  Its
 // keys are positions [0, ctx + last token + 1).  All items of a call, ordered
-// by sequence, cache head and tile, form one line whose length is the sum of
-// their key counts, and CTA c of C takes the c-th of C equal pieces of that
-// line (cut points rounded down to whole key steps inside an item).  So any
+// by sequence, cache head and tile, form one line; an item is as long on it as
+// it has keys, plus a constant for its start and output (in keys that take as
+// long).  CTA c of C takes the c-th of C equal pieces of that line (a cut point
+// inside an item rounded down to whole key steps).  So any
 // mix of lengths loads every CTA alike, with no table built on the host and
 // no launch per sequence.  An item cut by one or more cut points is computed
 // in parts: every part leaves its unnormalised output, row maxima and row sums
@@ -37,6 +38,7 @@ struct AttendParams {
     int32_t hq, hkv, group;
     int32_t tile_tokens;  // TT
     int32_t key_step;     // keys per step; cut points are multiples of it
+    int32_t item_cost;    // what an item costs beside its keys
     int32_t min_keys;     // a CTA's piece is at least this long (fewer CTAs take part in a small call)
     float scale_log2;     // scale * log2(e)
     Part *parts;          // [C][2]: the CTA's first part (of an item begun before) and its last
@@ -46,12 +48,12 @@ struct AttendParams {
 // Keys of tile i's last row: how far the item reaches.
 __device__ __forceinline__ int tile_keys(int ctx, int T, int tt, int i) { return ctx + min(T, (i + 1) * tt); }
 
-// Sum of tile_keys over the first m tiles of a sequence (m <= ceil(T / tt)).
-__device__ __forceinline__ long long tile_prefix(int ctx, int T, int tt, int m) {
-    const int full = min(m, T / tt);
+// Length on the line of the first m tiles of a sequence (m <= ceil(T / tt)).
+__device__ __forceinline__ long long tile_prefix(const AttendParams &p, int ctx, int T, int m) {
+    const int tt = p.tile_tokens, full = min(m, T / tt);
     long long s = static_cast<long long>(full) * ctx + static_cast<long long>(tt) * full * (full + 1) / 2;
     if (m > full) s += ctx + T;
-    return s;
+    return s + static_cast<long long>(p.item_cost) * m;
 }
 
 struct Cursor {  // a place on the line: key `key` of item (n, h, tile)
@@ -69,7 +71,7 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
     for (int n = n0; n < n1; ++n) {
         Seq s;
         if (load_seq(p.b, n, s, cta == 0) && s.T > 0)
-            sum += tile_prefix(s.L - s.T, s.T, tt, (s.T + tt - 1) / tt) * p.hkv;
+            sum += tile_prefix(p, s.L - s.T, s.T, (s.T + tt - 1) / tt) * p.hkv;
     }
     long long before = sum;  // inclusive scan over the lanes
 #pragma unroll
@@ -96,7 +98,7 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
                     Seq s;
                     if (!load_seq(p.b, n, s, false) || s.T == 0) continue;
                     const int ctx = s.L - s.T, tiles = (s.T + tt - 1) / tt;
-                    const long long head = tile_prefix(ctx, s.T, tt, tiles);
+                    const long long head = tile_prefix(p, ctx, s.T, tiles);
                     if (rest >= head * p.hkv) {
                         rest -= head * p.hkv;
                         continue;
@@ -107,11 +109,11 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
                     int lo = 0, hi = tiles - 1;  // last tile whose prefix is at most rest
                     while (lo < hi) {
                         const int mid = (lo + hi + 1) / 2;
-                        if (tile_prefix(ctx, s.T, tt, mid) <= rest) lo = mid;
+                        if (tile_prefix(p, ctx, s.T, mid) <= rest) lo = mid;
                         else hi = mid - 1;
                     }
                     c[e].tile = lo;
-                    const int key = int(rest - tile_prefix(ctx, s.T, tt, lo));
+                    const int key = max(int(rest - tile_prefix(p, ctx, s.T, lo)) - p.item_cost, 0);
                     c[e].key = key / p.key_step * p.key_step;
                     break;
                 }

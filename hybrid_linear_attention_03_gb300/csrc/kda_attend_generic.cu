@@ -230,6 +230,7 @@ kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) 
         return KDA_ERR_CUDA;
     }
     p.key_step = KS;
+    p.item_cost = KS;
     p.min_keys = 2 * KS;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
     return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), kThreads, size_t(smem), stream, p);

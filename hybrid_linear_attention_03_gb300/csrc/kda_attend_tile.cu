@@ -3,14 +3,16 @@
 // head sizes 64 and 128).
 //
 // Softmax in one pass, as in kda_attend_generic.cu: scores X = Q K^T (128 rows
-// x 128 keys) land in tensor memory, one thread per row turns them into
-// weights P = 2^(scale log2e X - ref) and leaves them as bf16 where the scores
-// were, and O += P V reads them from there.  Two of these run side by side so
-// that one's products cover the other's exponentials:
+// x 128 keys) land in tensor memory, one thread per row turns them into weights
+// P = 2^(scale log2e X - ref) and leaves them as bf16 where the scores were,
+// and O += P V reads them from there.  Two of these run side by side so that
+// one's products cover the other's exponentials:
 //   sides by rows  (row tiles of 256): side s has rows [128 s, 128 s + 128) and
 //                  both read every key tile (half the L2 traffic per product);
 //   sides by keys  (at most 128 rows an item): both have all rows, side s has
 //                  the key tiles of its parity, joined at the item's end.
+// The weights are handed over in two halves, so the product of the first runs
+// under the exponentials of the second.
 // ref is the row's maximum so far, but only moved (and O and the sums scaled
 // by 2^(ref - ref')) when a tile exceeds it by more than 8: weights then reach
 // 2^8 at most, which costs no precision in bf16 and fp32, and most tiles leave
@@ -18,16 +20,16 @@
 // size of the output's own rounding, and not correlated between keys); scores,
 // sums and O stay in 32 bits.
 //
-// Warps: 0-3 side 0, 4-7 side 1 (a thread a row), 8 issues the products, 9
-// fetches pages by TMA into a ring of tiles (K_0, V_0, K_1, V_1, ...), 10 and 11
-// fill the warpgroup; with
-// e4m3 pages warp 9 fetches them raw and warps 12-15 turn them into exact bf16
-// tiles.  Page sizes divide the tile, so a tile is 1 to 8 page boxes.
+// Warps: 0-3 side 0, 4-7 side 1 (a thread a row); 8 and 9 issue a side's
+// products each; 10 fetches pages by TMA into a ring of tiles (K_0, V_0, K_1,
+// V_1, ...); 12-15 bring the rows of Q and look value tiles over (below); with
+// e4m3 pages warp 10 fetches them raw with their scales, and warps 16-19 turn
+// them into exact bf16 tiles.
 //
 // A value behind a row's position weighs nothing, but 0 * NaN is NaN in the
-// product: in the few tiles where some row does not see some key, keys that
-// are absent are zeroed in the tile, and non-finite value rows are taken out of
-// it too and added by the threads whose rows do see them.
+// product.  So in the few tiles where some row does not see some key, warps
+// 12-15 zero the rows of absent keys in the value tile, and take non-finite
+// value rows out of it; the row threads that do see those add them one by one.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -44,14 +46,18 @@ using namespace sm100;
 constexpr int KT = 128;          // keys of a tile
 constexpr int kSideRows = 128;   // rows of a side
 constexpr float kRefSlack = 8.f;
+#ifndef ITEM_COST
+#define ITEM_COST 384
+#endif
+constexpr int kItemCost = ITEM_COST;
 
 template <int D, bool kE4m3> struct Cfg {
-    static constexpr int kThreads = kE4m3 ? 512 : 384;
+    static constexpr int kThreads = kE4m3 ? 640 : 512;
     // Registers a thread after the split: every SM quarter holds two softmax
-    // warps and one (bf16) or two (e4m3) others, 168 or 128 registers each at
-    // launch: 256 * 216 + 128 * 72 = 384 * 168, 256 * 192 + 256 * 64 = 512 * 128.
-    static constexpr int kRegsSoftmax = kE4m3 ? 192 : 216;
-    static constexpr int kRegsOther = kE4m3 ? 64 : 72;
+    // warps and two (bf16) or three (e4m3) others, 128 or 96 registers each at
+    // launch: 256 * 200 + 256 * 56 = 512 * 128, 256 * 152 + 384 * 56 < 640 * 96.
+    static constexpr int kRegsSoftmax = kE4m3 ? 152 : 200;
+    static constexpr int kRegsOther = 56;
     static constexpr int kTileBytes = KT * D * 2;
     static constexpr int kQBytes = kSideRows * D * 2;
     static constexpr int kStages = D == 128 ? (kE4m3 ? 4 : 5) : 8;
@@ -62,13 +68,23 @@ template <int D, bool kE4m3> struct Cfg {
     static constexpr int kMiscAt = kRawAt + kRawStages * kRawBytes;
 };
 
+// Barriers of the ring's fills, more than it has stages: fill f (K and V tiles
+// in turn) lands in stage f % stages but reports on barrier f % kFills.  A wait
+// by parity is only sound for a thread that sees every phase of its barrier, and
+// a side or a look-over that takes every second tile, or only the V tiles, sees
+// every phase of every barrier it uses (kFills is a multiple of 4), whatever the
+// number of stages and the order in which copies land.
+constexpr int kFills = 16;
+constexpr int kLooked = kFills / 2;  // of value tiles looked over
+
 struct Misc {
-    uint64_t full[8], empty[8], raw_full[2], raw_empty[2];
-    uint64_t s_full[2], p_ready[2], q_full[2], o_full[2], done;
+    uint64_t full[kFills], empty[kFills], clean[kLooked], raw_full[2], raw_empty[2];
+    uint64_t s_full[2], p_ready[2][2], q_full[2], q_free[2], o_full[2], done[2];
     uint32_t tmem;
     int has;
     Cursor piece[2];
-    uint32_t odd[2][4];     // per side: keys of the tile whose value row was taken out
+    uint32_t odd[kLooked][4];          // by tile: keys whose value row was taken out of it
+    alignas(16) uint8_t scale[2][KT];  // e4m3: the raw tile's scale exponents
     float m[kSideRows], l[kSideRows];  // side 1's row statistics, for the join
 };
 
@@ -101,14 +117,20 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
     return r;
 }
-// D[tmem] += A[tmem] * B[smem], A bf16 with two K values a column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+// D[tmem] (+)= A[tmem] * B[smem], A bf16 with two K values a column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, 1, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc)
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// 16-byte asynchronous copy, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void *smem_dst, const void *gsrc, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(there ? 16 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -159,27 +181,123 @@ __device__ __forceinline__ bool odd_bf16(const uint4 &w) {
 
 // A bounded wait that is skipped once one has given up.  The row warps then run
 // on with whatever is there (all in bounds, the error word is set), so that the
-// CTA's own barriers are met; the other roles stop issuing.
+// CTA's own barriers are met; the other roles stop issuing.  Each try sleeps for
+// up to a millisecond: a thread that polls takes issue slots from the others, and
+// reading the clock takes longer than most waits.
 __device__ __forceinline__ void wait_for(bool &ok, uint64_t *bar, uint32_t parity, uint32_t *err) {
-    if (ok) ok = mbar_wait(bar, parity, err);
+    if (!ok) return;
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (done) return;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > 2000000000ull) break;
+    }
+    atomicOr(err, KDA_DEVERR_TIMEOUT);
+    ok = false;
 }
+// The stage of fill f is free: the fill that was there before has been used.
+template <int kStages> __device__ __forceinline__ void wait_stage(bool &ok, uint64_t *empty, uint32_t f, uint32_t *err) {
+    if (f >= kStages) wait_for(ok, &empty[(f - kStages) % kFills], ((f - kStages) / kFills) & 1, err);
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// 32 bytes, one whole sector, to a 32-byte aligned place.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ bool any_odd(const uint32_t *odd) { return (odd[0] | odd[1] | odd[2] | odd[3]) != 0; }
 
 struct TileMaps {
     CUtensorMap k, v;
 };
 
-// Key tiles of an item's share that side s computes.
+__device__ __forceinline__ int item_tiles(const Item &it) { return (it.k1 - it.k0 + KT - 1) / KT; }
+// Key tiles of an item's share that side s computes, and the v-th of them.
 template <bool kByKeys> __device__ __forceinline__ int side_tiles(const Item &it, int s) {
-    const int nt = (it.k1 - it.k0 + KT - 1) / KT;
-    if (kByKeys) return (nt - s + 1) / 2;
-    return s * kSideRows < it.rows ? nt : 0;
+    if (kByKeys) return (item_tiles(it) - s + 1) / 2;
+    return s * kSideRows < it.rows ? item_tiles(it) : 0;
+}
+template <bool kByKeys> __device__ __forceinline__ int side_tile(int s, int v) { return kByKeys ? 2 * v + s : v; }
+
+// Bit g: keys [kb + 16 g, kb + 16 g + 16) are in a page outside the cache.
+__device__ __forceinline__ uint32_t absent_groups(const AttendParams &p, const Item &it, int kb, int lane) {
+    bool bad = false;
+    if (lane < KT / 16 && kb + lane * 16 < it.k1) bad = load_page(p.b, it.n, kb + lane * 16) < 0;
+    return __ballot_sync(0xffffffffu, bad);
+}
+// Some row of the item does not see some key of the tile at kb.
+__device__ __forceinline__ bool partly_seen(const Item &it, int kb, uint32_t absent) {
+    return absent != 0 || kb + KT - 1 > it.ctx + it.tok0;
+}
+
+// Adds the value rows that were taken out of a tile to O, for the rows that see
+// them (a row's weight is read back from its bf16 place over the scores).  Rare,
+// so short rather than fast.  Whole warp.
+template <int D, bool kE4m3>
+__device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it, int kb, int lim, const uint32_t *odd,
+                                          uint32_t t_s, uint32_t t_o, bool fresh) {
+    if (fresh) {
+        const float z[16] = {};
+        for (int c = 0; c < D; c += 16) tmem_st16(t_o + uint32_t(c), z);
+        tmem_wait_st();
+    }
+    for (int g = 0; g < KT / 32; ++g) {
+        for (uint32_t left = odd[g]; left; left &= left - 1) {
+            const int c = g * 32 + __ffs(left) - 1, j = kb + c;
+            const uint32_t pw = tmem_ld1(t_s + uint32_t(c / 2));
+            tmem_wait_ld();
+            const float w = __uint_as_float(c & 1 ? pw & 0xffff0000u : pw << 16);
+            const int page = load_page(p.b, it.n, j);
+            const size_t vec = ((size_t(max(page, 0)) * size_t(p.hkv) + size_t(it.h)) << p.b.page_shift) +
+                               size_t(j & ((1 << p.b.page_shift) - 1));
+            for (int ch = 0; ch < D; ch += 16) {
+                float o[16];
+                tmem_ld16(t_o + uint32_t(ch), o);
+                tmem_wait_ld();
+                if (j <= lim && w != 0.f) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float val;
+                        if constexpr (kE4m3)
+                            val = unpack_e4m3(static_cast<const uint8_t *>(p.pv)[vec * D + ch + i]).x * exp2_biased(p.sv[vec]);
+                        else
+                            val = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.pv)[vec * D + ch + i]);
+                        o[i] = fmaf(w, val, o[i]);
+                    }
+                }
+                __syncwarp();
+                tmem_st16(t_o + uint32_t(ch), o);
+                tmem_wait_st();
+            }
+        }
+    }
 }
 
 template <int D, bool kE4m3, bool kByKeys>
 __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
     attend_tile_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TileMaps maps) {
     using C = Cfg<D, kE4m3>;
-    constexpr int NST = C::kStages, BM = kByKeys ? kSideRows : 2 * kSideRows;
+    constexpr int NST = C::kStages, NRAW = kE4m3 ? C::kRawStages : 1, BM = kByKeys ? kSideRows : 2 * kSideRows;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc &ms = *reinterpret_cast<Misc *>(smem + C::kMiscAt);
@@ -187,20 +305,24 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
     unsigned char *ring = smem + C::kRingAt;
 
     if (tid == 0) {
-        for (int i = 0; i < NST; ++i) mbar_init(&ms.full[i], kE4m3 ? 4 : 1), mbar_init(&ms.empty[i], 1);
+        for (int i = 0; i < kFills; ++i) {
+            mbar_init(&ms.full[i], kE4m3 ? 4 : 1);
+            mbar_init(&ms.empty[i], kByKeys ? 1 : 2);  // by rows both sides are done with a tile
+        }
+        for (int i = 0; i < kLooked; ++i) mbar_init(&ms.clean[i], 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], 4);
-            mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4);
-            mbar_init(&ms.q_full[i], 4), mbar_init(&ms.o_full[i], 1);
+            mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i][0], 4), mbar_init(&ms.p_ready[i][1], 4);
+            mbar_init(&ms.q_full[i], 4), mbar_init(&ms.q_free[i], 1);
+            mbar_init(&ms.o_full[i], 1), mbar_init(&ms.done[i], 1);
         }
-        mbar_init(&ms.done, 1);
         fence_mbar_init();
     }
     if (warp == 8) tmem_alloc(&ms.tmem, 512);
     wait_prior_kernel();
     allow_next_kernel();
     if (tid < 2) p.parts[2 * cta + tid].state = 0;
-    if (warp == 9) {
+    if (warp == 10) {
         Cursor a, z;
         const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
         if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has;
@@ -210,6 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
     tc_fence_after();
     const uint32_t tm = ms.tmem;
     uint32_t *err = p.b.err;
+    bool ok = true;  // of this thread's waits
 
     if (warp < 8) {
         reg_inc<C::kRegsSoftmax>();
@@ -218,54 +341,19 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
             const int s = warp >> 2, row = tid & 127;
             const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
             const uint32_t t_s = tm + lanes + uint32_t(s) * 128u, t_o = tm + lanes + 256u + uint32_t(s) * 128u;
-            unsigned char *q_img = smem + s * C::kQBytes;
-            const int rb = kByKeys ? 0 : s * kSideRows, r = rb + row;
+            const int r = (kByKeys ? 0 : s * kSideRows) + row;
             ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it, nx;
-            bool ok = true, has = walk.next(p, it);
-            uint32_t n_s = 0, n_o = 0, n_o2 = 0;  // visits and items so far: barrier phases
-            uint32_t ring_base = 0;
-
-            auto load_q = [&](const Item &x) {
-                if (side_tiles<kByKeys>(x, s) == 0) return;
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                                   x.at(min(r, x.rows - 1), p.group, p.q_stride, D));
-#pragma unroll
-                for (int c0 = 0; c0 < D / 8; c0 += 8) {
-                    uint4 w[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) w[c] = r < x.rows ? src[c0 + c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(q_img + sw128_chunk(row, c0 + c, kSideRows)) = w[c];
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.q_full[s]);
-            };
-
-            if (has) load_q(it);
-            while (has) {
-                const int nv = side_tiles<kByKeys>(it, s), nt = (it.k1 - it.k0 + KT - 1) / KT;
+            Item it;
+            uint32_t n_s = 0, n_o = 0, tile_base = 0;  // tiles and items so far: barrier phases
+            while (walk.next(p, it)) {
+                const int nv = side_tiles<kByKeys>(it, s);
                 const int lim = it.ctx + it.tok0 + min(r, it.rows - 1) / p.group;  // last key this row sees
-                const int first_lim = it.ctx + it.tok0;                           // ... and the item's first row
                 float ref = -INFINITY, l = 0.f;
-                if (nv > 0) {
-                    uint32_t z[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = 0;
-#pragma unroll
-                    for (int c = 0; c < D; c += 16) tmem_st16u(t_o + uint32_t(c), z);
-                    tmem_wait_st();
-                }
-                for (int v = 0; v < nv; ++v) {
-                    const int t = kByKeys ? 2 * v + s : v, kb = it.k0 + t * KT;
-                    // pages of the tile, 16 keys a lane
-                    bool bad = false;
-                    if (lane < KT / 16 && kb + lane * 16 < it.k1) bad = load_page(p.b, it.n, kb + lane * 16) < 0;
-                    const uint32_t absent = __ballot_sync(0xffffffffu, bad);
-                    const bool check = absent != 0 || kb + KT - 1 > first_lim;
-                    wait_for(ok, &ms.s_full[s], n_s++ & 1, err);
+                for (int v = 0; v < nv; ++v, ++n_s) {
+                    const int t = side_tile<kByKeys>(s, v), kb = it.k0 + t * KT;
+                    const uint32_t absent = absent_groups(p, it, kb, lane);
+                    const bool check = partly_seen(it, kb, absent);
+                    wait_for(ok, &ms.s_full[s], n_s & 1, err);  // and with it the product before
                     __syncwarp();
                     tc_fence_after();
                     float x[KT];
@@ -281,13 +369,14 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
 #pragma unroll
                     for (int c = 4; c < KT; c += 8) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mx[i] = c + 4 + i < KT ? fmaxf(fmaxf(mx[i], x[c + i]), x[c + 4 + i]) : fmaxf(mx[i], x[c + i]);
+                        for (int i = 0; i < 4; ++i)
+                            mx[i] = c + 4 + i < KT ? fmaxf(fmaxf(mx[i], x[c + i]), x[c + 4 + i]) : fmaxf(mx[i], x[c + i]);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
                     const bool move = top > ref + kRefSlack;
                     if (__any_sync(0xffffffffu, move)) {
                         const float to = move ? top : ref, f = move ? ex2(ref - to) : 1.f;
-                        if (v > 0) {  // O holds zeros until the first product
+                        if (v > 0) {  // O is new with the first product
 #pragma unroll
                             for (int c = 0; c < D; c += 16) {
                                 float o[16];
@@ -315,100 +404,39 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
                             w[i] = pack_bf16(e.x, e.y);
                         }
                         tmem_st16u(t_s + uint32_t(c / 2), w);
+                        if (c == KT / 2 - 32 && !check) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&ms.p_ready[s][0]);
+                        }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     if (check) {
-                        // this thread's key: absent, or a non-finite value row behind some row's position
-                        const int j = kb + row;
-                        const uint32_t slot = ring_base + 2u * uint32_t(t) + 1u;
-                        unsigned char *v_img = ring + (slot % NST) * C::kTileBytes;
-                        const int page = j < it.k1 && !(absent >> (row / 16) & 1) ? load_page(p.b, it.n, j) : -1;
-                        const size_t vec = page < 0 ? 0 : ((size_t(page) * size_t(p.hkv) + size_t(it.h)) << p.b.page_shift) +
-                                                              size_t(j & ((1 << p.b.page_shift) - 1));
-                        bool odd = false;
-                        if (page >= 0 && j > first_lim) {
-                            if constexpr (kE4m3) {
-                                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.pv) + vec * D);
-                                for (int c = 0; c < D / 16; ++c) {
-                                    const uint4 w = src[c];
-                                    odd |= ((__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                                             __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0);
-                                }
-                                odd |= p.sv[vec] >= 247;  // 448 * 2^(247 - 127) is past bf16's range
-                            } else {
-                                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.pv) + vec * D);
-                                for (int c = 0; c < D / 8; ++c) odd |= odd_bf16(src[c]);
-                            }
-                        }
-                        const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                        if (lane == 0) ms.odd[s][warp & 3] = word;
-                        wait_for(ok, &ms.full[slot % NST], (slot / NST) & 1, err);
+                        const uint32_t at = tile_base + uint32_t(t), lk = at % kLooked;
+                        wait_for(ok, &ms.clean[lk], (at / kLooked) & 1, err);
                         __syncwarp();
-                        if (page < 0 || odd) {
-#pragma unroll
-                            for (int c = 0; c < D / 8; ++c)
-                                *reinterpret_cast<uint4 *>(v_img + sw128_chunk(row, c, KT)) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        if (s) named_sync<2, 128>();
-                        else named_sync<1, 128>();
-                        for (int g = 0; g < 4; ++g) {
-                            for (uint32_t left = ms.odd[s][g]; left; left &= left - 1) {
-                                const int c = g * 32 + __ffs(left) - 1, jj = kb + c;
-                                const uint32_t pw = tmem_ld1(t_s + uint32_t(c / 2));
-                                tmem_wait_ld();
-                                const float w = __uint_as_float(c & 1 ? pw & 0xffff0000u : pw << 16);
-                                const int pg = load_page(p.b, it.n, jj);
-                                const size_t at = ((size_t(pg) * size_t(p.hkv) + size_t(it.h)) << p.b.page_shift) +
-                                                  size_t(jj & ((1 << p.b.page_shift) - 1));
-                                for (int ch = 0; ch < D; ch += 16) {
-                                    float o[16];
-                                    tmem_ld16(t_o + uint32_t(ch), o);
-                                    tmem_wait_ld();
-                                    if (jj <= lim && w != 0.f) {
-                                        for (int i = 0; i < 16; ++i) {
-                                            float val;
-                                            if constexpr (kE4m3)
-                                                val = unpack_e4m3(static_cast<const uint8_t *>(p.pv)[at * D + ch + i]).x *
-                                                      exp2_biased(p.sv[at]);
-                                            else
-                                                val = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.pv)[at * D + ch + i]);
-                                            o[i] = fmaf(w, val, o[i]);
-                                        }
-                                    }
-                                    tmem_st16(t_o + uint32_t(ch), o);
-                                }
-                                tmem_wait_st();
-                            }
-                        }
-                        if (s) named_sync<2, 128>();
-                        else named_sync<1, 128>();  // odd[s] is rewritten by the next such tile
+                        if (any_odd(ms.odd[lk])) add_odd_rows<D, kE4m3>(p, it, kb, lim, ms.odd[lk], t_s, t_o, v == 0);
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.p_ready[s]);
+                    if (lane == 0) {
+                        if (check) mbar_arrive(&ms.p_ready[s][0]);
+                        mbar_arrive(&ms.p_ready[s][1]);
+                    }
                 }
-                has = walk.next(p, nx);
-                if (has) load_q(nx);  // every score product of this side has completed
-                ring_base += 2u * uint32_t(nt);
+                tile_base += uint32_t(item_tiles(it));
 
                 // ---- output ----------------------------------------------------------------
                 const int nv_other = kByKeys ? side_tiles<kByKeys>(it, 1 - s) : 0;
                 if (nv > 0) wait_for(ok, &ms.o_full[s], n_o++ & 1, err);
                 __syncwarp();
-                bool writes = nv > 0 && r < it.rows;
                 float f0 = 1.f, f1 = 0.f;
                 if (kByKeys) {
-                    if (s == 1) {
-                        ms.m[row] = ref, ms.l[row] = l;
-                        writes = false;
-                    } else if (nv_other > 0) {
-                        wait_for(ok, &ms.o_full[1], n_o2++ & 1, err);
-                        __syncwarp();
-                    }
+                    if (s == 1) ms.m[row] = ref, ms.l[row] = l;  // its products are done: side 0 may read both
                     tc_fence_before();
-                    named_sync<3, 256>();
+                    named_sync<1, 256>();
                     if (s == 0 && nv_other > 0) {
                         const float m1 = ms.m[row], top = fmaxf(ref, m1), base = top == -INFINITY ? 0.f : top;
                         f0 = ex2(ref - base), f1 = ex2(m1 - base);
@@ -419,9 +447,11 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
                 tc_fence_after();
                 if (!(kByKeys && s == 1) && nv > 0) {
                     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-                    const bool whole = it.whole();
+                    const bool whole = it.whole(), writes = r < it.rows;
+                    const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | uintptr_t(p.out_stride * 2)) & 31) == 0;
                     float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * (D + 2);
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p.group, p.out_stride, D);
+                    __nv_bfloat16 *dst =
+                        static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p.group, p.out_stride, D);
 #pragma unroll
                     for (int c = 0; c < D; c += 16) {
                         float o[16];
@@ -440,13 +470,20 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
                             uint32_t w[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) w[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-                            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            if (wide) {
+                                store32(dst + c, w);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4)
-                                *reinterpret_cast<float4 *>(data + size_t(r) * D + c + i) =
-                                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            for (int i = 0; i < 16; i += 8) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[i + e]);
+                                store32(data + size_t(r) * D + c + i, w);
+                            }
                         }
                     }
                     if (!whole) {
@@ -454,105 +491,129 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
                         if (s == 0 && row == 0) p.parts[2 * cta + it.slot()] = it.part();
                     }
                 }
-                if (kByKeys) {
-                    tc_fence_before();
-                    named_sync<3, 256>();  // side 1 clears its O for the next item
-                    tc_fence_after();
-                }
-                it = nx;
+                tc_fence_before();  // the next item's products rewrite O
+                if (kByKeys) named_sync<1, 256>();
             }
         }
     } else {
         reg_dec<C::kRegsOther>();
-        if (ms.has && warp == 8 && lane == 0) {
-            // ---- products --------------------------------------------------------------
+        if (ms.has && warp < 10) {
+            // ---- products of a side (converged warp, one lane issues) ----------------------
+            const int s = warp - 8;
             const uint32_t id_s = idesc_bf16_f32(128, KT), id_o = idesc_bf16_f32(128, D, false, true);
-            const uint32_t q_at = smem_u32(smem), ring_at = smem_u32(ring);
+            const uint32_t t_s = tm + uint32_t(s) * 128u, t_o = tm + 256u + uint32_t(s) * 128u;
+            const uint64_t q_desc = sdesc_sw128(smem_u32(smem) + uint32_t(s) * C::kQBytes);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(ring)), v_desc = sdesc_sw128_mn(smem_u32(ring), KT * 128u);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it;
-            bool ok = true;
-            uint32_t base = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-            auto scores = [&](int s, int t, bool last_user) {
-                const uint32_t slot = base + 2u * uint32_t(t), st = slot % NST;
-                wait_for(ok, &ms.full[st], (slot / NST) & 1, err);
-                if (!ok) return;
+            uint32_t base = 0, n_q = 0, n_p = 0;
+            int nv = 0;
+            // scores of the side's v-th tile (descriptors count 16-byte units)
+            auto scores = [&](int v) {
+                const uint32_t fill = base + 2u * uint32_t(side_tile<kByKeys>(s, v)), st = fill % NST;
+                wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+                if (!(ok = __all_sync(0xffffffffu, ok))) return;
                 tc_fence_after();
-                const uint32_t a = q_at + uint32_t(s) * C::kQBytes, b = ring_at + st * C::kTileBytes;
+                if (elect_one()) {
+                    const uint64_t kd = k_desc + uint64_t(st * (C::kTileBytes >> 4));
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = uint32_t(k >> 2) * (128u * 128u) + uint32_t(k & 3) * 32u;
-                    mma_bf16(tm + uint32_t(s) * 128u, sdesc_sw128(a + off), sdesc_sw128(b + off), id_s, k > 0);
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_bf16(t_s, q_desc + uint64_t((k >> 2) * (kSideRows * 8) + (k & 3) * 2),
+                                 kd + uint64_t((k >> 2) * (KT * 8) + (k & 3) * 2), id_s, k > 0);
+                    mma_commit(&ms.s_full[s]);
+                    mma_commit(&ms.empty[fill % kFills]);
+                    if (v + 1 == nv) mma_commit(&ms.q_free[s]);
                 }
-                if (last_user) mma_commit(&ms.empty[st]);
-                mma_commit(&ms.s_full[s]);
+                __syncwarp();
             };
             while (ok && walk.next(p, it)) {
-                const int nv[2] = {side_tiles<kByKeys>(it, 0), side_tiles<kByKeys>(it, 1)};
-                const int last_side = kByKeys ? -1 : (nv[1] > 0 ? 1 : 0);  // the last user of a shared tile
-                for (int s = 0; s < 2 && ok; ++s) {
-                    if (nv[s] == 0) continue;
-                    wait_for(ok, &ms.q_full[s], n_q[s]++ & 1, err);
-                    scores(s, kByKeys ? s : 0, kByKeys || s == last_side);
+                nv = side_tiles<kByKeys>(it, s);
+                if (nv > 0) {
+                    wait_for(ok, &ms.q_full[s], n_q++ & 1, err);
+                    scores(0);
                 }
-                for (int v = 0; v < max(nv[0], nv[1]) && ok; ++v) {
-                    for (int s = 0; s < 2 && ok; ++s) {
-                        if (v >= nv[s]) continue;
-                        const int t = kByKeys ? 2 * v + s : v;
-                        const uint32_t slot = base + 2u * uint32_t(t) + 1u, st = slot % NST;
-                        wait_for(ok, &ms.p_ready[s], n_p[s]++ & 1, err);
-                        wait_for(ok, &ms.full[st], (slot / NST) & 1, err);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t b = ring_at + st * C::kTileBytes;
+                for (int v = 0; v < nv && ok; ++v, ++n_p) {
+                    const uint32_t fill = base + 2u * uint32_t(side_tile<kByKeys>(s, v)) + 1u, st = fill % NST;
+                    wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+                    const uint32_t lk = (fill >> 1) % kLooked;
+                    wait_for(ok, &ms.clean[lk], ((fill >> 1) / kLooked) & 1, err);
+                    // the first product starts O, unless value rows were added to it by hand
+                    const uint32_t acc = v > 0 || any_odd(ms.odd[lk]);
+                    const uint64_t vd = v_desc + uint64_t(st * (C::kTileBytes >> 4));
 #pragma unroll
-                        for (int k = 0; k < KT / 16; ++k)
-                            mma_bf16_ta(tm + 256u + uint32_t(s) * 128u, tm + uint32_t(s) * 128u + uint32_t(k) * 8u,
-                                        sdesc_sw128_mn(b + uint32_t(k) * 2048u, KT * 128u), id_o);
-                        if (kByKeys || s == last_side) mma_commit(&ms.empty[st]);
-                        if (v + 1 < nv[s]) scores(s, kByKeys ? t + 2 : t + 1, kByKeys || s == last_side);
-                        else mma_commit(&ms.o_full[s]);
+                    for (int half = 0; half < 2; ++half) {
+                        wait_for(ok, &ms.p_ready[s][half], n_p & 1, err);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = half * (KT / 32); k < (half + 1) * (KT / 32); ++k)
+                                mma_bf16_ta(t_o, t_s + uint32_t(k) * 8u, vd + uint64_t(k * 128), id_o, k > 0 || acc);
+                            if (half == 1) {
+                                mma_commit(&ms.empty[fill % kFills]);
+                                if (v + 1 == nv) mma_commit(&ms.o_full[s]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && v + 1 < nv) scores(v + 1);
+                }
+                if (!kByKeys && nv == 0) {  // a tile is free once both sides have said so
+                    for (int i = 0; i < 2 * item_tiles(it) && ok; ++i) {
+                        const uint32_t fill = base + uint32_t(i);
+                        wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        if (lane == 0) mbar_arrive(&ms.empty[fill % kFills]);
                     }
                 }
-                base += 2u * uint32_t((it.k1 - it.k0 + KT - 1) / KT);
+                base += 2u * uint32_t(item_tiles(it));
             }
-            mma_commit(&ms.done);  // nothing of this CTA's is in flight when its tensor memory goes
-            mbar_wait(&ms.done, 0, err);
-        } else if (ms.has && warp == 9) {
+            // nothing of this side's is in flight when the tensor memory goes
+            if (elect_one()) mma_commit(&ms.done[s]);
+            __syncwarp();
+            bool end_ok = true;
+            wait_for(end_ok, &ms.done[s], 0, err);
+        } else if (ms.has && warp == 10) {
             // ---- page fetches ------------------------------------------------------------
-            const int page_rows = 1 << p.b.page_shift, boxes = KT >> p.b.page_shift;
+            const int page_size = 1 << p.b.page_shift, box = min(page_size, KT);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it;
-            bool ok = true;
-            uint32_t slot = 0;
+            uint32_t fill = 0;
             while (ok && walk.next(p, it)) {
                 for (int kb = it.k0; kb < it.k1 && ok; kb += KT) {
+                    const int j = kb + lane * box, line = j & (page_size - 1);
                     int page = -1;
-                    if (lane < boxes && kb + lane * page_rows < it.k1) page = load_page(p.b, it.n, kb + lane * page_rows);
-                    const int there = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    if (lane * box < KT && j < it.k1) page = load_page(p.b, it.n, j);
+                    const int there = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box;
                     const int plane = page * p.hkv + it.h;  // below 2^31 (checked on the host)
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++slot) {
+                    for (int kv = 0; kv < 2; ++kv, ++fill) {
                         const CUtensorMap *map = kv ? &maps.v : &maps.k;
                         if constexpr (kE4m3) {
-                            const uint32_t st = slot % 2;
-                            wait_for(ok, &ms.raw_empty[st], ((slot / 2) & 1) ^ 1, err);
+                            const uint32_t st = fill % NRAW;
+                            wait_for(ok, &ms.raw_empty[st], ((fill / NRAW) & 1) ^ 1, err);
                             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], uint32_t(there * page_rows * D));
-                            __syncwarp();
-                            if (page >= 0)
-                                tma_load_3d(smem + C::kRawAt + st * C::kRawBytes + lane * page_rows * D, map, &ms.raw_full[st],
-                                            0, 0, plane);
-                        } else {
-                            const uint32_t st = slot % NST;
-                            wait_for(ok, &ms.empty[st], ((slot / NST) & 1) ^ 1, err);
-                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&ms.full[st], uint32_t(there * page_rows * D * 2));
+                            if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], uint32_t(there * (D + 1)));
                             __syncwarp();
                             if (page >= 0) {
-                                unsigned char *dst = ring + st * C::kTileBytes + lane * page_rows * 128;
+                                tma_load_3d(smem + C::kRawAt + st * C::kRawBytes + lane * box * D, map, &ms.raw_full[st], 0,
+                                            line, plane);
+                                bulk_load(&ms.scale[st][lane * box],
+                                          (kv ? p.sv : p.sk) + (size_t(plane) << p.b.page_shift) + line, uint32_t(box),
+                                          &ms.raw_full[st]);
+                            }
+                        } else {
+                            const uint32_t st = fill % NST;
+                            uint64_t *full = &ms.full[fill % kFills];
+                            wait_stage<NST>(ok, ms.empty, fill, err);
+                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(there * D * 2));
+                            __syncwarp();
+                            if (page >= 0) {
+                                unsigned char *dst = ring + st * C::kTileBytes + lane * box * 128;
 #pragma unroll
                                 for (int c = 0; c < D / 64; ++c)
-                                    tma_load_3d(dst + c * KT * 128, map, &ms.full[st], c * 64, 0, plane);
+                                    tma_load_3d(dst + c * KT * 128, map, full, c * 64, line, plane);
                             }
                         }
                     }
@@ -560,62 +621,103 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
             }
             // a given-up wait elsewhere may leave copies in flight: they land before the CTA ends
             if (!ok) {
-                for (uint32_t i = 1; i <= (kE4m3 ? 2u : uint32_t(NST)) && i <= slot; ++i) {
-                    const uint32_t c = slot - i;
-                    if (kE4m3) mbar_wait(&ms.raw_full[c % 2], (c / 2) & 1, err);
-                    else mbar_wait(&ms.full[c % NST], (c / NST) & 1, err);
+                constexpr uint32_t kDepth = kE4m3 ? NRAW : NST;
+                for (uint32_t i = 1; i <= kDepth && i <= fill; ++i) {
+                    const uint32_t c = fill - i;
+                    if (kE4m3) mbar_wait(&ms.raw_full[c % NRAW], (c / NRAW) & 1, err);
+                    else mbar_wait(&ms.full[c % kFills], (c / kFills) & 1, err);
                 }
             }
-        } else if (kE4m3 && ms.has && warp >= 12) {
-            // ---- e4m3 tiles to bf16 ---------------------------------------------------------
-            constexpr int UPK = D / 16;  // 16-byte pieces of a key
-            const int ct = tid - 384;
+        } else if (ms.has && warp >= 12 && warp < 16) {
+            // ---- rows of Q, and value tiles looked over ------------------------------------
+            const int w = warp - 12, qt = tid - 384;
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it;
-            bool ok = true;
-            uint32_t slot = 0;
+            uint32_t n_q[2] = {0, 0}, tile = 0;
             while (ok && walk.next(p, it)) {
-                for (int kb = it.k0; kb < it.k1 && ok; kb += KT) {
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++slot) {
-                        // scales first: thread i looks up key i's, and the pieces get theirs by shuffle or memory
-                        const uint8_t *scales = kv ? p.sv : p.sk;
-                        float f[UPK];
-#pragma unroll
-                        for (int i = 0; i < UPK; ++i) {
-                            const int key = (i * 128 + ct) / UPK, j = kb + key;
-                            f[i] = 0.f;
-                            if (j < it.k1) {
-                                const int page = p.b.table[size_t(it.n) * size_t(p.b.table_stride) + size_t(j >> p.b.page_shift)];
-                                if (page >= 0 && page < p.b.num_pages)
-                                    f[i] = exp2_biased(scales[((size_t(page) * size_t(p.hkv) + size_t(it.h)) << p.b.page_shift) +
-                                                              size_t(j & ((1 << p.b.page_shift) - 1))]);
-                            }
-                        }
-                        const uint32_t rs = slot % 2, st = slot % NST;
-                        wait_for(ok, &ms.raw_full[rs], (slot / 2) & 1, err);
-                        wait_for(ok, &ms.empty[st], ((slot / NST) & 1) ^ 1, err);
-                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                        const uint4 *raw = reinterpret_cast<const uint4 *>(smem + C::kRawAt + rs * C::kRawBytes);
-                        unsigned char *dst = ring + st * C::kTileBytes;
-#pragma unroll
-                        for (int i = 0; i < UPK; ++i) {
-                            const int key = (i * 128 + ct) / UPK, c = (i * 128 + ct) % UPK;
-                            const uint4 w = raw[i * 128 + ct];
-                            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float2 t = unpack_e4m3(uint16_t(in[e / 2] >> ((e & 1) * 16)));
-                                o[e] = pack_bf16(t.x * f[i], t.y * f[i]);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + sw128_chunk(key, 2 * c, KT)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(dst + sw128_chunk(key, 2 * c + 1, KT)) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ms.full[st]), mbar_arrive(&ms.raw_empty[rs]);
+                for (int s = 0; s < 2; ++s) {
+                    if (side_tiles<kByKeys>(it, s) == 0) continue;
+                    wait_for(ok, &ms.q_free[s], (n_q[s]++ & 1) ^ 1, err);  // the last item's scores have read it
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    unsigned char *q_img = smem + s * C::kQBytes;
+                    constexpr int CPR = D / 8;  // 16-byte pieces of a row
+                    const int c = qt % CPR;
+                    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
+#pragma unroll 4
+                    for (int row = qt / CPR; row < kSideRows; row += 128 / CPR) {
+                        const int r = (kByKeys ? 0 : s * kSideRows) + row;
+                        cp_async16_or_zero(q_img + sw128_chunk(row, c, kSideRows),
+                                           q + it.at(min(r, it.rows - 1), p.group, p.q_stride, D), r < it.rows);
                     }
+                    cp_async_wait_all();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.q_full[s]);
+                }
+                for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tile) {
+                    const uint32_t absent = absent_groups(p, it, kb, lane), fill = 2u * tile + 1u, st = fill % NST;
+                    wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    uint32_t odd = 0;
+                    if (partly_seen(it, kb, absent)) {
+                        // a lane looks over one value row, each at a bank of its own
+                        const int row = w * 32 + lane, j = kb + row;
+                        unsigned char *img = ring + st * C::kTileBytes + row * 128;
+                        const bool gone = j >= it.k1 || (absent >> (row / 16) & 1);
+                        bool bad = false;
+                        for (int c = 0; c < D / 8; ++c)
+                            bad |= odd_bf16(*reinterpret_cast<const uint4 *>(img + (c >> 3) * KT * 128 +
+                                                                             (((c & 7) ^ (lane & 7)) << 4)));
+                        bad = bad && !gone && j > it.ctx + it.tok0;  // rows that every query sees stay
+                        if (gone || bad) {
+                            for (int c = 0; c < D / 8; ++c)
+                                *reinterpret_cast<uint4 *>(img + (c >> 3) * KT * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        odd = __ballot_sync(0xffffffffu, bad);
+                        fence_proxy_async_smem();
+                    }
+                    const uint32_t lk = tile % kLooked;
+                    if (lane == 0) ms.odd[lk][w] = odd;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.clean[lk]);
+                }
+            }
+        } else if (kE4m3 && ms.has && warp >= 16) {
+            // ---- e4m3 tiles to bf16 ---------------------------------------------------------
+            constexpr int UPK = D / 16;             // 16-byte pieces of a key
+            constexpr int UPT = KT * UPK / 128;     // of a thread
+            const int ct = tid - 512;
+            ItemWalk walk(ms.piece[0], ms.piece[1]);
+            Item it;
+            uint32_t fill = 0;
+            while (ok && walk.next(p, it)) {
+                const int fills = 2 * item_tiles(it);
+                for (int i = 0; i < fills && ok; ++i, ++fill) {
+                    const uint32_t rs = fill % NRAW, st = fill % NST;
+                    wait_for(ok, &ms.raw_full[rs], (fill / NRAW) & 1, err);
+                    wait_stage<NST>(ok, ms.empty, fill, err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const uint4 *raw = reinterpret_cast<const uint4 *>(smem + C::kRawAt + rs * C::kRawBytes);
+                    unsigned char *dst = ring + st * C::kTileBytes;
+#pragma unroll
+                    for (int u = 0; u < UPT; ++u) {
+                        const int key = (u * 128 + ct) / UPK, c = ct % UPK;
+                        const uint4 q = raw[u * 128 + ct];
+                        const float f = exp2_biased(ms.scale[rs][key]);
+                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 t = unpack_e4m3(uint16_t(in[e / 2] >> ((e & 1) * 16)));
+                            o[e] = pack_bf16(t.x * f, t.y * f);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + sw128_chunk(key, 2 * c, KT)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(dst + sw128_chunk(key, 2 * c + 1, KT)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.full[fill % kFills]), mbar_arrive(&ms.raw_empty[rs]);
                 }
             }
         }
@@ -639,15 +741,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [num_pages * num_kv_heads][page_size][head_dim]; a box is one page of one
-// head (64 channels of it for bf16, whose tiles are 128-byte swizzled).
+// [num_pages * num_kv_heads][page_size][head_dim]; a box is a tile's part of
+// one page and head (64 channels of it for bf16, whose tiles are 128-byte
+// swizzled).
 bool page_map(CUtensorMap *m, const void *base, const kda_kv_cache *c, bool e4m3) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t esize = e4m3 ? 1 : 2, D = cuuint64_t(c->head_dim), P = cuuint64_t(c->page_size);
     const cuuint64_t dims[3] = {D, P, cuuint64_t(c->num_pages) * cuuint64_t(c->num_kv_heads)};
     const cuuint64_t strides[2] = {D * esize, D * P * esize};
-    const cuuint32_t box[3] = {cuuint32_t(e4m3 ? c->head_dim : 64), cuuint32_t(c->page_size), 1u};
+    const cuuint32_t box[3] = {cuuint32_t(e4m3 ? c->head_dim : 64), cuuint32_t(c->page_size < KT ? c->page_size : KT), 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -667,7 +770,8 @@ kda_status launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan
         return KDA_ERR_CUDA;
     }
     p.key_step = KT;
-    p.min_keys = (kByKeys ? 4 : 2) * KT;
+    p.item_cost = kItemCost;
+    p.min_keys = (kByKeys ? 2 : 1) * KT;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
     return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), Cfg<D, kE4m3>::kThreads, smem, stream, p, maps);
 }

@@ -24,7 +24,7 @@ kda_status check_cache(const kda_kv_cache *c) {
         return KDA_ERR_INVALID_ARG;
     if ((c->act != KDA_F32 && c->act != KDA_BF16) || (c->format != KDA_KV_ACT && c->format != KDA_KV_E4M3))
         return KDA_ERR_INVALID_ARG;
-    if (c->format == KDA_KV_E4M3 && (!c->k_scale || !c->v_scale)) return KDA_ERR_INVALID_ARG;
+    if (c->format == KDA_KV_E4M3 && (!good(c->k_scale) || !good(c->v_scale))) return KDA_ERR_INVALID_ARG;
     if (c->num_heads % c->num_kv_heads != 0) return KDA_ERR_INVALID_ARG;
     const int P = c->page_size, D = c->head_dim;
     if (P != 16 && P != 32 && P != 64 && P != 128) return KDA_ERR_UNSUPPORTED;

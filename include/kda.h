@@ -450,7 +450,7 @@ typedef enum { KDA_KV_ACT = 0, KDA_KV_E4M3 = 1 } kda_kv_format;
 
 typedef struct {
     void *k, *v;                /* 16-byte aligned */
-    uint8_t *k_scale, *v_scale; /* NULL for KDA_KV_ACT */
+    uint8_t *k_scale, *v_scale; /* 16-byte aligned; NULL for KDA_KV_ACT */
     uint32_t *err;
     int32_t num_pages;    /* > 0 */
     int32_t page_size;    /* 16, 32, 64 or 128 */

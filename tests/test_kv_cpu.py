@@ -50,7 +50,7 @@ ref = ctypes.byref
 BAD, UNSUP = kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED
 CACHES = [(dict(k=None), BAD), (dict(v=A + 8), BAD), (dict(err=None), BAD), (dict(num_pages=0), BAD),
           (dict(num_heads=7), BAD), (dict(num_kv_heads=0), BAD), (dict(act=2), BAD), (dict(format=2), BAD),
-          (dict(format=kda.KDA_KV_E4M3), BAD), (dict(page_size=48), UNSUP), (dict(page_size=256), UNSUP),
+          (dict(format=kda.KDA_KV_E4M3), BAD), (dict(format=kda.KDA_KV_E4M3, k_scale=A, v_scale=A + 8), BAD), (dict(page_size=48), UNSUP), (dict(page_size=256), UNSUP),
           (dict(head_dim=96), UNSUP), (dict(num_heads=130, num_kv_heads=1), UNSUP),
           (dict(num_pages=1 << 30, num_kv_heads=8), UNSUP)]
 BATCHES = [dict(n_seqs=-1), dict(max_rows=-1), dict(max_new=0), dict(max_new=-1), dict(cu_seqlens=None),
