@@ -11,8 +11,10 @@
 //                  both read every key tile (half the L2 traffic per product);
 //   sides by keys  (at most 128 rows an item): both have all rows, side s has
 //                  the key tiles of its parity, joined at the item's end.
-// The weights are handed over in two halves, so the product of the first runs
-// under the exponentials of the second.
+// A tile is worked on in two halves of 64 keys, each with its own score columns:
+// while the threads of a side turn one half into weights, the other half's
+// product and the scores that follow in its place are under way, so the threads
+// seldom wait and the tensor cores seldom idle.
 // ref is the row's maximum so far, but only moved (and O and the sums scaled
 // by 2^(ref - ref')) when a tile exceeds it by more than 8: weights then reach
 // 2^8 at most, which costs no precision in bf16 and fp32, and most tiles leave
@@ -21,10 +23,14 @@
 // sums and O stay in 32 bits.
 //
 // Warps: 0-3 side 0, 4-7 side 1 (a thread a row); 8 and 9 issue a side's
-// products each; 10 fetches pages by TMA into a ring of tiles (K_0, V_0, K_1,
-// V_1, ...); 12-15 bring the rows of Q and look value tiles over (below); with
-// e4m3 pages warp 10 fetches them raw with their scales, and warps 16-19 turn
-// them into exact bf16 tiles.
+// products each; 10 and 11 fetch
+// pages by TMA into rings of key and value tiles; 12-15 bring the
+// rows of Q and look value tiles over (below).
+//
+// e4m3 pages: keys go to the tensor cores as they are, against Q as the sum of
+// two e4m3 terms, which is Q itself (as many cycles as bf16 products take), and
+// the keys' scales multiply the scores.  Values meet bf16 weights, so warps
+// 16-23 turn raw value tiles into bf16 ones, scale included and exact.
 //
 // A value behind a row's position weighs nothing, but 0 * NaN is NaN in the
 // product.  So in the few tiles where some row does not see some key, warps
@@ -44,6 +50,7 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 128;          // keys of a tile
+constexpr int KH = KT / 2;        // keys of a half
 constexpr int kSideRows = 128;   // rows of a side
 constexpr float kRefSlack = 8.f;
 #ifndef ITEM_COST
@@ -51,44 +58,55 @@ constexpr float kRefSlack = 8.f;
 #endif
 constexpr int kItemCost = ITEM_COST;
 
-template <int D, bool kE4m3> struct Cfg {
-    static constexpr int kThreads = kE4m3 ? 640 : 512;
+template <int D, bool kE4m3, bool kByKeys> struct Cfg {
+    static constexpr int kThreads = kE4m3 ? 768 : 512;
     // Registers a thread after the split: every SM quarter holds two softmax
-    // warps and two (bf16) or three (e4m3) others, 128 or 96 registers each at
-    // launch: 256 * 200 + 256 * 56 = 512 * 128, 256 * 152 + 384 * 56 < 640 * 96.
-    static constexpr int kRegsSoftmax = kE4m3 ? 152 : 200;
-    static constexpr int kRegsOther = 56;
-    static constexpr int kTileBytes = KT * D * 2;
-    static constexpr int kQBytes = kSideRows * D * 2;
-    static constexpr int kStages = D == 128 ? (kE4m3 ? 4 : 5) : 8;
-    static constexpr int kRawStages = kE4m3 ? 2 : 0;
-    static constexpr int kRawBytes = KT * D;
-    static constexpr int kRingAt = 2 * kQBytes;
-    static constexpr int kRawAt = kRingAt + kStages * kTileBytes;
-    static constexpr int kMiscAt = kRawAt + kRawStages * kRawBytes;
+    // warps and two (bf16) or four (e4m3) others, 128 or 80 registers each at
+    // launch: 256 * 200 + 256 * 56 = 512 * 128, 256 * 112 + 512 * 64 = 768 * 80.
+    static constexpr int kRegsSoftmax = kE4m3 ? 112 : 200;
+    static constexpr int kRegsOther = kE4m3 ? 64 : 56;
+    static constexpr int kQBytes = kSideRows * D * 2;            // bf16, or two e4m3 terms
+    static constexpr int kKBytes = KT * D * (kE4m3 ? 1 : 2), kVBytes = KT * D * 2, kRawBytes = KT * D;
+    // Shared memory: the rows of Q once (by keys) or a side (by rows), and rings
+    // of key tiles, bf16 value tiles and (e4m3) raw value tiles.  By keys the
+    // bytes in flight set the pace (HBM latency), by rows the products do.
+    static constexpr int kQImages = kByKeys ? 1 : 2;
+    static constexpr int kStagesK = D == 64 ? 6 : 3;
+    static constexpr int kStagesV = D == 64 ? 6 : kE4m3 ? 2 : kByKeys ? 3 : 2;
+    static constexpr int kStagesRaw = !kE4m3 ? 1 : D == 64 ? 4 : kByKeys ? 4 : 2;
+    static constexpr int kKAt = kQImages * kQBytes;
+    static constexpr int kVAt = kKAt + kStagesK * kKBytes;
+    static constexpr int kRawAt = kVAt + kStagesV * kVBytes;
+    static constexpr int kMiscAt = kRawAt + (kE4m3 ? kStagesRaw * kRawBytes : 0);
 };
+// Barriers of a ring's tiles, more than it has stages: tile t lands in stage
+// t % stages but reports on barrier t % kBars.  A wait by parity is only sound for
+// a thread that sees every phase of its barrier, and a side that takes every
+// second tile sees every phase of every barrier it uses (kBars is even), whatever
+// the number of stages and the order in which copies land.
+constexpr int kBars = 8;
 
-// Barriers of the ring's fills, more than it has stages: fill f (K and V tiles
-// in turn) lands in stage f % stages but reports on barrier f % kFills.  A wait
-// by parity is only sound for a thread that sees every phase of its barrier, and
-// a side or a look-over that takes every second tile, or only the V tiles, sees
-// every phase of every barrier it uses (kFills is a multiple of 4), whatever the
-// number of stages and the order in which copies land.
-constexpr int kFills = 16;
-constexpr int kLooked = kFills / 2;  // of value tiles looked over
-
-struct Misc {
-    uint64_t full[kFills], empty[kFills], clean[kLooked], raw_full[2], raw_empty[2];
-    uint64_t s_full[2], p_ready[2][2], q_full[2], q_free[2], o_full[2], done[2];
+template <typename C> struct alignas(16) Misc {
+    uint64_t k_full[kBars], k_empty[kBars], v_full[kBars], v_empty[kBars], clean[kBars];
+    uint64_t raw_full[kBars], raw_empty[kBars];
+    uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];  // by side and half
+    uint64_t q_full[2], q_free[2], done[2];
     uint32_t tmem;
     int has;
     Cursor piece[2];
-    uint32_t odd[kLooked][4];          // by tile: keys whose value row was taken out of it
-    alignas(16) uint8_t scale[2][KT];  // e4m3: the raw tile's scale exponents
-    float m[kSideRows], l[kSideRows];  // side 1's row statistics, for the join
+    uint32_t odd[kBars][4];                        // by tile: keys whose value row was taken out of it
+    float m[kSideRows], l[kSideRows];              // side 1's row statistics, for the join
+};
+template <typename C> struct ScaleMisc {  // e4m3 pages only
+    alignas(16) uint8_t k[C::kStagesK][KT];  // the tiles' scale exponents
+    alignas(16) uint8_t v[C::kStagesRaw][KT];
+    alignas(16) float k_unit[2][2][KT];      // by side and tile parity, the keys' scales
+    float q_unit[2][2][kSideRows];           // by item parity and image, the rows' scales
 };
 
-template <int D, bool kE4m3> constexpr size_t smem_bytes() { return 1024 + Cfg<D, kE4m3>::kMiscAt + sizeof(Misc); }
+template <typename C, bool kE4m3> constexpr size_t smem_bytes() {
+    return 1024 + C::kMiscAt + (kE4m3 ? sizeof(ScaleMisc<C>) : 0) + sizeof(Misc<C>);
+}
 
 // ---- PTX of this kernel ---------------------------------------------------------
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
@@ -126,6 +144,37 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs (32 K values an instruction).
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: e4m3 A and B, both K-major, fp32 D.
+constexpr uint32_t idesc_e4m3_f32(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
+// Rows of D e4m3 values, K-major, swizzled over their 128 or 64 bytes: byte
+// offset of a row's 16-byte piece, and the operand descriptor (8 rows a group).
+template <int D> __host__ __device__ __forceinline__ uint32_t row8_piece(int row, int c) {
+    return uint32_t(row * D) + uint32_t((D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
+}
+template <int D> __device__ __forceinline__ uint64_t sdesc_row8(uint32_t saddr) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | uint64_t(1) << 16 | uint64_t(8 * D >> 4) << 32 | uint64_t(1) << 46 |
+           uint64_t(D == 128 ? 2 : 4) << 61;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 // 16-byte asynchronous copy, or zeros.
 __device__ __forceinline__ void cp_async16_or_zero(void *smem_dst, const void *gsrc, bool there) {
@@ -170,6 +219,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// 16 e4m3 values times 2^(e - 127) as bf16, exactly: s eeee mmm put at the same
+// places of a bf16 is the value times 2^-120, and one packed product with a
+// power of two (subnormal values included) makes it the value times the scale.
+// Not for NaN codes, nor for scales above 2^7, whose factor a bf16 cannot hold.
+__device__ __forceinline__ void widen_plain(const uint4 &q, uint32_t e, uint32_t (&o)[8]) {
+    const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t half = (e + 120u) << 7, f = half | half << 16;  // bf16 2^(e - 7)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t x = __byte_perm(in[i / 2], 0, i & 1 ? 0x3424 : 0x1404);  // a byte in the top of each half
+        const uint32_t v = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(v), "r"(f));
+    }
+}
+// Bit 7 of a byte is set where one of the 16 codes is NaN.
+__device__ __forceinline__ uint32_t nan_codes(const uint4 &q) {
+    return (((q.x & 0x7f7f7f7fu) + 0x01010101u) | ((q.y & 0x7f7f7f7fu) + 0x01010101u) |
+            ((q.z & 0x7f7f7f7fu) + 0x01010101u) | ((q.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+}
 // Any bf16 infinity or NaN among eight.
 __device__ __forceinline__ bool odd_bf16(const uint4 &w) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -204,9 +272,14 @@ __device__ __forceinline__ void wait_for(bool &ok, uint64_t *bar, uint32_t parit
     atomicOr(err, KDA_DEVERR_TIMEOUT);
     ok = false;
 }
-// The stage of fill f is free: the fill that was there before has been used.
-template <int kStages> __device__ __forceinline__ void wait_stage(bool &ok, uint64_t *empty, uint32_t f, uint32_t *err) {
-    if (f >= kStages) wait_for(ok, &empty[(f - kStages) % kFills], ((f - kStages) / kFills) & 1, err);
+// Tile t's barrier of a ring has been passed.
+__device__ __forceinline__ void wait_tile(bool &ok, uint64_t *bars, uint32_t t, uint32_t *err) {
+    wait_for(ok, &bars[t % kBars], (t / kBars) & 1, err);
+}
+// The stage that tile t will take is free: the tile before it there has been used.
+template <int kStages> __device__ __forceinline__ void wait_stage(bool &ok, uint64_t *empty, uint32_t t, uint32_t *err) {
+    static_assert(kStages < kBars, "a tile's barrier is free before its stage");
+    if (t >= kStages) wait_tile(ok, empty, t - kStages, err);
 }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -225,7 +298,7 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-__device__ __forceinline__ bool any_odd(const uint32_t *odd) { return (odd[0] | odd[1] | odd[2] | odd[3]) != 0; }
+__device__ __forceinline__ bool any_odd(const uint32_t *odd) { return (odd[0] | odd[1]) != 0; }  // of a half
 
 struct TileMaps {
     CUtensorMap k, v;
@@ -261,7 +334,7 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
         for (int c = 0; c < D; c += 16) tmem_st16(t_o + uint32_t(c), z);
         tmem_wait_st();
     }
-    for (int g = 0; g < KT / 32; ++g) {
+    for (int g = 0; g < KH / 32; ++g) {
         for (uint32_t left = odd[g]; left; left &= left - 1) {
             const int c = g * 32 + __ffs(left) - 1, j = kb + c;
             const uint32_t pw = tmem_ld1(t_s + uint32_t(c / 2));
@@ -293,28 +366,58 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
     }
 }
 
+// Piece u of a lane in the widening of a raw e4m3 tile: a warp has 16 keys, and
+// 8 neighbouring lanes take the same 16-byte piece of 8 keys, which both tiles'
+// swizzles put into different banks.
+template <int D> struct RawPiece {
+    int key;
+    uint32_t from, to;  // byte offsets in the raw and the wide tile (whose next 16 bytes are at to ^ 16)
+    __device__ __forceinline__ RawPiece(int w, int lane, int u) {
+        const int c = (lane >> 3) + (D == 128 ? 4 * (u & 1) : 0);
+        key = w * 16 + (lane & 7) + 8 * (D == 128 ? u >> 1 : u);
+        from = row8_piece<D>(key, c);
+        to = sw128_chunk(key, 2 * c, KT);
+    }
+};
+// The pieces of a lane by the conversion instructions, whatever they hold.
+template <int D>
+__device__ __noinline__ void widen_any(const unsigned char *raw, unsigned char *dst, const uint8_t *scale, int w, int lane) {
+#pragma unroll 1
+    for (int u = 0; u < KT * D / 16 / 256; ++u) {
+        const RawPiece<D> r(w, lane, u);
+        const float f = exp2_biased(scale[r.key]);
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const float2 t = unpack_e4m3(*reinterpret_cast<const uint16_t *>(raw + r.from + 2 * i));
+            *reinterpret_cast<uint32_t *>(dst + (i < 4 ? r.to : r.to ^ 16u) + 4 * (i & 3)) = pack_bf16(t.x * f, t.y * f);
+        }
+    }
+}
+
 template <int D, bool kE4m3, bool kByKeys>
-__global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
     attend_tile_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TileMaps maps) {
-    using C = Cfg<D, kE4m3>;
-    constexpr int NST = C::kStages, NRAW = kE4m3 ? C::kRawStages : 1, BM = kByKeys ? kSideRows : 2 * kSideRows;
+    using C = Cfg<D, kE4m3, kByKeys>;
+    constexpr int NK = C::kStagesK, NV = C::kStagesV, NR = C::kStagesRaw, BM = kByKeys ? kSideRows : 2 * kSideRows;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Misc &ms = *reinterpret_cast<Misc *>(smem + C::kMiscAt);
+    Misc<C> &ms = *reinterpret_cast<Misc<C> *>(smem + C::kMiscAt);
+    ScaleMisc<C> &sc8 = *reinterpret_cast<ScaleMisc<C> *>(smem + C::kMiscAt + sizeof(Misc<C>));  // kE4m3 only
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
-    unsigned char *ring = smem + C::kRingAt;
+    unsigned char *k_ring = smem + C::kKAt, *v_ring = smem + C::kVAt, *raw_ring = smem + C::kRawAt;
 
     if (tid == 0) {
-        for (int i = 0; i < kFills; ++i) {
-            mbar_init(&ms.full[i], kE4m3 ? 4 : 1);
-            mbar_init(&ms.empty[i], kByKeys ? 1 : 2);  // by rows both sides are done with a tile
+        for (int i = 0; i < kBars; ++i) {
+            mbar_init(&ms.k_full[i], 1), mbar_init(&ms.v_full[i], kE4m3 ? 8 : 1);
+            // by rows both sides are done with a tile
+            mbar_init(&ms.k_empty[i], kByKeys ? 1 : 2), mbar_init(&ms.v_empty[i], kByKeys ? 1 : 2);
+            mbar_init(&ms.clean[i], 4), mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], 8);
         }
-        for (int i = 0; i < kLooked; ++i) mbar_init(&ms.clean[i], 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], 4);
-            mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i][0], 4), mbar_init(&ms.p_ready[i][1], 4);
-            mbar_init(&ms.q_full[i], 4), mbar_init(&ms.q_free[i], 1);
-            mbar_init(&ms.o_full[i], 1), mbar_init(&ms.done[i], 1);
+            for (int h = 0; h < 2; ++h)
+                mbar_init(&ms.s_full[i][h], 1), mbar_init(&ms.p_ready[i][h], 4), mbar_init(&ms.pv_done[i][h], 1);
+            mbar_init(&ms.q_full[i], 4), mbar_init(&ms.q_free[i], kByKeys ? 2 : 1);
+            mbar_init(&ms.done[i], 1);
         }
         fence_mbar_init();
     }
@@ -343,95 +446,131 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
             const uint32_t t_s = tm + lanes + uint32_t(s) * 128u, t_o = tm + lanes + 256u + uint32_t(s) * 128u;
             const int r = (kByKeys ? 0 : s * kSideRows) + row;
             ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it;
-            uint32_t n_s = 0, n_o = 0, tile_base = 0;  // tiles and items so far: barrier phases
+            Item it = {};
+            uint32_t n_s = 0, n_it = 0, tile_base = 0;  // tiles and items so far: barrier phases
+            // O holds this side's products up to half h of its n-th tile
+            auto wait_o = [&](uint32_t n, int h) {
+                wait_for(ok, &ms.pv_done[s][h], n & 1, err);
+                __syncwarp();
+                tc_fence_after();
+            };
             while (walk.next(p, it)) {
                 const int nv = side_tiles<kByKeys>(it, s);
                 const int lim = it.ctx + it.tok0 + min(r, it.rows - 1) / p.group;  // last key this row sees
-                float ref = -INFINITY, l = 0.f;
+                const bool live = r - lane < it.rows;  // this warp has rows of the item
+                float ref = -INFINITY, l = 0.f, scale = p.scale_log2;
+                if constexpr (kE4m3) {
+                    if (kByKeys || nv > 0) {
+                        constexpr int kImage1 = kByKeys ? 0 : 1;
+                        const int qi = s ? kImage1 : 0;
+                        wait_for(ok, &ms.q_full[qi], n_it & 1, err);
+                        scale *= sc8.q_unit[n_it & 1][qi][row];
+                        ++n_it;
+                    }
+                }
                 for (int v = 0; v < nv; ++v, ++n_s) {
                     const int t = side_tile<kByKeys>(s, v), kb = it.k0 + t * KT;
                     const uint32_t absent = absent_groups(p, it, kb, lane);
                     const bool check = partly_seen(it, kb, absent);
-                    wait_for(ok, &ms.s_full[s], n_s & 1, err);  // and with it the product before
-                    __syncwarp();
-                    tc_fence_after();
-                    float x[KT];
-#pragma unroll
-                    for (int c = 0; c < KT; c += 32) tmem_ld32(t_s + uint32_t(c), x + c);
-                    tmem_wait_ld();
-                    if (check) {
-#pragma unroll
-                        for (int c = 0; c < KT; ++c)
-                            if (kb + c > lim || (absent >> (c / 16) & 1)) x[c] = -INFINITY;
+                    if constexpr (kE4m3) {  // the keys' scales as numbers, a key a thread
+                        const uint32_t tg = tile_base + uint32_t(t);
+                        wait_tile(ok, ms.k_full, tg, err);
+                        sc8.k_unit[s][n_s & 1][row] = exp2_biased(sc8.k[tg % NK][row]);
+                        if (s) named_sync<3, 128>();
+                        else named_sync<2, 128>();
                     }
-                    float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int c = 4; c < KT; c += 8) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mx[i] = c + 4 + i < KT ? fmaxf(fmaxf(mx[i], x[c + i]), x[c + 4 + i]) : fmaxf(mx[i], x[c + i]);
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-                    const bool move = top > ref + kRefSlack;
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float to = move ? top : ref, f = move ? ex2(ref - to) : 1.f;
-                        if (v > 0) {  // O is new with the first product
-#pragma unroll
-                            for (int c = 0; c < D; c += 16) {
-                                float o[16];
-                                tmem_ld16(t_o + uint32_t(c), o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= f;
-                                tmem_st16(t_o + uint32_t(c), o);
-                            }
-                        }
-                        l *= f;
-                        ref = to;
-                    }
-                    const float base = ref == -INFINITY ? 0.f : ref;
-                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), sh = make_float2(-base, -base);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int c = 0; c < KT; c += 32) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 e = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), sc, sh);
-                            e.x = ex2(e.x), e.y = ex2(e.y);
-                            sum[i & 1] = add2(sum[i & 1], e);
-                            w[i] = pack_bf16(e.x, e.y);
-                        }
-                        tmem_st16u(t_s + uint32_t(c / 2), w);
-                        if (c == KT / 2 - 32 && !check) {
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&ms.p_ready[s][0]);
-                        }
-                    }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_wait_st();
-                    if (check) {
-                        const uint32_t at = tile_base + uint32_t(t), lk = at % kLooked;
-                        wait_for(ok, &ms.clean[lk], (at / kLooked) & 1, err);
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t t_h = t_s + uint32_t(h) * KH;
+                        const int kh = kb + h * KH;
+                        // Scores of a half are issued after its last product, so a half's barriers are
+                        // never more than a phase ahead.
+                        wait_for(ok, &ms.s_full[s][h], n_s & 1, err);
                         __syncwarp();
-                        if (any_odd(ms.odd[lk])) add_odd_rows<D, kE4m3>(p, it, kb, lim, ms.odd[lk], t_s, t_o, v == 0);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (check) mbar_arrive(&ms.p_ready[s][0]);
-                        mbar_arrive(&ms.p_ready[s][1]);
+                        tc_fence_after();
+                        if (live) {
+                            float x[KH];
+#pragma unroll
+                            for (int c = 0; c < KH; c += 32) tmem_ld32(t_h + uint32_t(c), x + c);
+                            tmem_wait_ld();
+                            if constexpr (kE4m3) {
+#pragma unroll
+                                for (int c = 0; c < KH; c += 4) {
+                                    const float4 u = *reinterpret_cast<const float4 *>(&sc8.k_unit[s][n_s & 1][h * KH + c]);
+                                    const float2 a = mul2(make_float2(x[c], x[c + 1]), make_float2(u.x, u.y));
+                                    const float2 b = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(u.z, u.w));
+                                    x[c] = a.x, x[c + 1] = a.y, x[c + 2] = b.x, x[c + 3] = b.y;
+                                }
+                            }
+                            if (check) {
+#pragma unroll
+                                for (int c = 0; c < KH; ++c)
+                                    if (kh + c > lim || (absent >> (h * (KH / 16) + c / 16) & 1)) x[c] = -INFINITY;
+                            }
+                            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                            for (int c = 4; c < KH; c += 8)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mx[i] = c + 4 + i < KH ? fmaxf(fmaxf(mx[i], x[c + i]), x[c + 4 + i]) : fmaxf(mx[i], x[c + i]);
+                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                            const bool move = top > ref + kRefSlack;
+                            const bool started = v > 0 || h > 0;  // O is new with the first product
+                            if (__any_sync(0xffffffffu, move)) {
+                                const float to = move ? top : ref, f = move ? ex2(ref - to) : 1.f;
+                                if (started) {
+                                    wait_o(h == 0 ? n_s - 1 : n_s, h ^ 1);
+#pragma unroll
+                                    for (int c = 0; c < D; c += 16) {
+                                        float o[16];
+                                        tmem_ld16(t_o + uint32_t(c), o);
+                                        tmem_wait_ld();
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i) o[i] *= f;
+                                        tmem_st16(t_o + uint32_t(c), o);
+                                    }
+                                }
+                                l *= f;
+                                ref = to;
+                            }
+                            const float base = ref == -INFINITY ? 0.f : ref;
+                            const float2 sc = make_float2(scale, scale), sh = make_float2(-base, -base);
+                            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                            for (int c = 0; c < KH; c += 32) {
+                                uint32_t w[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float2 e = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), sc, sh);
+                                    e.x = ex2(e.x), e.y = ex2(e.y);
+                                    sum[i & 1] = add2(sum[i & 1], e);
+                                    w[i] = pack_bf16(e.x, e.y);
+                                }
+                                tmem_st16u(t_h + uint32_t(c / 2), w);
+                            }
+                            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                            tmem_wait_st();
+                            if (check) {
+                                const uint32_t tg = tile_base + uint32_t(t);
+                                wait_tile(ok, ms.clean, tg, err);
+                                __syncwarp();
+                                const uint32_t *odd = &ms.odd[tg % kBars][h * (KH / 32)];
+                                if (any_odd(odd)) {
+                                    if (started) wait_o(h == 0 ? n_s - 1 : n_s, h ^ 1);
+                                    add_odd_rows<D, kE4m3>(p, it, kh, lim, odd, t_h, t_o, !started);
+                                }
+                            }
+                        }  // else rows of nobody: their weights may be anything
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.p_ready[s][h]);
                     }
                 }
                 tile_base += uint32_t(item_tiles(it));
 
                 // ---- output ----------------------------------------------------------------
                 const int nv_other = kByKeys ? side_tiles<kByKeys>(it, 1 - s) : 0;
-                if (nv > 0) wait_for(ok, &ms.o_full[s], n_o++ & 1, err);
-                __syncwarp();
+                if (nv > 0) wait_o(n_s - 1, 1);
                 float f0 = 1.f, f1 = 0.f;
                 if (kByKeys) {
                     if (s == 1) ms.m[row] = ref, ms.l[row] = l;  // its products are done: side 0 may read both
@@ -500,142 +639,149 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
         if (ms.has && warp < 10) {
             // ---- products of a side (converged warp, one lane issues) ----------------------
             const int s = warp - 8;
-            const uint32_t id_s = idesc_bf16_f32(128, KT), id_o = idesc_bf16_f32(128, D, false, true);
+            const uint32_t id_s = kE4m3 ? idesc_e4m3_f32(128, KH) : idesc_bf16_f32(128, KH);
+            const uint32_t id_o = idesc_bf16_f32(128, D, false, true);
             const uint32_t t_s = tm + uint32_t(s) * 128u, t_o = tm + 256u + uint32_t(s) * 128u;
-            const uint64_t q_desc = sdesc_sw128(smem_u32(smem) + uint32_t(s) * C::kQBytes);
-            const uint64_t k_desc = sdesc_sw128(smem_u32(ring)), v_desc = sdesc_sw128_mn(smem_u32(ring), KT * 128u);
+            const int qi = kByKeys ? 0 : s;  // the image of Q
+            const uint32_t q_at = smem_u32(smem) + uint32_t(qi) * C::kQBytes;
+            const uint64_t q_desc = kE4m3 ? sdesc_row8<D>(q_at) : sdesc_sw128(q_at);
+            const uint64_t k_desc = kE4m3 ? sdesc_row8<D>(smem_u32(k_ring)) : sdesc_sw128(smem_u32(k_ring));
+            const uint64_t v_desc = sdesc_sw128_mn(smem_u32(v_ring), KT * 128u);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it;
+            Item it = {};
             uint32_t base = 0, n_q = 0, n_p = 0;
             int nv = 0;
-            // scores of the side's v-th tile (descriptors count 16-byte units)
-            auto scores = [&](int v) {
-                const uint32_t fill = base + 2u * uint32_t(side_tile<kByKeys>(s, v)), st = fill % NST;
-                wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+            // scores of half h of the side's v-th tile (descriptors count 16-byte units)
+            auto scores = [&](int v, int h) {
+                const uint32_t tg = base + uint32_t(side_tile<kByKeys>(s, v));
+                if (h == 0) wait_tile(ok, ms.k_full, tg, err);
                 if (!(ok = __all_sync(0xffffffffu, ok))) return;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t kd = k_desc + uint64_t(st * (C::kTileBytes >> 4));
+                    const uint32_t t_h = t_s + uint32_t(h) * KH;
+                    const uint64_t kd = k_desc + uint64_t(tg % NK * uint32_t(C::kKBytes >> 4)) +
+                                        uint64_t(h * (KH * (kE4m3 ? D : 128) >> 4));
+                    if constexpr (kE4m3) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_bf16(t_s, q_desc + uint64_t((k >> 2) * (kSideRows * 8) + (k & 3) * 2),
-                                 kd + uint64_t((k >> 2) * (KT * 8) + (k & 3) * 2), id_s, k > 0);
-                    mma_commit(&ms.s_full[s]);
-                    mma_commit(&ms.empty[fill % kFills]);
-                    if (v + 1 == nv) mma_commit(&ms.q_free[s]);
+                        for (int k = 0; k < 2 * D / 32; ++k)  // both terms of Q against the same keys
+                            mma_e4m3(t_h, q_desc + uint64_t((k / (D / 32)) * (kSideRows * D / 16) + (k % (D / 32)) * 2),
+                                     kd + uint64_t((k % (D / 32)) * 2), id_s, k > 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_bf16(t_h, q_desc + uint64_t((k >> 2) * (kSideRows * 8) + (k & 3) * 2),
+                                     kd + uint64_t((k >> 2) * (KT * 8) + (k & 3) * 2), id_s, k > 0);
+                    }
+                    mma_commit(&ms.s_full[s][h]);
+                    if (h == 1) {
+                        mma_commit(&ms.k_empty[tg % kBars]);
+                        if (v + 1 == nv) mma_commit(&ms.q_free[qi]);
+                    }
                 }
                 __syncwarp();
             };
             while (ok && walk.next(p, it)) {
                 nv = side_tiles<kByKeys>(it, s);
+                if (kByKeys || nv > 0) wait_for(ok, &ms.q_full[qi], n_q++ & 1, err);
                 if (nv > 0) {
-                    wait_for(ok, &ms.q_full[s], n_q++ & 1, err);
-                    scores(0);
+                    scores(0, 0), scores(0, 1);
+                } else if (kByKeys) {
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) mbar_arrive(&ms.q_free[0]);
                 }
                 for (int v = 0; v < nv && ok; ++v, ++n_p) {
-                    const uint32_t fill = base + 2u * uint32_t(side_tile<kByKeys>(s, v)) + 1u, st = fill % NST;
-                    wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
-                    const uint32_t lk = (fill >> 1) % kLooked;
-                    wait_for(ok, &ms.clean[lk], ((fill >> 1) / kLooked) & 1, err);
+                    const uint32_t tg = base + uint32_t(side_tile<kByKeys>(s, v));
+                    wait_tile(ok, ms.v_full, tg, err);
+                    wait_tile(ok, ms.clean, tg, err);
                     // the first product starts O, unless value rows were added to it by hand
-                    const uint32_t acc = v > 0 || any_odd(ms.odd[lk]);
-                    const uint64_t vd = v_desc + uint64_t(st * (C::kTileBytes >> 4));
+                    const uint32_t acc = v > 0 || any_odd(ms.odd[tg % kBars]);
+                    const uint64_t vd = v_desc + uint64_t(tg % NV * uint32_t(C::kVBytes >> 4));
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait_for(ok, &ms.p_ready[s][half], n_p & 1, err);
+                    for (int h = 0; h < 2; ++h) {
+                        wait_for(ok, &ms.p_ready[s][h], n_p & 1, err);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
                         tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
-                            for (int k = half * (KT / 32); k < (half + 1) * (KT / 32); ++k)
-                                mma_bf16_ta(t_o, t_s + uint32_t(k) * 8u, vd + uint64_t(k * 128), id_o, k > 0 || acc);
-                            if (half == 1) {
-                                mma_commit(&ms.empty[fill % kFills]);
-                                if (v + 1 == nv) mma_commit(&ms.o_full[s]);
-                            }
+                            for (int k = 0; k < KH / 16; ++k)
+                                mma_bf16_ta(t_o, t_s + uint32_t(h) * KH + uint32_t(k) * 8u,
+                                            vd + uint64_t((h * (KH / 16) + k) * 128), id_o, h > 0 || k > 0 || acc);
+                            mma_commit(&ms.pv_done[s][h]);
+                            if (h == 1) mma_commit(&ms.v_empty[tg % kBars]);
                         }
                         __syncwarp();
+                        if (v + 1 < nv) scores(v + 1, h);
                     }
-                    if (ok && v + 1 < nv) scores(v + 1);
                 }
                 if (!kByKeys && nv == 0) {  // a tile is free once both sides have said so
-                    for (int i = 0; i < 2 * item_tiles(it) && ok; ++i) {
-                        const uint32_t fill = base + uint32_t(i);
-                        wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+                    for (int i = 0; i < item_tiles(it) && ok; ++i) {
+                        const uint32_t tg = base + uint32_t(i);
+                        wait_tile(ok, ms.k_full, tg, err);
+                        wait_tile(ok, ms.v_full, tg, err);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                        if (lane == 0) mbar_arrive(&ms.empty[fill % kFills]);
+                        if (lane == 0) mbar_arrive(&ms.k_empty[tg % kBars]), mbar_arrive(&ms.v_empty[tg % kBars]);
                     }
                 }
-                base += 2u * uint32_t(item_tiles(it));
+                base += uint32_t(item_tiles(it));
             }
             // nothing of this side's is in flight when the tensor memory goes
             if (elect_one()) mma_commit(&ms.done[s]);
             __syncwarp();
             bool end_ok = true;
             wait_for(end_ok, &ms.done[s], 0, err);
-        } else if (ms.has && warp == 10) {
-            // ---- page fetches ------------------------------------------------------------
+        } else if (ms.has && warp < 12) {
+            // ---- page fetches: keys, or values ------------------------------------------------
+            const bool values = warp == 11;
+            const CUtensorMap *map = values ? &maps.v : &maps.k;
             const int page_size = 1 << p.b.page_shift, box = min(page_size, KT);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it;
-            uint32_t fill = 0;
+            Item it = {};
+            uint32_t tg = 0;
+            auto fetch = [&](int kb, uint64_t *full, unsigned char *dst, uint8_t *scales) {
+                const int j = kb + lane * box, line = j & (page_size - 1);
+                int page = -1;
+                if (lane * box < KT && j < it.k1) page = load_page(p.b, it.n, j);
+                const int there = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box;
+                const int plane = page * p.hkv + it.h;  // below 2^31 (checked on the host)
+                if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(there * (kE4m3 ? D + 1 : 2 * D)));
+                __syncwarp();
+                if (page < 0) return;
+                if constexpr (kE4m3) {
+                    tma_load_3d(dst + lane * box * D, map, full, 0, line, plane);
+                    bulk_load(scales + lane * box, (values ? p.sv : p.sk) + (size_t(plane) << p.b.page_shift) + line,
+                              uint32_t(box), full);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(dst + lane * box * 128 + c * KT * 128, map, full, c * 64, line, plane);
+                }
+            };
             while (ok && walk.next(p, it)) {
-                for (int kb = it.k0; kb < it.k1 && ok; kb += KT) {
-                    const int j = kb + lane * box, line = j & (page_size - 1);
-                    int page = -1;
-                    if (lane * box < KT && j < it.k1) page = load_page(p.b, it.n, j);
-                    const int there = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box;
-                    const int plane = page * p.hkv + it.h;  // below 2^31 (checked on the host)
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++fill) {
-                        const CUtensorMap *map = kv ? &maps.v : &maps.k;
-                        if constexpr (kE4m3) {
-                            const uint32_t st = fill % NRAW;
-                            wait_for(ok, &ms.raw_empty[st], ((fill / NRAW) & 1) ^ 1, err);
-                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[st], uint32_t(there * (D + 1)));
-                            __syncwarp();
-                            if (page >= 0) {
-                                tma_load_3d(smem + C::kRawAt + st * C::kRawBytes + lane * box * D, map, &ms.raw_full[st], 0,
-                                            line, plane);
-                                bulk_load(&ms.scale[st][lane * box],
-                                          (kv ? p.sv : p.sk) + (size_t(plane) << p.b.page_shift) + line, uint32_t(box),
-                                          &ms.raw_full[st]);
-                            }
-                        } else {
-                            const uint32_t st = fill % NST;
-                            uint64_t *full = &ms.full[fill % kFills];
-                            wait_stage<NST>(ok, ms.empty, fill, err);
-                            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                            if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(there * D * 2));
-                            __syncwarp();
-                            if (page >= 0) {
-                                unsigned char *dst = ring + st * C::kTileBytes + lane * box * 128;
-#pragma unroll
-                                for (int c = 0; c < D / 64; ++c)
-                                    tma_load_3d(dst + c * KT * 128, map, full, c * 64, line, plane);
-                            }
-                        }
-                    }
+                for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tg) {
+                    if (!values) wait_stage<NK>(ok, ms.k_empty, tg, err);
+                    else if (kE4m3) wait_stage<NR>(ok, ms.raw_empty, tg, err);
+                    else wait_stage<NV>(ok, ms.v_empty, tg, err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (!values) fetch(kb, &ms.k_full[tg % kBars], k_ring + tg % NK * C::kKBytes, sc8.k[tg % NK]);
+                    else if (kE4m3) fetch(kb, &ms.raw_full[tg % kBars], raw_ring + tg % NR * C::kRawBytes, sc8.v[tg % NR]);
+                    else fetch(kb, &ms.v_full[tg % kBars], v_ring + tg % NV * C::kVBytes, nullptr);
                 }
             }
             // a given-up wait elsewhere may leave copies in flight: they land before the CTA ends
             if (!ok) {
-                constexpr uint32_t kDepth = kE4m3 ? NRAW : NST;
-                for (uint32_t i = 1; i <= kDepth && i <= fill; ++i) {
-                    const uint32_t c = fill - i;
-                    if (kE4m3) mbar_wait(&ms.raw_full[c % NRAW], (c / NRAW) & 1, err);
-                    else mbar_wait(&ms.full[c % kFills], (c / kFills) & 1, err);
-                }
+                uint64_t *bars = !values ? ms.k_full : kE4m3 ? ms.raw_full : ms.v_full;
+                const uint32_t depth = uint32_t(!values ? NK : kE4m3 ? NR : NV);
+                bool end_ok = true;
+                for (uint32_t t = tg - min(tg, depth); t < tg; ++t) wait_tile(end_ok, bars, t, err);
             }
         } else if (ms.has && warp >= 12 && warp < 16) {
             // ---- rows of Q, and value tiles looked over ------------------------------------
             const int w = warp - 12, qt = tid - 384;
             ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it;
+            Item it = {};
             uint32_t n_q[2] = {0, 0}, tile = 0;
             while (ok && walk.next(p, it)) {
-                for (int s = 0; s < 2; ++s) {
+                for (int s = 0; s < C::kQImages; ++s) {
                     if (side_tiles<kByKeys>(it, s) == 0) continue;
                     wait_for(ok, &ms.q_free[s], (n_q[s]++ & 1) ^ 1, err);  // the last item's scores have read it
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -643,26 +789,61 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
                     constexpr int CPR = D / 8;  // 16-byte pieces of a row
                     const int c = qt % CPR;
                     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
+                    if constexpr (kE4m3) {
+                        // a row as 2^e (q1 + q2): e4m3 keeps 4 significant bits, so q1 and what q1 leaves
+                        // hold all 8 of a bf16 (down to 2^-18 of the row's largest value)
+#pragma unroll 2
+                        for (int row = qt / CPR; row < kSideRows; row += 128 / CPR) {
+                            const int r = (kByKeys ? 0 : s * kSideRows) + row;
+                            uint4 raw = make_uint4(0, 0, 0, 0);
+                            if (r < it.rows) raw = *reinterpret_cast<const uint4 *>(q + it.at(r, p.group, p.q_stride, D));
+                            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                            float y[8], m = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                y[i] = __uint_as_float(i & 1 ? in[i / 2] & 0xffff0000u : in[i / 2] << 16);
+                                m = fmaxf(m, isfinite(y[i]) ? fabsf(y[i]) : 0.f);
+                            }
+#pragma unroll
+                            for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                            const int e = max(scale_exponent(m), 1);
+                            const float f = exp2_neg_biased(e);
+                            uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float a = isfinite(y[i]) ? y[i] * f : NAN, b = isfinite(y[i + 1]) ? y[i + 1] * f : NAN;
+                                const uint16_t h1 = pack_e4m3(a, b);
+                                const float2 t = unpack_e4m3(h1);
+                                w1[i / 4] |= uint32_t(h1) << (i & 2) * 8;
+                                w2[i / 4] |= uint32_t(pack_e4m3(a - t.x, b - t.y)) << (i & 2) * 8;
+                            }
+                            const uint32_t at = row8_piece<D>(row, c >> 1) + uint32_t(c & 1) * 8u;
+                            *reinterpret_cast<uint2 *>(q_img + at) = make_uint2(w1[0], w1[1]);
+                            *reinterpret_cast<uint2 *>(q_img + kSideRows * D + at) = make_uint2(w2[0], w2[1]);
+                            if (c == 0) sc8.q_unit[(n_q[s] - 1) & 1][s][row] = exp2_biased(e);
+                        }
+                    } else {
 #pragma unroll 4
-                    for (int row = qt / CPR; row < kSideRows; row += 128 / CPR) {
-                        const int r = (kByKeys ? 0 : s * kSideRows) + row;
-                        cp_async16_or_zero(q_img + sw128_chunk(row, c, kSideRows),
-                                           q + it.at(min(r, it.rows - 1), p.group, p.q_stride, D), r < it.rows);
+                        for (int row = qt / CPR; row < kSideRows; row += 128 / CPR) {
+                            const int r = (kByKeys ? 0 : s * kSideRows) + row;
+                            cp_async16_or_zero(q_img + sw128_chunk(row, c, kSideRows),
+                                               q + it.at(min(r, it.rows - 1), p.group, p.q_stride, D), r < it.rows);
+                        }
+                        cp_async_wait_all();
                     }
-                    cp_async_wait_all();
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.q_full[s]);
                 }
                 for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tile) {
-                    const uint32_t absent = absent_groups(p, it, kb, lane), fill = 2u * tile + 1u, st = fill % NST;
-                    wait_for(ok, &ms.full[fill % kFills], (fill / kFills) & 1, err);
+                    const uint32_t absent = absent_groups(p, it, kb, lane);
+                    wait_tile(ok, ms.v_full, tile, err);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     uint32_t odd = 0;
                     if (partly_seen(it, kb, absent)) {
                         // a lane looks over one value row, each at a bank of its own
                         const int row = w * 32 + lane, j = kb + row;
-                        unsigned char *img = ring + st * C::kTileBytes + row * 128;
+                        unsigned char *img = v_ring + tile % NV * C::kVBytes + row * 128;
                         const bool gone = j >= it.k1 || (absent >> (row / 16) & 1);
                         bool bad = false;
                         for (int c = 0; c < D / 8; ++c)
@@ -677,47 +858,50 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3>::kThreads, 1)
                         odd = __ballot_sync(0xffffffffu, bad);
                         fence_proxy_async_smem();
                     }
-                    const uint32_t lk = tile % kLooked;
-                    if (lane == 0) ms.odd[lk][w] = odd;
+                    if (lane == 0) ms.odd[tile % kBars][w] = odd;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.clean[lk]);
+                    if (lane == 0) mbar_arrive(&ms.clean[tile % kBars]);
                 }
             }
         } else if (kE4m3 && ms.has && warp >= 16) {
-            // ---- e4m3 tiles to bf16 ---------------------------------------------------------
-            constexpr int UPK = D / 16;             // 16-byte pieces of a key
-            constexpr int UPT = KT * UPK / 128;     // of a thread
-            const int ct = tid - 512;
+            // ---- e4m3 value tiles to bf16 ---------------------------------------------------------
+            constexpr int UPT = KT * D / 16 / 256;  // pieces of a thread
+            const int cw = warp - 16;
             ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it;
-            uint32_t fill = 0;
+            Item it = {};
+            uint32_t tile = 0;
             while (ok && walk.next(p, it)) {
-                const int fills = 2 * item_tiles(it);
-                for (int i = 0; i < fills && ok; ++i, ++fill) {
-                    const uint32_t rs = fill % NRAW, st = fill % NST;
-                    wait_for(ok, &ms.raw_full[rs], (fill / NRAW) & 1, err);
-                    wait_stage<NST>(ok, ms.empty, fill, err);
+                for (int i = 0; i < item_tiles(it) && ok; ++i, ++tile) {
+                    wait_tile(ok, ms.raw_full, tile, err);
+                    wait_stage<NV>(ok, ms.v_empty, tile, err);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    const uint4 *raw = reinterpret_cast<const uint4 *>(smem + C::kRawAt + rs * C::kRawBytes);
-                    unsigned char *dst = ring + st * C::kTileBytes;
+                    const unsigned char *raw = raw_ring + tile % NR * C::kRawBytes;
+                    const uint8_t *scale = sc8.v[tile % NR];
+                    unsigned char *dst = v_ring + tile % NV * C::kVBytes;
+                    uint4 q[UPT];
+                    uint32_t e[UPT], odd = 0;
 #pragma unroll
                     for (int u = 0; u < UPT; ++u) {
-                        const int key = (u * 128 + ct) / UPK, c = ct % UPK;
-                        const uint4 q = raw[u * 128 + ct];
-                        const float f = exp2_biased(ms.scale[rs][key]);
-                        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-                        uint32_t o[8];
+                        const RawPiece<D> r(cw, lane, u);
+                        q[u] = *reinterpret_cast<const uint4 *>(raw + r.from);
+                        e[u] = scale[r.key];
+                        odd |= nan_codes(q[u]) | uint32_t(e[u] > 134u);
+                    }
+                    if (odd == 0) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 t = unpack_e4m3(uint16_t(in[e / 2] >> ((e & 1) * 16)));
-                            o[e] = pack_bf16(t.x * f, t.y * f);
+                        for (int u = 0; u < UPT; ++u) {
+                            const RawPiece<D> r(cw, lane, u);
+                            uint32_t o[8];
+                            widen_plain(q[u], e[u], o);
+                            *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
-                        *reinterpret_cast<uint4 *>(dst + sw128_chunk(key, 2 * c, KT)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(dst + sw128_chunk(key, 2 * c + 1, KT)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else {
+                        widen_any<D>(raw, dst, scale, cw, lane);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.full[fill % kFills]), mbar_arrive(&ms.raw_empty[rs]);
+                    if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                 }
             }
         }
@@ -742,8 +926,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // [num_pages * num_kv_heads][page_size][head_dim]; a box is a tile's part of
-// one page and head (64 channels of it for bf16, whose tiles are 128-byte
-// swizzled).
+// one page and head (64 channels of it for bf16), swizzled over its row of 128
+// or 64 bytes.
 bool page_map(CUtensorMap *m, const void *base, const kda_kv_cache *c, bool e4m3) {
     auto fn = encode_fn();
     if (!fn) return false;
@@ -754,16 +938,17 @@ bool page_map(CUtensorMap *m, const void *base, const kda_kv_cache *c, bool e4m3
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              e4m3 && c->head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, bool kE4m3, bool kByKeys>
 kda_status launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    using C = Cfg<D, kE4m3, kByKeys>;
     TileMaps maps;
     if (!page_map(&maps.k, c->k, c, kE4m3) || !page_map(&maps.v, c->v, c, kE4m3)) return KDA_ERR_CUDA;
     auto kern = attend_tile_kernel<D, kE4m3, kByKeys>;
-    constexpr size_t smem = smem_bytes<D, kE4m3>();
+    constexpr size_t smem = smem_bytes<C, kE4m3>();
     static_assert(smem <= 232448, "shared memory of a CTA");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) {
         cudaGetLastError();
@@ -773,7 +958,7 @@ kda_status launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan
     p.item_cost = kItemCost;
     p.min_keys = (kByKeys ? 2 : 1) * KT;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
-    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), Cfg<D, kE4m3>::kThreads, smem, stream, p, maps);
+    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), C::kThreads, smem, stream, p, maps);
 }
 
 template <int D>
@@ -788,7 +973,7 @@ kda_status by_type(const kda_kv_cache *c, AttendParams &p, const AttendPlan &pla
 
 bool tile_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
     const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
-    if (c->act != KDA_BF16 || (c->head_dim != 64 && c->head_dim != 128) || rows <= 16) return false;
+    if (c->act != KDA_BF16 || (c->head_dim != 64 && c->head_dim != 128)) return false;
     plan->bm = rows <= kSideRows ? kSideRows : 2 * kSideRows;
     plan->n_cta = sm_count();
     return true;

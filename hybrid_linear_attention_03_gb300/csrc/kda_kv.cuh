@@ -87,8 +87,8 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // 2^(127 - e) for the biased exponent e >= 1 (the quantising factor; e = 254
 // gives a subnormal, which a finite amax never reaches).
 __device__ __forceinline__ float exp2_neg_biased(int e) { return __uint_as_float(uint32_t(254 - e) << 23); }
-// 2^(e - 127); 0 for e = 0, the exponent of a zero vector.
-__device__ __forceinline__ float exp2_biased(int e) { return __uint_as_float(uint32_t(e) << 23); }
+// 2^(e - 127), e in [0, 254].
+__device__ __forceinline__ float exp2_biased(int e) { return __uint_as_float(e == 0 ? 0x400000u : uint32_t(e) << 23); }
 
 __device__ __forceinline__ uint16_t pack_e4m3(float lo, float hi) {  // round to nearest even, saturating
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
