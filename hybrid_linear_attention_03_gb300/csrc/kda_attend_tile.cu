@@ -24,13 +24,13 @@
 //
 // Warps: 0-3 side 0, 4-7 side 1 (a thread a row); 8 and 9 issue a side's
 // products each; 10 and 11 fetch
-// pages by TMA into rings of key and value tiles; 12-15 bring the
-// rows of Q and look value tiles over (below).
+// pages by TMA into rings of key and value tiles; 12-15 bring the rows of Q and
+// look value tiles over (below).
 //
 // e4m3 pages: keys go to the tensor cores as they are, against Q as the sum of
 // two e4m3 terms, which is Q itself (as many cycles as bf16 products take), and
 // the keys' scales multiply the scores.  Values meet bf16 weights, so warps
-// 16-23 turn raw value tiles into bf16 ones, scale included and exact.
+// 12-19 turn raw value tiles into bf16 ones, scale included and exact.
 //
 // A value behind a row's position weighs nothing, but 0 * NaN is NaN in the
 // product.  So in the few tiles where some row does not see some key, warps
@@ -52,6 +52,14 @@ using namespace sm100;
 constexpr int KT = 128;          // keys of a tile
 constexpr int KH = KT / 2;        // keys of a half
 constexpr int kSideRows = 128;   // rows of a side
+// Warps: 8 of softmax, 4 that issue, then those of Q and the value tiles (8 where
+// these are e4m3 and have to be widened).  Registers a thread after the split,
+// of 128 (bf16) or 96 (e4m3) at launch.
+template <bool kE4m3> struct Warps {
+    static constexpr int kRowWarps = kE4m3 ? 8 : 4, kThreads = (12 + kRowWarps) * 32, kLaunch = kE4m3 ? 96 : 128;
+    static constexpr int kSoftmax = kE4m3 ? 144 : 200, kIssue = kE4m3 ? 48 : 56, kRows = kE4m3 ? 72 : 56;
+    static_assert(8 * kSoftmax + 4 * kIssue + kRowWarps * kRows == (12 + kRowWarps) * kLaunch, "the split uses what the launch has");
+};
 constexpr float kRefSlack = 8.f;
 #ifndef ITEM_COST
 #define ITEM_COST 384
@@ -59,12 +67,6 @@ constexpr float kRefSlack = 8.f;
 constexpr int kItemCost = ITEM_COST;
 
 template <int D, bool kE4m3, bool kByKeys> struct Cfg {
-    static constexpr int kThreads = kE4m3 ? 768 : 512;
-    // Registers a thread after the split: every SM quarter holds two softmax
-    // warps and two (bf16) or four (e4m3) others, 128 or 80 registers each at
-    // launch: 256 * 200 + 256 * 56 = 512 * 128, 256 * 112 + 512 * 64 = 768 * 80.
-    static constexpr int kRegsSoftmax = kE4m3 ? 112 : 200;
-    static constexpr int kRegsOther = kE4m3 ? 64 : 56;
     static constexpr int kQBytes = kSideRows * D * 2;            // bf16, or two e4m3 terms
     static constexpr int kKBytes = KT * D * (kE4m3 ? 1 : 2), kVBytes = KT * D * 2, kRawBytes = KT * D;
     // Shared memory: the rows of Q once (by keys) or a side (by rows), and rings
@@ -88,19 +90,24 @@ constexpr int kBars = 8;
 
 template <typename C> struct alignas(16) Misc {
     uint64_t k_full[kBars], k_empty[kBars], v_full[kBars], v_empty[kBars], clean[kBars];
-    uint64_t raw_full[kBars], raw_empty[kBars];
+    uint64_t raw_full[kBars], raw_empty[kBars], unit_full[kBars];
     uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];  // by side and half
     uint64_t q_full[2], q_free[2], done[2];
+    uint64_t row_unit[2][2];  // e4m3, by image and item parity: the rows' scales are there
     uint32_t tmem;
     int has;
     Cursor piece[2];
     uint32_t odd[kBars][4];                        // by tile: keys whose value row was taken out of it
     float m[kSideRows], l[kSideRows];              // side 1's row statistics, for the join
 };
+// A tile's key scales are written once its keys have landed, in a stage that the
+// scores of the tile kStagesK before have left; those come after the same side's
+// weights of two tiles before that, so kUnits sets are enough.
+constexpr int kUnits = 8;
 template <typename C> struct ScaleMisc {  // e4m3 pages only
     alignas(16) uint8_t k[C::kStagesK][KT];  // the tiles' scale exponents
     alignas(16) uint8_t v[C::kStagesRaw][KT];
-    alignas(16) float k_unit[2][2][KT];      // by side and tile parity, the keys' scales
+    alignas(16) float k_unit[kUnits][KT];    // by tile, the keys' scales
     float q_unit[2][2][kSideRows];           // by item parity and image, the rows' scales
 };
 
@@ -184,10 +191,12 @@ __device__ __forceinline__ void cp_async16_or_zero(void *smem_dst, const void *g
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int kId, int kThreads> __device__ __forceinline__ void named_sync() {
-    asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kThreads) : "memory");
+template <int N, int kLaunch> __device__ __forceinline__ void set_regs() {
+    if constexpr (N > kLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int kId, int kCount> __device__ __forceinline__ void named_sync() {
+    asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kCount) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -233,6 +242,31 @@ __device__ __forceinline__ void widen_plain(const uint4 &q, uint32_t e, uint32_t
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(v), "r"(f));
     }
 }
+// Eight bf16 of a row of Q, of which kLanes neighbouring lanes hold one row, as
+// two e4m3 terms times a power of two; returns its biased exponent.
+template <int kLanes> __device__ __forceinline__ int split_row(const uint4 &raw, uint32_t (&w1)[2], uint32_t (&w2)[2]) {
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    // the largest magnitude as a bf16 pattern, of finite values (a row with others is NaN all the same)
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, in[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool odd = m >= 0x7f80u;
+    const int e = odd ? 127 : max(scale_exponent(__uint_as_float(m << 16)), 1);
+    const float f = odd ? NAN : exp2_neg_biased(e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = __uint_as_float(in[i] << 16) * f, b = __uint_as_float(in[i] & 0xffff0000u) * f;
+        const uint16_t h1 = pack_e4m3(a, b);
+        const float2 t = unpack_e4m3(h1);
+        const uint16_t h2 = pack_e4m3(a - t.x, b - t.y);
+        if (i % 2 == 0) w1[i / 2] = h1, w2[i / 2] = h2;
+        else w1[i / 2] |= uint32_t(h1) << 16, w2[i / 2] |= uint32_t(h2) << 16;
+    }
+    return e;
+}
 // Bit 7 of a byte is set where one of the 16 codes is NaN.
 __device__ __forceinline__ uint32_t nan_codes(const uint4 &q) {
     return (((q.x & 0x7f7f7f7fu) + 0x01010101u) | ((q.y & 0x7f7f7f7fu) + 0x01010101u) |
@@ -249,28 +283,9 @@ __device__ __forceinline__ bool odd_bf16(const uint4 &w) {
 
 // A bounded wait that is skipped once one has given up.  The row warps then run
 // on with whatever is there (all in bounds, the error word is set), so that the
-// CTA's own barriers are met; the other roles stop issuing.  Each try sleeps for
-// up to a millisecond: a thread that polls takes issue slots from the others, and
-// reading the clock takes longer than most waits.
+// CTA's own barriers are met; the other roles stop issuing.
 __device__ __forceinline__ void wait_for(bool &ok, uint64_t *bar, uint32_t parity, uint32_t *err) {
-    if (!ok) return;
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-            : "memory");
-        if (done) return;
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > 2000000000ull) break;
-    }
-    atomicOr(err, KDA_DEVERR_TIMEOUT);
-    ok = false;
+    if (ok) ok = mbar_wait(bar, parity, err);
 }
 // Tile t's barrier of a ring has been passed.
 __device__ __forceinline__ void wait_tile(bool &ok, uint64_t *bars, uint32_t t, uint32_t *err) {
@@ -304,6 +319,15 @@ struct TileMaps {
     CUtensorMap k, v;
 };
 
+// ItemWalk::next out of line (every role has a copy of the walk); the caller's
+// item stays in its registers.
+__device__ __forceinline__ bool next_item_call(const AttendParams &p, ItemWalk *walk, Item *it) { return walk->next(p, *it); }
+__device__ __forceinline__ bool next_item(const AttendParams &p, ItemWalk &walk, Item &it) {
+    Item got;
+    const bool has = next_item_call(p, &walk, &got);
+    if (has) it = got;
+    return has;
+}
 __device__ __forceinline__ int item_tiles(const Item &it) { return (it.k1 - it.k0 + KT - 1) / KT; }
 // Key tiles of an item's share that side s computes, and the v-th of them.
 template <bool kByKeys> __device__ __forceinline__ int side_tiles(const Item &it, int s) {
@@ -370,20 +394,21 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
 // 8 neighbouring lanes take the same 16-byte piece of 8 keys, which both tiles'
 // swizzles put into different banks.
 template <int D> struct RawPiece {
+    static constexpr int kPerKey = D / 64, kCount = 2 * kPerKey;  // of a key, of a lane
     int key;
     uint32_t from, to;  // byte offsets in the raw and the wide tile (whose next 16 bytes are at to ^ 16)
     __device__ __forceinline__ RawPiece(int w, int lane, int u) {
-        const int c = (lane >> 3) + (D == 128 ? 4 * (u & 1) : 0);
-        key = w * 16 + (lane & 7) + 8 * (D == 128 ? u >> 1 : u);
-        from = row8_piece<D>(key, c);
-        to = sw128_chunk(key, 2 * c, KT);
+        const int c = lane >> 3, k0 = w * 16 + (lane & 7), g = u / kPerKey, i = u % kPerKey;
+        key = k0 + 8 * g;
+        from = (row8_piece<D>(k0, c) ^ uint32_t(i * 64)) + uint32_t(8 * g * D);
+        to = sw128_chunk(k0, 2 * c, KT) + uint32_t(g * 1024 + i * KT * 128);
     }
 };
 // The pieces of a lane by the conversion instructions, whatever they hold.
 template <int D>
 __device__ __noinline__ void widen_any(const unsigned char *raw, unsigned char *dst, const uint8_t *scale, int w, int lane) {
 #pragma unroll 1
-    for (int u = 0; u < KT * D / 16 / 256; ++u) {
+    for (int u = 0; u < RawPiece<D>::kCount; ++u) {
         const RawPiece<D> r(w, lane, u);
         const float f = exp2_biased(scale[r.key]);
 #pragma unroll 1
@@ -393,11 +418,41 @@ __device__ __noinline__ void widen_any(const unsigned char *raw, unsigned char *
         }
     }
 }
+// A widened tile of which some row does not see some key: zeroes the rows of
+// absent keys and takes out the non-finite ones that not every row sees.
+// Returns the keys taken out, a bit each of the warp's 16.
+template <int D>
+__device__ __noinline__ uint32_t look_over_raw(const AttendParams &p, const Item &it, int kb, uint32_t absent,
+                                               const unsigned char *raw, unsigned char *dst, const uint8_t *scale, int w,
+                                               int lane) {
+    uint32_t odd = 0;
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+        const int key = w * 16 + 8 * g + (lane & 7), j = kb + key;
+        uint32_t nan = scale[key] >= 247;  // 448 * 2^(247 - 127) is past bf16's range, and 255 is NaN
+        for (int i = 0; i < RawPiece<D>::kPerKey; ++i)
+            nan |= nan_codes(*reinterpret_cast<const uint4 *>(raw + RawPiece<D>(w, lane, g * RawPiece<D>::kPerKey + i).from));
+        nan |= __shfl_xor_sync(0xffffffffu, nan, 8);
+        nan |= __shfl_xor_sync(0xffffffffu, nan, 16);
+        const bool gone = j >= it.k1 || (absent >> (key / 16) & 1);
+        const bool out = !gone && nan != 0 && j > it.ctx + it.tok0;
+        odd |= (__ballot_sync(0xffffffffu, out) & 0xffu) << (8 * g);
+        if (gone || out) {
+            for (int i = 0; i < RawPiece<D>::kPerKey; ++i) {
+                const uint32_t to = RawPiece<D>(w, lane, g * RawPiece<D>::kPerKey + i).to;
+                *reinterpret_cast<uint4 *>(dst + to) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(dst + (to ^ 16u)) = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    return odd;
+}
 
 template <int D, bool kE4m3, bool kByKeys>
-__global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
+__global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
     attend_tile_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TileMaps maps) {
     using C = Cfg<D, kE4m3, kByKeys>;
+    using W = Warps<kE4m3>;
     constexpr int NK = C::kStagesK, NV = C::kStagesV, NR = C::kStagesRaw, BM = kByKeys ? kSideRows : 2 * kSideRows;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -408,16 +463,19 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
-            mbar_init(&ms.k_full[i], 1), mbar_init(&ms.v_full[i], kE4m3 ? 8 : 1);
+            mbar_init(&ms.k_full[i], 1), mbar_init(&ms.v_full[i], kE4m3 ? W::kRowWarps : 1);
             // by rows both sides are done with a tile
-            mbar_init(&ms.k_empty[i], kByKeys ? 1 : 2), mbar_init(&ms.v_empty[i], kByKeys ? 1 : 2);
-            mbar_init(&ms.clean[i], 4), mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], 8);
+            mbar_init(&ms.k_empty[i], (kByKeys ? 1 : 2) + (kE4m3 ? W::kRowWarps : 0));  // and the scales read
+            mbar_init(&ms.v_empty[i], kByKeys ? 1 : 2);
+            mbar_init(&ms.clean[i], 4), mbar_init(&ms.raw_full[i], 1), mbar_init(&ms.raw_empty[i], W::kRowWarps);
+            mbar_init(&ms.unit_full[i], W::kRowWarps);
         }
         for (int i = 0; i < 2; ++i) {
             for (int h = 0; h < 2; ++h)
                 mbar_init(&ms.s_full[i][h], 1), mbar_init(&ms.p_ready[i][h], 4), mbar_init(&ms.pv_done[i][h], 1);
-            mbar_init(&ms.q_full[i], 4), mbar_init(&ms.q_free[i], kByKeys ? 2 : 1);
+            mbar_init(&ms.q_full[i], W::kRowWarps), mbar_init(&ms.q_free[i], kByKeys ? 2 : 1);
             mbar_init(&ms.done[i], 1);
+            for (int h = 0; h < 2; ++h) mbar_init(&ms.row_unit[i][h], W::kRowWarps);
         }
         fence_mbar_init();
     }
@@ -438,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
     bool ok = true;  // of this thread's waits
 
     if (warp < 8) {
-        reg_inc<C::kRegsSoftmax>();
+        set_regs<W::kSoftmax, W::kLaunch>();
         if (ms.has) {
             // ---- softmax: thread = row -------------------------------------------------
             const int s = warp >> 2, row = tid & 127;
@@ -454,31 +512,26 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                 __syncwarp();
                 tc_fence_after();
             };
-            while (walk.next(p, it)) {
+            while (next_item(p, walk, it)) {
                 const int nv = side_tiles<kByKeys>(it, s);
                 const int lim = it.ctx + it.tok0 + min(r, it.rows - 1) / p.group;  // last key this row sees
                 const bool live = r - lane < it.rows;  // this warp has rows of the item
                 float ref = -INFINITY, l = 0.f, scale = p.scale_log2;
                 if constexpr (kE4m3) {
-                    if (kByKeys || nv > 0) {
-                        constexpr int kImage1 = kByKeys ? 0 : 1;
-                        const int qi = s ? kImage1 : 0;
-                        wait_for(ok, &ms.q_full[qi], n_it & 1, err);
+                    if (nv > 0) {
+                        // by item parity: Q may be an item ahead of this side's threads, never two
+                        const int qi = kByKeys ? 0 : s;
+                        wait_for(ok, &ms.row_unit[qi][n_it & 1], (n_it >> 1) & 1, err);
                         scale *= sc8.q_unit[n_it & 1][qi][row];
-                        ++n_it;
                     }
+                    if (kByKeys || nv > 0) ++n_it;
                 }
                 for (int v = 0; v < nv; ++v, ++n_s) {
                     const int t = side_tile<kByKeys>(s, v), kb = it.k0 + t * KT;
                     const uint32_t absent = absent_groups(p, it, kb, lane);
                     const bool check = partly_seen(it, kb, absent);
-                    if constexpr (kE4m3) {  // the keys' scales as numbers, a key a thread
-                        const uint32_t tg = tile_base + uint32_t(t);
-                        wait_tile(ok, ms.k_full, tg, err);
-                        sc8.k_unit[s][n_s & 1][row] = exp2_biased(sc8.k[tg % NK][row]);
-                        if (s) named_sync<3, 128>();
-                        else named_sync<2, 128>();
-                    }
+                    const uint32_t tg = tile_base + uint32_t(t);
+                    if constexpr (kE4m3) wait_tile(ok, ms.unit_full, tg, err);
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t t_h = t_s + uint32_t(h) * KH;
@@ -496,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                             if constexpr (kE4m3) {
 #pragma unroll
                                 for (int c = 0; c < KH; c += 4) {
-                                    const float4 u = *reinterpret_cast<const float4 *>(&sc8.k_unit[s][n_s & 1][h * KH + c]);
+                                    const float4 u = *reinterpret_cast<const float4 *>(&sc8.k_unit[tg % kUnits][h * KH + c]);
                                     const float2 a = mul2(make_float2(x[c], x[c + 1]), make_float2(u.x, u.y));
                                     const float2 b = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(u.z, u.w));
                                     x[c] = a.x, x[c + 1] = a.y, x[c + 2] = b.x, x[c + 3] = b.y;
@@ -520,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                                 const float to = move ? top : ref, f = move ? ex2(ref - to) : 1.f;
                                 if (started) {
                                     wait_o(h == 0 ? n_s - 1 : n_s, h ^ 1);
-#pragma unroll
+#pragma unroll 1
                                     for (int c = 0; c < D; c += 16) {
                                         float o[16];
                                         tmem_ld16(t_o + uint32_t(c), o);
@@ -551,13 +604,13 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                             tmem_wait_st();
                             if (check) {
-                                const uint32_t tg = tile_base + uint32_t(t);
-                                wait_tile(ok, ms.clean, tg, err);
+                                wait_tile(ok, kE4m3 ? ms.v_full : ms.clean, tg, err);
                                 __syncwarp();
                                 const uint32_t *odd = &ms.odd[tg % kBars][h * (KH / 32)];
                                 if (any_odd(odd)) {
                                     if (started) wait_o(h == 0 ? n_s - 1 : n_s, h ^ 1);
-                                    add_odd_rows<D, kE4m3>(p, it, kh, lim, odd, t_h, t_o, !started);
+                                    const Item copy = it;
+                                    add_odd_rows<D, kE4m3>(p, copy, kh, lim, odd, t_h, t_o, !started);
                                 }
                             }
                         }  // else rows of nobody: their weights may be anything
@@ -591,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                     float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * (D + 2);
                     __nv_bfloat16 *dst =
                         static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p.group, p.out_stride, D);
-#pragma unroll
+#pragma unroll 2
                     for (int c = 0; c < D; c += 16) {
                         float o[16];
                         tmem_ld16(t_o + uint32_t(c), o);
@@ -634,8 +687,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                 if (kByKeys) named_sync<1, 256>();
             }
         }
-    } else {
-        reg_dec<C::kRegsOther>();
+    } else if (warp < 12) {
+        set_regs<W::kIssue, W::kLaunch>();
         if (ms.has && warp < 10) {
             // ---- products of a side (converged warp, one lane issues) ----------------------
             const int s = warp - 8;
@@ -680,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                 }
                 __syncwarp();
             };
-            while (ok && walk.next(p, it)) {
+            while (ok && next_item(p, walk, it)) {
                 nv = side_tiles<kByKeys>(it, s);
                 if (kByKeys || nv > 0) wait_for(ok, &ms.q_full[qi], n_q++ & 1, err);
                 if (nv > 0) {
@@ -692,7 +745,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                 for (int v = 0; v < nv && ok; ++v, ++n_p) {
                     const uint32_t tg = base + uint32_t(side_tile<kByKeys>(s, v));
                     wait_tile(ok, ms.v_full, tg, err);
-                    wait_tile(ok, ms.clean, tg, err);
+                    if (!kE4m3) wait_tile(ok, ms.clean, tg, err);
                     // the first product starts O, unless value rows were added to it by hand
                     const uint32_t acc = v > 0 || any_odd(ms.odd[tg % kBars]);
                     const uint64_t vd = v_desc + uint64_t(tg % NV * uint32_t(C::kVBytes >> 4));
@@ -729,7 +782,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
             __syncwarp();
             bool end_ok = true;
             wait_for(end_ok, &ms.done[s], 0, err);
-        } else if (ms.has && warp < 12) {
+        } else if (ms.has) {
             // ---- page fetches: keys, or values ------------------------------------------------
             const bool values = warp == 11;
             const CUtensorMap *map = values ? &maps.v : &maps.k;
@@ -756,7 +809,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                         tma_load_3d(dst + lane * box * 128 + c * KT * 128, map, full, c * 64, line, plane);
                 }
             };
-            while (ok && walk.next(p, it)) {
+            while (ok && next_item(p, walk, it)) {
                 for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tg) {
                     if (!values) wait_stage<NK>(ok, ms.k_empty, tg, err);
                     else if (kE4m3) wait_stage<NR>(ok, ms.raw_empty, tg, err);
@@ -774,134 +827,146 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kByKeys>::kThreads, 1)
                 bool end_ok = true;
                 for (uint32_t t = tg - min(tg, depth); t < tg; ++t) wait_tile(end_ok, bars, t, err);
             }
-        } else if (ms.has && warp >= 12 && warp < 16) {
-            // ---- rows of Q, and value tiles looked over ------------------------------------
+        }
+    } else {
+        set_regs<W::kRows, W::kLaunch>();
+        if (ms.has) {
+            // ---- rows of Q; value tiles looked over, and (e4m3) made bf16 ---------------------
             const int w = warp - 12, qt = tid - 384;
+            constexpr int kRowThreads = W::kRowWarps * 32;
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t n_q[2] = {0, 0}, tile = 0;
-            while (ok && walk.next(p, it)) {
+            while (ok && next_item(p, walk, it)) {
                 for (int s = 0; s < C::kQImages; ++s) {
                     if (side_tiles<kByKeys>(it, s) == 0) continue;
-                    wait_for(ok, &ms.q_free[s], (n_q[s]++ & 1) ^ 1, err);  // the last item's scores have read it
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     unsigned char *q_img = smem + s * C::kQBytes;
-                    constexpr int CPR = D / 8;  // 16-byte pieces of a row
+                    constexpr int CPR = D / 8, RPP = kRowThreads / CPR;  // 16-byte pieces of a row, rows a pass
                     const int c = qt % CPR;
                     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
+                    auto row_at = [&](int row) {  // this thread's piece of a row of the item
+                        return q + it.at(min((kByKeys ? 0 : s * kSideRows) + row, it.rows - 1), p.group, p.q_stride, D);
+                    };
+                    auto is_there = [&](int row) { return (kByKeys ? 0 : s * kSideRows) + row < it.rows; };
+                    auto wait_image = [&] {  // the last item's scores have read it
+                        wait_for(ok, &ms.q_free[s], (n_q[s] & 1) ^ 1, err);
+                        ok = __all_sync(0xffffffffu, ok);
+                    };
                     if constexpr (kE4m3) {
                         // a row as 2^e (q1 + q2): e4m3 keeps 4 significant bits, so q1 and what q1 leaves
                         // hold all 8 of a bf16 (down to 2^-18 of the row's largest value)
-#pragma unroll 2
-                        for (int row = qt / CPR; row < kSideRows; row += 128 / CPR) {
-                            const int r = (kByKeys ? 0 : s * kSideRows) + row;
-                            uint4 raw = make_uint4(0, 0, 0, 0);
-                            if (r < it.rows) raw = *reinterpret_cast<const uint4 *>(q + it.at(r, p.group, p.q_stride, D));
-                            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                            float y[8], m = 0.f;
+                        constexpr int kBatch = 4;
+#pragma unroll 1
+                        for (int r0 = qt / CPR; r0 < kSideRows; r0 += RPP * kBatch) {
+                            uint4 raw[kBatch];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                y[i] = __uint_as_float(i & 1 ? in[i / 2] & 0xffff0000u : in[i / 2] << 16);
-                                m = fmaxf(m, isfinite(y[i]) ? fabsf(y[i]) : 0.f);
+                            for (int b = 0; b < kBatch; ++b) {
+                                const int row = r0 + b * RPP;
+                                raw[b] = is_there(row) ? *reinterpret_cast<const uint4 *>(row_at(row)) : make_uint4(0, 0, 0, 0);
                             }
+                            if (r0 < RPP) wait_image();
+                            if (!ok) break;
 #pragma unroll
-                            for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            const int e = max(scale_exponent(m), 1);
-                            const float f = exp2_neg_biased(e);
-                            uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const float a = isfinite(y[i]) ? y[i] * f : NAN, b = isfinite(y[i + 1]) ? y[i + 1] * f : NAN;
-                                const uint16_t h1 = pack_e4m3(a, b);
-                                const float2 t = unpack_e4m3(h1);
-                                w1[i / 4] |= uint32_t(h1) << (i & 2) * 8;
-                                w2[i / 4] |= uint32_t(pack_e4m3(a - t.x, b - t.y)) << (i & 2) * 8;
+                            for (int b = 0; b < kBatch; ++b) {
+                                const int row = r0 + b * RPP;
+                                uint32_t w1[2], w2[2];
+                                const int e = split_row<CPR>(raw[b], w1, w2);
+                                const uint32_t at = row8_piece<D>(row, c >> 1) + uint32_t(c & 1) * 8u;
+                                *reinterpret_cast<uint2 *>(q_img + at) = make_uint2(w1[0], w1[1]);
+                                *reinterpret_cast<uint2 *>(q_img + kSideRows * D + at) = make_uint2(w2[0], w2[1]);
+                                if (c == 0) sc8.q_unit[n_q[s] & 1][s][row] = exp2_biased(e);
                             }
-                            const uint32_t at = row8_piece<D>(row, c >> 1) + uint32_t(c & 1) * 8u;
-                            *reinterpret_cast<uint2 *>(q_img + at) = make_uint2(w1[0], w1[1]);
-                            *reinterpret_cast<uint2 *>(q_img + kSideRows * D + at) = make_uint2(w2[0], w2[1]);
-                            if (c == 0) sc8.q_unit[(n_q[s] - 1) & 1][s][row] = exp2_biased(e);
                         }
+                        __syncwarp();
+                        if (ok && lane == 0) mbar_arrive(&ms.row_unit[s][n_q[s] & 1]);
                     } else {
+                        wait_image();
+                        if (ok) {
 #pragma unroll 4
-                        for (int row = qt / CPR; row < kSideRows; row += 128 / CPR) {
-                            const int r = (kByKeys ? 0 : s * kSideRows) + row;
-                            cp_async16_or_zero(q_img + sw128_chunk(row, c, kSideRows),
-                                               q + it.at(min(r, it.rows - 1), p.group, p.q_stride, D), r < it.rows);
+                            for (int row = qt / CPR; row < kSideRows; row += RPP)
+                                cp_async16_or_zero(q_img + sw128_chunk(row, c, kSideRows), row_at(row), is_there(row));
+                            cp_async_wait_all();
                         }
-                        cp_async_wait_all();
                     }
+                    if (!ok) break;
+                    ++n_q[s];
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.q_full[s]);
                 }
                 for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tile) {
                     const uint32_t absent = absent_groups(p, it, kb, lane);
-                    wait_tile(ok, ms.v_full, tile, err);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    uint32_t odd = 0;
-                    if (partly_seen(it, kb, absent)) {
-                        // a lane looks over one value row, each at a bank of its own
-                        const int row = w * 32 + lane, j = kb + row;
-                        unsigned char *img = v_ring + tile % NV * C::kVBytes + row * 128;
-                        const bool gone = j >= it.k1 || (absent >> (row / 16) & 1);
-                        bool bad = false;
-                        for (int c = 0; c < D / 8; ++c)
-                            bad |= odd_bf16(*reinterpret_cast<const uint4 *>(img + (c >> 3) * KT * 128 +
-                                                                             (((c & 7) ^ (lane & 7)) << 4)));
-                        bad = bad && !gone && j > it.ctx + it.tok0;  // rows that every query sees stay
-                        if (gone || bad) {
-                            for (int c = 0; c < D / 8; ++c)
-                                *reinterpret_cast<uint4 *>(img + (c >> 3) * KT * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        odd = __ballot_sync(0xffffffffu, bad);
-                        fence_proxy_async_smem();
-                    }
-                    if (lane == 0) ms.odd[tile % kBars][w] = odd;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.clean[tile % kBars]);
-                }
-            }
-        } else if (kE4m3 && ms.has && warp >= 16) {
-            // ---- e4m3 value tiles to bf16 ---------------------------------------------------------
-            constexpr int UPT = KT * D / 16 / 256;  // pieces of a thread
-            const int cw = warp - 16;
-            ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it = {};
-            uint32_t tile = 0;
-            while (ok && walk.next(p, it)) {
-                for (int i = 0; i < item_tiles(it) && ok; ++i, ++tile) {
-                    wait_tile(ok, ms.raw_full, tile, err);
-                    wait_stage<NV>(ok, ms.v_empty, tile, err);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    const unsigned char *raw = raw_ring + tile % NR * C::kRawBytes;
-                    const uint8_t *scale = sc8.v[tile % NR];
                     unsigned char *dst = v_ring + tile % NV * C::kVBytes;
-                    uint4 q[UPT];
-                    uint32_t e[UPT], odd = 0;
+                    uint32_t odd = 0;  // keys taken out, of this warp's
+                    if constexpr (kE4m3) {
+                        using RP = RawPiece<D>;
+                        const unsigned char *raw = raw_ring + tile % NR * C::kRawBytes;
+                        const uint8_t *scale = sc8.v[tile % NR];
+                        wait_tile(ok, ms.k_full, tile, err);  // the keys' scales as numbers
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        if (qt < KT) sc8.k_unit[tile % kUnits][qt] = exp2_biased(sc8.k[tile % NK][qt]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.unit_full[tile % kBars]), mbar_arrive(&ms.k_empty[tile % kBars]);
+                        wait_tile(ok, ms.raw_full, tile, err);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        uint4 x[RP::kCount];
+                        uint32_t e[2], rare = 0;
 #pragma unroll
-                    for (int u = 0; u < UPT; ++u) {
-                        const RawPiece<D> r(cw, lane, u);
-                        q[u] = *reinterpret_cast<const uint4 *>(raw + r.from);
-                        e[u] = scale[r.key];
-                        odd |= nan_codes(q[u]) | uint32_t(e[u] > 134u);
-                    }
-                    if (odd == 0) {
-#pragma unroll
-                        for (int u = 0; u < UPT; ++u) {
-                            const RawPiece<D> r(cw, lane, u);
-                            uint32_t o[8];
-                            widen_plain(q[u], e[u], o);
-                            *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+                        for (int u = 0; u < RP::kCount; ++u) {
+                            const RP r(w, lane, u);
+                            x[u] = *reinterpret_cast<const uint4 *>(raw + r.from);
+                            if (u % RP::kPerKey == 0) e[u / RP::kPerKey] = scale[r.key];
+                            rare |= nan_codes(x[u]);
                         }
+                        rare |= uint32_t(max(e[0], e[1]) > 134u);
+                        wait_stage<NV>(ok, ms.v_empty, tile, err);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        if (rare == 0) {
+#pragma unroll
+                            for (int u = 0; u < RP::kCount; ++u) {
+                                const RP r(w, lane, u);
+                                uint32_t o[8];
+                                widen_plain(x[u], e[u / RP::kPerKey], o);
+                                *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
+                                *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
+                            }
+                        } else {
+                            widen_any<D>(raw, dst, scale, w, lane);
+                        }
+                        __syncwarp();
+                        if (partly_seen(it, kb, absent)) {
+                            const Item copy = it;
+                            odd = look_over_raw<D>(p, copy, kb, absent, raw, dst, scale, w, lane);
+                        }
+                        fence_proxy_async_smem();
+                        if (lane == 0) reinterpret_cast<uint16_t *>(ms.odd[tile % kBars])[w] = uint16_t(odd);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                     } else {
-                        widen_any<D>(raw, dst, scale, cw, lane);
+                        wait_tile(ok, ms.v_full, tile, err);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        if (partly_seen(it, kb, absent)) {
+                            // a lane looks over one value row, each at a bank of its own
+                            const int row = w * 32 + lane, j = kb + row;
+                            unsigned char *img = dst + row * 128;
+                            const bool gone = j >= it.k1 || (absent >> (row / 16) & 1);
+                            bool bad = false;
+                            for (int c = 0; c < D / 8; ++c)
+                                bad |= odd_bf16(*reinterpret_cast<const uint4 *>(img + (c >> 3) * KT * 128 +
+                                                                                 (((c & 7) ^ (lane & 7)) << 4)));
+                            bad = bad && !gone && j > it.ctx + it.tok0;  // rows that every query sees stay
+                            if (gone || bad) {
+                                for (int c = 0; c < D / 8; ++c)
+                                    *reinterpret_cast<uint4 *>(img + (c >> 3) * KT * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
+                            odd = __ballot_sync(0xffffffffu, bad);
+                            fence_proxy_async_smem();
+                        }
+                        if (lane == 0) ms.odd[tile % kBars][w] = odd;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ms.clean[tile % kBars]);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                 }
             }
         }
@@ -958,7 +1023,7 @@ kda_status launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan
     p.item_cost = kItemCost;
     p.min_keys = (kByKeys ? 2 : 1) * KT;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
-    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), C::kThreads, smem, stream, p, maps);
+    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), Warps<kE4m3>::kThreads, smem, stream, p, maps);
 }
 
 template <int D>
