@@ -95,7 +95,7 @@ template <typename C> struct alignas(16) Misc {
     uint64_t q_full[2], q_free[2], done[2];
     uint64_t row_unit[2][2];  // e4m3, by image and item parity: the rows' scales are there
     uint32_t tmem;
-    int has;
+    int has, rows_gave_up;
     Cursor piece[2];
     uint32_t odd[kBars][4];                        // by tile: keys whose value row was taken out of it
     float m[kSideRows], l[kSideRows];              // side 1's row statistics, for the join
@@ -228,18 +228,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// 16 e4m3 values times 2^(e - 127) as bf16, exactly: s eeee mmm put at the same
-// places of a bf16 is the value times 2^-120, and one packed product with a
-// power of two (subnormal values included) makes it the value times the scale.
-// Not for NaN codes, nor for scales above 2^7, whose factor a bf16 cannot hold.
-__device__ __forceinline__ void widen_plain(const uint4 &q, uint32_t e, uint32_t (&o)[8]) {
+// 16 e4m3 values times a power of two as bf16, exactly.  (Moving the bits by
+// integer instructions and one packed product takes as long and loses the ALU
+// time that the softmax wants.)
+__device__ __forceinline__ void widen_e4m3(const uint4 &q, float f, uint32_t (&o)[8]) {
     const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-    const uint32_t half = (e + 120u) << 7, f = half | half << 16;  // bf16 2^(e - 7)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t x = __byte_perm(in[i / 2], 0, i & 1 ? 0x3424 : 0x1404);  // a byte in the top of each half
-        const uint32_t v = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(v), "r"(f));
+        const float2 t = mul2(unpack_e4m3(uint16_t(in[i / 2] >> ((i & 1) * 16))), make_float2(f, f));
+        o[i] = pack_bf16(t.x, t.y);
     }
 }
 // Eight bf16 of a row of Q, of which kLanes neighbouring lanes hold one row, as
@@ -404,20 +401,6 @@ template <int D> struct RawPiece {
         to = sw128_chunk(k0, 2 * c, KT) + uint32_t(g * 1024 + i * KT * 128);
     }
 };
-// The pieces of a lane by the conversion instructions, whatever they hold.
-template <int D>
-__device__ __noinline__ void widen_any(const unsigned char *raw, unsigned char *dst, const uint8_t *scale, int w, int lane) {
-#pragma unroll 1
-    for (int u = 0; u < RawPiece<D>::kCount; ++u) {
-        const RawPiece<D> r(w, lane, u);
-        const float f = exp2_biased(scale[r.key]);
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            const float2 t = unpack_e4m3(*reinterpret_cast<const uint16_t *>(raw + r.from + 2 * i));
-            *reinterpret_cast<uint32_t *>(dst + (i < 4 ? r.to : r.to ^ 16u) + 4 * (i & 3)) = pack_bf16(t.x * f, t.y * f);
-        }
-    }
-}
 // A widened tile of which some row does not see some key: zeroes the rows of
 // absent keys and takes out the non-finite ones that not every row sees.
 // Returns the keys taken out, a bit each of the warp's 16.
@@ -486,7 +469,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
     if (warp == 10) {
         Cursor a, z;
         const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
-        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has;
+        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has, ms.rows_gave_up = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -837,6 +820,13 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t n_q[2] = {0, 0}, tile = 0;
+            // Only the first of these warps waits by polling, which takes issue slots; the others
+            // meet it at a barrier of the hardware's, and learn there whether it gave up.
+            auto meet = [&] {
+                if (w == 0 && !ok) ms.rows_gave_up = 1;
+                named_sync<4, kRowThreads>();
+                ok = ms.rows_gave_up == 0;
+            };
             while (ok && next_item(p, walk, it)) {
                 for (int s = 0; s < C::kQImages; ++s) {
                     if (side_tiles<kByKeys>(it, s) == 0) continue;
@@ -849,8 +839,8 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     };
                     auto is_there = [&](int row) { return (kByKeys ? 0 : s * kSideRows) + row < it.rows; };
                     auto wait_image = [&] {  // the last item's scores have read it
-                        wait_for(ok, &ms.q_free[s], (n_q[s] & 1) ^ 1, err);
-                        ok = __all_sync(0xffffffffu, ok);
+                        if (w == 0) wait_for(ok, &ms.q_free[s], (n_q[s] & 1) ^ 1, err);
+                        meet();
                     };
                     if constexpr (kE4m3) {
                         // a row as 2^e (q1 + q2): e4m3 keeps 4 significant bits, so q1 and what q1 leaves
@@ -902,36 +892,30 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                         using RP = RawPiece<D>;
                         const unsigned char *raw = raw_ring + tile % NR * C::kRawBytes;
                         const uint8_t *scale = sc8.v[tile % NR];
-                        wait_tile(ok, ms.k_full, tile, err);  // the keys' scales as numbers
-                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                        if (qt < KT) sc8.k_unit[tile % kUnits][qt] = exp2_biased(sc8.k[tile % NK][qt]);
+                        if (w == 0) {
+                            wait_tile(ok, ms.k_full, tile, err), wait_tile(ok, ms.raw_full, tile, err);
+                            wait_stage<NV>(ok, ms.v_empty, tile, err);
+                        }
+                        meet();
+                        if (!ok) break;
+                        if (qt < KT) sc8.k_unit[tile % kUnits][qt] = exp2_biased(sc8.k[tile % NK][qt]);  // as numbers
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ms.unit_full[tile % kBars]), mbar_arrive(&ms.k_empty[tile % kBars]);
-                        wait_tile(ok, ms.raw_full, tile, err);
-                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
                         uint4 x[RP::kCount];
-                        uint32_t e[2], rare = 0;
+                        float f[2];
 #pragma unroll
                         for (int u = 0; u < RP::kCount; ++u) {
                             const RP r(w, lane, u);
                             x[u] = *reinterpret_cast<const uint4 *>(raw + r.from);
-                            if (u % RP::kPerKey == 0) e[u / RP::kPerKey] = scale[r.key];
-                            rare |= nan_codes(x[u]);
+                            if (u % RP::kPerKey == 0) f[u / RP::kPerKey] = exp2_biased(scale[r.key]);
                         }
-                        rare |= uint32_t(max(e[0], e[1]) > 134u);
-                        wait_stage<NV>(ok, ms.v_empty, tile, err);
-                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                        if (rare == 0) {
 #pragma unroll
-                            for (int u = 0; u < RP::kCount; ++u) {
-                                const RP r(w, lane, u);
-                                uint32_t o[8];
-                                widen_plain(x[u], e[u / RP::kPerKey], o);
-                                *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
-                                *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
-                            }
-                        } else {
-                            widen_any<D>(raw, dst, scale, w, lane);
+                        for (int u = 0; u < RP::kCount; ++u) {
+                            const RP r(w, lane, u);
+                            uint32_t o[8];
+                            widen_e4m3(x[u], f[u / RP::kPerKey], o);
+                            *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         __syncwarp();
                         if (partly_seen(it, kb, absent)) {
@@ -943,8 +927,9 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                     } else {
-                        wait_tile(ok, ms.v_full, tile, err);
-                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        if (w == 0) wait_tile(ok, ms.v_full, tile, err);
+                        meet();
+                        if (!ok) break;
                         if (partly_seen(it, kb, absent)) {
                             // a lane looks over one value row, each at a bank of its own
                             const int row = w * 32 + lane, j = kb + row;
