@@ -3,11 +3,13 @@
 // kda_kv_read.  Formulas, layout and contracts: include/kda.h.
 //
 // Both only move data: append reads (Hq + 2 Hkv) d values a token and writes
-// as many (half for e4m3 pages), about 10 operations each, so HBM bounds
-// them.  A vector of head_dim channels is owned by the head_dim * size / 16
-// lanes that hold it in 16-byte loads; its sum of squares, its largest
-// magnitude and its rotation partners move by shuffles, and nothing but the
-// rotation's cosines (once per row) passes through shared memory.
+// as many (half for e4m3 pages), about 10 operations each, so HBM bounds them
+// as long as the instructions around a 16-byte load stay few.  A vector of
+// head_dim channels is owned by the head_dim * size / 16 lanes that hold it in
+// 16-byte loads (a lane group).  A group keeps to one row: the row's position,
+// page and cosines are worked out once, and then its heads go by with no more
+// than a pointer step between them.  Sums of squares, largest magnitudes and
+// rotation partners move by shuffles.
 #include "kda_kv.cuh"
 
 #include <cmath>
@@ -17,13 +19,8 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerCta = 4;  // many rows: the rows of a CTA, which share one set of cosines
+constexpr int kRowsPerCta = 4;  // many rows: the rows of a CTA
 constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
-// Cosine / sine pairs of one row: 32 chunks of two pairs, chunk c at
-// (c & 3) * 18 + (c >> 2), which the 16-byte reads of 8 neighbouring lanes
-// meet without a bank conflict in both pair orders.
-constexpr int kCsChunks = 4 * 18;
-__device__ __forceinline__ int cs_at(int c) { return (c & 3) * 18 + (c >> 2); }
 
 struct AppendParams {
     BatchView b;
@@ -82,160 +79,174 @@ template <int N> __device__ __forceinline__ void store_e4m3(void *dst, const flo
         *reinterpret_cast<uint32_t *>(dst) = w[0];
 }
 
+// The row of a CTA that a warp works on: its position and page, or pos = -1 for
+// a row past the last sequence or of one whose tables are inconsistent.  Whole warp.
+__device__ __forceinline__ void find_row(const BatchView &b, int r, int lane, int &pos, int &page) {
+    pos = page = -1;
+    const int n = r < b.max_rows ? find_seq(b, r, lane) : -1;
+    if (lane == 0 && n >= 0 && n < b.n_seqs) {
+        Seq s;
+        if (load_seq(b, n, s, true)) {
+            pos = s.L - s.T + (r - s.row0);
+            page = load_page(b, n, pos);
+        }
+    }
+}
+
+enum { kNoRot = 0, kHalves = 1, kPairs = 2 };  // rotation: none, channels (i, i + half), channels (2i, 2i + 1)
+
 // One CTA: rows_per_cta rows x heads_per_cta of the hq + 2 hkv heads.
-template <typename Act, int D, bool kE4m3>
+template <typename Act, int D, bool kE4m3, int kRot>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
     using V = Vec<Act>;
-    constexpr int N = V::N, LPH = D / N;  // values per lane, lanes per head
-    __shared__ float4 cs[kRowsPerCta][kCsChunks];
+    constexpr int N = V::N, LPH = D / N, kGroups = kThreads / LPH;  // values per lane, lanes per group
+    __shared__ float2 cs[kRowsPerCta][D / 2];
     __shared__ int s_pos[kRowsPerCta], s_page[kRowsPerCta];
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int row_base = int(blockIdx.x) * p.rows_per_cta;
     wait_prior_kernel();
     allow_next_kernel();
-
     if (warp < p.rows_per_cta) {
-        const int r = row_base + warp;
-        int pos = -1, page = -1;
-        const int n = r < p.b.max_rows ? find_seq(p.b, r, lane) : -1;
-        if (lane == 0 && n >= 0 && n < p.b.n_seqs) {
-            Seq s;
-            if (load_seq(p.b, n, s, true)) {
-                pos = s.L - s.T + (r - s.row0);
-                page = load_page(p.b, n, pos);
-            }
-        }
+        int pos, page;
+        find_row(p.b, row_base + warp, lane, pos, page);
         if (lane == 0) s_pos[warp] = pos, s_page[warp] = page;
     }
     __syncthreads();
-    if (p.half_rot) {
+    if constexpr (kRot != kNoRot) {
         // angle p * f in turns is a 64-bit product mod 2^64: exact for any position
         for (int i = tid; i < p.rows_per_cta * p.half_rot; i += kThreads) {
             const int row = i / p.half_rot, pair = i % p.half_rot;
             const uint64_t ph = uint64_t(uint32_t(max(s_pos[row], 0))) * p.turn[pair];
             float sn, cn;
             sincospif(float(int64_t(ph)) * 0x1p-63f, &sn, &cn);
-            reinterpret_cast<float2 *>(&cs[row][cs_at(pair >> 1)])[pair & 1] = make_float2(cn, sn);
+            cs[row][pair] = make_float2(cn, sn);
         }
         __syncthreads();
     }
 
-    const int heads = p.hq + 2 * p.hkv;
-    const int h0 = int(blockIdx.y) * p.heads_per_cta, nh = min(p.heads_per_cta, heads - h0);
+    // This lane group: row `row`, heads j, j + step, ...  Groups of a warp may have different rows and
+    // head counts, so the loops below run to the same end for all and the lanes' work is masked.
+    const int step = kGroups / p.rows_per_cta, row = (tid / LPH) / step, j = (tid / LPH) % step;
     const int l = tid % LPH, c0 = l * N;
-    const int items = p.rows_per_cta * nh;
-    const int mine = tid / LPH;
+    const int pos = s_pos[row], page = s_page[row];
+    const size_t r = size_t(row_base + row);
+    float cn[N], sn[N];  // of this lane's channels; the sine with the sign it takes
+    if constexpr (kRot != kNoRot) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int c = c0 + e;
+            const bool turned = c < 2 * p.half_rot;
+            const bool second = kRot == kPairs ? (e & 1) != 0 : c >= p.half_rot;
+            const int pair = !turned ? 0 : kRot == kPairs ? c / 2 : second ? c - p.half_rot : c;
+            const float2 t = turned ? cs[row][pair] : make_float2(1.f, 0.f);
+            cn[e] = t.x, sn[e] = second ? t.y : -t.y;
+        }
+    }
+    // halves: the partner of channel i is i +- half; half is a multiple of 4, so with 8 values a lane
+    // it may sit 4 further along (odd4)
+    const int q = p.half_rot / N;
+    const bool odd4 = p.half_rot % N != 0, first = c0 < p.half_rot;
+
+    // x: 16 bytes of a q or k head -> normalised and rotated
+    auto norm_rotate = [&](float (&x)[N], const uint4 &w_raw, bool norm) {
+        if (norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float rs = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+            float w[N];
+            V::unpack(w_raw, w);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = x[e] * rs * w[e];
+        }
+        if constexpr (kRot == kPairs) {
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const float a = x[e], b = x[e + 1];
+                x[e] = fmaf(a, cn[e], b * sn[e]), x[e + 1] = fmaf(b, cn[e + 1], a * sn[e + 1]);
+            }
+        } else if constexpr (kRot == kHalves) {
+            float y[N];
+            if (!odd4) {
+                const int src = first ? l + q : l - q;
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], src, LPH);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const bool fst = c0 + e < p.half_rot;
+                    const int src = fst ? l + q + (e >= 4 ? 1 : 0) : l - q - (e < 4 ? 1 : 0);
+                    y[e] = __shfl_sync(0xffffffffu, x[(e + 4) % N], src, LPH);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], cn[e], y[e] * sn[e]);
+        }
+    };
+    // x to head h of the pages
+    const int line = pos & ((1 << p.b.page_shift) - 1);
+    const size_t vec0 = (size_t(max(page, 0)) * size_t(p.hkv) << p.b.page_shift) + size_t(max(line, 0));
+    auto to_page = [&](float (&x)[N], int h, void *pages, uint8_t *scales, bool live) {
+        const size_t vec = vec0 + (size_t(h) << p.b.page_shift);
+        if constexpr (kE4m3) {
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int ex = scale_exponent(m);
+            const float f = exp2_neg_biased(max(ex, 1));
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = isfinite(x[e]) ? x[e] * f : __int_as_float(0x7fffffff);
+            if (live) {
+                store_e4m3<N>(static_cast<uint8_t *>(pages) + vec * D + c0, x);
+                if (l == 0) scales[vec] = uint8_t(ex);
+            }
+        } else if (live) {
+            *reinterpret_cast<uint4 *>(static_cast<Act *>(pages) + vec * D + c0) = V::pack(x);
+        }
+    };
+    // heads [lo, hi) of this CTA among one kind's n heads at `src`; f(x, head, live) for each
+    const int cta0 = int(blockIdx.y) * p.heads_per_cta, cta1 = cta0 + p.heads_per_cta;
+    auto each_head = [&](const void *base, long long stride, int kind0, int n, auto f) {
+        const int lo = max(cta0 - kind0, 0), hi = min(cta1 - kind0, n);
+        const Act *src = static_cast<const Act *>(base) + r * size_t(stride) + c0;
+        for (int h0 = lo; h0 < hi; h0 += kUnroll * step) {
+            uint4 raw[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int h = h0 + u * step + j;
+                raw[u] = make_uint4(0, 0, 0, 0);
+                if (h < hi && pos >= 0) raw[u] = *reinterpret_cast<const uint4 *>(src + size_t(h) * D);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (h0 + u * step >= hi) break;
+                const int h = h0 + u * step + j;
+                float x[N];
+                V::unpack(raw[u], x);
+                f(x, h, h < hi && pos >= 0);
+            }
+        }
+    };
+
     uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
     const bool norm_q = p.wq != nullptr, norm_k = p.wk != nullptr;
     if (norm_q) wq = __ldg(reinterpret_cast<const uint4 *>(p.wq) + l);
     if (norm_k) wk = __ldg(reinterpret_cast<const uint4 *>(p.wk) + l);
-
-    for (int base = 0; base < items; base += kUnroll * (kThreads / LPH)) {
-        uint4 raw[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int it = base + u * (kThreads / LPH) + mine;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (it >= items) continue;
-            const int row = it / nh, h = h0 + it % nh;
-            if (s_pos[row] < 0) continue;
-            const size_t r = size_t(row_base + row);
-            const Act *src;
-            if (h < p.hq) src = static_cast<const Act *>(p.q) + r * size_t(p.q_stride) + size_t(h) * D;
-            else if (h < p.hq + p.hkv) src = static_cast<const Act *>(p.k) + r * size_t(p.k_stride) + size_t(h - p.hq) * D;
-            else src = static_cast<const Act *>(p.v) + r * size_t(p.v_stride) + size_t(h - p.hq - p.hkv) * D;
-            raw[u] = *reinterpret_cast<const uint4 *>(src + c0);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            // every lane of the warp takes part in the shuffles; the branches below are uniform
-            const int it = base + u * (kThreads / LPH) + mine;
-            const bool live = it < items;
-            const int row = live ? it / nh : 0, h = live ? h0 + it % nh : 0;
-            const bool is_q = h < p.hq, is_v = h >= p.hq + p.hkv;
-            float x[N];
-            V::unpack(raw[u], x);
-            if (norm_q || norm_k) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < N; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (!is_v && (is_q ? norm_q : norm_k)) {
-                    const float rs = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-                    float w[N];
-                    V::unpack(is_q ? wq : wk, w);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) x[e] = x[e] * rs * w[e];
-                }
-            }
-            if (p.half_rot) {
-                const float4 *c = cs[row];
-                if (p.interleaved) {
-                    if (!is_v && c0 < 2 * p.half_rot) {
-#pragma unroll
-                        for (int e = 0; e < N; e += 4) {
-                            const float4 t = c[cs_at((c0 + e) >> 2)];  // pairs (c0 + e) / 2 and the next
-                            const float a0 = x[e], b0 = x[e + 1], a1 = x[e + 2], b1 = x[e + 3];
-                            x[e] = a0 * t.x - b0 * t.y, x[e + 1] = a0 * t.y + b0 * t.x;
-                            x[e + 2] = a1 * t.z - b1 * t.w, x[e + 3] = a1 * t.w + b1 * t.z;
-                        }
-                    }
-                } else {
-                    // partner of channel i: i + half (first half) or i - half; half is a
-                    // multiple of 4, so with 8 values a lane it may sit 4 further along
-                    const int q = p.half_rot / N, sh = p.half_rot % N;
-                    float y[N];
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const bool first = c0 + e < p.half_rot;
-                        const int carry = sh ? (first ? (e >= 4 ? 1 : 0) : (e < 4 ? 1 : 0)) : 0;
-                        const int src = first ? l + q + carry : l - q - carry;
-                        const float v0 = sh ? x[(e + 4) % N] : x[e];
-                        y[e] = __shfl_sync(0xffffffffu, v0, src, LPH);
-                    }
-#pragma unroll
-                    for (int e = 0; e < N; e += 2) {
-                        const int i = c0 + e;
-                        if (!is_v && i < 2 * p.half_rot) {
-                            const bool first = i < p.half_rot;
-                            const float4 t = c[cs_at((first ? i : i - p.half_rot) >> 1)];
-                            x[e] = first ? x[e] * t.x - y[e] * t.y : x[e] * t.x + y[e] * t.y;
-                            x[e + 1] = first ? x[e + 1] * t.z - y[e + 1] * t.w : x[e + 1] * t.z + y[e + 1] * t.w;
-                        }
-                    }
-                }
-            }
-            int ex = 0;
-            if constexpr (kE4m3) {
-                float m = 0.f;
-#pragma unroll
-                for (int e = 0; e < N; ++e) m = fmaxf(m, isfinite(x[e]) ? fabsf(x[e]) : 0.f);
-#pragma unroll
-                for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                ex = scale_exponent(m);
-            }
-            if (!live || s_pos[row] < 0) continue;
-            if (is_q) {
-                Act *dst = static_cast<Act *>(p.q_out) + size_t(row_base + row) * size_t(p.qo_stride) + size_t(h) * D + c0;
-                *reinterpret_cast<uint4 *>(dst) = V::pack(x);
-                continue;
-            }
-            if (s_page[row] < 0) continue;
-            const int line = s_pos[row] & ((1 << p.b.page_shift) - 1), hk = is_v ? h - p.hq - p.hkv : h - p.hq;
-            const size_t vec = ((size_t(s_page[row]) * size_t(p.hkv) + size_t(hk)) << p.b.page_shift) + size_t(line);
-            void *pages = is_v ? p.pv : p.pk;
-            if constexpr (kE4m3) {
-                const float f = exp2_neg_biased(max(ex, 1));
-#pragma unroll
-                for (int e = 0; e < N; ++e) x[e] = isfinite(x[e]) ? x[e] * f : __int_as_float(0x7fffffff);
-                store_e4m3<N>(static_cast<uint8_t *>(pages) + vec * D + c0, x);
-                if (l == 0) (is_v ? p.sv : p.sk)[vec] = uint8_t(ex);
-            } else {
-                *reinterpret_cast<uint4 *>(static_cast<Act *>(pages) + vec * D + c0) = V::pack(x);
-            }
-        }
-    }
+    Act *q_out = static_cast<Act *>(p.q_out) + r * size_t(p.qo_stride) + c0;
+    each_head(p.q, p.q_stride, 0, p.hq, [&](float (&x)[N], int h, bool live) {
+        norm_rotate(x, wq, norm_q);
+        if (live) *reinterpret_cast<uint4 *>(q_out + size_t(h) * D) = V::pack(x);
+    });
+    each_head(p.k, p.k_stride, p.hq, p.hkv, [&](float (&x)[N], int h, bool live) {
+        norm_rotate(x, wk, norm_k);
+        to_page(x, h, p.pk, p.sk, live && page >= 0);
+    });
+    each_head(p.v, p.v_stride, p.hq + p.hkv, p.hkv,
+              [&](float (&x)[N], int h, bool live) { to_page(x, h, p.pv, p.sv, live && page >= 0); });
 }
 
 struct ReadParams {
@@ -246,79 +257,68 @@ struct ReadParams {
     int32_t hkv, rows_per_cta;
 };
 
+// Lane groups as above, each 16 bytes of a page line per lane.
 template <typename Act, int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
-    using V = Vec<Act>;
-    constexpr int N = V::N, LPH = D / N;
+    constexpr int N = kE4m3 ? 16 : Vec<Act>::N, LPH = D / N, kGroups = kThreads / LPH;
     __shared__ int s_pos[kRowsPerCta], s_page[kRowsPerCta];
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int row_base = int(blockIdx.x) * p.rows_per_cta;
     wait_prior_kernel();
     allow_next_kernel();
     if (warp < p.rows_per_cta) {
-        const int r = row_base + warp;
-        int pos = -1, page = -1;
-        const int n = r < p.b.max_rows ? find_seq(p.b, r, lane) : -1;
-        if (lane == 0 && n >= 0 && n < p.b.n_seqs) {
-            Seq s;
-            if (load_seq(p.b, n, s, true)) {
-                pos = s.L - s.T + (r - s.row0);
-                page = load_page(p.b, n, pos);
-            }
-        }
+        int pos, page;
+        find_row(p.b, row_base + warp, lane, pos, page);
         if (lane == 0) s_pos[warp] = pos, s_page[warp] = page;
     }
     __syncthreads();
-    const int items = p.rows_per_cta * 2 * p.hkv, mine = tid / LPH, c0 = (tid % LPH) * N;
-    for (int base = 0; base < items; base += kUnroll * (kThreads / LPH)) {
+    const int step = kGroups / p.rows_per_cta, row = (tid / LPH) / step, j = (tid / LPH) % step;
+    const int c0 = (tid % LPH) * N, pos = s_pos[row], page = s_page[row];
+    if (pos < 0) return;
+    const int line = pos & ((1 << p.b.page_shift) - 1);
+    const size_t vec0 = (size_t(max(page, 0)) * size_t(p.hkv) << p.b.page_shift) + size_t(line);
+    // head h of both: 2 hkv lines, keys first
+    auto load = [&](int h, uint4 &raw, int &ex) {
+        raw = make_uint4(0, 0, 0, 0);
+        ex = 0;
+        if (page < 0 || h >= 2 * p.hkv) return;
+        const bool is_v = h >= p.hkv;
+        const size_t vec = vec0 + (size_t(is_v ? h - p.hkv : h) << p.b.page_shift);
+        const size_t at = (vec * D + size_t(c0)) * (kE4m3 ? 1 : sizeof(Act));
+        raw = *reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(is_v ? p.pv : p.pk) + at);
+        if constexpr (kE4m3) ex = (is_v ? p.sv : p.sk)[vec];
+    };
+    auto store = [&](int h, const uint4 &raw, int ex) {
+        if (h >= 2 * p.hkv) return;
+        const bool is_v = h >= p.hkv;
+        Act *dst = static_cast<Act *>(is_v ? p.v_out : p.k_out) +
+                   (size_t(row_base + row) * size_t(p.hkv) + size_t(is_v ? h - p.hkv : h)) * D + c0;
+        if constexpr (kE4m3) {
+            const float f = exp2_biased(ex);
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+            constexpr int M = Vec<Act>::N;
+#pragma unroll
+            for (int i = 0; i < N / M; ++i) {
+                float x[M];
+#pragma unroll
+                for (int e = 0; e < M; e += 2) {
+                    const int at = i * M + e;
+                    const float2 t = unpack_e4m3(uint16_t(w[at / 4] >> ((at & 2) * 8)));
+                    x[e] = t.x * f, x[e + 1] = t.y * f;
+                }
+                *reinterpret_cast<uint4 *>(dst + i * M) = Vec<Act>::pack(x);
+            }
+        } else {
+            *reinterpret_cast<uint4 *>(dst) = raw;
+        }
+    };
+    for (int h0 = j; h0 < 2 * p.hkv; h0 += kUnroll * step) {
         uint4 raw[kUnroll];
         int ex[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int it = base + u * (kThreads / LPH) + mine;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            ex[u] = 0;
-            if (it >= items) continue;
-            const int row = it / (2 * p.hkv), j = it % (2 * p.hkv), hk = j % p.hkv;
-            if (s_pos[row] < 0 || s_page[row] < 0) continue;
-            const bool is_v = j >= p.hkv;
-            const int line = s_pos[row] & ((1 << p.b.page_shift) - 1);
-            const size_t vec = ((size_t(s_page[row]) * size_t(p.hkv) + size_t(hk)) << p.b.page_shift) + size_t(line);
-            const void *pages = is_v ? p.pv : p.pk;
-            if constexpr (kE4m3) {
-                const uint8_t *src = static_cast<const uint8_t *>(pages) + vec * D + c0;
-                if constexpr (N == 8) {
-                    const uint2 t = *reinterpret_cast<const uint2 *>(src);
-                    raw[u].x = t.x, raw[u].y = t.y;
-                } else {
-                    raw[u].x = *reinterpret_cast<const uint32_t *>(src);
-                }
-                ex[u] = (is_v ? p.sv : p.sk)[vec];
-            } else {
-                raw[u] = *reinterpret_cast<const uint4 *>(static_cast<const Act *>(pages) + vec * D + c0);
-            }
-        }
+        for (int u = 0; u < kUnroll; ++u) load(h0 + u * step, raw[u], ex[u]);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int it = base + u * (kThreads / LPH) + mine;
-            if (it >= items) continue;
-            const int row = it / (2 * p.hkv), j = it % (2 * p.hkv), hk = j % p.hkv;
-            if (s_pos[row] < 0) continue;
-            uint4 o = raw[u];
-            if constexpr (kE4m3) {
-                const float f = exp2_biased(ex[u]);
-                const uint32_t w[2] = {raw[u].x, raw[u].y};
-                float x[N];
-#pragma unroll
-                for (int e = 0; e < N; e += 2) {
-                    const float2 t = unpack_e4m3(uint16_t(w[e / 4] >> ((e & 2) * 8)));
-                    x[e] = t.x * f, x[e + 1] = t.y * f;
-                }
-                o = V::pack(x);
-            }
-            Act *dst = static_cast<Act *>(j >= p.hkv ? p.v_out : p.k_out);
-            *reinterpret_cast<uint4 *>(dst + (size_t(row_base + row) * size_t(p.hkv) + size_t(hk)) * D + c0) = o;
-        }
+        for (int u = 0; u < kUnroll; ++u) store(h0 + u * step, raw[u], ex[u]);
     }
 }
 
@@ -337,8 +337,11 @@ kda_status append_d(AppendParams &p, int rows, cudaStream_t stream) {
     p.heads_per_cta = few ? kThreads / (D / Vec<Act>::N) : heads;
     const dim3 grid(unsigned((rows + p.rows_per_cta - 1) / p.rows_per_cta),
                     unsigned((heads + p.heads_per_cta - 1) / p.heads_per_cta));
+    auto kern = p.half_rot == 0   ? kv_append_kernel<Act, D, kE4m3, kNoRot>
+                : p.interleaved ? kv_append_kernel<Act, D, kE4m3, kPairs>
+                                : kv_append_kernel<Act, D, kE4m3, kHalves>;
     const ProfScope prof(KDA_KERNEL_KV_APPEND, stream);
-    return launch_overlapped(kv_append_kernel<Act, D, kE4m3>, grid, kThreads, 0, stream, p);
+    return launch_overlapped(kern, grid, kThreads, 0, stream, p);
 }
 
 template <typename Act, int D, bool kE4m3>
