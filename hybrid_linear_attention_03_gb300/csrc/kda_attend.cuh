@@ -16,6 +16,8 @@
 // not depend on timing.
 #pragma once
 
+#include <mutex>
+
 #include "kda_kv.cuh"
 
 namespace kda {
@@ -23,9 +25,9 @@ namespace kv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct Part {
-    int32_t n, h, tile;  // item
-    int32_t state;       // 0 none, 1 there, 2 there and the item's last
+struct alignas(16) Part {
+    int32_t state;          // 0 none, 1 there, 2 there and the item's last
+    int32_t row, rows, h;  // item: its first token's row, its rows, its cache head
 };
 
 struct AttendParams {
@@ -48,12 +50,19 @@ struct AttendParams {
 // Keys of tile i's last row: how far the item reaches.
 __device__ __forceinline__ int tile_keys(int ctx, int T, int tt, int i) { return ctx + min(T, (i + 1) * tt); }
 
-// Length on the line of the first m tiles of a sequence (m <= ceil(T / tt)).
-__device__ __forceinline__ long long tile_prefix(const AttendParams &p, int ctx, int T, int m) {
-    const int tt = p.tile_tokens, full = min(m, T / tt);
+// Length on the line of the first m tiles of a sequence (m <= ceil(T / tt)),
+// an item costing `cost` beside its keys.
+__device__ __forceinline__ long long tile_prefix(int ctx, int T, int tt, int m, int cost) {
+    const int full = min(m, T / tt);
     long long s = static_cast<long long>(full) * ctx + static_cast<long long>(tt) * full * (full + 1) / 2;
     if (m > full) s += ctx + T;
-    return s + static_cast<long long>(p.item_cost) * m;
+    return s + static_cast<long long>(cost) * m;
+}
+
+// a / b for a >= 0 and b > 0: most lines are shorter than 2^32.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+    if ((a | b) >> 32 == 0) return static_cast<long long>(uint32_t(a) / uint32_t(b));
+    return a / b;
 }
 
 struct Cursor {  // a place on the line: key `key` of item (n, h, tile)
@@ -67,27 +76,33 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
                                            Cursor &to) {
     const int N = p.b.n_seqs, per = (N + 31) / 32, tt = p.tile_tokens;
     const int n0 = min(lane * per, N), n1 = min(n0 + per, N);
-    long long sum = 0;
+    long long keys = 0, items = 0;  // of this lane's sequences, then of all lanes up to this one
     for (int n = n0; n < n1; ++n) {
         Seq s;
-        if (load_seq(p.b, n, s, cta == 0) && s.T > 0)
-            sum += tile_prefix(p, s.L - s.T, s.T, (s.T + tt - 1) / tt) * p.hkv;
+        if (load_seq(p.b, n, s, cta == 0) && s.T > 0) {
+            const int tiles = (s.T + tt - 1) / tt;
+            keys += tile_prefix(s.L - s.T, s.T, tt, tiles, 0) * p.hkv;
+            items += static_cast<long long>(tiles) * p.hkv;
+        }
     }
-    long long before = sum;  // inclusive scan over the lanes
+    const long long my_keys = keys, my_items = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += t;
+        const long long k = __shfl_up_sync(0xffffffffu, keys, o), i = __shfl_up_sync(0xffffffffu, items, o);
+        if (lane >= o) keys += k, items += i;
     }
-    const long long total = __shfl_sync(0xffffffffu, before, 31);
-    before -= sum;
-    const long long want = (total + p.min_keys - 1) / p.min_keys;
-    const int active = int(min(static_cast<long long>(n_cta), want));
+    const long long all_items = __shfl_sync(0xffffffffu, items, 31);
+    const int cost = all_items > n_cta ? p.item_cost : 0;
+    const long long sum = my_keys + cost * my_items, before = keys + cost * items - sum;
+    const long long total = __shfl_sync(0xffffffffu, before + sum, 31);
+    const int active = int(min(static_cast<long long>(n_cta), div_pos(total + p.min_keys - 1, p.min_keys)));
     if (cta >= active) return false;
+    const long long share = div_pos(total, active);
+    const int over = int(total - share * active);
     Cursor c[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const long long x = total / active * (cta + e) + total % active * (cta + e) / active;
+        const long long x = share * (cta + e) + over * (cta + e) / active;
         c[e] = Cursor{N, 0, 0, 0};
         if (x < total) {  // the lane whose sequences hold x walks them
             const unsigned owner = __ballot_sync(0xffffffffu, x >= before && x < before + sum);
@@ -98,22 +113,22 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
                     Seq s;
                     if (!load_seq(p.b, n, s, false) || s.T == 0) continue;
                     const int ctx = s.L - s.T, tiles = (s.T + tt - 1) / tt;
-                    const long long head = tile_prefix(p, ctx, s.T, tiles);
+                    const long long head = tile_prefix(ctx, s.T, tt, tiles, cost);
                     if (rest >= head * p.hkv) {
                         rest -= head * p.hkv;
                         continue;
                     }
                     c[e].n = n;
-                    c[e].h = int(rest / head);
+                    c[e].h = int(div_pos(rest, head));
                     rest -= head * c[e].h;
                     int lo = 0, hi = tiles - 1;  // last tile whose prefix is at most rest
                     while (lo < hi) {
                         const int mid = (lo + hi + 1) / 2;
-                        if (tile_prefix(p, ctx, s.T, mid) <= rest) lo = mid;
+                        if (tile_prefix(ctx, s.T, tt, mid, cost) <= rest) lo = mid;
                         else hi = mid - 1;
                     }
                     c[e].tile = lo;
-                    const int key = max(int(rest - tile_prefix(p, ctx, s.T, lo)) - p.item_cost, 0);
+                    const int key = max(int(rest - tile_prefix(ctx, s.T, tt, lo, cost)) - cost, 0);
                     c[e].key = key / p.key_step * p.key_step;
                     break;
                 }
@@ -139,7 +154,7 @@ struct Item {
     __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == keys; }
     // where a part goes: the CTA's first part slot, or its last one for a part that begins its item
     __device__ __forceinline__ int slot() const { return k0 == 0 ? 1 : 0; }
-    __device__ __forceinline__ Part part() const { return Part{n, h, tile, k1 == keys ? 2 : 1}; }
+    __device__ __forceinline__ Part part() const { return Part{k1 == keys ? 2 : 1, row0 + tok0, rows, h}; }
     // element offset of row r's channels in a row tensor
     __device__ __forceinline__ size_t at(int r, int group, long long stride, int D) const {
         return size_t(row0 + tok0 + r / group) * size_t(stride) + size_t(h * group + r % group) * size_t(D);
@@ -185,6 +200,22 @@ __host__ __device__ __forceinline__ size_t parts_bytes(int n_cta) {
 }
 inline size_t share_bytes(int n_cta, int bm, int D) {
     return parts_bytes(n_cta) + sizeof(float) * size_t(n_cta) * 2 * size_t(bm) * size_t(D + 2);
+}
+
+// Raises a kernel's shared memory limit, once per device.
+template <auto kKernel> inline bool allow_smem(int bytes) {
+    static std::once_flag once[64];
+    static bool ok[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return false;
+    }
+    std::call_once(once[dev], [&] {
+        ok[dev] = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+        if (!ok[dev]) cudaGetLastError();
+    });
+    return ok[dev];
 }
 
 // What a kernel of this family needs from the host: its row tile, its grid

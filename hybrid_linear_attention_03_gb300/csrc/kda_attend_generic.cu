@@ -225,10 +225,7 @@ template <typename Act, typename Kv, int BM, int D>
 kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
     auto kern = attend_generic_kernel<Act, Kv, BM, D>;
     const int smem = int(sizeof(Smem<BM, D>));
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
+    if (!allow_smem<attend_generic_kernel<Act, Kv, BM, D>>(smem)) return KDA_ERR_CUDA;
     p.key_step = KS;
     p.item_cost = KS;
     p.min_keys = 2 * KS;

@@ -61,10 +61,7 @@ template <bool kE4m3> struct Warps {
     static_assert(8 * kSoftmax + 4 * kIssue + kRowWarps * kRows == (12 + kRowWarps) * kLaunch, "the split uses what the launch has");
 };
 constexpr float kRefSlack = 8.f;
-#ifndef ITEM_COST
-#define ITEM_COST 384
-#endif
-constexpr int kItemCost = ITEM_COST;
+constexpr int kItemCost = 512;  // keys that take as long as an item's start and output
 
 template <int D, bool kE4m3, bool kByKeys> struct Cfg {
     static constexpr int kQBytes = kSideRows * D * 2;            // bf16, or two e4m3 terms
@@ -1000,10 +997,7 @@ kda_status launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan
     auto kern = attend_tile_kernel<D, kE4m3, kByKeys>;
     constexpr size_t smem = smem_bytes<C, kE4m3>();
     static_assert(smem <= 232448, "shared memory of a CTA");
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) {
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
+    if (!allow_smem<attend_tile_kernel<D, kE4m3, kByKeys>>(int(smem))) return KDA_ERR_CUDA;
     p.key_step = KT;
     p.item_cost = kItemCost;
     p.min_keys = (kByKeys ? 2 : 1) * KT;

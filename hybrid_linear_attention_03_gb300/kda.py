@@ -609,6 +609,10 @@ class PagedKV:
         self.desc = kda_kv_cache(self.k.data_ptr(), self.v.data_ptr(), _addr(self.k_scale), _addr(self.v_scale),
                                  self.err.data_ptr(), num_pages, page_size, num_heads, num_kv_heads, head_dim,
                                  act_code(act), KDA_KV_E4M3 if e4m3 else KDA_KV_ACT)
+        self.ref = ctypes.byref(self.desc)
+        self.q_kind = (self.device, act, num_heads, head_dim)  # of row tensors, see _kind
+        self.kv_kind = (self.device, act, num_kv_heads, head_dim)
+        self.norm_kind = (self.device, act, head_dim)
 
     def error_word(self) -> torch.Tensor:
         return self.err
@@ -631,6 +635,11 @@ def _row_stride(t, name):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
 
 
+def _kind(t):
+    """What a call checks of a row tensor: (device, type, heads, head_dim); None for no tensor."""
+    return None if t is None else (t.device, t.dtype, t.shape[1], t.shape[2])
+
+
 def make_kv_batch(cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor, max_rows: int,
                   max_new: int) -> kda_kv_batch:
     """The batch's device tables (int32: cu_seqlens [n + 1], kv_lens [n],
@@ -638,13 +647,15 @@ def make_kv_batch(cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, page_table: t
     n = kv_lens.numel()
     for name, t, shape in (("cu_seqlens", cu_seqlens, (n + 1,)), ("kv_lens", kv_lens, (n,)),
                            ("page_table", page_table, (n,) + tuple(page_table.shape[1:]))):
-        if not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {shape}")
+        if not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() \
+                or t.device != cu_seqlens.device:
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {shape}, all on one device")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_seqs, pages]")
     b = kda_kv_batch(cu_seqlens.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), n, page_table.shape[1],
                      int(max_rows), int(max_new))
     b._tensors = (cu_seqlens, kv_lens, page_table)
+    b._device = cu_seqlens.device
     return b
 
 
@@ -657,6 +668,10 @@ def make_qk_params(q_norm_w: torch.Tensor | None = None, k_norm_w: torch.Tensor 
     p = kda_qk_params(_addr(q_norm_w), _addr(k_norm_w), float(eps), 2 * len(freq), int(bool(interleaved)),
                       ctypes.cast(arr, ctypes.POINTER(ctypes.c_double)) if freq else None)
     p._tensors = (q_norm_w, k_norm_w, arr)
+    for name, w in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
+        if w is not None and (w.dim() != 1 or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor [head_dim]")
+    p._kinds = tuple(None if w is None else (w.device, w.dtype, w.shape[0]) for w in (q_norm_w, k_norm_w))
     return p
 
 
@@ -666,6 +681,8 @@ def make_kv_io(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, q_out: 
     io = kda_kv_io(_addr(q), k.data_ptr(), v.data_ptr(), _addr(q_out), _row_stride(q, "q") if q is not None else 0,
                    _row_stride(k, "k"), _row_stride(v, "v"), _row_stride(q_out, "q_out") if q_out is not None else 0)
     io._tensors = (q, k, v, q_out)
+    io._kinds = tuple(_kind(t) for t in io._tensors)
+    io._rows = min(t.shape[0] for t in io._tensors if t is not None)
     return io
 
 
@@ -674,73 +691,79 @@ def make_attn_io(q: torch.Tensor, out: torch.Tensor, scale: float | None = None)
     s = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
     io = kda_attn_io(q.data_ptr(), out.data_ptr(), _row_stride(q, "q"), _row_stride(out, "out"), s)
     io._tensors = (q, out)
+    io._kinds = tuple(_kind(t) for t in io._tensors)
+    io._rows = min(q.shape[0], out.shape[0])
     return io
 
 
-def _check_rows(kv: PagedKV, batch: kda_kv_batch, where: str, **tensors) -> None:
+def _check_rows(kv: PagedKV, batch: kda_kv_batch, where: str, names, kinds, rows) -> None:
     """The row tensors hold max_rows rows of the cache's heads, type and device."""
-    for name, (t, heads) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != kv.act or t.device != kv.device or t.shape[0] < batch.max_rows or t.shape[1] != heads \
-                or t.shape[2] != kv.head_dim:
-            raise ValueError(f"{where}: {name} must be a {kv.act} tensor on {kv.device} of shape "
-                             f"[>= {batch.max_rows}, {heads}, {kv.head_dim}]")
+    for name, kind in zip(names, kinds):
+        if kind is not None and kind != (kv.kv_kind if name[0] != "q" and name != "out" else kv.q_kind):
+            raise ValueError(f"{where}: {name} must be a {kv.act} tensor on {kv.device} of the cache's heads and "
+                             f"head_dim, not {kind}")
+    if rows < batch.max_rows:
+        raise ValueError(f"{where}: the batch has up to {batch.max_rows} rows, the tensors {rows}")
 
 
-def _kv_stream(kv: PagedKV, batch: kda_kv_batch, stream, where: str) -> ctypes.c_void_p:
+def _kv_stream(kv: PagedKV, batch: kda_kv_batch, stream, where: str) -> int:
     """The call's stream; it, the cache, the batch and the current device must be on one GPU."""
     if stream is None:
-        stream = torch.cuda.current_stream(kv.device)
+        stream = torch.cuda.current_stream()
     if stream.device != kv.device or torch.cuda.current_device() != kv.device.index:
         raise ValueError(f"{where}: the cache is on {kv.device}: make it the current device and use its stream")
-    if batch is not None and batch._tensors[0].device != kv.device:
+    if batch is not None and batch._device != kv.device:
         raise ValueError(f"{where}: the batch's tables are not on {kv.device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def kda_kv_append(kv: PagedKV, params: kda_qk_params | None, io: kda_kv_io, batch: kda_kv_batch, stream=None) -> None:
     """Norm and rotation of q and k per head, q to q_out, k and v to their pages."""
-    q, k, v, q_out = io._tensors
-    _check_rows(kv, batch, "kda_kv_append", q=(q, kv.num_heads), k=(k, kv.num_kv_heads), v=(v, kv.num_kv_heads),
-                q_out=(q_out, kv.num_heads))
+    _check_rows(kv, batch, "kda_kv_append", ("q", "k", "v", "q_out"), io._kinds, io._rows)
     if params is not None:
-        for name, w in (("q_norm_w", params._tensors[0]), ("k_norm_w", params._tensors[1])):
-            if w is not None and (w.dtype != kv.act or w.device != kv.device or tuple(w.shape) != (kv.head_dim,)
-                                  or not w.is_contiguous()):
-                raise ValueError(f"kda_kv_append: {name} must be a contiguous {kv.act} tensor [{kv.head_dim}]")
-    st = lib().kda_kv_append(ctypes.byref(kv.desc), ctypes.byref(params) if params is not None else None,
-                             ctypes.byref(io), ctypes.byref(batch), _kv_stream(kv, batch, stream, "kda_kv_append"))
-    _check(st, "kda_kv_append")
+        for kind in params._kinds:
+            if kind is not None and kind != kv.norm_kind:
+                raise ValueError(f"kda_kv_append: norm weights must be {kv.act} tensors [{kv.head_dim}] on {kv.device}")
+        params = ctypes.byref(params)
+    st = lib().kda_kv_append(kv.ref, params, ctypes.byref(io), ctypes.byref(batch),
+                             _kv_stream(kv, batch, stream, "kda_kv_append"))
+    if st != KDA_OK:
+        _check(st, "kda_kv_append")
 
 
 def kda_kv_read(kv: PagedKV, batch: kda_kv_batch, k_out: torch.Tensor, v_out: torch.Tensor, stream=None) -> None:
     """The batch's tokens read back from their pages into contiguous rows."""
-    _check_rows(kv, batch, "kda_kv_read", k_out=(k_out, kv.num_kv_heads), v_out=(v_out, kv.num_kv_heads))
-    if not k_out.is_contiguous() or not v_out.is_contiguous():
-        raise ValueError("kda_kv_read: k_out and v_out must be contiguous")
-    _check(lib().kda_kv_read(ctypes.byref(kv.desc), ctypes.byref(batch), k_out.data_ptr(), v_out.data_ptr(),
-                             _kv_stream(kv, batch, stream, "kda_kv_read")), "kda_kv_read")
+    if k_out.dim() != 3 or v_out.dim() != 3 or not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError("kda_kv_read: k_out and v_out must be contiguous [rows, heads, head_dim] tensors")
+    _check_rows(kv, batch, "kda_kv_read", ("k_out", "v_out"), (_kind(k_out), _kind(v_out)),
+                min(k_out.shape[0], v_out.shape[0]))
+    st = lib().kda_kv_read(kv.ref, ctypes.byref(batch), k_out.data_ptr(), v_out.data_ptr(),
+                           _kv_stream(kv, batch, stream, "kda_kv_read"))
+    if st != KDA_OK:
+        _check(st, "kda_kv_read")
 
 
 def kda_kv_attend_workspace_bytes(kv: PagedKV, batch: kda_kv_batch) -> int:
-    return int(lib().kda_kv_attend_workspace_bytes(ctypes.byref(kv.desc), ctypes.byref(batch)))
+    return int(lib().kda_kv_attend_workspace_bytes(kv.ref, ctypes.byref(batch)))
 
 
 def kda_kv_attend(kv: PagedKV, io: kda_attn_io, batch: kda_kv_batch, workspace: torch.Tensor, stream=None) -> None:
     """Causal attention of the batch's tokens over their sequences' pages."""
-    q, out = io._tensors
-    _check_rows(kv, batch, "kda_kv_attend", q=(q, kv.num_heads), out=(out, kv.num_heads))
-    if workspace is not None and workspace.device != kv.device:
-        raise ValueError(f"kda_kv_attend: the workspace is not on {kv.device}")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().kda_kv_attend(ctypes.byref(kv.desc), ctypes.byref(io), ctypes.byref(batch), _dptr(workspace), ws_bytes,
-                               _kv_stream(kv, batch, stream, "kda_kv_attend")), "kda_kv_attend")
+    _check_rows(kv, batch, "kda_kv_attend", ("q", "out"), io._kinds, io._rows)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.device != kv.device or not workspace.is_contiguous():
+            raise ValueError(f"kda_kv_attend: the workspace must be a contiguous tensor on {kv.device}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    st = lib().kda_kv_attend(kv.ref, ctypes.byref(io), ctypes.byref(batch), ws, ws_bytes,
+                             _kv_stream(kv, batch, stream, "kda_kv_attend"))
+    if st != KDA_OK:
+        _check(st, "kda_kv_attend")
 
 
 def kda_kv_poll_device_error(kv: PagedKV, stream=None) -> tuple[int, int]:
     """Returns (status, flags) of the cache's error word; reading clears it."""
     flags = ctypes.c_uint32(0)
-    st = int(lib().kda_kv_poll_device_error(ctypes.byref(kv.desc), _kv_stream(kv, None, stream, "kda_kv_poll_device_error"),
+    st = int(lib().kda_kv_poll_device_error(kv.ref, _kv_stream(kv, None, stream, "kda_kv_poll_device_error"),
                                             ctypes.byref(flags)))
     return st, int(flags.value)
