@@ -25,6 +25,18 @@ namespace kv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Two 32-bit multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 struct alignas(16) Part {
     int32_t state;          // 0 none, 1 there, 2 there and the item's last
     int32_t row, rows, h;  // item: its first token's row, its rows, its cache head

@@ -8,7 +8,9 @@
 // A CTA holds a tile of BM rows (query heads of one cache head, consecutive
 // tokens) and walks 64 keys a step through shared memory, each of its 256
 // threads keeping BM / 16 rows x 4 keys of the scores and BM / 16 rows x D / 16
-// channels of the output in registers.  FFMA issue bounds the 64-row tile.
+// channels of the output in registers.  Multiply-adds set the pace of the 64-row
+// tile, two to an instruction: scores sum even and odd channels apart, and the
+// weights lie twice in shared memory for the pairs of output channels.
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -34,11 +36,13 @@ template <> __device__ __forceinline__ void load4<uint8_t>(const uint8_t *src, f
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
+// Rows are padded to an odd number of 16-byte pieces, so that the 8 lanes of a
+// read that take one piece of 8 rows meet no bank twice.
 template <int BM, int D> struct Smem {
-    float q[D][BM];      // channel-major
-    float k[D][KS + 4];  // channel-major
+    float q[BM][D + 4];
+    float k[KS][D + 4];
     float v[KS][D];
-    float p[KS][BM + 4];
+    float2 p[KS][BM + 2];  // each weight twice
     int64_t line[KS];  // vector index of each key's line, -1 where there is none
     Cursor piece[2];
     int has;
@@ -46,7 +50,7 @@ template <int BM, int D> struct Smem {
 
 template <typename Act, typename Kv, int BM, int D>
 __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_constant__ AttendParams p) {
-    constexpr int RT = BM / 16, CT = D / 16;  // rows and channels of a thread
+    constexpr int RT = BM / 16, CT = D / 16, CV = CT >= 4 ? 4 : CT;  // rows and channels of a thread
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<BM, D> &s = *reinterpret_cast<Smem<BM, D> *>(smem_raw);
     const int tid = int(threadIdx.x), ty = tid >> 4, tx = tid & 15;
@@ -69,11 +73,11 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
     while (walk.next(p, it)) {
         __syncthreads();
         for (int i = tid; i < BM * D / 4; i += kThreads) {
-            const int r = i % BM, c = i / BM * 4;
+            const int r = i / (D / 4), c = i % (D / 4) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f};
             if (r < it.rows) load4<Act>(static_cast<const Act *>(p.q) + it.at(r, p.group, p.q_stride, D) + c, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s.q[c + e][r] = x[e] * p.scale_log2;
+            *reinterpret_cast<float4 *>(&s.q[r][c]) =
+                make_float4(x[0] * p.scale_log2, x[1] * p.scale_log2, x[2] * p.scale_log2, x[3] * p.scale_log2);
         }
         float o[RT][CT], m[RT], l[RT];
 #pragma unroll
@@ -116,42 +120,43 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
                         for (int e = 0; e < 4; ++e) xk[e] *= fk, xv[e] *= fv;
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s.k[c + e][j] = xk[e];
+                *reinterpret_cast<float4 *>(&s.k[j][c]) = make_float4(xk[0], xk[1], xk[2], xk[3]);
                 *reinterpret_cast<float4 *>(&s.v[j][c]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
             }
             __syncthreads();
+            // keys of a thread: tx, tx + 16, tx + 32, tx + 48
+            float2 x2[RT][4];
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x2[a][e] = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                float4 kk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk[e] = *reinterpret_cast<const float4 *>(&s.k[tx + 16 * e][c]);
+#pragma unroll
+                for (int a = 0; a < RT; ++a) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(&s.q[ty * RT + a][c]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x2[a][e] = fma2(make_float2(qq.x, qq.y), make_float2(kk[e].x, kk[e].y), x2[a][e]);
+                        x2[a][e] = fma2(make_float2(qq.z, qq.w), make_float2(kk[e].z, kk[e].w), x2[a][e]);
+                    }
+                }
+            }
             float x[RT][4];
 #pragma unroll
             for (int a = 0; a < RT; ++a)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[a][e] = 0.f;
-#pragma unroll 8
-            for (int c = 0; c < D; ++c) {
-                const float4 kk = *reinterpret_cast<const float4 *>(&s.k[c][tx * 4]);
-                float qq[RT];
-                if constexpr (RT == 4) {
-                    const float4 t = *reinterpret_cast<const float4 *>(&s.q[c][ty * 4]);
-                    qq[0] = t.x, qq[1] = t.y, qq[2] = t.z, qq[3] = t.w;
-                } else {
-#pragma unroll
-                    for (int a = 0; a < RT; ++a) qq[a] = s.q[c][ty * RT + a];
-                }
-#pragma unroll
-                for (int a = 0; a < RT; ++a) {
-                    x[a][0] = fmaf(qq[a], kk.x, x[a][0]);
-                    x[a][1] = fmaf(qq[a], kk.y, x[a][1]);
-                    x[a][2] = fmaf(qq[a], kk.z, x[a][2]);
-                    x[a][3] = fmaf(qq[a], kk.w, x[a][3]);
-                }
-            }
+                for (int e = 0; e < 4; ++e) x[a][e] = x2[a][e].x + x2[a][e].y;
             if (masked) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const bool there = s.line[tx * 4 + e] >= 0;
+                    const bool there = s.line[tx + 16 * e] >= 0;
 #pragma unroll
                     for (int a = 0; a < RT; ++a)
-                        if (!there || kb + tx * 4 + e > lim[a]) x[a][e] = -INFINITY;
+                        if (!there || kb + tx + 16 * e > lim[a]) x[a][e] = -INFINITY;
                 }
             }
 #pragma unroll
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
                 for (int e = 0; e < 4; ++e) {
                     x[a][e] = exp2f(x[a][e] - ref);
                     sum += x[a][e];
-                    s.p[tx * 4 + e][ty * RT + a] = x[a][e];
+                    s.p[tx + 16 * e][ty * RT + a] = make_float2(x[a][e], x[a][e]);
                 }
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -177,30 +182,44 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
             }
             __syncwarp();  // a row's weights are written and read by the same half warp
             // channels of a thread: groups of four (or the D / 16 there are) 16 groups apart
-            constexpr int CV = CT >= 4 ? 4 : CT;
 #pragma unroll 4
             for (int j = 0; j < KS; ++j) {
-                float w[RT], vv[CT];
+                float2 w[RT];
+                if constexpr (RT == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(&s.p[j][ty * 4]);
+                    const float4 u = *reinterpret_cast<const float4 *>(&s.p[j][ty * 4 + 2]);
+                    w[0] = make_float2(t.x, t.y), w[1] = make_float2(t.z, t.w);
+                    w[2] = make_float2(u.x, u.y), w[3] = make_float2(u.z, u.w);
+                } else {
 #pragma unroll
-                for (int a = 0; a < RT; ++a) w[a] = s.p[j][ty * RT + a];
+                    for (int a = 0; a < RT; ++a) w[a] = s.p[j][ty * RT + a];
+                }
+                float vv[CT];
 #pragma unroll
                 for (int g = 0; g < CT / CV; ++g)
 #pragma unroll
                     for (int e = 0; e < CV; ++e) vv[g * CV + e] = s.v[j][g * 16 * CV + tx * CV + e];
                 if (!masked) {
 #pragma unroll
-                    for (int a = 0; a < RT; ++a)
+                    for (int a = 0; a < RT; ++a) {
+                        if constexpr (CT >= 2) {
 #pragma unroll
-                        for (int c = 0; c < CT; ++c) o[a][c] = fmaf(w[a], vv[c], o[a][c]);
+                            for (int c = 0; c < CT; c += 2) {
+                                const float2 t = fma2(w[a], make_float2(vv[c], vv[c + 1]), make_float2(o[a][c], o[a][c + 1]));
+                                o[a][c] = t.x, o[a][c + 1] = t.y;
+                            }
+                        } else {
+                            o[a][0] = fmaf(w[a].x, vv[0], o[a][0]);
+                        }
+                    }
                 } else {  // a value of a key that the row does not see may be anything
 #pragma unroll
                     for (int a = 0; a < RT; ++a)
 #pragma unroll
-                        for (int c = 0; c < CT; ++c) o[a][c] = w[a] != 0.f ? fmaf(w[a], vv[c], o[a][c]) : o[a][c];
+                        for (int c = 0; c < CT; ++c) o[a][c] = w[a].x != 0.f ? fmaf(w[a].x, vv[c], o[a][c]) : o[a][c];
                 }
             }
         }
-        constexpr int CV = CT >= 4 ? 4 : CT;
         const bool whole = it.whole();
         float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * (D + 2);
         if (!whole && tid == 0) my_parts[it.slot()] = it.part();

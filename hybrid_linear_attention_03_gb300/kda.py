@@ -706,15 +706,18 @@ def _check_rows(kv: PagedKV, batch: kda_kv_batch, where: str, names, kinds, rows
         raise ValueError(f"{where}: the batch has up to {batch.max_rows} rows, the tensors {rows}")
 
 
+# The current stream's handle without a Stream object, which costs more than a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _kv_stream(kv: PagedKV, batch: kda_kv_batch, stream, where: str) -> int:
     """The call's stream; it, the cache, the batch and the current device must be on one GPU."""
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    if stream.device != kv.device or torch.cuda.current_device() != kv.device.index:
+    if torch.cuda.current_device() != kv.device.index or (stream is not None and stream.device != kv.device):
         raise ValueError(f"{where}: the cache is on {kv.device}: make it the current device and use its stream")
     if batch is not None and batch._device != kv.device:
         raise ValueError(f"{where}: the batch's tables are not on {kv.device}")
-    return stream.cuda_stream
+    return _raw_stream(kv.device.index) if stream is None else stream.cuda_stream
 
 
 def kda_kv_append(kv: PagedKV, params: kda_qk_params | None, io: kda_kv_io, batch: kda_kv_batch, stream=None) -> None:
