@@ -6,19 +6,21 @@
 //   m' = max(m, max_j x_j),  l <- l 2^(m - m') + sum_j 2^(x_j - m'),
 //   o <- o 2^(m - m') + sum_j 2^(x_j - m') v_j,   out = o / l.
 // A CTA holds a tile of BM rows (query heads of one cache head, consecutive
-// tokens) and walks 64 keys a step through shared memory, each of its 256
-// threads keeping BM / 16 rows x 4 keys of the scores and BM / 16 rows x D / 16
-// channels of the output in registers.  Multiply-adds set the pace of the 64-row
-// tile, two to an instruction: scores sum even and odd channels apart, and the
-// weights lie twice in shared memory for the pairs of output channels.
+// tokens) and walks 64 keys a step through shared memory; 16 threads side by
+// side share RT rows, each with 4 of the keys of the scores and D / 16 channels
+// of the output in registers.  Multiply-adds go two to an instruction (scores sum
+// even and odd channels apart).  Shared memory reads set the pace where a thread
+// has 4 rows or fewer, so the tiles of many rows give it 8: 64 rows on 128
+// threads, or 128 rows on 256 where head size 128 leaves room for one CTA an SM.
 #include "kda_attend.cuh"
 
 namespace kda {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int KS = 64;  // keys a step
+// Threads of a CTA: 8 rows each, one row each for the 16-row tile.
+constexpr int threads_of(int bm) { return bm == 16 ? 256 : bm * 2; }
 
 template <typename Kv> __device__ __forceinline__ void load4(const Kv *src, float (&x)[4]);
 template <> __device__ __forceinline__ void load4<float>(const float *src, float (&x)[4]) {
@@ -42,15 +44,15 @@ template <int BM, int D> struct Smem {
     float q[BM][D + 4];
     float k[KS][D + 4];
     float v[KS][D];
-    float2 p[KS][BM + 2];  // each weight twice
+    float p[KS][BM + 4];
     int64_t line[KS];  // vector index of each key's line, -1 where there is none
     Cursor piece[2];
     int has;
 };
 
 template <typename Act, typename Kv, int BM, int D>
-__global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_constant__ AttendParams p) {
-    constexpr int RT = BM / 16, CT = D / 16, CV = CT >= 4 ? 4 : CT;  // rows and channels of a thread
+__global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_generic_kernel(const __grid_constant__ AttendParams p) {
+    constexpr int kThreads = threads_of(BM), RT = BM * 16 / kThreads, CT = D / 16, CV = CT >= 4 ? 4 : CT;  // rows and channels of a thread
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<BM, D> &s = *reinterpret_cast<Smem<BM, D> *>(smem_raw);
     const int tid = int(threadIdx.x), ty = tid >> 4, tx = tid & 15;
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
             for (int a = 0; a < RT; ++a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x2[a][e] = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 1
             for (int c = 0; c < D; c += 4) {
                 float4 kk[4];
 #pragma unroll
@@ -171,7 +173,6 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
                 for (int e = 0; e < 4; ++e) {
                     x[a][e] = exp2f(x[a][e] - ref);
                     sum += x[a][e];
-                    s.p[tx + 16 * e][ty * RT + a] = make_float2(x[a][e], x[a][e]);
                 }
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -180,19 +181,27 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
 #pragma unroll
                 for (int c = 0; c < CT; ++c) o[a][c] *= f;
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float *dst = &s.p[tx + 16 * e][ty * RT];
+                if constexpr (RT == 8) {
+                    reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0][e], x[1][e], x[2][e], x[3][e]);
+                    reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4][e], x[5][e], x[6][e], x[7][e]);
+                } else {
+                    dst[0] = x[0][e];
+                }
+            }
             __syncwarp();  // a row's weights are written and read by the same half warp
             // channels of a thread: groups of four (or the D / 16 there are) 16 groups apart
-#pragma unroll 4
+#pragma unroll 1
             for (int j = 0; j < KS; ++j) {
-                float2 w[RT];
-                if constexpr (RT == 4) {
-                    const float4 t = *reinterpret_cast<const float4 *>(&s.p[j][ty * 4]);
-                    const float4 u = *reinterpret_cast<const float4 *>(&s.p[j][ty * 4 + 2]);
-                    w[0] = make_float2(t.x, t.y), w[1] = make_float2(t.z, t.w);
-                    w[2] = make_float2(u.x, u.y), w[3] = make_float2(u.z, u.w);
+                float w[RT];
+                if constexpr (RT == 8) {
+                    const float4 t = *reinterpret_cast<const float4 *>(&s.p[j][ty * 8]);
+                    const float4 u = *reinterpret_cast<const float4 *>(&s.p[j][ty * 8 + 4]);
+                    w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w, w[4] = u.x, w[5] = u.y, w[6] = u.z, w[7] = u.w;
                 } else {
-#pragma unroll
-                    for (int a = 0; a < RT; ++a) w[a] = s.p[j][ty * RT + a];
+                    w[0] = s.p[j][ty];
                 }
                 float vv[CT];
 #pragma unroll
@@ -205,18 +214,19 @@ __global__ void __launch_bounds__(kThreads) attend_generic_kernel(const __grid_c
                         if constexpr (CT >= 2) {
 #pragma unroll
                             for (int c = 0; c < CT; c += 2) {
-                                const float2 t = fma2(w[a], make_float2(vv[c], vv[c + 1]), make_float2(o[a][c], o[a][c + 1]));
+                                const float2 t = fma2(make_float2(w[a], w[a]), make_float2(vv[c], vv[c + 1]),
+                                                      make_float2(o[a][c], o[a][c + 1]));
                                 o[a][c] = t.x, o[a][c + 1] = t.y;
                             }
                         } else {
-                            o[a][0] = fmaf(w[a].x, vv[0], o[a][0]);
+                            o[a][0] = fmaf(w[a], vv[0], o[a][0]);
                         }
                     }
                 } else {  // a value of a key that the row does not see may be anything
 #pragma unroll
                     for (int a = 0; a < RT; ++a)
 #pragma unroll
-                        for (int c = 0; c < CT; ++c) o[a][c] = w[a].x != 0.f ? fmaf(w[a].x, vv[c], o[a][c]) : o[a][c];
+                        for (int c = 0; c < CT; ++c) o[a][c] = w[a] != 0.f ? fmaf(w[a], vv[c], o[a][c]) : o[a][c];
                 }
             }
         }
@@ -249,7 +259,7 @@ kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) 
     p.item_cost = KS;
     p.min_keys = 2 * KS;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
-    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), kThreads, size_t(smem), stream, p);
+    return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), threads_of(BM), size_t(smem), stream, p);
 }
 
 template <typename Act, typename Kv>
@@ -262,7 +272,7 @@ kda_status by_size(int D, AttendParams &p, const AttendPlan &plan, cudaStream_t 
         case 6416: return launch<Act, Kv, 16, 64>(p, plan, s);
         case 6464: return launch<Act, Kv, 64, 64>(p, plan, s);
         case 12816: return launch<Act, Kv, 16, 128>(p, plan, s);
-        case 12864: return launch<Act, Kv, 64, 128>(p, plan, s);
+        case 12928: return launch<Act, Kv, 128, 128>(p, plan, s);
     }
     return KDA_ERR_UNSUPPORTED;
 }
@@ -271,8 +281,8 @@ kda_status by_size(int D, AttendParams &p, const AttendPlan &plan, cudaStream_t 
 
 bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
     const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
-    plan->bm = rows <= 16 ? 16 : 64;
-    plan->n_cta = 2 * sm_count();
+    plan->bm = rows <= 16 ? 16 : c->head_dim == 128 ? 128 : 64;
+    plan->n_cta = (plan->bm == 128 ? 1 : plan->bm == 64 ? 3 : 2) * sm_count();
     return true;
 }
 
