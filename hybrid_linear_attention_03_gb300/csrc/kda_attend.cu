@@ -122,17 +122,28 @@ kda_status combine(int D, const AttendParams &p, const AttendPlan &plan, cudaStr
 
 }  // namespace
 
-size_t attend_workspace_bytes(const kda_kv_cache *c, const kda_kv_batch *b) {
+// The kernel of a call, from its sizes and types alone.
+struct Choice {
     AttendPlan plan;
-    if (!tile_plan(c, b, &plan)) generic_plan(c, b, &plan);
+    kda_status (*launch)(const kda_kv_cache *, AttendParams &, const AttendPlan &, cudaStream_t);
+};
+static Choice choose(const kda_kv_cache *c, const kda_kv_batch *b) {
+    Choice ch;
+    if (few_plan(c, b, &ch.plan)) ch.launch = few_launch;
+    else if (tile_plan(c, b, &ch.plan)) ch.launch = tile_launch;
+    else generic_plan(c, b, &ch.plan), ch.launch = generic_launch;
+    return ch;
+}
+
+size_t attend_workspace_bytes(const kda_kv_cache *c, const kda_kv_batch *b) {
+    const AttendPlan plan = choose(c, b).plan;
     return share_bytes(plan.n_cta, plan.bm, c->head_dim);
 }
 
 kda_status launch_attend(const kda_kv_cache *c, const kda_attn_io *io, const kda_kv_batch *b, void *workspace,
                          cudaStream_t stream) {
-    AttendPlan plan;
-    const bool tile = tile_plan(c, b, &plan);
-    if (!tile) generic_plan(c, b, &plan);
+    const Choice ch = choose(c, b);
+    const AttendPlan &plan = ch.plan;
     AttendParams p = {};
     p.b = make_view(c, b);
     p.q = io->q, p.out = io->out, p.q_stride = io->q_stride, p.out_stride = io->out_stride;
@@ -142,7 +153,7 @@ kda_status launch_attend(const kda_kv_cache *c, const kda_attn_io *io, const kda
     p.scale_log2 = io->scale * kLog2e;
     p.parts = static_cast<Part *>(workspace);
     p.part_data = reinterpret_cast<float *>(static_cast<char *>(workspace) + parts_bytes(plan.n_cta));
-    const kda_status st = tile ? tile_launch(c, p, plan, stream) : generic_launch(c, p, plan, stream);
+    const kda_status st = ch.launch(c, p, plan, stream);
     if (st != KDA_OK) return st;
     return c->act == KDA_BF16 ? combine<__nv_bfloat16>(c->head_dim, p, plan, stream)
                               : combine<float>(c->head_dim, p, plan, stream);

@@ -236,6 +236,8 @@ struct AttendPlan {
     int bm;     // rows of a tile
     int n_cta;  // grid
 };
+bool few_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
+kda_status few_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 bool tile_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
 kda_status tile_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);

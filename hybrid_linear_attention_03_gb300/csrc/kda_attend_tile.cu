@@ -36,20 +36,12 @@
 // product.  So in the few tiles where some row does not see some key, warps
 // 12-15 zero the rows of absent keys in the value tile, and take non-finite
 // value rows out of it; the row threads that do see those add them one by one.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
-#include "kda_attend.cuh"
-#include "kda_sm100.cuh"
+#include "kda_attend_tc.cuh"
 
 namespace kda {
 namespace kv {
 namespace {
 
-using namespace sm100;
-
-constexpr int KT = 128;          // keys of a tile
 constexpr int KH = KT / 2;        // keys of a half
 constexpr int kSideRows = 128;   // rows of a side
 // Warps: 8 of softmax, 4 that issue, then those of Q and the value tiles (8 where
@@ -78,13 +70,6 @@ template <int D, bool kE4m3, bool kByKeys> struct Cfg {
     static constexpr int kRawAt = kVAt + kStagesV * kVBytes;
     static constexpr int kMiscAt = kRawAt + (kE4m3 ? kStagesRaw * kRawBytes : 0);
 };
-// Barriers of a ring's tiles, more than it has stages: tile t lands in stage
-// t % stages but reports on barrier t % kBars.  A wait by parity is only sound for
-// a thread that sees every phase of its barrier, and a side that takes every
-// second tile sees every phase of every barrier it uses (kBars is even), whatever
-// the number of stages and the order in which copies land.
-constexpr int kBars = 8;
-
 template <typename C> struct alignas(16) Misc {
     uint64_t k_full[kBars], k_empty[kBars], v_full[kBars], v_empty[kBars], clean[kBars];
     uint64_t raw_full[kBars], raw_empty[kBars], unit_full[kBars];
@@ -112,223 +97,12 @@ template <typename C, bool kE4m3> constexpr size_t smem_bytes() {
     return 1024 + C::kMiscAt + (kE4m3 ? sizeof(ScaleMisc<C>) : 0) + sizeof(Misc<C>);
 }
 
-// ---- PTX of this kernel ---------------------------------------------------------
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
-    uint32_t r;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-    return r;
-}
-// D[tmem] (+)= A[tmem] * B[smem], A bf16 with two K values a column.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs (32 K values an instruction).
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Instruction descriptor: e4m3 A and B, both K-major, fp32 D.
-constexpr uint32_t idesc_e4m3_f32(int M, int N) { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
-// Rows of D e4m3 values, K-major, swizzled over their 128 or 64 bytes: byte
-// offset of a row's 16-byte piece, and the operand descriptor (8 rows a group).
-template <int D> __host__ __device__ __forceinline__ uint32_t row8_piece(int row, int c) {
-    return uint32_t(row * D) + uint32_t((D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-}
-template <int D> __device__ __forceinline__ uint64_t sdesc_row8(uint32_t saddr) {
-    return uint64_t((saddr & 0x3FFFFu) >> 4) | uint64_t(1) << 16 | uint64_t(8 * D >> 4) << 32 | uint64_t(1) << 46 |
-           uint64_t(D == 128 ? 2 : 4) << 61;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-// 16-byte asynchronous copy, or zeros.
-__device__ __forceinline__ void cp_async16_or_zero(void *smem_dst, const void *gsrc, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "r"(there ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-template <int N, int kLaunch> __device__ __forceinline__ void set_regs() {
-    if constexpr (N > kLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int kId, int kCount> __device__ __forceinline__ void named_sync() {
-    asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kCount) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// 16 e4m3 values times a power of two as bf16, exactly.  (Moving the bits by
-// integer instructions and one packed product takes as long and loses the ALU
-// time that the softmax wants.)
-__device__ __forceinline__ void widen_e4m3(const uint4 &q, float f, uint32_t (&o)[8]) {
-    const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 t = mul2(unpack_e4m3(uint16_t(in[i / 2] >> ((i & 1) * 16))), make_float2(f, f));
-        o[i] = pack_bf16(t.x, t.y);
-    }
-}
-// Eight bf16 of a row of Q, of which kLanes neighbouring lanes hold one row, as
-// two e4m3 terms times a power of two; returns its biased exponent.
-template <int kLanes> __device__ __forceinline__ int split_row(const uint4 &raw, uint32_t (&w1)[2], uint32_t (&w2)[2]) {
-    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    // the largest magnitude as a bf16 pattern, of finite values (a row with others is NaN all the same)
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, in[i] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool odd = m >= 0x7f80u;
-    const int e = odd ? 127 : max(scale_exponent(__uint_as_float(m << 16)), 1);
-    const float f = odd ? NAN : exp2_neg_biased(e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = __uint_as_float(in[i] << 16) * f, b = __uint_as_float(in[i] & 0xffff0000u) * f;
-        const uint16_t h1 = pack_e4m3(a, b);
-        const float2 t = unpack_e4m3(h1);
-        const uint16_t h2 = pack_e4m3(a - t.x, b - t.y);
-        if (i % 2 == 0) w1[i / 2] = h1, w2[i / 2] = h2;
-        else w1[i / 2] |= uint32_t(h1) << 16, w2[i / 2] |= uint32_t(h2) << 16;
-    }
-    return e;
-}
-// Bit 7 of a byte is set where one of the 16 codes is NaN.
-__device__ __forceinline__ uint32_t nan_codes(const uint4 &q) {
-    return (((q.x & 0x7f7f7f7fu) + 0x01010101u) | ((q.y & 0x7f7f7f7fu) + 0x01010101u) |
-            ((q.z & 0x7f7f7f7fu) + 0x01010101u) | ((q.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
-}
-// Any bf16 infinity or NaN among eight.
-__device__ __forceinline__ bool odd_bf16(const uint4 &w) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) odd |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
-    return odd;
-}
-
-// A bounded wait that is skipped once one has given up.  The row warps then run
-// on with whatever is there (all in bounds, the error word is set), so that the
-// CTA's own barriers are met; the other roles stop issuing.
-__device__ __forceinline__ void wait_for(bool &ok, uint64_t *bar, uint32_t parity, uint32_t *err) {
-    if (ok) ok = mbar_wait(bar, parity, err);
-}
-// Tile t's barrier of a ring has been passed.
-__device__ __forceinline__ void wait_tile(bool &ok, uint64_t *bars, uint32_t t, uint32_t *err) {
-    wait_for(ok, &bars[t % kBars], (t / kBars) & 1, err);
-}
-// The stage that tile t will take is free: the tile before it there has been used.
-template <int kStages> __device__ __forceinline__ void wait_stage(bool &ok, uint64_t *empty, uint32_t t, uint32_t *err) {
-    static_assert(kStages < kBars, "a tile's barrier is free before its stage");
-    if (t >= kStages) wait_tile(ok, empty, t - kStages, err);
-}
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(one));
-    return one != 0;
-}
-
-// 32 bytes, one whole sector, to a 32-byte aligned place.
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-__device__ __forceinline__ bool any_odd(const uint32_t *odd) { return (odd[0] | odd[1]) != 0; }  // of a half
-
-struct TileMaps {
-    CUtensorMap k, v;
-};
-
-// ItemWalk::next out of line (every role has a copy of the walk); the caller's
-// item stays in its registers.
-__device__ __forceinline__ bool next_item_call(const AttendParams &p, ItemWalk *walk, Item *it) { return walk->next(p, *it); }
-__device__ __forceinline__ bool next_item(const AttendParams &p, ItemWalk &walk, Item &it) {
-    Item got;
-    const bool has = next_item_call(p, &walk, &got);
-    if (has) it = got;
-    return has;
-}
-__device__ __forceinline__ int item_tiles(const Item &it) { return (it.k1 - it.k0 + KT - 1) / KT; }
 // Key tiles of an item's share that side s computes, and the v-th of them.
 template <bool kByKeys> __device__ __forceinline__ int side_tiles(const Item &it, int s) {
     if (kByKeys) return (item_tiles(it) - s + 1) / 2;
     return s * kSideRows < it.rows ? item_tiles(it) : 0;
 }
 template <bool kByKeys> __device__ __forceinline__ int side_tile(int s, int v) { return kByKeys ? 2 * v + s : v; }
-
-// Bit g: keys [kb + 16 g, kb + 16 g + 16) are in a page outside the cache.
-__device__ __forceinline__ uint32_t absent_groups(const AttendParams &p, const Item &it, int kb, int lane) {
-    bool bad = false;
-    if (lane < KT / 16 && kb + lane * 16 < it.k1) bad = load_page(p.b, it.n, kb + lane * 16) < 0;
-    return __ballot_sync(0xffffffffu, bad);
-}
-// Some row of the item does not see some key of the tile at kb.
-__device__ __forceinline__ bool partly_seen(const Item &it, int kb, uint32_t absent) {
-    return absent != 0 || kb + KT - 1 > it.ctx + it.tok0;
-}
 
 // Adds the value rows that were taken out of a tile to O, for the rows that see
 // them (a row's weight is read back from its bf16 place over the scores).  Rare,
@@ -371,50 +145,6 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
             }
         }
     }
-}
-
-// Piece u of a lane in the widening of a raw e4m3 tile: a warp has 16 keys, and
-// 8 neighbouring lanes take the same 16-byte piece of 8 keys, which both tiles'
-// swizzles put into different banks.
-template <int D> struct RawPiece {
-    static constexpr int kPerKey = D / 64, kCount = 2 * kPerKey;  // of a key, of a lane
-    int key;
-    uint32_t from, to;  // byte offsets in the raw and the wide tile (whose next 16 bytes are at to ^ 16)
-    __device__ __forceinline__ RawPiece(int w, int lane, int u) {
-        const int c = lane >> 3, k0 = w * 16 + (lane & 7), g = u / kPerKey, i = u % kPerKey;
-        key = k0 + 8 * g;
-        from = (row8_piece<D>(k0, c) ^ uint32_t(i * 64)) + uint32_t(8 * g * D);
-        to = sw128_chunk(k0, 2 * c, KT) + uint32_t(g * 1024 + i * KT * 128);
-    }
-};
-// A widened tile of which some row does not see some key: zeroes the rows of
-// absent keys and takes out the non-finite ones that not every row sees.
-// Returns the keys taken out, a bit each of the warp's 16.
-template <int D>
-__device__ __noinline__ uint32_t look_over_raw(const AttendParams &p, const Item &it, int kb, uint32_t absent,
-                                               const unsigned char *raw, unsigned char *dst, const uint8_t *scale, int w,
-                                               int lane) {
-    uint32_t odd = 0;
-#pragma unroll 1
-    for (int g = 0; g < 2; ++g) {
-        const int key = w * 16 + 8 * g + (lane & 7), j = kb + key;
-        uint32_t nan = scale[key] >= 247;  // 448 * 2^(247 - 127) is past bf16's range, and 255 is NaN
-        for (int i = 0; i < RawPiece<D>::kPerKey; ++i)
-            nan |= nan_codes(*reinterpret_cast<const uint4 *>(raw + RawPiece<D>(w, lane, g * RawPiece<D>::kPerKey + i).from));
-        nan |= __shfl_xor_sync(0xffffffffu, nan, 8);
-        nan |= __shfl_xor_sync(0xffffffffu, nan, 16);
-        const bool gone = j >= it.k1 || (absent >> (key / 16) & 1);
-        const bool out = !gone && nan != 0 && j > it.ctx + it.tok0;
-        odd |= (__ballot_sync(0xffffffffu, out) & 0xffu) << (8 * g);
-        if (gone || out) {
-            for (int i = 0; i < RawPiece<D>::kPerKey; ++i) {
-                const uint32_t to = RawPiece<D>(w, lane, g * RawPiece<D>::kPerKey + i).to;
-                *reinterpret_cast<uint4 *>(dst + to) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(dst + (to ^ 16u)) = make_uint4(0, 0, 0, 0);
-            }
-        }
-    }
-    return odd;
 }
 
 template <int D, bool kE4m3, bool kByKeys>
@@ -481,7 +211,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                 __syncwarp();
                 tc_fence_after();
             };
-            while (next_item(p, walk, it)) {
+            while (walk.next(p, it)) {
                 const int nv = side_tiles<kByKeys>(it, s);
                 const int lim = it.ctx + it.tok0 + min(r, it.rows - 1) / p.group;  // last key this row sees
                 const bool live = r - lane < it.rows;  // this warp has rows of the item
@@ -702,7 +432,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                 }
                 __syncwarp();
             };
-            while (ok && next_item(p, walk, it)) {
+            while (ok && walk.next(p, it)) {
                 nv = side_tiles<kByKeys>(it, s);
                 if (kByKeys || nv > 0) wait_for(ok, &ms.q_full[qi], n_q++ & 1, err);
                 if (nv > 0) {
@@ -753,49 +483,18 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
             wait_for(end_ok, &ms.done[s], 0, err);
         } else if (ms.has) {
             // ---- page fetches: keys, or values ------------------------------------------------
-            const bool values = warp == 11;
-            const CUtensorMap *map = values ? &maps.v : &maps.k;
-            const int page_size = 1 << p.b.page_shift, box = min(page_size, KT);
-            ItemWalk walk(ms.piece[0], ms.piece[1]);
-            Item it = {};
-            uint32_t tg = 0;
-            auto fetch = [&](int kb, uint64_t *full, unsigned char *dst, uint8_t *scales) {
-                const int j = kb + lane * box, line = j & (page_size - 1);
-                int page = -1;
-                if (lane * box < KT && j < it.k1) page = load_page(p.b, it.n, j);
-                const int there = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box;
-                const int plane = page * p.hkv + it.h;  // below 2^31 (checked on the host)
-                if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(there * (kE4m3 ? D + 1 : 2 * D)));
-                __syncwarp();
-                if (page < 0) return;
+            fetch_pages<D, kE4m3>(p, maps, ms.piece[0], ms.piece[1], warp == 11, ok, [&](uint32_t t, bool values) {
+                if (!values) {
+                    wait_stage<NK>(ok, ms.k_empty, t, err);
+                    return Landing{&ms.k_full[t % kBars], k_ring + t % NK * C::kKBytes, sc8.k[t % NK]};
+                }
                 if constexpr (kE4m3) {
-                    tma_load_3d(dst + lane * box * D, map, full, 0, line, plane);
-                    bulk_load(scales + lane * box, (values ? p.sv : p.sk) + (size_t(plane) << p.b.page_shift) + line,
-                              uint32_t(box), full);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(dst + lane * box * 128 + c * KT * 128, map, full, c * 64, line, plane);
+                    wait_stage<NR>(ok, ms.raw_empty, t, err);
+                    return Landing{&ms.raw_full[t % kBars], raw_ring + t % NR * C::kRawBytes, sc8.v[t % NR]};
                 }
-            };
-            while (ok && next_item(p, walk, it)) {
-                for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tg) {
-                    if (!values) wait_stage<NK>(ok, ms.k_empty, tg, err);
-                    else if (kE4m3) wait_stage<NR>(ok, ms.raw_empty, tg, err);
-                    else wait_stage<NV>(ok, ms.v_empty, tg, err);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    if (!values) fetch(kb, &ms.k_full[tg % kBars], k_ring + tg % NK * C::kKBytes, sc8.k[tg % NK]);
-                    else if (kE4m3) fetch(kb, &ms.raw_full[tg % kBars], raw_ring + tg % NR * C::kRawBytes, sc8.v[tg % NR]);
-                    else fetch(kb, &ms.v_full[tg % kBars], v_ring + tg % NV * C::kVBytes, nullptr);
-                }
-            }
-            // a given-up wait elsewhere may leave copies in flight: they land before the CTA ends
-            if (!ok) {
-                uint64_t *bars = !values ? ms.k_full : kE4m3 ? ms.raw_full : ms.v_full;
-                const uint32_t depth = uint32_t(!values ? NK : kE4m3 ? NR : NV);
-                bool end_ok = true;
-                for (uint32_t t = tg - min(tg, depth); t < tg; ++t) wait_tile(end_ok, bars, t, err);
-            }
+                wait_stage<NV>(ok, ms.v_empty, t, err);
+                return Landing{&ms.v_full[t % kBars], v_ring + t % NV * C::kVBytes, nullptr};
+            }, warp == 11 ? (kE4m3 ? ms.raw_full : ms.v_full) : ms.k_full, warp == 11 ? (kE4m3 ? NR : NV) : NK);
         }
     } else {
         set_regs<W::kRows, W::kLaunch>();
@@ -813,7 +512,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                 named_sync<4, kRowThreads>();
                 ok = ms.rows_gave_up == 0;
             };
-            while (ok && next_item(p, walk, it)) {
+            while (ok && walk.next(p, it)) {
                 for (int s = 0; s < C::kQImages; ++s) {
                     if (side_tiles<kByKeys>(it, s) == 0) continue;
                     unsigned char *q_img = smem + s * C::kQBytes;
@@ -871,71 +570,26 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&ms.q_full[s]);
                 }
                 for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tile) {
-                    const uint32_t absent = absent_groups(p, it, kb, lane);
                     unsigned char *dst = v_ring + tile % NV * C::kVBytes;
-                    uint32_t odd = 0;  // keys taken out, of this warp's
-                    if constexpr (kE4m3) {
-                        using RP = RawPiece<D>;
-                        const unsigned char *raw = raw_ring + tile % NR * C::kRawBytes;
-                        const uint8_t *scale = sc8.v[tile % NR];
-                        if (w == 0) {
+                    if (w == 0) {
+                        if constexpr (kE4m3) {
                             wait_tile(ok, ms.k_full, tile, err), wait_tile(ok, ms.raw_full, tile, err);
                             wait_stage<NV>(ok, ms.v_empty, tile, err);
+                        } else {
+                            wait_tile(ok, ms.v_full, tile, err);
                         }
-                        meet();
-                        if (!ok) break;
+                    }
+                    meet();
+                    if (!ok) break;
+                    if constexpr (kE4m3) {
                         if (qt < KT) sc8.k_unit[tile % kUnits][qt] = exp2_biased(sc8.k[tile % NK][qt]);  // as numbers
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ms.unit_full[tile % kBars]), mbar_arrive(&ms.k_empty[tile % kBars]);
-                        uint4 x[RP::kCount];
-                        float f[2];
-#pragma unroll
-                        for (int u = 0; u < RP::kCount; ++u) {
-                            const RP r(w, lane, u);
-                            x[u] = *reinterpret_cast<const uint4 *>(raw + r.from);
-                            if (u % RP::kPerKey == 0) f[u / RP::kPerKey] = exp2_biased(scale[r.key]);
-                        }
-#pragma unroll
-                        for (int u = 0; u < RP::kCount; ++u) {
-                            const RP r(w, lane, u);
-                            uint32_t o[8];
-                            widen_e4m3(x[u], f[u / RP::kPerKey], o);
-                            *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                        __syncwarp();
-                        if (partly_seen(it, kb, absent)) {
-                            const Item copy = it;
-                            odd = look_over_raw<D>(p, copy, kb, absent, raw, dst, scale, w, lane);
-                        }
-                        fence_proxy_async_smem();
-                        if (lane == 0) reinterpret_cast<uint16_t *>(ms.odd[tile % kBars])[w] = uint16_t(odd);
-                        __syncwarp();
+                        widen_tile<D>(p, it, kb, raw_ring + tile % NR * C::kRawBytes, dst, sc8.v[tile % NR], w, lane,
+                                      ms.odd[tile % kBars]);
                         if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                     } else {
-                        if (w == 0) wait_tile(ok, ms.v_full, tile, err);
-                        meet();
-                        if (!ok) break;
-                        if (partly_seen(it, kb, absent)) {
-                            // a lane looks over one value row, each at a bank of its own
-                            const int row = w * 32 + lane, j = kb + row;
-                            unsigned char *img = dst + row * 128;
-                            const bool gone = j >= it.k1 || (absent >> (row / 16) & 1);
-                            bool bad = false;
-                            for (int c = 0; c < D / 8; ++c)
-                                bad |= odd_bf16(*reinterpret_cast<const uint4 *>(img + (c >> 3) * KT * 128 +
-                                                                                 (((c & 7) ^ (lane & 7)) << 4)));
-                            bad = bad && !gone && j > it.ctx + it.tok0;  // rows that every query sees stay
-                            if (gone || bad) {
-                                for (int c = 0; c < D / 8; ++c)
-                                    *reinterpret_cast<uint4 *>(img + (c >> 3) * KT * 128 + (((c & 7) ^ (lane & 7)) << 4)) =
-                                        make_uint4(0, 0, 0, 0);
-                            }
-                            odd = __ballot_sync(0xffffffffu, bad);
-                            fence_proxy_async_smem();
-                        }
-                        if (lane == 0) ms.odd[tile % kBars][w] = odd;
-                        __syncwarp();
+                        look_over_tile<D>(p, it, kb, dst, w, lane, ms.odd[tile % kBars]);
                         if (lane == 0) mbar_arrive(&ms.clean[tile % kBars]);
                     }
                 }
@@ -946,36 +600,6 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 8) tmem_dealloc(tm, 512);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
-// [num_pages * num_kv_heads][page_size][head_dim]; a box is a tile's part of
-// one page and head (64 channels of it for bf16), swizzled over its row of 128
-// or 64 bytes.
-bool page_map(CUtensorMap *m, const void *base, const kda_kv_cache *c, bool e4m3) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t esize = e4m3 ? 1 : 2, D = cuuint64_t(c->head_dim), P = cuuint64_t(c->page_size);
-    const cuuint64_t dims[3] = {D, P, cuuint64_t(c->num_pages) * cuuint64_t(c->num_kv_heads)};
-    const cuuint64_t strides[2] = {D * esize, D * P * esize};
-    const cuuint32_t box[3] = {cuuint32_t(e4m3 ? c->head_dim : 64), cuuint32_t(c->page_size < KT ? c->page_size : KT), 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
-              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              e4m3 && c->head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, bool kE4m3, bool kByKeys>
