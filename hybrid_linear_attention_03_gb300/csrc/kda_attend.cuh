@@ -53,7 +53,7 @@ struct AttendParams {
     int32_t tile_tokens;  // TT
     int32_t key_step;     // keys per step; cut points are multiples of it
     int32_t item_cost;    // what an item costs beside its keys
-    int32_t min_keys;     // a CTA's piece is at least this long (fewer CTAs take part in a small call)
+    int32_t min_keys;     // a CTA's piece is at least this long, key_step or more (fewer CTAs take part in a small call)
     float scale_log2;     // scale * log2(e)
     Part *parts;          // [C][2]: the CTA's first part (of an item begun before) and its last
     float *part_data;     // [C][2][BM * (D + 2)]: out [BM][D], then row maxima [BM], then row sums [BM]
@@ -107,7 +107,10 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
     const int cost = all_items > n_cta ? p.item_cost : 0;
     const long long sum = my_keys + cost * my_items, before = keys + cost * items - sum;
     const long long total = __shfl_sync(0xffffffffu, before + sum, 31);
-    const int active = int(min(static_cast<long long>(n_cta), div_pos(total + p.min_keys - 1, p.min_keys)));
+    if (total == 0) return false;
+    // A piece is never shorter than a key step: two cuts in one step would leave a CTA with nothing in the
+    // middle of an item, whose parts are those of consecutive CTAs.
+    const int active = int(min(static_cast<long long>(n_cta), max(div_pos(total, p.min_keys), 1LL)));
     if (cta >= active) return false;
     const long long share = div_pos(total, active);
     const int over = int(total - share * active);

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                 const bool check = partly_seen(it, kb, absent);
                 int hidden = 0;  // rows before this one do not see the thread's key
                 if (check) {
-                    hidden = max((j - first_lim) * p.group, 0);
+                    hidden = max(j - first_lim, 0) * p.group;
                     if (j >= it.k1 || (absent >> (tid / 16) & 1)) hidden = N;
                 }
                 float unit = 1.f;

@@ -20,7 +20,11 @@ struct BatchView {
     uint32_t *err;
     int32_t n_seqs, table_stride, max_rows, max_new;
     int32_t num_pages, page_shift;
+    int32_t max_len;  // tokens a sequence may have
 };
+
+// Positions are 32-bit, and a tile of keys may reach this far past the last one.
+constexpr int32_t kMaxPositions = 0x7fffff00;
 
 struct Seq {
     int row0, T, L;  // first row, new tokens, cache length with them
@@ -32,7 +36,7 @@ struct Seq {
 __device__ __forceinline__ bool load_seq(const BatchView &b, int n, Seq &s, bool report) {
     const int a = b.cu[n], e = b.cu[n + 1], L = b.lens[n];
     const bool ok = a >= 0 && e >= a && e <= b.max_rows && e - a <= b.max_new && L >= e - a &&
-                    L <= (static_cast<long long>(b.table_stride) << b.page_shift);
+                    L <= b.max_len;
     s.row0 = a;
     s.T = ok ? e - a : 0;
     s.L = L;
@@ -113,6 +117,8 @@ inline BatchView make_view(const kda_kv_cache *c, const kda_kv_batch *b) {
     v.max_new = b->max_new;
     v.num_pages = c->num_pages;
     v.page_shift = page_shift_of(c->page_size);
+    const long long pages_hold = static_cast<long long>(b->table_stride) << v.page_shift;
+    v.max_len = pages_hold < kMaxPositions ? int32_t(pages_hold) : kMaxPositions;
     return v;
 }
 

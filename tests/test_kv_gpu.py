@@ -442,6 +442,224 @@ def test_no_sequences_and_no_rows_are_no_ops():
     assert (out == 9.0).all()
 
 
+MANY = [
+    # lengths from one token up, sequences by the hundred: items of one tile, and pieces that hold many items
+    ([1] * 300, [1 + 37 * i % 160 for i in range(300)], 8, 1, 128, 16),
+    ([1] * 180, [1 + 211 * i % 1500 for i in range(180)], 16, 2, 128, 64),
+    ([3] * 200, [3 + 53 * i % 400 for i in range(200)], 8, 1, 128, 32),
+    ([5] * 170, [5 + i % 123 for i in range(170)], 4, 2, 64, 128),
+    ([1 + 7 * i % 40 for i in range(60)], [40 + 97 * i % 700 for i in range(60)], 8, 1, 128, 128),
+    ([128 * (i % 3) for i in range(30)], [256 + 64 * (i % 5) for i in range(30)], 2, 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attend_many_sequences(case, fmt):
+    new, total, hq, hkv, d, page = MANY[case]
+    b = R.Batch(new, total, hq, hkv, d, page, BF, fmt, seed=200 + case, fill=float("nan"))
+    cache = fill_cache(b)
+    q = b.randn(b.rows, hq).cuda()
+    out = torch.full_like(q, 9.0)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+    no_device_error(b.kv)
+    check_attend(b, q, out, cache, d ** -0.5)
+
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("new,group,d", [(1, 16, 128), (1, 17, 128), (2, 8, 128), (16, 1, 128), (17, 1, 128), (8, 16, 128),
+                                         (43, 3, 128), (1, 1, 64), (64, 2, 64), (129, 1, 64)])
+def test_attend_rows_of_a_tile(new, group, d, page, fmt):
+    """One row to a little over a tile, over caches that end at a tile's border and one token to either side of it."""
+    tops = [max(t, new) for t in (127, 128, 129, 256, 384)]
+    b = R.Batch([new] * 5, tops, group, 1, d, page, BF, fmt, seed=300 + new, fill=float("nan"))
+    cache = fill_cache(b)
+    q = b.randn(b.rows, group).cuda()
+    out = torch.full_like(q, 9.0)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+    no_device_error(b.kv)
+    check_attend(b, q, out, cache, d ** -0.5)
+
+
+@pytest.mark.parametrize("new,group,d,act", [(1, 2, 128, BF), (4, 8, 128, BF), (40, 8, 64, BF), (1, 2, 64, BF), (1, 3, 32, F32),
+                                             (5, 2, 16, BF)])
+def test_attend_few_items_of_any_length(new, group, d, act):
+    """Fewer items than CTAs, of lengths that put the cuts between CTAs at every place of a key step."""
+    rng = np.random.default_rng(73)
+    for trial in range(25):
+        total = [new + int(x) for x in rng.integers(0, int(rng.choice([300, 1500, 4000])), int(rng.integers(1, 7)))]
+        b = R.Batch([new] * len(total), total, group, 1, d, 64, act, "act", seed=400 + trial)
+        cache = fill_cache(b)
+        q = b.randn(b.rows, group).cuda()
+        out = torch.full_like(q, 9.0)
+        kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+        no_device_error(b.kv)
+        check_attend(b, q, out, cache, d ** -0.5)
+
+
+@pytest.mark.parametrize("new,hq,hkv,d", [(4, 4, 2, 128), (100, 4, 2, 128), (300, 2, 1, 64), (20, 3, 1, 32)])
+def test_masked_e4m3_lines_may_be_anything(new, hq, hkv, d):
+    """A quantised line that holds NaN, or a scale past bf16's range, reaches its own and later rows only."""
+    total = new + 70
+    for act in (BF, F32):
+        b = R.Batch([new], [total], hq, hkv, d, 32, act, "e4m3", seed=43)
+        cache = fill_cache(b)
+        at = total - new // 2
+        page, line = int(b.table[0, at // 32]), at % 32
+        b.kv.v.view(torch.uint8)[page, :, line, 1] = 0xFF
+        page, line = int(b.table[0, (total - 1) // 32]), (total - 1) % 32
+        b.kv.v_scale[page, :, line] = 255
+        b.kv.k.view(torch.uint8)[page, :, line, 0] = 0x7F
+        q = b.randn(b.rows, hq).cuda()
+        out = torch.empty_like(q)
+        kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+        got = out.double().cpu()
+        t_bad = at - (total - new)
+        assert torch.isfinite(got[:t_bad]).all()
+        assert torch.isnan(got[t_bad:-1, :, 1]).all()
+        assert torch.isfinite(got[t_bad:-1, :, 2:]).all() and torch.isfinite(got[t_bad:-1, :, 0]).all()
+        assert torch.isnan(got[-1]).all()
+        k, v = cache[0]
+        ref, mag = R.attend(q[:t_bad].double().cpu(), k, v, total - new, d ** -0.5, hq // hkv)
+        assert ((got[:t_bad] - ref).abs() <= 3 * half_step(BF) * mag + 1e-12).all()
+
+
+@pytest.mark.parametrize("act,fmt", [(BF, "act"), (BF, "e4m3"), (F32, "act"), (F32, "e4m3")])
+@pytest.mark.parametrize("new,hq,d", [(2, 4, 128), (30, 2, 128), (150, 2, 64), (3, 64, 32)])
+def test_far_positions_and_absent_pages(new, hq, d, act, fmt):
+    """A context of tens of millions of tokens of which only the last pages are there (a window)."""
+    page, far = 128, 40_000_000
+    b = R.Batch([new], [new + 200], hq, 1, d, page, act, fmt, seed=47)
+    cache = fill_cache(b)
+    skip = far // page
+    table = torch.full((1, skip + b.table.shape[1]), -1, dtype=torch.int32)
+    table[0, skip:] = b.table[0]
+    lens = torch.tensor([skip * page + new + 200], dtype=torch.int32).cuda()
+    batch = kda.make_kv_batch(b.dev[0], lens, table.cuda(), max_rows=b.rows, max_new=new)
+    q = b.randn(b.rows, hq).cuda()
+    out = torch.full_like(q, 9.0)
+    ws = torch.empty(kda.kda_kv_attend_workspace_bytes(b.kv, batch), dtype=torch.uint8, device="cuda")
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), batch, ws)
+    assert kda.kda_kv_poll_device_error(b.kv) == (kda.KDA_ERR_DEVICE, kda.KDA_DEVERR_PAGE_RANGE)
+    check_attend(b, q, out, cache, d ** -0.5)
+
+
+def test_longest_positions_are_refused():
+    """Past 2^31 - 256 tokens a tile's last positions would not be 32-bit numbers: the sequence is left alone."""
+    page = 128
+    b = R.Batch([1, 1], [100, 50], 2, 1, 64, page, BF, "act", seed=53)
+    cache = fill_cache(b)
+    width = (1 << 31) // page
+    table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+    table[:, :1] = b.dev[2]
+    b.dev[1][0] = (1 << 31) - 1
+    batch = kda.make_kv_batch(b.dev[0], b.dev[1], table, max_rows=2, max_new=1)
+    q = b.randn(2, 2).cuda()
+    out = torch.full_like(q, 9.0)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), batch, b.workspace())
+    assert kda.kda_kv_poll_device_error(b.kv) == (kda.KDA_ERR_DEVICE, kda.KDA_DEVERR_META)
+    assert (out[0] == 9.0).all()
+    ref, mag = R.attend(q[1:].double().cpu(), *cache[1], 49, 64 ** -0.5, 2)
+    assert ((out[1:].double().cpu() - ref).abs() <= 4 * half_step(BF) * mag).all()
+
+
+@pytest.mark.parametrize("act,fmt", [(BF, "act"), (BF, "e4m3"), (F32, "act")])
+@pytest.mark.parametrize("new,hq,hkv,d", [(1, 8, 2, 128), (9, 8, 2, 128), (150, 4, 2, 64), (40, 4, 2, 16)])
+def test_rows_16_bytes_apart_and_loose_bounds(new, hq, hkv, d, act, fmt):
+    """Rows that start at 16-byte but not 32-byte places, and host bounds larger than what the tables hold."""
+    b = R.Batch([new, 0, 1], [new + 150, 20, 33], hq, hkv, d, 32, act, fmt, seed=59, extra_rows=5)
+    cache = fill_cache(b)
+    pad = 8 if act == BF else 4
+    q_wide = torch.zeros(b.max_rows, hq * d + pad, dtype=act, device="cuda")
+    q = q_wide[:, pad:].unflatten(1, (hq, d))
+    q.copy_(b.randn(b.max_rows, hq))
+    wide = torch.full((b.max_rows, hq * d + pad), 9.0, dtype=act, device="cuda")
+    out = wide[:, pad:].unflatten(1, (hq, d))
+    for max_new in (new, new + 1, 70, 1000):
+        if max_new < new:
+            continue
+        wide.fill_(9.0)
+        batch = kda.make_kv_batch(*b.dev, max_rows=b.max_rows, max_new=max_new)
+        ws = torch.empty(kda.kda_kv_attend_workspace_bytes(b.kv, batch), dtype=torch.uint8, device="cuda")
+        kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), batch, ws)
+        no_device_error(b.kv)
+        check_attend(b, q, out, cache, d ** -0.5)
+        assert (out[b.rows:] == 9.0).all() and (wide[:, :pad] == 9.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+def test_two_calls_at_once(fmt):
+    """Two streams, each with its own workspace, over one cache and at the same time: what each gives alone."""
+    streams, work = [torch.cuda.Stream() for _ in range(2)], []
+    b = R.Batch([1] * 20, [900 + 31 * i for i in range(20)], 8, 2, 128, 64, BF, fmt, seed=61)
+    fill_cache(b)
+    c = R.Batch.__new__(R.Batch)
+    c.__dict__.update(b.__dict__)
+    c.new, c.rows = [30] * 20, 600
+    c.cu = torch.arange(21, dtype=torch.int32) * 30
+    c.dev = (c.cu.cuda(), b.dev[1], b.dev[2])
+    c.batch = kda.make_kv_batch(*c.dev, max_rows=600, max_new=30)
+    for x in (b, c):
+        q = x.randn(x.rows, 8).cuda()
+        io, ws = kda.make_attn_io(q, torch.empty_like(q)), x.workspace()
+        kda.kda_kv_attend(x.kv, io, x.batch, ws)
+        work.append((x, io, ws, io._tensors[1], io._tensors[1].clone()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (x, io, ws, out, _) in zip(streams, work):
+            kda.kda_kv_attend(x.kv, io, x.batch, ws, stream=st)
+    torch.cuda.synchronize()
+    no_device_error(b.kv)
+    for _, _, _, out, alone in work:
+        assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("act,fmt,new", [(BF, "e4m3", 1), (BF, "e4m3", 8), (BF, "act", 40), (F32, "act", 2)])
+def test_replayed_with_other_lengths(act, fmt, new):
+    """Captured once, replayed with tables that move work between CTAs, sequences that drop out and new pages."""
+    hq, hkv, d, page = 8, 2, 128, 16
+    b = R.Batch([new] * 3, [700, 600, 500], hq, hkv, d, page, act, fmt, seed=67)
+    fill_cache(b)
+    q = b.randn(b.rows, hq).cuda()
+    out = torch.empty_like(q)
+    ws, st = b.workspace(), torch.cuda.Stream()
+    io = kda.make_attn_io(q, out)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        kda.kda_kv_attend(b.kv, io, b.batch, ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            kda.kda_kv_attend(b.kv, io, b.batch, ws)
+    torch.cuda.synchronize()
+    for news, lens in (([new] * 3, [700, 600, 500]), ([new, 0, new], [new, 600, 333]), ([0, new, 0], [9, 17 + new, 9]),
+                       ([1, 1, 1], [1, 2, 3]), ([new] * 3, [128, 640, 127 + new])):
+        b.new, b.total, b.rows = news, lens, sum(news)
+        b.cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32)
+        b.dev[0].copy_(b.cu), b.dev[1].copy_(torch.tensor(lens, dtype=torch.int32))
+        b.dev[2].copy_(b.table.flip(1)[:, :b.table.shape[1]].clamp(min=0))
+        out.fill_(9.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            g.replay()
+        torch.cuda.synchronize()
+        no_device_error(b.kv)
+        check_attend(b, q, out, held(b), d ** -0.5)
+        assert (out[b.rows:] == 9.0).all()
+
+
+def test_a_page_twice_in_a_sequence():
+    """A table may name a page more than once: its tokens then stand at several positions."""
+    b = R.Batch([1, 20], [300, 310], 4, 2, 128, 32, BF, "act", seed=71)
+    fill_cache(b)
+    b.dev[2][:, 1:5] = b.dev[2][0, 0]
+    q = b.randn(b.rows, 4).cuda()
+    out = torch.empty_like(q)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+    no_device_error(b.kv)
+    check_attend(b, q, out, held(b), 128 ** -0.5)
+
+
 # ---- together ----------------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("act,fmt", [(BF, "act"), (BF, "e4m3"), (F32, "act")], ids=["bf16", "bf16-e4m3", "f32"])
