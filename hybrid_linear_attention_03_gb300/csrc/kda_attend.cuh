@@ -6,8 +6,9 @@
 // them) for TT consecutive tokens of one sequence, rows r = t * G + g.  Its
 // keys are positions [0, ctx + last token + 1).  All items of a call, ordered
 // by sequence, cache head and tile, form one line; an item is as long on it as
-// it has keys, plus a constant for its start and output (in keys that take as
-// long).  CTA c of C takes the c-th of C equal pieces of that line (a cut point
+// it has keys, plus a constant: where there are more items than CTAs that of its
+// start and output (in keys that take as long), else the shortest piece that a CTA
+// is given, so that short items get a CTA each.  CTA c of C takes the c-th of C equal pieces of that line (a cut point
 // inside an item rounded down to whole key steps).  So any
 // mix of lengths loads every CTA alike, with no table built on the host and
 // no launch per sequence.  An item cut by one or more cut points is computed
@@ -104,7 +105,7 @@ __device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n
         if (lane >= o) keys += k, items += i;
     }
     const long long all_items = __shfl_sync(0xffffffffu, items, 31);
-    const int cost = all_items > n_cta ? p.item_cost : 0;
+    const int cost = all_items > n_cta ? p.item_cost : p.min_keys;
     const long long sum = my_keys + cost * my_items, before = keys + cost * items - sum;
     const long long total = __shfl_sync(0xffffffffu, before + sum, 31);
     if (total == 0) return false;

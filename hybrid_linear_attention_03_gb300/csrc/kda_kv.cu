@@ -19,7 +19,8 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerCta = 4;  // many rows: the rows of a CTA
+// Most rows of a CTA, for lane groups of `lanes` lanes.
+constexpr int max_rows_per_cta(int lanes) { return kThreads / lanes < 32 ? kThreads / lanes : 32; }
 constexpr int kUnroll = 4;      // 16-byte loads in flight per thread
 
 struct AppendParams {
@@ -100,16 +101,17 @@ template <typename Act, int D, bool kE4m3, int kRot>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
     using V = Vec<Act>;
     constexpr int N = V::N, LPH = D / N, kGroups = kThreads / LPH;  // values per lane, lanes per group
-    __shared__ float2 cs[kRowsPerCta][D / 2];
-    __shared__ int s_pos[kRowsPerCta], s_page[kRowsPerCta];
+    constexpr int kRows = max_rows_per_cta(LPH);
+    __shared__ float2 cs[kRows][D / 2];
+    __shared__ int s_pos[kRows], s_page[kRows];
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int row_base = int(blockIdx.x) * p.rows_per_cta;
     wait_prior_kernel();
     allow_next_kernel();
-    if (warp < p.rows_per_cta) {
+    for (int i = warp; i < p.rows_per_cta; i += kThreads / 32) {
         int pos, page;
-        find_row(p.b, row_base + warp, lane, pos, page);
-        if (lane == 0) s_pos[warp] = pos, s_page[warp] = page;
+        find_row(p.b, row_base + i, lane, pos, page);
+        if (lane == 0) s_pos[i] = pos, s_page[i] = page;
     }
     __syncthreads();
     if constexpr (kRot != kNoRot) {
@@ -261,15 +263,16 @@ struct ReadParams {
 template <typename Act, int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
     constexpr int N = kE4m3 ? 16 : Vec<Act>::N, LPH = D / N, kGroups = kThreads / LPH;
-    __shared__ int s_pos[kRowsPerCta], s_page[kRowsPerCta];
+    constexpr int kRows = max_rows_per_cta(LPH);
+    __shared__ int s_pos[kRows], s_page[kRows];
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int row_base = int(blockIdx.x) * p.rows_per_cta;
     wait_prior_kernel();
     allow_next_kernel();
-    if (warp < p.rows_per_cta) {
+    for (int i = warp; i < p.rows_per_cta; i += kThreads / 32) {
         int pos, page;
-        find_row(p.b, row_base + warp, lane, pos, page);
-        if (lane == 0) s_pos[warp] = pos, s_page[warp] = page;
+        find_row(p.b, row_base + i, lane, pos, page);
+        if (lane == 0) s_pos[i] = pos, s_page[i] = page;
     }
     __syncthreads();
     const int step = kGroups / p.rows_per_cta, row = (tid / LPH) / step, j = (tid / LPH) % step;
@@ -322,19 +325,29 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
     }
 }
 
-// Few rows: one row a CTA and its heads spread over CTAs so that every thread
-// has one 16-byte item (latency).  Many rows: kRowsPerCta rows a CTA.  The
-// border is where one item per thread fills every SM once.
-template <typename Act, int D> bool few_rows(int rows, int heads) {
-    return static_cast<long long>(rows) * heads * (D / Vec<Act>::N) <= 2048LL * sm_count();
+// Rows of a CTA.  Few rows: as few as leave every thread one 16-byte piece of
+// the row's heads (latency); the border is where one piece per thread fills every
+// SM once.  Many rows: 4, or more where a row's heads of one kind (at most
+// `kind`) are fewer than the lane groups that it would get.
+struct RowSplit {
+    int rows_per_cta;
+    bool few;
+};
+inline RowSplit split_rows(int rows, int lanes, int heads, int kind) {
+    const int groups = kThreads / lanes, most = max_rows_per_cta(lanes);
+    RowSplit s = {1, static_cast<long long>(rows) * heads * lanes <= 2048LL * sm_count()};
+    if (!s.few) s.rows_per_cta = most < 4 ? most : 4;
+    while (s.rows_per_cta < most && groups / s.rows_per_cta / 2 >= (s.few ? heads : kind)) s.rows_per_cta *= 2;
+    return s;
 }
 
 template <typename Act, int D, bool kE4m3>
 kda_status append_d(AppendParams &p, int rows, cudaStream_t stream) {
     const int heads = p.hq + 2 * p.hkv;
-    const bool few = few_rows<Act, D>(rows, heads);
-    p.rows_per_cta = few ? 1 : kRowsPerCta;
-    p.heads_per_cta = few ? kThreads / (D / Vec<Act>::N) : heads;
+    constexpr int lanes = D / Vec<Act>::N;
+    const RowSplit split = split_rows(rows, lanes, heads, p.hq > p.hkv ? p.hq : p.hkv);
+    p.rows_per_cta = split.rows_per_cta;
+    p.heads_per_cta = split.few ? kThreads / lanes / split.rows_per_cta : heads;
     const dim3 grid(unsigned((rows + p.rows_per_cta - 1) / p.rows_per_cta),
                     unsigned((heads + p.heads_per_cta - 1) / p.heads_per_cta));
     auto kern = p.half_rot == 0   ? kv_append_kernel<Act, D, kE4m3, kNoRot>
@@ -346,7 +359,8 @@ kda_status append_d(AppendParams &p, int rows, cudaStream_t stream) {
 
 template <typename Act, int D, bool kE4m3>
 kda_status read_d(ReadParams &p, int rows, cudaStream_t stream) {
-    p.rows_per_cta = few_rows<Act, D>(rows, 2 * p.hkv) ? 1 : kRowsPerCta;
+    constexpr int lanes = D / (kE4m3 ? 16 : Vec<Act>::N);
+    p.rows_per_cta = split_rows(rows, lanes, 2 * p.hkv, 2 * p.hkv).rows_per_cta;
     const ProfScope prof(KDA_KERNEL_KV_READ, stream);
     return launch_overlapped(kv_read_kernel<Act, D, kE4m3>, dim3(unsigned((rows + p.rows_per_cta - 1) / p.rows_per_cta)),
                              kThreads, 0, stream, p);
