@@ -130,6 +130,7 @@ struct Choice {
 static Choice choose(const kda_kv_cache *c, const kda_kv_batch *b) {
     Choice ch;
     if (few_plan(c, b, &ch.plan)) ch.launch = few_launch;
+    else if (lanes_plan(c, b, &ch.plan)) ch.launch = lanes_launch;
     else if (tile_plan(c, b, &ch.plan)) ch.launch = tile_launch;
     else generic_plan(c, b, &ch.plan), ch.launch = generic_launch;
     return ch;
@@ -148,7 +149,7 @@ kda_status launch_attend(const kda_kv_cache *c, const kda_attn_io *io, const kda
     p.b = make_view(c, b);
     p.q = io->q, p.out = io->out, p.q_stride = io->q_stride, p.out_stride = io->out_stride;
     p.pk = c->k, p.pv = c->v, p.sk = c->k_scale, p.sv = c->v_scale;
-    p.hq = c->num_heads, p.hkv = c->num_kv_heads, p.group = c->num_heads / c->num_kv_heads;
+    p.hq = c->num_heads, p.hkv = c->num_kv_heads, p.group = c->num_heads / c->num_kv_heads, p.dim = c->head_dim;
     p.tile_tokens = plan.bm / p.group;
     p.scale_log2 = io->scale * kLog2e;
     p.parts = static_cast<Part *>(workspace);

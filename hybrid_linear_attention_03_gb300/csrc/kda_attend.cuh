@@ -50,7 +50,7 @@ struct AttendParams {
     long long q_stride, out_stride;
     const void *pk, *pv;
     const uint8_t *sk, *sv;
-    int32_t hq, hkv, group;
+    int32_t hq, hkv, group, dim;
     int32_t tile_tokens;  // TT
     int32_t key_step;     // keys per step; cut points are multiples of it
     int32_t item_cost;    // what an item costs beside its keys
@@ -244,6 +244,8 @@ bool few_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
 kda_status few_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 bool tile_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
 kda_status tile_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+bool lanes_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
+kda_status lanes_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan);
 kda_status generic_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 

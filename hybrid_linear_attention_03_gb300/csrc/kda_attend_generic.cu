@@ -1,5 +1,5 @@
-// kda_attend_generic.cu -- kda_kv_attend in 32-bit arithmetic on the CUDA
-// cores, for every activation type, cache format and head size.
+// kda_attend_generic.cu -- kda_kv_attend for more than 16 rows a cache head in
+// 32 bits, on the CUDA cores (the tensor cores have no 32-bit products).
 //
 // One pass over the keys with the running row maximum m and sum l of a
 // softmax (in powers of two, x = scale * log2(e) * q . k):
@@ -7,11 +7,13 @@
 //   o <- o 2^(m - m') + sum_j 2^(x_j - m') v_j,   out = o / l.
 // A CTA holds a tile of BM rows (query heads of one cache head, consecutive
 // tokens) and walks 64 keys a step through shared memory; 16 threads side by
-// side share RT rows, each with 4 of the keys of the scores and D / 16 channels
+// side share 8 rows, each with 4 of the keys of the scores and D / 16 channels
 // of the output in registers.  Multiply-adds go two to an instruction (scores sum
-// even and odd channels apart).  Shared memory reads set the pace where a thread
-// has 4 rows or fewer, so the tiles of many rows give it 8: 64 rows on 128
-// threads, or 128 rows on 256 where head size 128 leaves room for one CTA an SM.
+// even and odd channels apart).  They bound it, with the shared memory reads that
+// feed them close behind: at 4 rows a thread the reads came first (ragged prompts
+// of 777 to 1500 tokens, 12 heads of 64: 305 us against 258 at 8, 30 TFLOP/s).
+// 64 rows on 128 threads leave room for three CTAs an SM, whose loads and sums
+// cover each other; head size 128 takes 128 rows on 256 threads, one CTA an SM.
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -19,18 +21,12 @@ namespace kv {
 namespace {
 
 constexpr int KS = 64;  // keys a step
-// Threads of a CTA: 8 rows each, one row each for the 16-row tile.
-constexpr int threads_of(int bm) { return bm == 16 ? 256 : bm * 2; }
+constexpr int threads_of(int bm) { return bm * 2; }  // 16 threads for 8 rows
 
 template <typename Kv> __device__ __forceinline__ void load4(const Kv *src, float (&x)[4]);
 template <> __device__ __forceinline__ void load4<float>(const float *src, float (&x)[4]) {
     const float4 t = *reinterpret_cast<const float4 *>(src);
     x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
-}
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16 *src, float (&x)[4]) {
-    const uint2 t = *reinterpret_cast<const uint2 *>(src);
-    x[0] = __uint_as_float(t.x << 16), x[1] = __uint_as_float(t.x & 0xffff0000u);
-    x[2] = __uint_as_float(t.y << 16), x[3] = __uint_as_float(t.y & 0xffff0000u);
 }
 template <> __device__ __forceinline__ void load4<uint8_t>(const uint8_t *src, float (&x)[4]) {
     const uint32_t t = *reinterpret_cast<const uint32_t *>(src);
@@ -50,9 +46,9 @@ template <int BM, int D> struct Smem {
     int has;
 };
 
-template <typename Act, typename Kv, int BM, int D>
+template <typename Kv, int BM, int D>
 __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_generic_kernel(const __grid_constant__ AttendParams p) {
-    constexpr int kThreads = threads_of(BM), RT = BM * 16 / kThreads, CT = D / 16, CV = CT >= 4 ? 4 : CT;  // rows and channels of a thread
+    constexpr int kThreads = threads_of(BM), RT = 8, CT = D / 16, CV = CT >= 4 ? 4 : CT;  // rows and channels of a thread
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<BM, D> &s = *reinterpret_cast<Smem<BM, D> *>(smem_raw);
     const int tid = int(threadIdx.x), ty = tid >> 4, tx = tid & 15;
@@ -77,7 +73,7 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
         for (int i = tid; i < BM * D / 4; i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < it.rows) load4<Act>(static_cast<const Act *>(p.q) + it.at(r, p.group, p.q_stride, D) + c, x);
+            if (r < it.rows) load4<float>(static_cast<const float *>(p.q) + it.at(r, p.group, p.q_stride, D) + c, x);
             *reinterpret_cast<float4 *>(&s.q[r][c]) =
                 make_float4(x[0] * p.scale_log2, x[1] * p.scale_log2, x[2] * p.scale_log2, x[3] * p.scale_log2);
         }
@@ -184,25 +180,16 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float *dst = &s.p[tx + 16 * e][ty * RT];
-                if constexpr (RT == 8) {
-                    reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0][e], x[1][e], x[2][e], x[3][e]);
-                    reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4][e], x[5][e], x[6][e], x[7][e]);
-                } else {
-                    dst[0] = x[0][e];
-                }
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0][e], x[1][e], x[2][e], x[3][e]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4][e], x[5][e], x[6][e], x[7][e]);
             }
             __syncwarp();  // a row's weights are written and read by the same half warp
             // channels of a thread: groups of four (or the D / 16 there are) 16 groups apart
 #pragma unroll 1
             for (int j = 0; j < KS; ++j) {
-                float w[RT];
-                if constexpr (RT == 8) {
-                    const float4 t = *reinterpret_cast<const float4 *>(&s.p[j][ty * 8]);
-                    const float4 u = *reinterpret_cast<const float4 *>(&s.p[j][ty * 8 + 4]);
-                    w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w, w[4] = u.x, w[5] = u.y, w[6] = u.z, w[7] = u.w;
-                } else {
-                    w[0] = s.p[j][ty];
-                }
+                const float4 t = *reinterpret_cast<const float4 *>(&s.p[j][ty * 8]);
+                const float4 u = *reinterpret_cast<const float4 *>(&s.p[j][ty * 8 + 4]);
+                const float w[RT] = {t.x, t.y, t.z, t.w, u.x, u.y, u.z, u.w};
                 float vv[CT];
 #pragma unroll
                 for (int g = 0; g < CT / CV; ++g)
@@ -238,11 +225,11 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
             const int r = ty * RT + a;
             if (r >= it.rows) continue;
             const float inv = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
-            Act *dst = static_cast<Act *>(p.out) + it.at(r, p.group, p.out_stride, D);
+            float *dst = static_cast<float *>(p.out) + it.at(r, p.group, p.out_stride, D);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const int ch = c / CV * 16 * CV + tx * CV + c % CV;
-                if (whole) dst[ch] = from_f32<Act>(o[a][c] * inv);
+                if (whole) dst[ch] = o[a][c] * inv;
                 else data[size_t(r) * D + ch] = o[a][c];
             }
             if (!whole && tx == 0) data[BM * D + r] = m[a], data[BM * D + BM + r] = l[a];
@@ -250,11 +237,11 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
     }
 }
 
-template <typename Act, typename Kv, int BM, int D>
+template <typename Kv, int BM, int D>
 kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
-    auto kern = attend_generic_kernel<Act, Kv, BM, D>;
+    auto kern = attend_generic_kernel<Kv, BM, D>;
     const int smem = int(sizeof(Smem<BM, D>));
-    if (!allow_smem<attend_generic_kernel<Act, Kv, BM, D>>(smem)) return KDA_ERR_CUDA;
+    if (!allow_smem<attend_generic_kernel<Kv, BM, D>>(smem)) return KDA_ERR_CUDA;
     p.key_step = KS;
     p.item_cost = KS;
     p.min_keys = 2 * KS;
@@ -262,17 +249,12 @@ kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) 
     return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), threads_of(BM), size_t(smem), stream, p);
 }
 
-template <typename Act, typename Kv>
-kda_status by_size(int D, AttendParams &p, const AttendPlan &plan, cudaStream_t s) {
-    switch (D * 100 + plan.bm) {
-        case 1616: return launch<Act, Kv, 16, 16>(p, plan, s);
-        case 1664: return launch<Act, Kv, 64, 16>(p, plan, s);
-        case 3216: return launch<Act, Kv, 16, 32>(p, plan, s);
-        case 3264: return launch<Act, Kv, 64, 32>(p, plan, s);
-        case 6416: return launch<Act, Kv, 16, 64>(p, plan, s);
-        case 6464: return launch<Act, Kv, 64, 64>(p, plan, s);
-        case 12816: return launch<Act, Kv, 16, 128>(p, plan, s);
-        case 12928: return launch<Act, Kv, 128, 128>(p, plan, s);
+template <typename Kv> kda_status by_size(int D, AttendParams &p, const AttendPlan &plan, cudaStream_t s) {
+    switch (D) {
+        case 16: return launch<Kv, 64, 16>(p, plan, s);
+        case 32: return launch<Kv, 64, 32>(p, plan, s);
+        case 64: return launch<Kv, 64, 64>(p, plan, s);
+        case 128: return launch<Kv, 128, 128>(p, plan, s);
     }
     return KDA_ERR_UNSUPPORTED;
 }
@@ -280,19 +262,14 @@ kda_status by_size(int D, AttendParams &p, const AttendPlan &plan, cudaStream_t 
 }  // namespace
 
 bool generic_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
-    const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
-    plan->bm = rows <= 16 ? 16 : c->head_dim == 128 ? 128 : 64;
-    plan->n_cta = (plan->bm == 128 ? 1 : plan->bm == 64 ? 3 : 2) * sm_count();
+    plan->bm = c->head_dim == 128 ? 128 : 64;
+    plan->n_cta = (plan->bm == 128 ? 1 : 3) * sm_count();
     return true;
 }
 
 kda_status generic_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
-    const int D = c->head_dim;
-    const bool e4 = c->format == KDA_KV_E4M3;
-    if (c->act == KDA_BF16)
-        return e4 ? by_size<__nv_bfloat16, uint8_t>(D, p, plan, stream)
-                  : by_size<__nv_bfloat16, __nv_bfloat16>(D, p, plan, stream);
-    return e4 ? by_size<float, uint8_t>(D, p, plan, stream) : by_size<float, float>(D, p, plan, stream);
+    return c->format == KDA_KV_E4M3 ? by_size<uint8_t>(c->head_dim, p, plan, stream)
+                                    : by_size<float>(c->head_dim, p, plan, stream);
 }
 
 }  // namespace kv

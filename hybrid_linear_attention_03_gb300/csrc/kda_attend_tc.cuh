@@ -391,18 +391,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // [num_pages * num_kv_heads][page_size][head_dim]; a box is a tile's part of
 // one page and head (64 channels of it for bf16), swizzled over its row of 128
-// or 64 bytes.
+// or 64 bytes.  Heads of 16 or 32 channels fill the first of a box's 64 (the
+// copy fills the others with zeros, which add nothing to a product).
 inline bool page_map(CUtensorMap *m, const void *base, const kda_kv_cache *c, bool e4m3) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t esize = e4m3 ? 1 : 2, D = cuuint64_t(c->head_dim), P = cuuint64_t(c->page_size);
     const cuuint64_t dims[3] = {D, P, cuuint64_t(c->num_pages) * cuuint64_t(c->num_kv_heads)};
     const cuuint64_t strides[2] = {D * esize, D * P * esize};
-    const cuuint32_t box[3] = {cuuint32_t(e4m3 ? c->head_dim : 64), cuuint32_t(c->page_size < KT ? c->page_size : KT), 1u};
+    const int image = c->head_dim < 64 ? 64 : c->head_dim;
+    const cuuint32_t box[3] = {cuuint32_t(e4m3 ? image : 64), cuuint32_t(c->page_size < KT ? c->page_size : KT), 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              e4m3 && c->head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              e4m3 && image == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -107,6 +107,8 @@ template <bool kByKeys> __device__ __forceinline__ int side_tile(int s, int v) {
 // Adds the value rows that were taken out of a tile to O, for the rows that see
 // them (a row's weight is read back from its bf16 place over the scores).  Rare,
 // so short rather than fast.  Whole warp.
+// Channels of a head: images of 64 also hold heads of 16 and 32.
+template <int D> __device__ __forceinline__ int head_dim(const AttendParams &p) { return D == 64 ? p.dim : D; }
 template <int D, bool kE4m3>
 __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it, int kb, int lim, const uint32_t *odd,
                                           uint32_t t_s, uint32_t t_o, bool fresh) {
@@ -115,6 +117,7 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
         for (int c = 0; c < D; c += 16) tmem_st16(t_o + uint32_t(c), z);
         tmem_wait_st();
     }
+    const int dim = head_dim<D>(p);
     for (int g = 0; g < KH / 32; ++g) {
         for (uint32_t left = odd[g]; left; left &= left - 1) {
             const int c = g * 32 + __ffs(left) - 1, j = kb + c;
@@ -124,7 +127,7 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
             const int page = load_page(p.b, it.n, j);
             const size_t vec = ((size_t(max(page, 0)) * size_t(p.hkv) + size_t(it.h)) << p.b.page_shift) +
                                size_t(j & ((1 << p.b.page_shift) - 1));
-            for (int ch = 0; ch < D; ch += 16) {
+            for (int ch = 0; ch < dim; ch += 16) {
                 float o[16];
                 tmem_ld16(t_o + uint32_t(ch), o);
                 tmem_wait_ld();
@@ -133,9 +136,9 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
                     for (int i = 0; i < 16; ++i) {
                         float val;
                         if constexpr (kE4m3)
-                            val = unpack_e4m3(static_cast<const uint8_t *>(p.pv)[vec * D + ch + i]).x * exp2_biased(p.sv[vec]);
+                            val = unpack_e4m3(static_cast<const uint8_t *>(p.pv)[vec * size_t(dim) + ch + i]).x * exp2_biased(p.sv[vec]);
                         else
-                            val = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.pv)[vec * D + ch + i]);
+                            val = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.pv)[vec * size_t(dim) + ch + i]);
                         o[i] = fmaf(w, val, o[i]);
                     }
                 }
@@ -340,11 +343,12 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
                     const bool whole = it.whole(), writes = r < it.rows;
                     const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | uintptr_t(p.out_stride * 2)) & 31) == 0;
-                    float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * (D + 2);
+                    const int dim = head_dim<D>(p);
+                    float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * size_t(dim + 2);
                     __nv_bfloat16 *dst =
-                        static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p.group, p.out_stride, D);
+                        static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p.group, p.out_stride, dim);
 #pragma unroll 2
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = 0; c < dim; c += 16) {
                         float o[16];
                         tmem_ld16(t_o + uint32_t(c), o);
                         if (kByKeys && nv_other > 0) {
@@ -373,12 +377,12 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                                 uint32_t w[8];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(o[i + e]);
-                                store32(data + size_t(r) * D + c + i, w);
+                                store32(data + size_t(r) * size_t(dim) + c + i, w);
                             }
                         }
                     }
                     if (!whole) {
-                        if (writes) data[BM * D + r] = ref, data[BM * D + BM + r] = l;
+                        if (writes) data[BM * dim + r] = ref, data[BM * dim + BM + r] = l;
                         if (s == 0 && row == 0) p.parts[2 * cta + it.slot()] = it.part();
                     }
                 }
@@ -517,12 +521,12 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     if (side_tiles<kByKeys>(it, s) == 0) continue;
                     unsigned char *q_img = smem + s * C::kQBytes;
                     constexpr int CPR = D / 8, RPP = kRowThreads / CPR;  // 16-byte pieces of a row, rows a pass
-                    const int c = qt % CPR;
+                    const int c = qt % CPR, dim = head_dim<D>(p);
                     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
                     auto row_at = [&](int row) {  // this thread's piece of a row of the item
-                        return q + it.at(min((kByKeys ? 0 : s * kSideRows) + row, it.rows - 1), p.group, p.q_stride, D);
+                        return q + it.at(min((kByKeys ? 0 : s * kSideRows) + row, it.rows - 1), p.group, p.q_stride, dim);
                     };
-                    auto is_there = [&](int row) { return (kByKeys ? 0 : s * kSideRows) + row < it.rows; };
+                    auto is_there = [&](int row) { return (kByKeys ? 0 : s * kSideRows) + row < it.rows && c * 8 < dim; };
                     auto wait_image = [&] {  // the last item's scores have read it
                         if (w == 0) wait_for(ok, &ms.q_free[s], (n_q[s] & 1) ^ 1, err);
                         meet();
@@ -630,14 +634,14 @@ kda_status by_type(const kda_kv_cache *c, AttendParams &p, const AttendPlan &pla
 
 bool tile_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
     const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
-    if (c->act != KDA_BF16 || (c->head_dim != 64 && c->head_dim != 128)) return false;
+    if (c->act != KDA_BF16) return false;
     plan->bm = rows <= kSideRows ? kSideRows : 2 * kSideRows;
     plan->n_cta = sm_count();
     return true;
 }
 
 kda_status tile_launch(const kda_kv_cache *c, AttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
-    return c->head_dim == 64 ? by_type<64>(c, p, plan, stream) : by_type<128>(c, p, plan, stream);
+    return c->head_dim <= 64 ? by_type<64>(c, p, plan, stream) : by_type<128>(c, p, plan, stream);
 }
 
 }  // namespace kv
