@@ -53,7 +53,7 @@ struct AttendParams {
     int32_t hq, hkv, group, dim;
     int32_t tile_tokens;  // TT
     int32_t key_step;     // keys per step; cut points are multiples of it
-    int32_t item_cost;    // what an item costs beside its keys
+    int32_t item_cost;    // what an item costs beside its keys, key_step or more
     int32_t min_keys;     // a CTA's piece is at least this long, key_step or more (fewer CTAs take part in a small call)
     float scale_log2;     // scale * log2(e)
     Part *parts;          // [C][2]: the CTA's first part (of an item begun before) and its last

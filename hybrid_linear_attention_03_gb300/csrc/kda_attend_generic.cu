@@ -243,6 +243,8 @@ kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) 
     const int smem = int(sizeof(Smem<BM, D>));
     if (!allow_smem<attend_generic_kernel<Kv, BM, D>>(smem)) return KDA_ERR_CUDA;
     p.key_step = KS;
+    // Measured at 0, 64, 128, 256, 1024: 16 sequences of 30 to 60 new tokens behind 100 to 1500, heads of 128,
+    // take 512, 460, 478, 495, 630 us.
     p.item_cost = KS;
     p.min_keys = 2 * KS;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);

@@ -1,6 +1,8 @@
 // kda_attend_tile.cu -- kda_kv_attend for bf16 rows on the tensor cores: the
-// kernel of chunks, verifies and wide groups (more than 16 rows an item,
-// head sizes 64 and 128).
+// kernel of chunks, verifies and wide groups (all bf16 calls but those of few
+// rows, see kda_attend_few.cu and kda_attend_lanes.cu).  Heads of 16 and 32
+// channels are worked on as if they had 64, the others zero: the products cost
+// more than they need, but the softmax bounds such calls.
 //
 // Softmax in one pass, as in kda_attend_generic.cu: scores X = Q K^T (128 rows
 // x 128 keys) land in tensor memory, one thread per row turns them into weights
@@ -23,9 +25,8 @@
 // sums and O stay in 32 bits.
 //
 // Warps: 0-3 side 0, 4-7 side 1 (a thread a row); 8 and 9 issue a side's
-// products each; 10 and 11 fetch
-// pages by TMA into rings of key and value tiles; 12-15 bring the rows of Q and
-// look value tiles over (below).
+// products each; 10 and 11 fetch pages by TMA into rings of key and value tiles;
+// 12-15 bring the rows of Q and look value tiles over (below).
 //
 // e4m3 pages: keys go to the tensor cores as they are, against Q as the sum of
 // two e4m3 terms, which is Q itself (as many cycles as bf16 products take), and
@@ -36,6 +37,15 @@
 // product.  So in the few tiles where some row does not see some key, warps
 // 12-15 zero the rows of absent keys in the value tile, and take non-finite
 // value rows out of it; the row threads that do see those add them one by one.
+//
+// What bounds it: the softmax threads' instructions (scale, compare, ex2, round,
+// add) take about as long as the products at head size 128, and longer below it;
+// the rest is what the two wait for each other.  Measured, 64 heads over 8 cache
+// heads of 128: a prompt of 8192 tokens 797 us (1380 TFLOP/s, 71 % of the measured
+// bf16 peak), 512 tokens behind 32256 412 us (68 %); in e4m3 pages the prompt takes
+// 1235 us, bound by the threads that widen values and by the second term of Q.  64
+// verifies of 8 tokens over 1000 to 8192 in e4m3 take 222 us (2.8 TB/s).  Heads of
+// 64: the prompt 753 us, bound by the softmax.
 #include "kda_attend_tc.cuh"
 
 namespace kda {
@@ -53,7 +63,10 @@ template <bool kE4m3> struct Warps {
     static_assert(8 * kSoftmax + 4 * kIssue + kRowWarps * kRows == (12 + kRowWarps) * kLaunch, "the split uses what the launch has");
 };
 constexpr float kRefSlack = 8.f;
-constexpr int kItemCost = 512;  // keys that take as long as an item's start and output
+// Keys that take as long as an item's start and output.  Measured at 0, 128, 256,
+// 512, 1024: 8 sequences of 300 to 700 new tokens behind 100 to 1500 take 237, 216,
+// 201, 183, 187 us, 64 verifies of 8 tokens there 86, 75, 69, 64, 63 us.
+constexpr int kItemCost = 512;
 
 template <int D, bool kE4m3, bool kByKeys> struct Cfg {
     static constexpr int kQBytes = kSideRows * D * 2;            // bf16, or two e4m3 terms
@@ -632,6 +645,9 @@ kda_status by_type(const kda_kv_cache *c, AttendParams &p, const AttendPlan &pla
 
 }  // namespace
 
+// Sides by keys up to a side's rows, by rows past it: 32 sequences of 4000 to 8192
+// tokens, 128 rows an item, take 145 us by keys and 153 by rows (e4m3 160 and 191),
+// 16 of them with 136 rows 138 and 107.
 bool tile_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
     const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
     if (c->act != KDA_BF16) return false;
