@@ -165,10 +165,12 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < N; ++c) l[c] = 0.f;
             named_sync<2, 128>();
+            int page = peek_page(p, it, it.k0, lane);
             for (int v = 0; v < nt; ++v, ++tile) {
                 const int kb = it.k0 + v * KT, j = kb + tid;
-                const uint32_t absent = absent_groups(p, it, kb, lane), t_s = tm + lanes + (tile & 1) * N;
+                const uint32_t absent = absent_groups(p, page), t_s = tm + lanes + (tile & 1) * N;
                 const bool check = partly_seen(it, kb, absent);
+                page = peek_page(p, it, kb + KT, lane);
                 int hidden = 0;  // rows before this one do not see the thread's key
                 if (check) {
                     hidden = max(j - first_lim, 0) * p.group;
@@ -446,7 +448,10 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.q_full), mbar_arrive(&ms.row_unit[n_it & 1]);
             ++n_it;
+            int page = peek_page(p, it, it.k0, lane);
             for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tile) {
+                const uint32_t absent = absent_groups(p, page);
+                page = peek_page(p, it, kb + KT, lane);
                 if (w == 0) {
                     if constexpr (kE4m3) {
                         wait_tile(ok, ms.raw_full, tile, err);
@@ -459,11 +464,11 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                 if (!ok) break;
                 unsigned char *dst = v_ring + tile % NV * C::kVBytes;
                 if constexpr (kE4m3) {
-                    widen_tile<D>(p, it, kb, raw_ring + tile % NR * C::kRawBytes, dst, ms.v_scale[tile % NR], w, lane,
+                    widen_tile<D>(p, it, kb, absent, raw_ring + tile % NR * C::kRawBytes, dst, ms.v_scale[tile % NR], w, lane,
                                   ms.odd[tile % kBars]);
                     if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                 } else {
-                    look_over_tile<D>(p, it, kb, dst, w, lane, ms.odd[tile % kBars]);
+                    look_over_tile<D>(it, kb, absent, dst, w, lane, ms.odd[tile % kBars]);
                     if (lane == 0) mbar_arrive(&ms.clean[tile % kBars]);
                 }
             }

@@ -215,11 +215,17 @@ struct TileMaps {
 };
 
 __device__ __forceinline__ int item_tiles(const Item &it) { return (it.k1 - it.k0 + KT - 1) / KT; }
-// Bit g: keys [kb + 16 g, kb + 16 g + 16) are in a page outside the cache.
-__device__ __forceinline__ uint32_t absent_groups(const AttendParams &p, const Item &it, int kb, int lane) {
-    bool bad = false;
-    if (lane < KT / 16 && kb + lane * 16 < it.k1) bad = load_page(p.b, it.n, kb + lane * 16) < 0;
-    return __ballot_sync(0xffffffffu, bad);
+// The table's entry for keys [kb + 16 lane, kb + 16 lane + 16) of the tile at kb (page 0 where there
+// are none).  Asked for a tile ahead: a look-up on the way took a fifth of the softmax's time.
+__device__ __forceinline__ int peek_page(const AttendParams &p, const Item &it, int kb, int lane) {
+    const int j = kb + lane * 16;
+    if (lane >= KT / 16 || j >= it.k1) return 0;
+    return p.b.table[size_t(it.n) * size_t(p.b.table_stride) + size_t(j >> p.b.page_shift)];
+}
+// Bit g: keys [kb + 16 g, kb + 16 g + 16) are in a page outside the cache (which the warps that
+// fetch pages report).
+__device__ __forceinline__ uint32_t absent_groups(const AttendParams &p, int page) {
+    return __ballot_sync(0xffffffffu, uint32_t(page) >= uint32_t(p.b.num_pages));
 }
 // Some row of the item does not see some key of the tile at kb.
 __device__ __forceinline__ bool partly_seen(const Item &it, int kb, uint32_t absent) {
@@ -287,12 +293,16 @@ __device__ __forceinline__ void fetch_pages(const AttendParams &p, const TileMap
     Item it = {};
     uint32_t t = 0;
     while (ok && walk.next(p, it)) {
+        auto page_at = [&](int kb) {
+            const int j = kb + lane * box;
+            return lane * box < KT && j < it.k1 ? load_page(p.b, it.n, j) : -1;
+        };
+        int next = page_at(it.k0);
         for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++t) {
+            const int page = next, line = (kb + lane * box) & (page_size - 1);
+            next = page_at(kb + KT);
             const Landing to_ring = land(t, values);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            const int j = kb + lane * box, line = j & (page_size - 1);
-            int page = -1;
-            if (lane * box < KT && j < it.k1) page = load_page(p.b, it.n, j);
             const int there = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box;
             const int plane = page * p.hkv + it.h;  // below 2^31 (checked on the host)
             if (lane == 0) mbar_arrive_expect_tx(to_ring.full, uint32_t(there * (kE4m3 ? D + 1 : 2 * D)));
@@ -320,8 +330,8 @@ __device__ __forceinline__ void fetch_pages(const AttendParams &p, const TileMap
 // Warp w of eight widens its 16 keys of a raw value tile, and looks them over
 // where some row does not see some key; odd: the tile's keys taken out.
 template <int D>
-__device__ __forceinline__ void widen_tile(const AttendParams &p, const Item &it, int kb, const unsigned char *raw,
-                                           unsigned char *dst, const uint8_t *scale, int w, int lane, uint32_t *odd) {
+__device__ __forceinline__ void widen_tile(const AttendParams &p, const Item &it, int kb, uint32_t absent,
+                                           const unsigned char *raw, unsigned char *dst, const uint8_t *scale, int w, int lane, uint32_t *odd) {
     using RP = RawPiece<D>;
     uint4 x[RP::kCount];
     float f[2];
@@ -339,7 +349,6 @@ __device__ __forceinline__ void widen_tile(const AttendParams &p, const Item &it
         *reinterpret_cast<uint4 *>(dst + r.to) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4 *>(dst + (r.to ^ 16u)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    const uint32_t absent = absent_groups(p, it, kb, lane);
     uint32_t out = 0;
     if (partly_seen(it, kb, absent)) {
         const Item copy = it;
@@ -352,9 +361,8 @@ __device__ __forceinline__ void widen_tile(const AttendParams &p, const Item &it
 }
 // Warp w of four looks over 32 keys of a bf16 value tile, likewise.
 template <int D>
-__device__ __forceinline__ void look_over_tile(const AttendParams &p, const Item &it, int kb, unsigned char *tile, int w,
-                                               int lane, uint32_t *odd) {
-    const uint32_t absent = absent_groups(p, it, kb, lane);
+__device__ __forceinline__ void look_over_tile(const Item &it, int kb, uint32_t absent, unsigned char *tile, int w, int lane,
+                                               uint32_t *odd) {
     uint32_t out = 0;
     if (partly_seen(it, kb, absent)) {
         // a lane looks over one value row, each at a bank of its own

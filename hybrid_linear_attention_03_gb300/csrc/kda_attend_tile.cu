@@ -241,9 +241,11 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     }
                     if (kByKeys || nv > 0) ++n_it;
                 }
+                int page = peek_page(p, it, it.k0 + side_tile<kByKeys>(s, 0) * KT, lane);
                 for (int v = 0; v < nv; ++v, ++n_s) {
                     const int t = side_tile<kByKeys>(s, v), kb = it.k0 + t * KT;
-                    const uint32_t absent = absent_groups(p, it, kb, lane);
+                    const uint32_t absent = absent_groups(p, page);
+                    page = peek_page(p, it, it.k0 + side_tile<kByKeys>(s, v + 1) * KT, lane);
                     const bool check = partly_seen(it, kb, absent);
                     const uint32_t tg = tile_base + uint32_t(t);
                     if constexpr (kE4m3) wait_tile(ok, ms.unit_full, tg, err);
@@ -586,7 +588,10 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.q_full[s]);
                 }
+                int page = peek_page(p, it, it.k0, lane);
                 for (int kb = it.k0; kb < it.k1 && ok; kb += KT, ++tile) {
+                    const uint32_t absent = absent_groups(p, page);
+                    page = peek_page(p, it, kb + KT, lane);
                     unsigned char *dst = v_ring + tile % NV * C::kVBytes;
                     if (w == 0) {
                         if constexpr (kE4m3) {
@@ -602,11 +607,11 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                         if (qt < KT) sc8.k_unit[tile % kUnits][qt] = exp2_biased(sc8.k[tile % NK][qt]);  // as numbers
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ms.unit_full[tile % kBars]), mbar_arrive(&ms.k_empty[tile % kBars]);
-                        widen_tile<D>(p, it, kb, raw_ring + tile % NR * C::kRawBytes, dst, sc8.v[tile % NR], w, lane,
+                        widen_tile<D>(p, it, kb, absent, raw_ring + tile % NR * C::kRawBytes, dst, sc8.v[tile % NR], w, lane,
                                       ms.odd[tile % kBars]);
                         if (lane == 0) mbar_arrive(&ms.v_full[tile % kBars]), mbar_arrive(&ms.raw_empty[tile % kBars]);
                     } else {
-                        look_over_tile<D>(p, it, kb, dst, w, lane, ms.odd[tile % kBars]);
+                        look_over_tile<D>(it, kb, absent, dst, w, lane, ms.odd[tile % kBars]);
                         if (lane == 0) mbar_arrive(&ms.clean[tile % kBars]);
                     }
                 }

@@ -24,7 +24,7 @@ struct BatchView {
 };
 
 // Positions are 32-bit, and a tile of keys may reach this far past the last one.
-constexpr int32_t kMaxPositions = 0x7fffff00;
+constexpr int32_t kMaxPositions = 0x7ffffc00;
 
 struct Seq {
     int row0, T, L;  // first row, new tokens, cache length with them

@@ -438,7 +438,7 @@ KDA_API kda_status kda_poll_device_error(kda_pool *pool, kda_stream_t stream, ui
  * Rows past cu_seqlens[n_seqs] are neither read nor written.
  * Device errors: a sequence whose tables are inconsistent (cu_seqlens
  * decreasing or past max_rows, more than max_new tokens, kv_lens below T_n or
- * past page_table's width or 2^31 - 256) sets KDA_DEVERR_META and its rows are
+ * past page_table's width or 2^31 - 1024) sets KDA_DEVERR_META and its rows are
  * left as they were; a page outside the cache sets KDA_DEVERR_PAGE_RANGE, and
  * its tokens are not written, read back as zeros, and are absent from the
  * attention.

@@ -546,7 +546,7 @@ def test_far_positions_and_absent_pages(new, hq, d, act, fmt):
 
 
 def test_longest_positions_are_refused():
-    """Past 2^31 - 256 tokens a tile's last positions would not be 32-bit numbers: the sequence is left alone."""
+    """Past 2^31 - 1024 tokens a tile's last positions would not be 32-bit numbers: the sequence is left alone."""
     page = 128
     b = R.Batch([1, 1], [100, 50], 2, 1, 64, page, BF, "act", seed=53)
     cache = fill_cache(b)
