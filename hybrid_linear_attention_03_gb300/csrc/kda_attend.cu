@@ -93,8 +93,9 @@ __global__ void __launch_bounds__(kCombineThreads) attend_combine_kernel(const _
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
     if (ch < D) {
-        Act *dst = static_cast<Act *>(p.out) + size_t(first.row + r / p.group) * size_t(p.out_stride) +
-                   size_t(first.h * p.group + r % p.group) * D + ch;
+        const int t = p.token_of(r);
+        Act *dst = static_cast<Act *>(p.out) + size_t(first.row + t) * size_t(p.out_stride) +
+                   size_t(first.h * p.group + r - t * p.group) * D + ch;
 #pragma unroll
         for (int e = 0; e < CPL; ++e) dst[e] = from_f32<Act>(acc[e] * inv);
     }
@@ -150,6 +151,7 @@ kda_status launch_attend(const kda_kv_cache *c, const kda_attn_io *io, const kda
     p.q = io->q, p.out = io->out, p.q_stride = io->q_stride, p.out_stride = io->out_stride;
     p.pk = c->k, p.pv = c->v, p.sk = c->k_scale, p.sv = c->v_scale;
     p.hq = c->num_heads, p.hkv = c->num_kv_heads, p.group = c->num_heads / c->num_kv_heads, p.dim = c->head_dim;
+    p.group_inv = (65536u + uint32_t(p.group) - 1) / uint32_t(p.group);
     p.tile_tokens = plan.bm / p.group;
     p.scale_log2 = io->scale * kLog2e;
     p.parts = static_cast<Part *>(workspace);

@@ -58,6 +58,9 @@ struct AttendParams {
     float scale_log2;     // scale * log2(e)
     Part *parts;          // [C][2]: the CTA's first part (of an item begun before) and its last
     float *part_data;     // [C][2][BM * (D + 2)]: out [BM][D], then row maxima [BM], then row sums [BM]
+    uint32_t group_inv;   // ceil(2^16 / group)
+    // r / group, exact for the rows of a tile: r < 256 and group <= 64 leave the error below 1 / group
+    __device__ __forceinline__ int token_of(int r) const { return int(uint32_t(r) * group_inv >> 16); }
 };
 
 // Keys of tile i's last row: how far the item reaches.
@@ -172,8 +175,9 @@ struct Item {
     __device__ __forceinline__ int slot() const { return k0 == 0 ? 1 : 0; }
     __device__ __forceinline__ Part part() const { return Part{k1 == keys ? 2 : 1, row0 + tok0, rows, h}; }
     // element offset of row r's channels in a row tensor
-    __device__ __forceinline__ size_t at(int r, int group, long long stride, int D) const {
-        return size_t(row0 + tok0 + r / group) * size_t(stride) + size_t(h * group + r % group) * size_t(D);
+    __device__ __forceinline__ size_t at(int r, const AttendParams &p, long long stride, int D) const {
+        const int t = p.token_of(r);
+        return size_t(row0 + tok0 + t) * size_t(stride) + size_t(h * p.group + r - t * p.group) * size_t(D);
     }
 };
 

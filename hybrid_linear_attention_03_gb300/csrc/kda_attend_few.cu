@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
             float o[N];
             tmem_ld16(t_o, o);
             tmem_wait_ld();
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + it.at(0, p.group, p.out_stride, D) + tid;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + it.at(0, p, p.out_stride, D) + tid;
             int g = 0;  // query head of the group
 #pragma unroll
             for (int r = 0; r < N; ++r) {
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
 #pragma unroll
             for (int b = 0; b < N / RPP; ++b) {
                 const int row = qt / CPR + b * RPP;
-                raw[b] = row < it.rows ? *reinterpret_cast<const uint4 *>(q + it.at(row, p.group, p.q_stride, D))
+                raw[b] = row < it.rows ? *reinterpret_cast<const uint4 *>(q + it.at(row, p, p.q_stride, D))
                                        : make_uint4(0, 0, 0, 0);
             }
             if (w == 0) wait_for(ok, &ms.q_free, (n_it & 1) ^ 1, err);  // the last item's scores have read it

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
         for (int i = tid; i < BM * D / 4; i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < it.rows) load4<float>(static_cast<const float *>(p.q) + it.at(r, p.group, p.q_stride, D) + c, x);
+            if (r < it.rows) load4<float>(static_cast<const float *>(p.q) + it.at(r, p, p.q_stride, D) + c, x);
             *reinterpret_cast<float4 *>(&s.q[r][c]) =
                 make_float4(x[0] * p.scale_log2, x[1] * p.scale_log2, x[2] * p.scale_log2, x[3] * p.scale_log2);
         }
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
 #pragma unroll
         for (int a = 0; a < RT; ++a) {
             const int r = ty * RT + a;
-            lim[a] = r < it.rows ? it.ctx + it.tok0 + r / p.group : -1;
+            lim[a] = r < it.rows ? it.ctx + it.tok0 + p.token_of(r) : -1;
         }
         for (int kb = it.k0; kb < it.k1; kb += KS) {
             __syncthreads();  // the previous step's keys and values are done with
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
             const int r = ty * RT + a;
             if (r >= it.rows) continue;
             const float inv = l[a] > 0.f || l[a] != l[a] ? 1.0f / l[a] : 0.f;
-            float *dst = static_cast<float *>(p.out) + it.at(r, p.group, p.out_stride, D);
+            float *dst = static_cast<float *>(p.out) + it.at(r, p, p.out_stride, D);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const int ch = c / CV * 16 * CV + tx * CV + c % CV;

@@ -101,10 +101,10 @@ __global__ void __launch_bounds__(kThreads, 2) attend_lanes_kernel(const __grid_
         for (int a = 0; a < RW; ++a) {
             const int r = set * RW + a;
             m[a] = -INFINITY, l[a] = 0.f;
-            lim[a] = r < it.rows ? it.ctx + it.tok0 + r / p.group : -1;
+            lim[a] = r < it.rows ? it.ctx + it.tok0 + p.token_of(r) : -1;
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) q[a][i] = o[a][i] = make_float2(0.f, 0.f);
-            if (r < it.rows) load_channels(static_cast<const Act *>(p.q) + it.at(r, p.group, p.q_stride, D) + c0, q[a]);
+            if (r < it.rows) load_channels(static_cast<const Act *>(p.q) + it.at(r, p, p.q_stride, D) + c0, q[a]);
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) q[a][i].x *= p.scale_log2, q[a][i].y *= p.scale_log2;
         }
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_lanes_kernel(const __grid_
             }
             if (whole) {
                 const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-                static_cast<Act *>(p.out)[it.at(r, p.group, p.out_stride, D) + ch] = from_f32<Act>(out * inv);
+                static_cast<Act *>(p.out)[it.at(r, p, p.out_stride, D) + ch] = from_f32<Act>(out * inv);
             } else {
                 data[i] = out;
                 if (ch == 0) data[R * D + r] = top, data[R * D + R + r] = sum;

@@ -17,10 +17,15 @@
 // while the threads of a side turn one half into weights, the other half's
 // product and the scores that follow in its place are under way, so the threads
 // seldom wait and the tensor cores seldom idle.
-// ref is the row's maximum so far, but only moved (and O and the sums scaled
-// by 2^(ref - ref')) when a tile exceeds it by more than 8: weights then reach
-// 2^8 at most, which costs no precision in bf16 and fp32, and most tiles leave
-// O in tensor memory untouched.  P is rounded to bf16 (2^-9 relative, the
+// ref is the row's maximum at the time it was last moved.  bf16 pages: it moves
+// (and O and the sums are scaled by 2^(ref - ref')) when the weights of a half of
+// a tile sum to more than 2^16, which shows once they are formed; then they are
+// formed again.  e4m3 pages: when a half's maximum exceeds it by more than 8.
+// Weights of 2^16 cost no precision in bf16 and fp32, so most tiles leave O in
+// tensor memory untouched, and in bf16 need no maximum at all (the 8192-token
+// prompt with heads of 64: 653 us against 720 with a maximum for each half; with
+// heads of 128 783 either way; in e4m3 the registers are short for it, and verifies
+// take 261 us against 224).  P is rounded to bf16 (2^-9 relative, the
 // size of the output's own rounding, and not correlated between keys); scores,
 // sums and O stay in 32 bits.
 //
@@ -62,7 +67,8 @@ template <bool kE4m3> struct Warps {
     static constexpr int kSoftmax = kE4m3 ? 144 : 200, kIssue = kE4m3 ? 48 : 56, kRows = kE4m3 ? 72 : 56;
     static_assert(8 * kSoftmax + 4 * kIssue + kRowWarps * kRows == (12 + kRowWarps) * kLaunch, "the split uses what the launch has");
 };
-constexpr float kRefSlack = 8.f;
+// When a row's reference moves (see above): a maximum this far above it, or a sum of a half's weights.
+constexpr float kRefSlack = 8.f, kSumLimit = 65536.f;
 // Keys that take as long as an item's start and output.  Measured at 0, 128, 256,
 // 512, 1024: 8 sequences of 300 to 700 new tokens behind 100 to 1500 take 237, 216,
 // 201, 183, 187 us, 64 verifies of 8 tokens there 86, 75, 69, 64, 63 us.
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
             };
             while (walk.next(p, it)) {
                 const int nv = side_tiles<kByKeys>(it, s);
-                const int lim = it.ctx + it.tok0 + min(r, it.rows - 1) / p.group;  // last key this row sees
+                const int lim = it.ctx + it.tok0 + p.token_of(min(r, it.rows - 1));  // last key this row sees
                 const bool live = r - lane < it.rows;  // this warp has rows of the item
                 float ref = -INFINITY, l = 0.f, scale = p.scale_log2;
                 if constexpr (kE4m3) {
@@ -277,16 +283,18 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                                 for (int c = 0; c < KH; ++c)
                                     if (kh + c > lim || (absent >> (h * (KH / 16) + c / 16) & 1)) x[c] = -INFINITY;
                             }
-                            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                            for (int c = 4; c < KH; c += 8)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    mx[i] = c + 4 + i < KH ? fmaxf(fmaxf(mx[i], x[c + i]), x[c + 4 + i]) : fmaxf(mx[i], x[c + i]);
-                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-                            const bool move = top > ref + kRefSlack;
                             const bool started = v > 0 || h > 0;  // O is new with the first product
-                            if (__any_sync(0xffffffffu, move)) {
+                            // the reference moves up to a row's maximum in x, where that is more than `slack` above it
+                            auto move_ref = [&](float slack) {
+                                float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                                for (int c = 4; c < KH; c += 8)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        mx[i] = c + 4 + i < KH ? fmaxf(fmaxf(mx[i], x[c + i]), x[c + 4 + i]) : fmaxf(mx[i], x[c + i]);
+                                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                                const bool move = top > ref + slack;
+                                if (!__any_sync(0xffffffffu, move)) return;
                                 const float to = move ? top : ref, f = move ? ex2(ref - to) : 1.f;
                                 if (started) {
                                     wait_o(h == 0 ? n_s - 1 : n_s, h ^ 1);
@@ -302,24 +310,41 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                                 }
                                 l *= f;
                                 ref = to;
-                            }
-                            const float base = ref == -INFINITY ? 0.f : ref;
-                            const float2 sc = make_float2(scale, scale), sh = make_float2(-base, -base);
-                            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                            };
+                            // weights to the place of the scores; their sum
+                            auto weigh = [&] {
+                                const float base = ref == -INFINITY ? 0.f : ref;
+                                const float2 sc = make_float2(scale, scale), sh = make_float2(-base, -base);
+                                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                            for (int c = 0; c < KH; c += 32) {
-                                uint32_t w[16];
+                                for (int c = 0; c < KH; c += 32) {
+                                    uint32_t w[16];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    float2 e = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), sc, sh);
-                                    e.x = ex2(e.x), e.y = ex2(e.y);
-                                    sum[i & 1] = add2(sum[i & 1], e);
-                                    w[i] = pack_bf16(e.x, e.y);
+                                    for (int i = 0; i < 16; ++i) {
+                                        float2 e = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), sc, sh);
+                                        e.x = ex2(e.x), e.y = ex2(e.y);
+                                        sum[i & 1] = add2(sum[i & 1], e);
+                                        w[i] = pack_bf16(e.x, e.y);
+                                    }
+                                    tmem_st16u(t_h + uint32_t(c / 2), w);
                                 }
-                                tmem_st16u(t_h + uint32_t(c / 2), w);
+                                return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                            };
+                            float sum_h;
+                            if constexpr (kE4m3) {
+                                move_ref(kRefSlack);
+                                sum_h = weigh();
+                            } else {
+                                sum_h = weigh();
+                                // past the limit (or NaN), or a row without a reference yet
+                                if (__any_sync(0xffffffffu, !(sum_h <= kSumLimit) || ref == -INFINITY)) {
+                                    move_ref(0.f);
+                                    tmem_wait_st();
+                                    sum_h = weigh();
+                                }
                             }
-                            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                             tmem_wait_st();
+                            l += sum_h;
                             if (check) {
                                 wait_tile(ok, kE4m3 ? ms.v_full : ms.clean, tg, err);
                                 __syncwarp();
@@ -361,7 +386,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     const int dim = head_dim<D>(p);
                     float *data = p.part_data + (size_t(cta) * 2 + it.slot()) * size_t(BM) * size_t(dim + 2);
                     __nv_bfloat16 *dst =
-                        static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p.group, p.out_stride, dim);
+                        static_cast<__nv_bfloat16 *>(p.out) + it.at(min(r, it.rows - 1), p, p.out_stride, dim);
 #pragma unroll 2
                     for (int c = 0; c < dim; c += 16) {
                         float o[16];
@@ -539,7 +564,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                     const int c = qt % CPR, dim = head_dim<D>(p);
                     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;
                     auto row_at = [&](int row) {  // this thread's piece of a row of the item
-                        return q + it.at(min((kByKeys ? 0 : s * kSideRows) + row, it.rows - 1), p.group, p.q_stride, dim);
+                        return q + it.at(min((kByKeys ? 0 : s * kSideRows) + row, it.rows - 1), p, p.q_stride, dim);
                     };
                     auto is_there = [&](int row) { return (kByKeys ? 0 : s * kSideRows) + row < it.rows && c * 8 < dim; };
                     auto wait_image = [&] {  // the last item's scores have read it
