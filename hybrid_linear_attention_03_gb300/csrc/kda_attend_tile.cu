@@ -169,6 +169,25 @@ __device__ __noinline__ void add_odd_rows(const AttendParams &p, const Item &it,
     }
 }
 
+// The scales of 32 keys, all loads in flight together (one by one, as they are used,
+// they took longer than the exponentials), and 32 scores times them.
+__device__ __forceinline__ void load_units(float4 (&u)[8], const float *src) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u[i].x), "=f"(u[i].y), "=f"(u[i].z), "=f"(u[i].w)
+                     : "r"(smem_u32(src + 4 * i))
+                     : "memory");
+}
+__device__ __forceinline__ void scale_keys(float *x, const float4 (&u)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(u[i].x, u[i].y));
+        const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(u[i].z, u[i].w));
+        x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
+    }
+}
+
 template <int D, bool kE4m3, bool kByKeys>
 __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
     attend_tile_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TileMaps maps) {
@@ -268,15 +287,13 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                             float x[KH];
 #pragma unroll
                             for (int c = 0; c < KH; c += 32) tmem_ld32(t_h + uint32_t(c), x + c);
+                            float4 unit[8];
+                            if constexpr (kE4m3) load_units(unit, &sc8.k_unit[tg % kUnits][h * KH]);
                             tmem_wait_ld();
                             if constexpr (kE4m3) {
-#pragma unroll
-                                for (int c = 0; c < KH; c += 4) {
-                                    const float4 u = *reinterpret_cast<const float4 *>(&sc8.k_unit[tg % kUnits][h * KH + c]);
-                                    const float2 a = mul2(make_float2(x[c], x[c + 1]), make_float2(u.x, u.y));
-                                    const float2 b = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(u.z, u.w));
-                                    x[c] = a.x, x[c + 1] = a.y, x[c + 2] = b.x, x[c + 3] = b.y;
-                                }
+                                scale_keys(&x[0], unit);
+                                load_units(unit, &sc8.k_unit[tg % kUnits][h * KH + 32]);
+                                scale_keys(&x[32], unit);
                             }
                             if (check) {
 #pragma unroll
