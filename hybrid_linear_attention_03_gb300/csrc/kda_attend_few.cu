@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
         mbar_init(&ms.q_full, C::kRowWarps), mbar_init(&ms.q_free, 1), mbar_init(&ms.done, 1);
         fence_mbar_init();
     }
+    if (tid == 32) prefetch_maps(maps);
     if (warp == kMma) tmem_alloc(&ms.tmem, C::kColumns);
     wait_prior_kernel();
     allow_next_kernel();

@@ -213,6 +213,11 @@ __device__ __forceinline__ bool any_odd(const uint32_t *odd) { return (odd[0] | 
 struct TileMaps {
     CUtensorMap k, v;
 };
+// Has a kernel's maps fetched while it sets up.
+__device__ __forceinline__ void prefetch_maps(const TileMaps &m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&m.k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&m.v) : "memory");
+}
 
 __device__ __forceinline__ int item_tiles(const Item &it) { return (it.k1 - it.k0 + KT - 1) / KT; }
 // The table's entry for keys [kb + 16 lane, kb + 16 lane + 16) of the tile at kb (page 0 where there

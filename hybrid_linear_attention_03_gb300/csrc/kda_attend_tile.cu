@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
         }
         fence_mbar_init();
     }
+    if (tid == 32) prefetch_maps(maps);
     if (warp == 8) tmem_alloc(&ms.tmem, 512);
     wait_prior_kernel();
     allow_next_kernel();

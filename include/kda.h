@@ -434,7 +434,8 @@ KDA_API kda_status kda_poll_device_error(kda_pool *pool, kda_stream_t stream, ui
  * the rows [cu_seqlens[n], cu_seqlens[n+1]), T_n of them, and row
  * cu_seqlens[n] + t is its token at position kv_lens[n] - T_n + t, so kv_lens
  * counts the call's own tokens.  T_n may be 0.  All three tables are DEVICE
- * arrays, read when the call runs, so the calls can sit in a CUDA graph.
+ * arrays, read when the call runs (and not to be written while it does), so
+ * the calls can sit in a CUDA graph.
  * Rows past cu_seqlens[n_seqs] are neither read nor written.
  * Device errors: a sequence whose tables are inconsistent (cu_seqlens
  * decreasing or past max_rows, more than max_new tokens, kv_lens below T_n or
