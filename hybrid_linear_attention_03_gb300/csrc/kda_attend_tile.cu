@@ -43,14 +43,15 @@
 // 12-15 zero the rows of absent keys in the value tile, and take non-finite
 // value rows out of it; the row threads that do see those add them one by one.
 //
-// What bounds it: the softmax threads' instructions (scale, compare, ex2, round,
-// add) take about as long as the products at head size 128, and longer below it;
-// the rest is what the two wait for each other.  Measured, 64 heads over 8 cache
-// heads of 128: a prompt of 8192 tokens 797 us (1380 TFLOP/s, 71 % of the measured
-// bf16 peak), 512 tokens behind 32256 412 us (68 %); in e4m3 pages the prompt takes
-// 1235 us, bound by the threads that widen values and by the second term of Q.  64
-// verifies of 8 tokens over 1000 to 8192 in e4m3 take 222 us (2.8 TB/s).  Heads of
-// 64: the prompt 753 us, bound by the softmax.
+// What bounds it: a half's products wait for its weights and its weights for its
+// scores; two sides with two halves each cover most of that, and tensor memory has
+// no columns for more (heads of 128: the tensor pipe is active in 62 % of the
+// cycles; heads of 64: the softmax threads are the slower part).  Measured, 64
+// heads over 8 cache heads of 128: a prompt of 8192 tokens 775 us (1420 TFLOP/s,
+// 73 % of the measured bf16 peak), 512 tokens behind 32256 410 us (69 %); in e4m3
+// pages the prompt takes 1106 us, bound by the threads that widen values and scale
+// scores and by the second term of Q.  64 verifies of 8 tokens over 1000 to 8192
+// in e4m3 take 208 us (3.0 TB/s).  Heads of 64: the prompt 659 us.
 #include "kda_attend_tc.cuh"
 
 namespace kda {
