@@ -727,7 +727,7 @@ def test_graph_replay_reads_new_tables():
 
 
 def test_calls_on_another_stream_and_profile():
-    b = R.Batch([9, 1], [90, 70], 4, 2, 64, 32, BF, "e4m3", seed=37)
+    b = R.Batch([9, 1], [190, 70], 4, 2, 64, 32, BF, "e4m3", seed=37)
     cache = fill_cache(b)
     q = b.randn(b.rows, 4).cuda()
     out = torch.empty_like(q)
@@ -740,6 +740,27 @@ def test_calls_on_another_stream_and_profile():
     st.synchronize()
     assert prof["kv_attend"][0] == 1 and prof["kv_combine"][0] == 1
     check_attend(b, q, out, cache, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("act,fmt,d,group,new", [(BF, "act", 128, 8, 1), (BF, "e4m3", 128, 4, 4), (BF, "act", 64, 8, 100),
+                                                 (BF, "e4m3", 32, 8, 3), (F32, "act", 64, 1, 1), (F32, "e4m3", 128, 2, 30)])
+def test_one_key_step_is_one_launch(act, fmt, d, group, new):
+    """A page table of one key step: no item is cut, so there is nothing to join."""
+    page = 32 if act == F32 and new == 1 else 64
+    b = R.Batch([new] * 3, [page - 1 if new < 30 else page, page, new] if new <= page else [new] * 3, group, 1, d,
+                page if new <= page else 128, act, fmt, seed=79)
+    cache = fill_cache(b)
+    q = b.randn(b.rows, group).cuda()
+    out = torch.full_like(q, 9.0)
+    ws = b.workspace(0xFF)
+    torch.cuda.synchronize()
+    kda.kda_profile_start(16)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, ws)
+    prof = kda.kda_profile_stop()
+    torch.cuda.synchronize()
+    assert prof["kv_attend"][0] == 1 and prof["kv_combine"][0] == 0
+    no_device_error(b.kv)
+    check_attend(b, q, out, cache, d ** -0.5)
 
 
 def test_shared_pages():
