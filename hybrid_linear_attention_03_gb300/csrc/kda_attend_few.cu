@@ -506,6 +506,8 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                 if (w == 0) wait_for(ok, &ms.q_free, (n_it & 1) ^ 1, err);  // the last item's scores have read it
                 meet();
                 if (!ok) break;
+                int e[N / RPP];
+                if constexpr (kE4m3) row_exponents<CPR>(raw, e);
 #pragma unroll
                 for (int b = 0; b < N / RPP; ++b) {
                     const int row = qt / CPR + b * RPP;
@@ -514,7 +516,8 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                         // a row as 2^e (q1 + q2): e4m3 keeps 4 significant bits, so q1 and what q1 leaves
                         // hold all 8 of a bf16 (down to 2^-18 of the row's largest value)
                         uint32_t w1[2], w2[2];
-                        unit = exp2_biased(split_row<CPR>(raw[b], w1, w2));
+                        split_row(raw[b], e[b], w1, w2);
+                        unit = exp2_biased(e[b] < 0 ? 127 : e[b]);
                         const uint32_t at = row8_piece<D>(row, c >> 1) + uint32_t(c & 1) * 8u;
                         *reinterpret_cast<uint2 *>(smem + at) = make_uint2(w1[0], w1[1]);
                         *reinterpret_cast<uint2 *>(smem + N * D + at) = make_uint2(w2[0], w2[1]);

@@ -137,20 +137,29 @@ __device__ __forceinline__ void widen_e4m3(const uint4 &q, float f, uint32_t (&o
         o[i] = pack_bf16(t.x, t.y);
     }
 }
-// Eight bf16 of a row of Q, of which kLanes neighbouring lanes hold one row, as
-// two e4m3 terms times a power of two; returns its biased exponent.
-template <int kLanes> __device__ __forceinline__ int split_row(const uint4 &raw, uint32_t (&w1)[2], uint32_t (&w2)[2]) {
+// Biased exponents for kB rows of Q, of each of which kLanes neighbouring lanes
+// hold eight bf16 a piece; -1 for a row with an infinity or NaN.  The rows'
+// shuffles go by turns, so that they do not wait for each other.
+template <int kLanes, int kB> __device__ __forceinline__ void row_exponents(const uint4 (&raw)[kB], int (&e)[kB]) {
+    uint32_t m[kB];  // the largest magnitude as a bf16 pattern
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+        const uint32_t t = __vmaxu2(__vmaxu2(raw[b].x & 0x7fff7fffu, raw[b].y & 0x7fff7fffu),
+                                    __vmaxu2(raw[b].z & 0x7fff7fffu, raw[b].w & 0x7fff7fffu));
+        m[b] = max(t & 0xffffu, t >> 16);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int b = 0; b < kB; ++b) m[b] = max(m[b], __shfl_xor_sync(0xffffffffu, m[b], o));
+#pragma unroll
+    for (int b = 0; b < kB; ++b) e[b] = m[b] >= 0x7f80u ? -1 : max(scale_exponent(__uint_as_float(m[b] << 16)), 1);
+}
+// Eight bf16 of a row with that exponent as two e4m3 terms times its power of two
+// (a row with infinities or NaN as NaN).
+__device__ __forceinline__ void split_row(const uint4 &raw, int e, uint32_t (&w1)[2], uint32_t (&w2)[2]) {
     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    // the largest magnitude as a bf16 pattern, of finite values (a row with others is NaN all the same)
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, in[i] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool odd = m >= 0x7f80u;
-    const int e = odd ? 127 : max(scale_exponent(__uint_as_float(m << 16)), 1);
-    const float f = odd ? NAN : exp2_neg_biased(e);
+    const float f = e < 0 ? NAN : exp2_neg_biased(e);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float a = __uint_as_float(in[i] << 16) * f, b = __uint_as_float(in[i] & 0xffff0000u) * f;
@@ -160,7 +169,6 @@ template <int kLanes> __device__ __forceinline__ int split_row(const uint4 &raw,
         if (i % 2 == 0) w1[i / 2] = h1, w2[i / 2] = h2;
         else w1[i / 2] |= uint32_t(h1) << 16, w2[i / 2] |= uint32_t(h2) << 16;
     }
-    return e;
 }
 // Bit 7 of a byte is set where one of the 16 codes is NaN.
 __device__ __forceinline__ uint32_t nan_codes(const uint4 &q) {

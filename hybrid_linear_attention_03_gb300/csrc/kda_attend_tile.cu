@@ -604,15 +604,17 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                             }
                             if (r0 < RPP) wait_image();
                             if (!ok) break;
+                            int e[kBatch];
+                            row_exponents<CPR>(raw, e);
 #pragma unroll
                             for (int b = 0; b < kBatch; ++b) {
                                 const int row = r0 + b * RPP;
                                 uint32_t w1[2], w2[2];
-                                const int e = split_row<CPR>(raw[b], w1, w2);
+                                split_row(raw[b], e[b], w1, w2);
                                 const uint32_t at = row8_piece<D>(row, c >> 1) + uint32_t(c & 1) * 8u;
                                 *reinterpret_cast<uint2 *>(q_img + at) = make_uint2(w1[0], w1[1]);
                                 *reinterpret_cast<uint2 *>(q_img + kSideRows * D + at) = make_uint2(w2[0], w2[1]);
-                                if (c == 0) sc8.q_unit[n_q[s] & 1][s][row] = exp2_biased(e);
+                                if (c == 0) sc8.q_unit[n_q[s] & 1][s][row] = exp2_biased(e[b] < 0 ? 127 : e[b]);
                             }
                         }
                         __syncwarp();
