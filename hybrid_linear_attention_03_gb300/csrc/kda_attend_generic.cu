@@ -11,9 +11,11 @@
 // of the output in registers.  Multiply-adds go two to an instruction (scores sum
 // even and odd channels apart).  They bound it, with the shared memory reads that
 // feed them close behind: at 4 rows a thread the reads came first (ragged prompts
-// of 777 to 1500 tokens, 12 heads of 64: 305 us against 258 at 8, 30 TFLOP/s).
+// of 777 to 1500 tokens, 12 heads of 64: 305 us against 258 at 8; 237 now, 33 TFLOP/s).
 // 64 rows on 128 threads leave room for three CTAs an SM, whose loads and sums
 // cover each other; head size 128 takes 128 rows on 256 threads, one CTA an SM.
+#include <type_traits>
+
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -23,15 +25,13 @@ namespace {
 constexpr int KS = 64;  // keys a step
 constexpr int threads_of(int bm) { return bm * 2; }  // 16 threads for 8 rows
 
-template <typename Kv> __device__ __forceinline__ void load4(const Kv *src, float (&x)[4]);
-template <> __device__ __forceinline__ void load4<float>(const float *src, float (&x)[4]) {
-    const float4 t = *reinterpret_cast<const float4 *>(src);
-    x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+// Four channels of a key or value; e4m3 times their scale.
+__device__ __forceinline__ float4 widen4(const uint4 &r, float) {
+    return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
 }
-template <> __device__ __forceinline__ void load4<uint8_t>(const uint8_t *src, float (&x)[4]) {
-    const uint32_t t = *reinterpret_cast<const uint32_t *>(src);
-    const float2 a = unpack_e4m3(uint16_t(t)), b = unpack_e4m3(uint16_t(t >> 16));
-    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+__device__ __forceinline__ float4 widen4(uint32_t r, float f) {
+    const float2 a = unpack_e4m3(uint16_t(r)), b = unpack_e4m3(uint16_t(r >> 16));
+    return make_float4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
 // Rows are padded to an odd number of 16-byte pieces, so that the 8 lanes of a
@@ -70,12 +70,14 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
 
     while (walk.next(p, it)) {
         __syncthreads();
+#pragma unroll 8
         for (int i = tid; i < BM * D / 4; i += kThreads) {
             const int r = i / (D / 4), c = i % (D / 4) * 4;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < it.rows) load4<float>(static_cast<const float *>(p.q) + it.at(r, p, p.q_stride, D) + c, x);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < it.rows)
+                x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + it.at(r, p, p.q_stride, D) + c);
             *reinterpret_cast<float4 *>(&s.q[r][c]) =
-                make_float4(x[0] * p.scale_log2, x[1] * p.scale_log2, x[2] * p.scale_log2, x[3] * p.scale_log2);
+                make_float4(x.x * p.scale_log2, x.y * p.scale_log2, x.z * p.scale_log2, x.w * p.scale_log2);
         }
         float o[RT][CT], m[RT], l[RT];
 #pragma unroll
@@ -105,21 +107,28 @@ __global__ void __launch_bounds__(threads_of(BM), BM == 64 ? 3 : 1) attend_gener
                 hidden = line < 0 || j > it.ctx + it.tok0;
             }
             const bool masked = __syncthreads_or(hidden);
-            for (int i = tid; i < KS * D / 4; i += kThreads) {
-                const int j = i / (D / 4), c = i % (D / 4) * 4;
-                float xk[4] = {0.f, 0.f, 0.f, 0.f}, xv[4] = {0.f, 0.f, 0.f, 0.f};
-                const int64_t line = s.line[j];
-                if (line >= 0) {
-                    load4<Kv>(static_cast<const Kv *>(p.pk) + line * D + c, xk);
-                    load4<Kv>(static_cast<const Kv *>(p.pv) + line * D + c, xv);
-                    if constexpr (sizeof(Kv) == 1) {
-                        const float fk = exp2_biased(p.sk[line]), fv = exp2_biased(p.sv[line]);
+            // all of a thread's pieces are asked for before the first is put down
+            using Raw = std::conditional_t<sizeof(Kv) == 1, uint32_t, uint4>;
+            constexpr int kPieces = KS * D / 4 / kThreads;
+            Raw rk[kPieces], rv[kPieces];
+            float fk[kPieces], fv[kPieces];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) xk[e] *= fk, xv[e] *= fv;
-                    }
+            for (int u = 0; u < kPieces; ++u) {
+                const int i = tid + u * kThreads, j = i / (D / 4), c = i % (D / 4) * 4;
+                const int64_t line = s.line[j];
+                rk[u] = rv[u] = Raw{};
+                fk[u] = fv[u] = 1.f;
+                if (line >= 0) {
+                    rk[u] = *reinterpret_cast<const Raw *>(static_cast<const Kv *>(p.pk) + line * D + c);
+                    rv[u] = *reinterpret_cast<const Raw *>(static_cast<const Kv *>(p.pv) + line * D + c);
+                    if constexpr (sizeof(Kv) == 1) fk[u] = exp2_biased(p.sk[line]), fv[u] = exp2_biased(p.sv[line]);
                 }
-                *reinterpret_cast<float4 *>(&s.k[j][c]) = make_float4(xk[0], xk[1], xk[2], xk[3]);
-                *reinterpret_cast<float4 *>(&s.v[j][c]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
+            }
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                const int i = tid + u * kThreads, j = i / (D / 4), c = i % (D / 4) * 4;
+                *reinterpret_cast<float4 *>(&s.k[j][c]) = widen4(rk[u], fk[u]);
+                *reinterpret_cast<float4 *>(&s.v[j][c]) = widen4(rv[u], fv[u]);
             }
             __syncthreads();
             // keys of a thread: tx, tx + 16, tx + 32, tx + 48
@@ -244,7 +253,7 @@ kda_status launch(AttendParams &p, const AttendPlan &plan, cudaStream_t stream) 
     if (!allow_smem<attend_generic_kernel<Kv, BM, D>>(smem)) return KDA_ERR_CUDA;
     p.key_step = KS;
     // Measured at 0, 64, 128, 256, 1024: 16 sequences of 30 to 60 new tokens behind 100 to 1500, heads of 128,
-    // take 512, 460, 478, 495, 630 us.
+    // take 512, 460, 478, 495, 630 us (before all of a step's loads went out together; 369 since).
     p.item_cost = KS;
     p.min_keys = 2 * KS;
     const ProfScope prof(KDA_KERNEL_KV_ATTEND, stream);
