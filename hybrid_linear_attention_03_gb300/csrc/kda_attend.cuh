@@ -238,8 +238,8 @@ template <auto kKernel> inline bool allow_smem(int bytes) {
     return ok[dev];
 }
 
-// What a kernel of this family needs from the host: its row tile, its grid
-// and its workspace.  supports() is decided on sizes and types alone.
+// What a kernel of this family needs from the host: its row tile and its grid.
+// A plan function says whether its kernel takes the call, on sizes and types alone.
 struct AttendPlan {
     int bm;     // rows of a tile
     int n_cta;  // grid

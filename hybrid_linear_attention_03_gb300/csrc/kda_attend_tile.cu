@@ -25,7 +25,7 @@
 // tensor memory untouched, and in bf16 need no maximum at all (the 8192-token
 // prompt with heads of 64: 653 us against 720 with a maximum for each half; with
 // heads of 128 783 either way; in e4m3 the registers are short for it, and verifies
-// take 261 us against 224).  P is rounded to bf16 (2^-9 relative, the
+// take 261 us against 224).  P is rounded to bf16 (2^-8 relative, the
 // size of the output's own rounding, and not correlated between keys); scores,
 // sums and O stay in 32 bits.
 //
@@ -45,13 +45,13 @@
 //
 // What bounds it: a half's products wait for its weights and its weights for its
 // scores; two sides with two halves each cover most of that, and tensor memory has
-// no columns for more (heads of 128: the tensor pipe is active in 62 % of the
+// no columns for more (heads of 128: the tensor pipe is active in 64 % of the
 // cycles; heads of 64: the softmax threads are the slower part).  Measured, 64
 // heads over 8 cache heads of 128: a prompt of 8192 tokens 775 us (1420 TFLOP/s,
 // 73 % of the measured bf16 peak), 512 tokens behind 32256 410 us (69 %); in e4m3
-// pages the prompt takes 1106 us, bound by the threads that widen values and scale
+// pages the prompt takes 1098 us, bound by the threads that widen values and scale
 // scores and by the second term of Q.  64 verifies of 8 tokens over 1000 to 8192
-// in e4m3 take 208 us (3.0 TB/s).  Heads of 64: the prompt 659 us.
+// in e4m3 take 207 us (3.0 TB/s).  Heads of 64: the prompt 659 us.
 #include "kda_attend_tc.cuh"
 
 namespace kda {
