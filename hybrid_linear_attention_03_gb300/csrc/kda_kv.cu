@@ -11,10 +11,12 @@
 // than a pointer step between them.  Sums of squares, largest magnitudes and
 // rotation partners move by shuffles.
 // Measured, 64 heads over 8 cache heads of 128 in bf16: 8 ragged prompts of 511 to
-// 2049 tokens written in 82 us (5.3 TB/s, 78 % of the measured copy rate); 32768
-// tokens written in e4m3 and read back 307 us (4.6 TB/s: beside the bytes there is
-// the search for a vector's largest magnitude, four shuffles and 8 conversions a
-// lane); one token 4.3 us, 64 of them written and read in e4m3 9 us (launches).
+// 2049 tokens written in 82 us (5.3 TB/s, 79 % of the measured copy rate); 32768
+// tokens written in e4m3 and read back 319 us (4.4 TB/s: beside the bytes there is
+// the search for a vector's largest magnitude, and the keys' roundings are carried
+// along, which takes 13 us and halves the share of values that a rounding before
+// the last puts on the wrong side of an e4m3 border); one token 4.4 us, 64 of them
+// written and read in e4m3 9 us (launches).
 #include "kda_kv.cuh"
 
 #include <cmath>
@@ -99,10 +101,30 @@ __device__ __forceinline__ void find_row(const BatchView &b, int r, int lane, in
     }
 }
 
+// Cosine and sine of the angle a * 2^-63 * pi (a two's complement), within 7e-8 (2.4e-8 in the mean: an
+// e4m3 page turns an error next to a rounding border into a whole step of e4m3, so
+// the last bit is worth having).  The quadrant comes off in integers; the rest, at
+// most pi / 4, is held as a sum p + e of two floats; then Taylor series, whose
+// terms past the first add less than a third of it.
+__device__ __forceinline__ float2 cos_sin(uint64_t a) {
+    constexpr float kPi = 3.14159274f, kPiRest = -8.74227766e-8f;  // their sum is pi to 48 bits
+    const int q = int((a + (uint64_t(1) << 61)) >> 62);
+    const int64_t r = int64_t(a - (uint64_t(q) << 62));
+    const float hi = float(r), u = hi * 0x1p-63f, lo = float(r - __float2ll_rn(hi)) * 0x1p-63f;
+    const float p = __fmul_rn(u, kPi), e = fmaf(lo, kPi, fmaf(u, kPiRest, fmaf(u, kPi, -p))), z = p * p;
+    const float s3 = fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6) * z;
+    const float sn = p + fmaf(p, s3, e * fmaf(z, -0.5f, 1.0f));
+    const float c2 = fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f);
+    const float cn = 1.0f + fmaf(z, c2, -p * e);
+    const float c = q & 1 ? sn : cn, s = q & 1 ? cn : sn;  // turned by a quarter
+    return make_float2(q == 1 || q == 2 ? -c : c, q >= 2 ? -s : s);
+}
+
 enum { kNoRot = 0, kHalves = 1, kPairs = 2 };  // rotation: none, channels (i, i + half), channels (2i, 2i + 1)
 
 // One CTA: rows_per_cta rows x heads_per_cta of the hq + 2 hkv heads.  Four CTAs an
-// SM (64 registers) against three at 72: 307 against 330 us for the 32768 tokens.
+// SM (64 registers) against three at 72: 307 against 330 us for the 32768 tokens
+// (before the keys carried their roundings).
 template <typename Act, int D, bool kE4m3, int kRot>
 __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_constant__ AppendParams p) {
     using V = Vec<Act>;
@@ -125,9 +147,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
         for (int i = tid; i < p.rows_per_cta * p.half_rot; i += kThreads) {
             const int row = i / p.half_rot, pair = i % p.half_rot;
             const uint64_t ph = uint64_t(uint32_t(max(s_pos[row], 0))) * p.turn[pair];
-            float sn, cn;
-            sincospif(float(int64_t(ph)) * 0x1p-63f, &sn, &cn);
-            cs[row][pair] = make_float2(cn, sn);
+            cs[row][pair] = cos_sin(ph);
         }
         __syncthreads();
     }
@@ -155,28 +175,33 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
     const int q = p.half_rot / N;
     const bool odd4 = p.half_rot % N != 0, first = c0 < p.half_rot;
 
-    // x: 16 bytes of a q or k head -> normalised and rotated
-    auto norm_rotate = [&](float (&x)[N], const uint4 &w_raw, bool norm) {
+    // x: 16 bytes of a q or k head -> normalised and rotated.  fine: every rounding but the last is carried along
+    // (keys that go to e4m3 pages).
+    auto norm_rotate = [&](float (&x)[N], const uint4 &w_raw, bool norm, bool fine) {
+        float rs = 1.f, rs_rest = 0.f;
         if (norm) {
-            float ss = 0.f;
+            float sq[N / 2];
 #pragma unroll
-            for (int e = 0; e < N; ++e) ss = fmaf(x[e], x[e], ss);
+            for (int e = 0; e < N / 2; ++e) sq[e] = fmaf(x[e], x[e], x[e + N / 2] * x[e + N / 2]);
+            float ss = N == 8 ? (sq[0] + sq[1]) + (sq[N / 2 - 2] + sq[N / 2 - 1]) : sq[0] + sq[1];
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rs = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+            const float y = fmaf(ss, 1.0f / D, p.eps);
+            rs = 1.0f / sqrtf(y);
+            if (fine) {  // 1 / sqrt(y) = rs + rs_rest: half of what y rs^2 misses of one
+                const float t = __fmul_rn(y, rs), miss = fmaf(-t, rs, 1.0f) - fmaf(y, rs, -t) * rs;
+                rs_rest = isfinite(miss) ? 0.5f * rs * miss : 0.f;
+            }
             float w[N];
             V::unpack(w_raw, w);
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = x[e] * rs * w[e];
+            for (int e = 0; e < N; ++e) x[e] = fine ? x[e] * w[e] : x[e] * w[e] * rs;  // the first product is exact in bf16
         }
+        float y[N] = {};  // the partners
         if constexpr (kRot == kPairs) {
 #pragma unroll
-            for (int e = 0; e < N; e += 2) {
-                const float a = x[e], b = x[e + 1];
-                x[e] = fmaf(a, cn[e], b * sn[e]), x[e + 1] = fmaf(b, cn[e + 1], a * sn[e + 1]);
-            }
+            for (int e = 0; e < N; e += 2) y[e] = x[e + 1], y[e + 1] = x[e];
         } else if constexpr (kRot == kHalves) {
-            float y[N];
             if (!odd4) {
                 const int src = first ? l + q : l - q;
 #pragma unroll
@@ -189,8 +214,23 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
                     y[e] = __shfl_sync(0xffffffffu, x[(e + 4) % N], src, LPH);
                 }
             }
+        }
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], cn[e], y[e] * sn[e]);
+        for (int e = 0; e < N; ++e) {
+            if (!fine) {
+                if (kRot != kNoRot) x[e] = fmaf(x[e], cn[e], y[e] * sn[e]);
+                continue;
+            }
+            float sum = x[e], rest = 0.f;
+            if (kRot != kNoRot) {
+                const float a = __fmul_rn(x[e], cn[e]), b = __fmul_rn(y[e], sn[e]);
+                sum = __fadd_rn(a, b);
+                const float b_in = __fsub_rn(sum, a);  // and what the sum lost of either
+                rest = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, b_in)), __fsub_rn(b, b_in)) + fmaf(x[e], cn[e], -a) +
+                       fmaf(y[e], sn[e], -b);
+            }
+            const float z = fmaf(sum, rs, fmaf(sum, rs_rest, rest * rs));
+            x[e] = isfinite(z) ? z : sum * rs;  // infinities come as they are
         }
     };
     // x to head h of the pages
@@ -246,11 +286,11 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
     if (norm_k) wk = __ldg(reinterpret_cast<const uint4 *>(p.wk) + l);
     Act *q_out = static_cast<Act *>(p.q_out) + r * size_t(p.qo_stride) + c0;
     each_head(p.q, p.q_stride, 0, p.hq, [&](float (&x)[N], int h, bool live) {
-        norm_rotate(x, wq, norm_q);
+        norm_rotate(x, wq, norm_q, false);
         if (live) *reinterpret_cast<uint4 *>(q_out + size_t(h) * D) = V::pack(x);
     });
     each_head(p.k, p.k_stride, p.hq, p.hkv, [&](float (&x)[N], int h, bool live) {
-        norm_rotate(x, wk, norm_k);
+        norm_rotate(x, wk, norm_k, kE4m3);
         to_page(x, h, p.pk, p.sk, live && page >= 0);
     });
     each_head(p.v, p.v_stride, p.hq + p.hkv, p.hkv,
