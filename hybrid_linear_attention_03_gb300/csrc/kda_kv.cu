@@ -12,7 +12,7 @@
 // rotation partners move by shuffles.
 // Measured, 64 heads over 8 cache heads of 128 in bf16: 8 ragged prompts of 511 to
 // 2049 tokens written in 82 us (5.3 TB/s, 79 % of the measured copy rate); 32768
-// tokens written in e4m3 and read back 319 us (4.4 TB/s: beside the bytes there is
+// tokens written in e4m3 and read back 316 us (4.5 TB/s: beside the bytes there is
 // the search for a vector's largest magnitude, and the keys' roundings are carried
 // along, which takes 13 us and halves the share of values that a rounding before
 // the last puts on the wrong side of an e4m3 border); one token 4.4 us, 64 of them
@@ -374,9 +374,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
 // Rows of a CTA.  Few rows: as few as leave every thread one 16-byte piece of
 // the row's heads (latency); the border is where one piece per thread fills every
 // SM once (64 heads over 8 of 128 in bf16, 240 rows: 9.5 us this way, 11.1 the
-// other; 320 rows: 12.4 and 11.1).  Many rows: 4, or more where a row's heads of one kind (at most
-// `kind`) are fewer than the lane groups that it would get (32768 rows of one head
-// and one cache head of 32 channels: 57 us at 4 rows a CTA, 17 at 32).
+// other; 320 rows: 12.4 and 11.1).  Many rows: 4, and 8 where that still gives every
+// place for a CTA four of them (32768 rows written and read in bf16 280 us against
+// 297, 10700 rows written 85 against 82).  More where a row's heads of one kind (at
+// most `kind`) are fewer than the lane groups that it would get (32768 rows of one
+// head and one cache head of 32 channels: 57 us at 4 rows a CTA, 17 at 32).
 struct RowSplit {
     int rows_per_cta;
     bool few;
@@ -384,7 +386,8 @@ struct RowSplit {
 inline RowSplit split_rows(int rows, int lanes, int heads, int kind) {
     const int groups = kThreads / lanes, most = max_rows_per_cta(lanes);
     RowSplit s = {1, static_cast<long long>(rows) * heads * lanes <= 2048LL * sm_count()};
-    if (!s.few) s.rows_per_cta = most < 4 ? most : 4;
+    const int many = rows >= 8 * 16 * sm_count() ? 8 : 4;
+    if (!s.few) s.rows_per_cta = most < many ? most : many;
     while (s.rows_per_cta < most && groups / s.rows_per_cta / 2 >= (s.few ? heads : kind)) s.rows_per_cta *= 2;
     return s;
 }

@@ -154,6 +154,34 @@ def test_append_in_place_and_keys_only():
     assert torch.equal(ks, k.double().cpu()) and torch.equal(vs, v.double().cpu())
 
 
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("act,hq,hkv,d", [(BF, 2, 1, 64), (F32, 3, 1, 16), (BF, 5, 5, 128)])
+def test_append_and_read_many_rows(act, hq, hkv, d, fmt):
+    """Tens of thousands of rows: every line is in its place in the raw pages, and comes back."""
+    b = R.Batch([9001, 0, 11000, 1], [9001, 5, 11033, 70], hq, hkv, d, 64, act, fmt, seed=83, extra_rows=7)
+    q, k, v = b.randn(b.max_rows, hq), b.randn(b.max_rows, hkv), b.randn(b.max_rows, hkv)
+    q_out = torch.full_like(q, 7.0, device="cuda")
+    kda.kda_kv_append(b.kv, None, kda.make_kv_io(q.cuda(), k.cuda(), v.cuda(), q_out), b.batch)
+    no_device_error(b.kv)
+    assert torch.equal(q_out[:b.rows].cpu(), q[:b.rows]) and (q_out[b.rows:] == 7.0).all()
+    seq = torch.tensor([i for i, T in enumerate(b.new) for _ in range(T)])
+    pos = torch.tensor(b.positions())
+    page, line = b.table[seq, pos // 64].long(), pos % 64
+    ko, vo = (torch.full((b.max_rows, hkv, d), 5.0, dtype=act, device="cuda") for _ in range(2))
+    kda.kda_kv_read(b.kv, b.batch, ko, vo)
+    no_device_error(b.kv)
+    for x, pages, exps, back in ((k, b.kv.k, b.kv.k_scale, ko), (v, b.kv.v, b.kv.v_scale, vo)):
+        raw = pages.float().cpu()[page, :, line].double()
+        if fmt == "act":
+            ref = x[:b.rows].double()
+            assert torch.equal(raw, ref)
+        else:
+            val, e = R.quantise(x[:b.rows].double().numpy())
+            assert np.array_equal(raw.numpy(), val) and np.array_equal(exps.cpu()[page, :, line].numpy(), e)
+            ref = torch.from_numpy(val * 2.0 ** (e - 127.0)[..., None])
+        assert torch.equal(back[:b.rows].double().cpu(), ref) and (back[b.rows:] == 5.0).all()
+
+
 def test_far_positions_keep_their_angle():
     """A position of tens of millions: an angle formed in 32 bits would be off by whole radians."""
     far = 50_000_003
