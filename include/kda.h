@@ -442,7 +442,8 @@ KDA_API kda_status kda_poll_device_error(kda_pool *pool, kda_stream_t stream, ui
  * past page_table's width or 2^31 - 1024) sets KDA_DEVERR_META and its rows are
  * left as they were; a page outside the cache sets KDA_DEVERR_PAGE_RANGE, and
  * its tokens are not written, read back as zeros, and are absent from the
- * attention.
+ * attention.  KDA_DEVERR_TIMEOUT (a bounded wait inside the attention gave up)
+ * leaves that call's outputs undefined.
  * The work may start while the preceding kernel on its stream finishes
  * (programmatic dependent launch); it reads nothing until that kernel has
  * completed. */
