@@ -89,14 +89,20 @@ template <int N> __device__ __forceinline__ void store_e4m3(void *dst, const flo
 
 // The row of a CTA that a warp works on: its position and page, or pos = -1 for
 // a row past the last sequence or of one whose tables are inconsistent.  Whole warp.
+// The search supposes that cu_seqlens does not decrease.  Where it does it may name a
+// sequence that the row is not in, whose position would lie outside the page table.
 __device__ __forceinline__ void find_row(const BatchView &b, int r, int lane, int &pos, int &page) {
     pos = page = -1;
     const int n = r < b.max_rows ? find_seq(b, r, lane) : -1;
     if (lane == 0 && n >= 0 && n < b.n_seqs) {
         Seq s;
         if (load_seq(b, n, s, true)) {
-            pos = s.L - s.T + (r - s.row0);
-            page = load_page(b, n, pos);
+            if (r >= s.row0 && r - s.row0 < s.T) {
+                pos = s.L - s.T + (r - s.row0);
+                page = load_page(b, n, pos);
+            } else {
+                atomicOr(b.err, KDA_DEVERR_META);
+            }
         }
     }
 }

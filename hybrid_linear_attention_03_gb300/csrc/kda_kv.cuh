@@ -31,8 +31,9 @@ struct Seq {
 };
 
 // Reads sequence n's tables; false (and KDA_DEVERR_META when `report`) if
-// they are inconsistent.  Everything a caller derives from a Seq that passed
-// is in range: rows in [0, max_rows), positions in [0, table_stride pages).
+// they are inconsistent.  Of a Seq that passed, rows [row0, row0 + T) are in
+// [0, max_rows) and positions [0, L) in the page table's row; a row from
+// elsewhere (a search in cu_seqlens) has to be shown to be one of these first.
 __device__ __forceinline__ bool load_seq(const BatchView &b, int n, Seq &s, bool report) {
     const int a = b.cu[n], e = b.cu[n + 1], L = b.lens[n];
     const bool ok = a >= 0 && e >= a && e <= b.max_rows && e - a <= b.max_new && L >= e - a &&

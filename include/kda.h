@@ -440,7 +440,10 @@ KDA_API kda_status kda_poll_device_error(kda_pool *pool, kda_stream_t stream, ui
  * Device errors: a sequence whose tables are inconsistent (cu_seqlens
  * decreasing or past max_rows, more than max_new tokens, kv_lens below T_n or
  * past page_table's width or 2^31 - 1024) sets KDA_DEVERR_META and its rows are
- * left as they were; a page outside the cache sets KDA_DEVERR_PAGE_RANGE, and
+ * left as they were (if cu_seqlens decreases anywhere, rows of other sequences
+ * may be left too, and a row that two sequences claim is written as either's;
+ * nothing outside the consistent sequences' rows and lines is written); a page
+ * outside the cache sets KDA_DEVERR_PAGE_RANGE, and
  * its tokens are not written, read back as zeros, and are absent from the
  * attention.  KDA_DEVERR_TIMEOUT (a bounded wait inside the attention gave up)
  * leaves that call's outputs undefined.
