@@ -126,6 +126,14 @@ __device__ __forceinline__ float2 cos_sin(uint64_t a) {
     return make_float2(q == 1 || q == 2 ? -c : c, q >= 2 ? -s : s);
 }
 
+// x <- x c + t where `on`, as one instruction under a predicate (32768 tokens written and
+// read in bf16: 282 us this way, 285 with a select or a branch, 280 if every channel turned).
+__device__ __forceinline__ void fma_where(bool on, float &x, float c, float t) {
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p fma.rn.f32 %0, %0, %1, %2;\n\t}"
+        : "+f"(x)
+        : "f"(c), "f"(t), "r"(uint32_t(on)));
+}
+
 enum { kNoRot = 0, kHalves = 1, kPairs = 2 };  // rotation: none, channels (i, i + half), channels (2i, 2i + 1)
 
 // One CTA: rows_per_cta rows x heads_per_cta of the hq + 2 hkv heads.  Four CTAs an
@@ -164,15 +172,15 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
     const int l = tid % LPH, c0 = l * N;
     const int pos = s_pos[row], page = s_page[row];
     const size_t r = size_t(row_base + row);
+    const bool turns = c0 < 2 * p.half_rot;  // all of this lane's channels or none: rot_dim is a multiple of 8
     float cn[N], sn[N];  // of this lane's channels; the sine with the sign it takes
     if constexpr (kRot != kNoRot) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const int c = c0 + e;
-            const bool turned = c < 2 * p.half_rot;
             const bool second = kRot == kPairs ? (e & 1) != 0 : c >= p.half_rot;
-            const int pair = !turned ? 0 : kRot == kPairs ? c / 2 : second ? c - p.half_rot : c;
-            const float2 t = turned ? cs[row][pair] : make_float2(1.f, 0.f);
+            const int pair = !turns ? 0 : kRot == kPairs ? c / 2 : second ? c - p.half_rot : c;
+            const float2 t = turns ? cs[row][pair] : make_float2(1.f, 0.f);
             cn[e] = t.x, sn[e] = second ? t.y : -t.y;
         }
     }
@@ -221,19 +229,21 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
                 }
             }
         }
+        // channels that do not turn get no multiple of a partner, which may be an infinity or NaN
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             if (!fine) {
-                if (kRot != kNoRot) x[e] = fmaf(x[e], cn[e], y[e] * sn[e]);
+                if (kRot != kNoRot) fma_where(turns, x[e], cn[e], y[e] * sn[e]);
                 continue;
             }
             float sum = x[e], rest = 0.f;
             if (kRot != kNoRot) {
-                const float a = __fmul_rn(x[e], cn[e]), b = __fmul_rn(y[e], sn[e]);
+                const float other = turns ? y[e] : 0.f;
+                const float a = __fmul_rn(x[e], cn[e]), b = __fmul_rn(other, sn[e]);
                 sum = __fadd_rn(a, b);
                 const float b_in = __fsub_rn(sum, a);  // and what the sum lost of either
                 rest = __fadd_rn(__fsub_rn(a, __fsub_rn(sum, b_in)), __fsub_rn(b, b_in)) + fmaf(x[e], cn[e], -a) +
-                       fmaf(y[e], sn[e], -b);
+                       fmaf(other, sn[e], -b);
             }
             const float z = fmaf(sum, rs, fmaf(sum, rs_rest, rest * rs));
             x[e] = isfinite(z) ? z : sum * rs;  // infinities come as they are

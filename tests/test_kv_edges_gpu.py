@@ -71,3 +71,45 @@ def test_decreasing_cu_seqlens_touch_no_other_line(cu, act, fmt):
     kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, ws)
     assert kda.kda_kv_poll_device_error(b.kv) == (kda.KDA_ERR_DEVICE, kda.KDA_DEVERR_META)
     assert (out.cpu()[~owned] == 9.0).all()
+
+
+# ---- values that are not finite ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("act", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("norm", [False, True], ids=["", "norm"])
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("d,rot", [(128, 64), (128, 96), (64, 24), (32, 24), (16, 8)])
+def test_non_finite_values_stay_in_their_pair(d, rot, inter, norm, act, fmt):
+    """An infinity or NaN reaches the other channel of its pair and, with the norm, the row; channels that do not turn are
+    those that came."""
+    b = R.Batch([6], [40], 2, 1, d, 16, act, fmt, seed=d + rot)
+    q, k, v = (b.randn(6, n) for n in (2, 1, 1))
+    for x in (q, k):
+        x[0, :, 1] = float("inf")           # turns
+        x[1, :, rot - 1] = float("-inf")    # turns
+        x[2, :, 0] = float("nan")           # turns
+        x[3, :, rot] = float("inf")         # does not turn
+        x[4, :, d - 1] = float("nan")       # does not turn
+    w = (1 + 0.1 * torch.randn(2, d, generator=b.gen)).to(act) if norm else (None, None)
+    freq = [1000.0 ** (-2.0 * i / rot) for i in range(rot // 2)]
+    params = kda.make_qk_params(*(None if x is None else x.cuda() for x in w), 1e-5, freq, inter)
+    q_out = torch.full_like(q, 7.0, device="cuda")
+    kda.kda_kv_append(b.kv, params, kda.make_kv_io(q.cuda(), k.cuda(), v.cuda(), q_out), b.batch)
+    ko, vo = (torch.full((6, 1, d), 5.0, dtype=act, device="cuda") for _ in range(2))
+    kda.kda_kv_read(b.kv, b.batch, ko, vo)
+    assert kda.kda_kv_poll_device_error(b.kv)[0] == kda.KDA_OK
+    for got, x, wx, e4m3 in ((q_out, q, w[0], False), (ko, k, w[1], fmt == "e4m3")):
+        got, ref = got.double().cpu(), R.norm_rotate(x, wx, b.positions(), freq, inter, 1e-5)
+        if e4m3:  # stored as NaN
+            ref = torch.where(torch.isfinite(ref), ref, torch.nan)
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        fin = torch.isfinite(ref)
+        assert torch.equal(got[~fin & ~torch.isnan(ref)], ref[~fin & ~torch.isnan(ref)])
+        top = torch.where(fin, ref, 0.0).abs().amax(-1, keepdim=True)
+        tol = ref.abs() * (2.0 ** -8 if act == BF else 0.0) + 2.0 ** -18 * top
+        if e4m3:  # half a step of e4m3, at the small end half of 2^-9 of a unit that is at most max / 224
+            tol = tol + ref.abs() * 2.0 ** -4 + top * (2.0 ** -10 / 224)
+        assert ((got - ref).abs() <= tol)[fin].all()
+        if not norm and not e4m3:
+            assert torch.equal(got[..., rot:].nan_to_num(), x[..., rot:].double().nan_to_num())
