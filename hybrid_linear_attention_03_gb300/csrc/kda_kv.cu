@@ -107,6 +107,15 @@ __device__ __forceinline__ void find_row(const BatchView &b, int r, int lane, in
     }
 }
 
+// Has the inconsistent sequences reported that no row leads to, as those without rows:
+// the grid's columns take 32 sequences a turn each (one warp, beside those that look up rows).
+__device__ __forceinline__ void report_seqs(const BatchView &b, int lane) {
+    for (long long n = blockIdx.x * 32LL + lane; n < b.n_seqs; n += gridDim.x * 32LL) {
+        Seq s;
+        load_seq(b, int(n), s, true);
+    }
+}
+
 // Cosine and sine of the angle a * 2^-63 * pi (a two's complement), within 7e-8 (2.4e-8 in the mean: an
 // e4m3 page turns an error next to a rounding border into a whole step of e4m3, so
 // the last bit is worth having).  The quadrant comes off in integers; the rest, at
@@ -155,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
         find_row(p.b, row_base + i, lane, pos, page);
         if (lane == 0) s_pos[i] = pos, s_page[i] = page;
     }
+    if (blockIdx.y == 0 && warp == kThreads / 32 - 1) report_seqs(p.b, lane);
     __syncthreads();
     if constexpr (kRot != kNoRot) {
         // angle p * f in turns is a 64-bit product mod 2^64: exact for any position
@@ -336,6 +346,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
         find_row(p.b, row_base + i, lane, pos, page);
         if (lane == 0) s_pos[i] = pos, s_page[i] = page;
     }
+    if (warp == kThreads / 32 - 1) report_seqs(p.b, lane);
     __syncthreads();
     const int step = kGroups / p.rows_per_cta, row = (tid / LPH) / step, j = (tid / LPH) % step;
     const int c0 = (tid % LPH) * N, pos = s_pos[row], page = s_page[row];

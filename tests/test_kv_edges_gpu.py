@@ -73,6 +73,28 @@ def test_decreasing_cu_seqlens_touch_no_other_line(cu, act, fmt):
     assert (out.cpu()[~owned] == 9.0).all()
 
 
+@pytest.mark.parametrize("which", ["first", "middle", "last"])
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 65, 2 ** 31 - 1])
+def test_empty_sequences_with_bad_lengths_are_reported(length, which):
+    """A sequence without rows in the call is as inconsistent as another: all three calls say so and serve the others."""
+    at = {"first": 0, "middle": 20, "last": 39}[which]
+    new = [1] * 40
+    new[at] = 0
+    b = R.Batch(new, [64] * 40, 2, 1, 32, 16, BF, "act", seed=3)
+    b.dev[1][at] = length
+    q, k, v = (b.randn(b.rows, n).cuda() for n in (2, 1, 1))
+    q_out, out = torch.full_like(q, 7.0), torch.full_like(q, 9.0)
+    bad = (kda.KDA_ERR_DEVICE, kda.KDA_DEVERR_META)
+    kda.kda_kv_append(b.kv, None, kda.make_kv_io(q, k, v, q_out), b.batch)
+    assert kda.kda_kv_poll_device_error(b.kv) == bad
+    ko, vo = torch.full_like(k, 5.0), torch.full_like(v, 5.0)
+    kda.kda_kv_read(b.kv, b.batch, ko, vo)
+    assert kda.kda_kv_poll_device_error(b.kv) == bad
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+    assert kda.kda_kv_poll_device_error(b.kv) == bad
+    assert torch.equal(q_out, q) and torch.equal(ko, k) and torch.equal(vo, v) and not (out == 9.0).any()
+
+
 # ---- values that are not finite ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", ["act", "e4m3"])
