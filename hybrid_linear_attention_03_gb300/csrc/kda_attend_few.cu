@@ -68,7 +68,7 @@ template <typename C> struct alignas(16) Misc {
     uint64_t q_full, q_free, done;
     uint64_t row_unit[2];  // by item parity
     uint32_t tmem;
-    int has, rows_gave_up;
+    int has, rows_gave_up[2];
     Cursor piece[2];
     uint32_t odd[kBars][4];                  // by tile: keys whose value row was taken out of it
     alignas(16) uint8_t k_scale[C::kStagesK][KT];  // e4m3: the tiles' scale exponents
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
     if (warp == kMma + 1) {
         Cursor a, z;
         const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
-        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has, ms.rows_gave_up = 0;
+        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has, ms.rows_gave_up[0] = ms.rows_gave_up[1] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                         wait_tile(ok, ms.k_full, tile, err);
                         unit = exp2_biased(ms.k_scale[tile % NK][key]);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&ms.k_empty[tile % kBars]);
+                        if (ok && lane == 0) mbar_arrive(&ms.k_empty[tile % kBars]);
                     }
                     wait_for(ok, &ms.s_full[tile & 1], (tile >> 1) & 1, err);
                     __syncwarp();
@@ -267,11 +267,11 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                     }
                     if (check) {
                         wait_tile(ok, kE4m3 ? ms.v_full : ms.clean, tile, err);
-                        __syncwarp();
+                        ok = __all_sync(0xffffffffu, ok);
                         const uint32_t *odd = ms.odd[tile % kBars];
-                        if ((odd[0] | odd[1] | odd[2] | odd[3]) != 0) {
+                        // (the group has to agree, and once it has met all weights are there)
+                        if (any_of_128(ok && (odd[0] | odd[1] | odd[2] | odd[3]) != 0, g)) {
                             // value rows taken out of the tile: thread = channel adds them for the rows that see them
-                            meet_128(g);  // all weights are there
                             float o[N];
                             if (started) {
                                 wait_o(tile - kG);
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < N; ++i) o[i] = started ? o[i] : 0.f;
                             for (int q = 0; q < 4; ++q) {
-                                for (uint32_t left = odd[q]; left; left &= left - 1) {
+                                for (uint32_t left = ok ? odd[q] : 0u; left; left &= left - 1) {
                                     const int out = q * 32 + __ffs(left) - 1, jj = kb + out;
                                     const size_t vec =
                                         ((size_t(max(load_page(p.b, it.n, jj), 0)) * size_t(p.hkv) + size_t(it.h))
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.p_ready[tile & 1]);
+                    if (ok && lane == 0) mbar_arrive(&ms.p_ready[tile & 1]);
                 }
 
                 // ---- output: thread = channel; rows by turns where both groups had tiles ----------
@@ -459,8 +459,7 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
             // nothing of this CTA's is in flight when its tensor memory goes
             if (elect_one()) mma_commit(&ms.done);
             __syncwarp();
-            bool end_ok = true;
-            wait_for(end_ok, &ms.done, 0, err);
+            mbar_wait(&ms.done, 0, err);
         } else if (ms.has && warp < kMma + 3) {
             const bool fetches_values = warp == kMma + 2;
             // ---- page fetches: keys, or values ------------------------------------------------
@@ -489,10 +488,13 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1)
             uint32_t n_it = 0, tile = 0;
             // Only the first of these warps waits by polling; the others meet it at a barrier of the
             // hardware's, and learn there whether it gave up.
+            // (by turns two words: the first may be an appointment ahead of a warp that still reads)
+            uint32_t turn = 0;
             auto meet = [&] {
-                if (w == 0 && !ok) ms.rows_gave_up = 1;
+                if (w == 0 && !ok) ms.rows_gave_up[turn] = 1;
                 named_sync<5, kRowThreads>();
-                ok = ms.rows_gave_up == 0;
+                ok = ms.rows_gave_up[turn] == 0;
+                turn ^= 1;
             };
             while (ok && walk.next(p, it)) {
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + c * 8;

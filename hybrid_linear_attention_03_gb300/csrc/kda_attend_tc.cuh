@@ -184,11 +184,34 @@ __device__ __forceinline__ bool odd_bf16(const uint4 &w) {
     return odd;
 }
 
-// A bounded wait that is skipped once one has given up.  The row warps then run
-// on with whatever is there (all in bounds, the error word is set), so that the
-// CTA's own barriers are met; the other roles stop issuing.
+// ---- waits that may give up ----------------------------------------------
+// Every wait is bounded, and skipped once the thread has given up.  A warp whose lane 0
+// has given up
+//   - arrives at no mbarrier any more, so none completes a phase that its owner did not
+//     reach: the roles that still run keep their order, and give up in their turn where
+//     they depend on this one (the lanes meet behind each wait, so that lane 0 speaks
+//     for all of them);
+//   - follows no address that others should have left in shared memory (the lists of keys
+//     taken out of a tile; scales, scores and weights may be anything);
+//   - meets the hardware's barriers as before (their number follows from the tables alone).
+// The issuing and fetching warps then stop, wait for their own products and copies, and
+// the CTA ends as usual.  KDA_ATTEND_LOOKS: a build for the test of all this, whose waits
+// look that often and no more.
 __device__ __forceinline__ void wait_for(bool &ok, uint64_t *bar, uint32_t parity, uint32_t *err) {
+#ifndef KDA_ATTEND_LOOKS
     if (ok) ok = mbar_wait(bar, parity, err);
+#else
+    uint32_t passed = ok ? 0 : 1;
+    for (int i = 0; i < KDA_ATTEND_LOOKS && !passed; ++i)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(passed)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    if (!passed) atomicOr(err, KDA_DEVERR_TIMEOUT), ok = false;
+#endif
 }
 // Tile t's barrier of a ring has been passed.
 __device__ __forceinline__ void wait_tile(bool &ok, uint64_t *bars, uint32_t t, uint32_t *err) {
@@ -334,11 +357,8 @@ __device__ __forceinline__ void fetch_pages(const AttendParams &p, const TileMap
             __syncwarp();
         }
     }
-    // a given-up wait elsewhere may leave copies in flight: they land before the CTA ends
-    if (!ok) {
-        bool end_ok = true;
-        for (uint32_t i = t - min(t, uint32_t(depth)); i < t; ++i) wait_tile(end_ok, bars, i, p.b.err);
-    }
+    // whichever role gives up, no copy is in flight when the CTA ends
+    for (uint32_t i = t - min(t, uint32_t(depth)); i < t; ++i) mbar_wait(&bars[i % kBars], (i / kBars) & 1, p.b.err);
 }
 // Warp w of eight widens its 16 keys of a raw value tile, and looks them over
 // where some row does not see some key; odd: the tile's keys taken out.

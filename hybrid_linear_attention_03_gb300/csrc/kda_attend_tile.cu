@@ -97,7 +97,7 @@ template <typename C> struct alignas(16) Misc {
     uint64_t q_full[2], q_free[2], done[2];
     uint64_t row_unit[2][2];  // e4m3, by image and item parity: the rows' scales are there
     uint32_t tmem;
-    int has, rows_gave_up;
+    int has, rows_gave_up[2];
     Cursor piece[2];
     uint32_t odd[kBars][4];                        // by tile: keys whose value row was taken out of it
     float m[kSideRows], l[kSideRows];              // side 1's row statistics, for the join
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
     if (warp == 10) {
         Cursor a, z;
         const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
-        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has, ms.rows_gave_up = 0;
+        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has, ms.rows_gave_up[0] = ms.rows_gave_up[1] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -366,9 +366,9 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                             l += sum_h;
                             if (check) {
                                 wait_tile(ok, kE4m3 ? ms.v_full : ms.clean, tg, err);
-                                __syncwarp();
+                                ok = __all_sync(0xffffffffu, ok);
                                 const uint32_t *odd = &ms.odd[tg % kBars][h * (KH / 32)];
-                                if (any_odd(odd)) {
+                                if (ok && any_odd(odd)) {
                                     if (started) wait_o(h == 0 ? n_s - 1 : n_s, h ^ 1);
                                     const Item copy = it;
                                     add_odd_rows<D, kE4m3>(p, copy, kh, lim, odd, t_h, t_o, !started);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                         }  // else rows of nobody: their weights may be anything
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&ms.p_ready[s][h]);
+                        if (ok && lane == 0) mbar_arrive(&ms.p_ready[s][h]);
                     }
                 }
                 tile_base += uint32_t(item_tiles(it));
@@ -542,8 +542,7 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
             // nothing of this side's is in flight when the tensor memory goes
             if (elect_one()) mma_commit(&ms.done[s]);
             __syncwarp();
-            bool end_ok = true;
-            wait_for(end_ok, &ms.done[s], 0, err);
+            mbar_wait(&ms.done[s], 0, err);
         } else if (ms.has) {
             // ---- page fetches: keys, or values ------------------------------------------------
             fetch_pages<D, kE4m3>(p, maps, ms.piece[0], ms.piece[1], warp == 11, ok, [&](uint32_t t, bool values) {
@@ -570,10 +569,13 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
             uint32_t n_q[2] = {0, 0}, tile = 0;
             // Only the first of these warps waits by polling, which takes issue slots; the others
             // meet it at a barrier of the hardware's, and learn there whether it gave up.
+            // (by turns two words: the first may be an appointment ahead of a warp that still reads)
+            uint32_t turn = 0;
             auto meet = [&] {
-                if (w == 0 && !ok) ms.rows_gave_up = 1;
+                if (w == 0 && !ok) ms.rows_gave_up[turn] = 1;
                 named_sync<4, kRowThreads>();
-                ok = ms.rows_gave_up == 0;
+                ok = ms.rows_gave_up[turn] == 0;
+                turn ^= 1;
             };
             while (ok && walk.next(p, it)) {
                 for (int s = 0; s < C::kQImages; ++s) {
