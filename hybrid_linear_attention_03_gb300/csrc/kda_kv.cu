@@ -41,7 +41,7 @@ struct AppendParams {
     int32_t rows_per_cta, heads_per_cta;
     int32_t half_rot, interleaved;
     float eps;
-    uint64_t turn[64];  // inv_freq / (2 pi) mod 1, in units of 2^-64 turns
+    uint64_t turn[64];  // inv_freq / (2 pi) mod 1, in units of 2^-64
 };
 
 template <typename Act> struct Vec;  // 16 bytes of activations
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
     if (blockIdx.y == 0 && warp == kThreads / 32 - 1) report_seqs(p.b, lane);
     __syncthreads();
     if constexpr (kRot != kNoRot) {
-        // angle p * f in turns is a 64-bit product mod 2^64: exact for any position
+        // angle p * f in turns is a 64-bit product mod 2^64, as good as the frequency there times the position
         for (int i = tid; i < p.rows_per_cta * p.half_rot; i += kThreads) {
             const int row = i / p.half_rot, pair = i % p.half_rot;
             const uint64_t ph = uint64_t(uint32_t(max(s_pos[row], 0))) * p.turn[pair];
@@ -478,6 +478,20 @@ int sm_count() {
     return sms > 0 ? sms : 152;
 }
 
+// f / (2 pi) mod 1 in units of 2^-64, within one of them (for |f| up to 1e12): the product with 1 / (2 pi) as a sum of
+// two doubles, the fractions of its halves taken exactly.  A position of 31 bits then turns by an angle that is off by
+// at most 2^-33 turns, 8e-10 (with the quotient as one double: by 5e-7).
+static uint64_t turn_of(double f) {
+    constexpr double kInvTwoPi = 0x1.45f306dc9c883p-3, kInvTwoPiRest = -0x1.6b01ec5417056p-57;
+    const double hi = f * kInvTwoPi, lo = std::fma(f, kInvTwoPi, -hi) + f * kInvTwoPiRest;
+    auto units = [](double t) {
+        t = std::remainder(t, 1.0);  // exact, in [-1/2, 1/2]
+        const uint64_t u = uint64_t(std::rint(std::fabs(t) * 0x1p64));
+        return t < 0 ? 0 - u : u;
+    };
+    return units(hi) + units(lo);
+}
+
 kda_status launch_append(const kda_kv_cache *c, const kda_qk_params *qp, const kda_kv_io *io, const kda_kv_batch *b,
                          cudaStream_t stream) {
     AppendParams p = {};
@@ -489,10 +503,7 @@ kda_status launch_append(const kda_kv_cache *c, const kda_qk_params *qp, const k
     if (qp) {
         p.wq = qp->q_norm_w, p.wk = qp->k_norm_w, p.eps = qp->eps;
         p.half_rot = qp->rot_dim / 2, p.interleaved = qp->interleaved;
-        for (int i = 0; i < p.half_rot; ++i) {
-            const double t = qp->inv_freq[i] / 6.283185307179586476925286766559, f = t - std::floor(t);
-            p.turn[i] = f < 1.0 ? uint64_t(f * 0x1p64) : 0;
-        }
+        for (int i = 0; i < p.half_rot; ++i) p.turn[i] = turn_of(qp->inv_freq[i]);
     }
     const int rows = b->max_rows, D = c->head_dim;
     const bool e4 = c->format == KDA_KV_E4M3;

@@ -506,8 +506,8 @@ typedef struct {
 
 /* Normalises and rotates q and k per head, writes q to q_out and k and v to
  * their pages (quantised once, from 32-bit values).  One launch.  p may be
- * NULL: no norm, no rotation.  Angles are exact to 32 bits at any position:
- * they are reduced in 64-bit fixed point.
+ * NULL: no norm, no rotation.  Angles are reduced in 64-bit fixed point, to
+ * within 8e-10 at any position, and their cosines and sines are good to 7e-8.
  * Errors: KDA_ERR_INVALID_ARG (null or misaligned pointers, bad sizes or
  * strides, only one of q and q_out), KDA_ERR_UNSUPPORTED (sizes outside the
  * lists above), KDA_ERR_CUDA.  n_seqs = 0 or max_rows = 0 is a no-op. */

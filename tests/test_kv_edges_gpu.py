@@ -3,6 +3,8 @@ finite, and what the plain tests of test_kv_gpu.py leave out.  Tolerances are th
 
 from __future__ import annotations
 
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -93,6 +95,38 @@ def test_empty_sequences_with_bad_lengths_are_reported(length, which):
     kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
     assert kda.kda_kv_poll_device_error(b.kv) == bad
     assert torch.equal(q_out, q) and torch.equal(ko, k) and torch.equal(vo, v) and not (out == 9.0).any()
+
+
+# ---- the last positions --------------------------------------------------------------------------------------------------
+
+def exact_angle(p, f):
+    """p * f in (-pi, pi], the product and its reduction exact (pi to 50 digits)."""
+    pi = Fraction("3.14159265358979323846264338327950288419716939937511")
+    x = Fraction(float(f)) * p
+    x -= 2 * pi * round(x / (2 * pi))
+    return float(x)
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0, None])
+def test_angles_of_the_last_positions(base):
+    """Angles are good to the cosine's 7e-8 up to the last position there is: a frequency in turns as a 53-bit number would
+    be off by up to 5e-7 there."""
+    page, d = 128, 128
+    last = 2 ** 31 - 1024
+    freq = ([base ** (-2.0 * i / d) for i in range(d // 2)] if base else
+            [-1.0, -0.3, 0.75, 1e-9, 37.5, 1000.0, -2500.125, 123456.789] * 8)
+    b = R.Batch([4], [4], 1, 1, d, page, F32, "act", seed=5)
+    table = torch.zeros(1, -(-last // page), dtype=torch.int32, device="cuda")
+    batch = kda.make_kv_batch(b.dev[0], torch.tensor([last], dtype=torch.int32, device="cuda"), table, max_rows=4, max_new=4)
+    q = torch.zeros(4, 1, d, device="cuda")
+    q[..., :d // 2] = 1.0
+    q_out, kv = torch.empty_like(q), torch.zeros_like(q)
+    kda.kda_kv_append(b.kv, kda.make_qk_params(None, None, 1e-5, freq), kda.make_kv_io(q, kv, kv, q_out), batch)
+    assert kda.kda_kv_poll_device_error(b.kv)[0] == kda.KDA_OK
+    ang = torch.tensor([[exact_angle(last - 4 + t, f) for f in freq] for t in range(4)], dtype=torch.float64)
+    got = q_out[:, 0].double().cpu()
+    worst = max(float((got[:, :d // 2] - ang.cos()).abs().max()), float((got[:, d // 2:] - ang.sin()).abs().max()))
+    assert worst <= 7.2e-8, worst
 
 
 # ---- values that are not finite ------------------------------------------------------------------------------------------
