@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(Warps<kE4m3>::kThreads, 1)
                         // by item parity: Q may be an item ahead of this side's threads, never two
                         const int qi = kByKeys ? 0 : s;
                         wait_for(ok, &ms.row_unit[qi][n_it & 1], (n_it >> 1) & 1, err);
-                        scale *= sc8.q_unit[n_it & 1][qi][row];
+                        // (never 0, which would make NaN of a masked score: rows of zeros have 2^-126 as their scale)
+                        scale = fmaxf(scale * sc8.q_unit[n_it & 1][qi][row], 0x1p-149f);
                     }
                     if (kByKeys || nv > 0) ++n_it;
                 }

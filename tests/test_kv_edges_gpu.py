@@ -169,3 +169,27 @@ def test_non_finite_values_stay_in_their_pair(d, rot, inter, norm, act, fmt):
         assert ((got - ref).abs() <= tol)[fin].all()
         if not norm and not e4m3:
             assert torch.equal(got[..., rot:].nan_to_num(), x[..., rot:].double().nan_to_num())
+
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("act", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new,hq,hkv,d", [(1, 2, 1, 128), (9, 2, 1, 128), (40, 8, 2, 128), (150, 4, 2, 64), (3, 2, 1, 32)])
+@pytest.mark.parametrize("scale", [1e-9, 1e-30, 2e-45])
+def test_rows_of_zeros_and_small_scales(scale, new, hq, hkv, d, act, fmt):
+    """A query of zeros weighs its keys alike, whatever the scale; so does any query at a scale this small."""
+    b = R.Batch([new], [new + 60], hq, hkv, d, 16, act, fmt, seed=89)
+    v = b.whole().randn(new + 60, hkv)
+    kda.kda_kv_append(b.kv, None, kda.make_kv_io(None, v.cuda(), v.cuda(), None), b.whole().batch)
+    ko, vo = (torch.empty(new + 60, hkv, d, dtype=act, device="cuda") for _ in range(2))
+    kda.kda_kv_read(b.kv, b.whole().batch, ko, vo)
+    q = b.randn(new, hq)
+    q[::2] = 0.0
+    out = torch.full_like(q, 9.0, device="cuda")
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q.cuda(), out, scale), b.batch, b.workspace())
+    assert kda.kda_kv_poll_device_error(b.kv)[0] == kda.KDA_OK
+    vo = vo.double().cpu()
+    for t in range(new):  # scores below 1e-6: weights alike to 1e-6
+        ref = vo[:61 + t].mean(0).repeat_interleave(hq // hkv, 0)
+        mag = vo[:61 + t].abs().mean(0).repeat_interleave(hq // hkv, 0)
+        tol = mag * (4e-6 + (2 * 2.0 ** -8 if act == BF else 0.0)) + (ref.abs() * 2.0 ** -8 if act == BF else 0.0)
+        assert ((out[t].double().cpu() - ref).abs() <= tol).all()
