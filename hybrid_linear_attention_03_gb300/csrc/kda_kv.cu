@@ -19,6 +19,7 @@
 // written and read in e4m3 9 us (launches).
 #include "kda_kv.cuh"
 
+#include <atomic>
 #include <cmath>
 
 namespace kda {
@@ -467,14 +468,15 @@ kda_status read_t(int D, ReadParams &p, int rows, cudaStream_t s) {
 }  // namespace
 
 int sm_count() {
-    static int cached[64] = {};
+    static std::atomic<int> cached[64] = {};  // calls may come from several threads
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
         cudaGetLastError();
         return 152;
     }
-    int sms = cached[dev];
-    if (sms == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) cached[dev] = sms;
+    int sms = cached[dev].load(std::memory_order_relaxed);
+    if (sms == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        cached[dev].store(sms, std::memory_order_relaxed);
     return sms > 0 ? sms : 152;
 }
 
