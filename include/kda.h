@@ -516,8 +516,10 @@ KDA_API kda_status kda_kv_append(const kda_kv_cache *cache, const kda_qk_params 
 
 /* Reads the batch's tokens back from their pages: k_out and v_out
  * [max_rows][num_kv_heads][head_dim] act, contiguous, 16-byte aligned.
- * KDA_KV_ACT lines come back bit for bit; e4m3 lines as value * 2^exponent
- * (exact in bf16 and fp32).  Errors as kda_kv_append's. */
+ * KDA_KV_ACT lines come back bit for bit; e4m3 lines as value * 2^exponent,
+ * exact but for two ends: magnitudes from 1.9375 * 2^127 on were rounded to
+ * 2^128, which is infinity in either type, and in bf16 values below 2^-126
+ * come back as multiples of 2^-133.  Errors as kda_kv_append's. */
 KDA_API kda_status kda_kv_read(const kda_kv_cache *cache, const kda_kv_batch *batch, void *k_out, void *v_out,
                                kda_stream_t stream);
 
@@ -526,6 +528,10 @@ KDA_API kda_status kda_kv_read(const kda_kv_cache *cache, const kda_kv_batch *ba
  * a decode step (max_new = 1), a speculative verify (a few) and a chunk of a
  * prompt; keys behind a row's position are never weighed, whatever they hold.
  * A row whose keys are all absent or score -inf gets zeros.
+ * Precision: scores, the softmax's sums and the outputs before their rounding
+ * are in 32 bits.  bf16 calls on the tensor cores round each weight to bf16
+ * (2^-8 of it) before it meets its value, not in the sum; over e4m3 pages
+ * elements of q below 2^-10 of their row's largest are rounded, by about 2^-18 of that at most.
  * workspace: device, 256-byte aligned, at least
  * kda_kv_attend_workspace_bytes(cache, batch) bytes (the host fields of batch
  * set it; 0 on invalid input); its contents mean nothing between calls, and

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 from fractions import Fraction
 
+import numpy as np
 import pytest
 import torch
 
@@ -12,6 +13,7 @@ from hybrid_linear_attention_03_gb300 import build as kbuild
 from hybrid_linear_attention_03_gb300 import kda
 
 import kv_ref as R
+from test_kv_gpu import check_attend, fill_cache, held, stored
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -193,3 +195,93 @@ def test_rows_of_zeros_and_small_scales(scale, new, hq, hkv, d, act, fmt):
         mag = vo[:61 + t].abs().mean(0).repeat_interleave(hq // hkv, 0)
         tol = mag * (4e-6 + (2 * 2.0 ** -8 if act == BF else 0.0)) + (ref.abs() * 2.0 ** -8 if act == BF else 0.0)
         assert ((out[t].double().cpu() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("act", [BF, F32], ids=["bf16", "f32"])
+def test_quantised_largest_and_smallest_values(act):
+    """The type's largest values (what rounds to 2^128 reads back as infinity), and vectors below every e4m3 step of the
+    smallest scale (in bf16 multiples of 2^-133 read back)."""
+    d, top = 16, torch.finfo(act).max
+    rows = torch.zeros(8, 1, d, dtype=torch.float64)
+    rows[0, 0, 0], rows[0, 0, 1] = top, -top / 3
+    rows[1, 0, 0] = -top
+    rows[2, 0, 0], rows[2, 0, 1] = 1.921875 * 2.0 ** 127, 1.0  # below the border at 1.9375 * 2^127
+    rows[3, 0, 0] = 1.75 * 2.0 ** 127
+    rows[4, 0] = torch.arange(d) * 2.0 ** -133
+    rows[5, 0, 0] = 2.0 ** -133
+    rows[6, 0, 0], rows[6, 0, 1] = 2.0 ** -126, -3 * 2.0 ** -133
+    rows[7, 0, 0], rows[7, 0, 1] = top, float("inf")
+    x = rows.to(act)
+    b = R.Batch([8], [8], 1, 1, d, 16, act, "e4m3")
+    kda.kda_kv_append(b.kv, None, kda.make_kv_io(None, x.cuda(), x.cuda(), None), b.batch)
+    qv, qe = R.quantise(x.double().numpy())
+    for vals, e in stored(b):
+        assert np.array_equal(e.numpy(), qe) and np.array_equal(vals.numpy(), qv, equal_nan=True)
+    ko, vo = (torch.empty(8, 1, d, dtype=act, device="cuda") for _ in range(2))
+    kda.kda_kv_read(b.kv, b.batch, ko, vo)
+    want = torch.from_numpy(qv * 2.0 ** (qe - 127.0)[..., None]).to(torch.float32).to(act)
+    assert torch.isinf(want[0, 0, 0]) and torch.isinf(want[1, 0, 0]) and torch.isfinite(want[2:7]).all()
+    for got in (ko, vo):
+        assert torch.equal(got.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+# ---- tighter looks at attention ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("act", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new,total,hq,hkv,d", [([1, 6], [300, 200], 4, 2, 64), ([1, 1], [900, 50], 16, 2, 128),
+                                                ([40, 7], [333, 7], 4, 2, 128), ([200], [390], 2, 1, 64),
+                                                ([3, 20], [100, 260], 2, 1, 32), ([1], [70], 3, 1, 16)])
+def test_far_apart_scores_pick_their_value(new, total, hq, hkv, d, act, fmt):
+    """Scores thousands apart: every row whose best key leads by more than the scores' error gives that key's value."""
+    b = R.Batch(new, total, hq, hkv, d, 16, act, fmt, seed=97)
+    cache = fill_cache(b, gain=100.0)
+    q = (b.randn(b.rows, hq) * 50).cuda()
+    out = torch.empty_like(q)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out, 1.0), b.batch, b.workspace())
+    assert kda.kda_kv_poll_device_error(b.kv)[0] == kda.KDA_OK
+    got, q = out.double().cpu(), q.double().cpu()
+    sure, at = 0, 0
+    for (T, L), (k, v) in zip(zip(new, total), cache):
+        for t in range(T):
+            for h in range(hq):
+                kk, vv, qq = k[:L - T + t + 1, h // b.group], v[:L - T + t + 1, h // b.group], q[at + t, h]
+                s, order = torch.sort(kk @ qq, descending=True)
+                # products and sums in 32 bits; with e4m3 keys q is good to 2^-18 of its largest channel
+                err = (d + 4) * 2.0 ** -24 * float(qq.norm() * kk.norm(dim=-1).max())
+                err += 2.0 ** -18 * float(qq.abs().max() * kk.abs().sum(-1).max())
+                if len(s) > 1 and float(s[0] - s[1]) < 40 + 2 * err:
+                    continue
+                sure += 1
+                ref = vv[order[0]]
+                # the others weigh e^-40 at most; bf16: rn(rn(w) v / w), two roundings by 2^-8 of what they round
+                tol = ref.abs() * (2 * 2.0 ** -8 + 2.0 ** -15 if act == BF else 2.0 ** -22) + 1e-12
+                assert ((got[at + t, h] - ref).abs() <= tol).all()
+        at += T
+    assert sure >= 0.8 * b.rows * hq
+
+
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("new,hq,hkv,d", [(4, 4, 2, 128), (100, 4, 2, 128), (300, 2, 1, 64), (20, 3, 1, 32)])
+def test_masked_values_may_be_anything_in_32_bits(bad, new, hq, hkv, d, fmt):
+    """The masked-value checks with the bound that 32-bit calls have, over all rows."""
+    total = new + 70
+    b = R.Batch([new], [total], hq, hkv, d, 32, F32, fmt, seed=11)
+    fill_cache(b)
+    at = total - new // 2
+    page, line = int(b.table[0, at // 32]), at % 32
+    last = int(b.table[0, (total - 1) // 32]), (total - 1) % 32
+    if fmt == "e4m3":
+        b.kv.v.view(torch.uint8)[page, :, line, 1] = 0xFF
+        b.kv.k.view(torch.uint8)[last[0], :, last[1], 0] = 0x7F
+    else:
+        b.kv.v[page, :, line, 1] = bad
+        b.kv.k[last[0], :, last[1], 0] = float("nan")
+    q = b.randn(b.rows, hq).cuda()
+    out = torch.empty_like(q)
+    kda.kda_kv_attend(b.kv, kda.make_attn_io(q, out), b.batch, b.workspace())
+    check_attend(b, q, out, held(b), d ** -0.5)
+    t_bad = at - (total - new)
+    assert torch.isfinite(out[:t_bad]).all() and not torch.isfinite(out[t_bad:, :, 1]).any()
+    assert torch.isfinite(out[t_bad:-1, :, 2:]).all() and torch.isnan(out[-1]).all()
