@@ -17,9 +17,12 @@
 // 398 us (6.7 TB/s, 99 % of the measured copy rate); the same in e4m3 318 us
 // (4.2 TB/s: widening the values and storing the weights bound it) against 447 with
 // the tile kernel; one sequence of 65536 in e4m3 46 us, of 1024 in bf16 13 us (launch,
-// one tile a CTA and the joining of parts).  With 32 or 64 rows a thread's share of a
-// tile grows and the tile kernel is faster: 237 against 247 us for 32 sequences of 8K
-// to 16K keys at 32 rows.
+// one tile a CTA and the joining of parts).
+// The border at 16 rows, us here and with the tile kernel: 128 sequences of 100 to 1500
+// tokens 91 and 100 (1 row: 83 and 97), in e4m3 107 and 146; 32 sequences of 8001 to 16384
+// 241 and 236 (1 row: 238 and 233), in e4m3 192 and 242.  So bf16 over long caches is level
+// from the first row on.  With 32 or 64 rows a thread's share of a tile grows and the
+// tile kernel is ahead everywhere (247 against 237 us at 32 rows over 8K to 16K).
 //
 // Warps: 0-3 softmax (a thread a key, later a channel), 4 issues the products, 5
 // and 6 fetch pages by TMA, 8-11 bring the rows of Q and look value tiles over, as in

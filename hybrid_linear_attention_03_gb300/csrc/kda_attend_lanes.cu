@@ -17,7 +17,7 @@
 // 128 channels 126 us for one or two rows (5.7 TB/s), 274 us for 8, 539 us for 16
 // (the tiles of kda_attend_generic.cu, which have room for more rows, 540 us for
 // any of these); bf16 pages of 32 channels 33 us for 2 rows, 50 for 4, 81 for 8,
-// where kda_attend_tile.cu takes 46 us for any number.
+// where kda_attend_tile.cu takes 42 us for any number (borders: lanes_plan).
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -281,7 +281,17 @@ template <typename Act, typename Kv> kda_status by_size(int D, AttendParams &p, 
 
 }  // namespace
 
-// The borders are where the kernel for more rows catches up (figures above).
+// The borders.  32 bits: where the kernel for more rows catches up (figures above).  bf16: us here and with
+// kda_attend_tile.cu, for 32 sequences of 3001 to 8192 tokens, and for 128 of 100 to 1500:
+//   channels  rows  bf16 pages             e4m3 pages
+//   16        2     23 / 40   20 / 42      23 / 59   20 / 62
+//   16        4     32 / 40   27 / 42      29 / 59   27 / 62
+//   32        2     33 / 42   25 / 45      30 / 60   22 / 64
+//   32        4     50 / 42   38 / 45      38 / 60   30 / 64
+//   64        2     48 / 44   36 / 47      55 / 62   39 / 66
+//   64        4     67 / 44   53 / 48      73 / 62   54 / 66
+// (3 rows as 4; one sequence of 3001 tokens: 14 to 17 us on either side up to 32 channels).  Up to 4 rows of at most
+// 32 channels is ahead in all but one of these, 32 channels of bf16 with 3 or 4 rows over long caches.
 bool lanes_plan(const kda_kv_cache *c, const kda_kv_batch *b, AttendPlan *plan) {
     const long long rows = static_cast<long long>(b->max_new) * (c->num_heads / c->num_kv_heads);
     if (c->act == KDA_BF16 ? rows > 4 || c->head_dim > 32 : rows > 16) return false;

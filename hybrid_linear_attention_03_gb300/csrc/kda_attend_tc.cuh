@@ -18,10 +18,19 @@ using namespace sm100;
 constexpr int KT = 128;  // keys of a tile
 
 // Barriers of a ring's tiles, more than it has stages: tile t lands in stage
-// t % stages but reports on barrier t % kBars.  A wait by parity is only sound for
-// a thread that sees every phase of its barrier, and a side that takes every
-// second tile sees every phase of every barrier it uses (kBars is even), whatever
-// the number of stages and the order in which copies land.
+// t % stages but reports on barrier t % kBars.  A wait for tile t by parity is sound
+// while the barrier is in t's phase or just past it.
+//   Not before: the phase of tile t - kBars has passed.  Inside an item that holds for
+// every role that takes all tiles or every second one, which has waited for that tile
+// itself (kBars is even).  From item to item it rests on the order of the items: an odd
+// number of tiles makes the sides swap barriers, a side may sit an item out, and the
+// softmax waits for values only where it checks them.  But nobody waits for an item's
+// tiles before its rows of Q (q_full, row_unit) or the scores that need them, and the
+// warps that bring those have first been through all value tiles (e4m3 in the tile
+// kernel: and key tiles) of the items before, and have waited for all their scores
+// (q_free).  Whoever brings Q earlier than that has to give these waits another order.
+//   Not two past: tile t + kBars takes a stage that the fetching warp finds free only
+// after it found that of tile t free, which t's users say when they are done with it.
 constexpr int kBars = 8;
 
 // ---- PTX ---------------------------------------------------------

@@ -45,13 +45,15 @@
 //
 // What bounds it: a half's products wait for its weights and its weights for its
 // scores; two sides with two halves each cover most of that, and tensor memory has
-// no columns for more (heads of 128: the tensor pipe is active in 64 % of the
-// cycles; heads of 64: the softmax threads are the slower part).  Measured, 64
-// heads over 8 cache heads of 128: a prompt of 8192 tokens 775 us (1420 TFLOP/s,
-// 73 % of the measured bf16 peak), 512 tokens behind 32256 410 us (69 %); in e4m3
-// pages the prompt takes 1098 us, bound by the threads that widen values and scale
+// no columns for more (heads of 128: the tensor pipe is active in 65 % of the
+// cycles; heads of 64 leave 128 columns idle, there the softmax threads are the slower
+// part).  Measured at 2070 MHz, 64
+// heads over 8 cache heads of 128: a prompt of 8192 tokens 771 us (1430 TFLOP/s,
+// 74 % of the measured bf16 peak), 512 tokens behind 32256 410 us (69 %); kept up for
+// seconds, under the power cap, 800 us at 1972 MHz and 437 us at 1762 MHz.  In e4m3
+// pages the prompt takes 1102 us, bound by the threads that widen values and scale
 // scores and by the second term of Q.  64 verifies of 8 tokens over 1000 to 8192
-// in e4m3 take 207 us (3.0 TB/s).  Heads of 64: the prompt 659 us.
+// in e4m3 take 208 us (3.0 TB/s).  Heads of 64: the prompt 670 us.
 #include "kda_attend_tc.cuh"
 
 namespace kda {

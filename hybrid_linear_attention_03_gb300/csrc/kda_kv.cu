@@ -12,10 +12,10 @@
 // rotation partners move by shuffles.
 // Measured, 64 heads over 8 cache heads of 128 in bf16: 8 ragged prompts of 511 to
 // 2049 tokens written in 82 us (5.3 TB/s, 79 % of the measured copy rate); 32768
-// tokens written in e4m3 and read back 316 us (4.5 TB/s: beside the bytes there is
+// tokens written in e4m3 and read back 318 us (4.4 TB/s: beside the bytes there is
 // the search for a vector's largest magnitude, and the keys' roundings are carried
 // along, which takes 13 us and halves the share of values that a rounding before
-// the last puts on the wrong side of an e4m3 border); one token 4.4 us, 64 of them
+// the last puts on the wrong side of an e4m3 border); one token 4.6 us, 64 of them
 // written and read in e4m3 9 us (launches).
 #include "kda_kv.cuh"
 
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
 // the row's heads (latency); the border is where one piece per thread fills every
 // SM once (64 heads over 8 of 128 in bf16, 240 rows: 9.5 us this way, 11.1 the
 // other; 320 rows: 12.4 and 11.1).  Many rows: 4, and 8 where that still gives every
-// place for a CTA four of them (32768 rows written and read in bf16 280 us against
-// 297, 10700 rows written 85 against 82).  More where a row's heads of one kind (at
+// place for a CTA four of them (32768 rows written and read in bf16 282 us against
+// 300, 10700 rows written 85 against 82).  More where a row's heads of one kind (at
 // most `kind`) are fewer than the lane groups that it would get (32768 rows of one
 // head and one cache head of 32 channels: 57 us at 4 rows a CTA, 17 at 32).
 struct RowSplit {

@@ -527,6 +527,9 @@ KDA_API kda_status kda_kv_read(const kda_kv_cache *cache, const kda_kv_batch *ba
  * tokens' own lines included, so kda_kv_append comes first).  One call serves
  * a decode step (max_new = 1), a speculative verify (a few) and a chunk of a
  * prompt; keys behind a row's position are never weighed, whatever they hold.
+ * The kernel is chosen by max_new (and the types and sizes), so a bound far
+ * above what the sequences bring, or single tokens beside a chunk, run as the
+ * chunk would: single tokens and chunks take less time in calls of their own.
  * A row whose keys are all absent or score -inf gets zeros.
  * Precision: scores, the softmax's sums and the outputs before their rounding
  * are in 32 bits.  bf16 calls on the tensor cores round each weight to bf16
