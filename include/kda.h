@@ -534,7 +534,8 @@ KDA_API kda_status kda_kv_read(const kda_kv_cache *cache, const kda_kv_batch *ba
  * Precision: scores, the softmax's sums and the outputs before their rounding
  * are in 32 bits.  bf16 calls on the tensor cores round each weight to bf16
  * (2^-8 of it) before it meets its value, not in the sum; over e4m3 pages
- * elements of q below 2^-10 of their row's largest are rounded, by about 2^-18 of that at most.
+ * elements of q below 2^-10 of their row's largest are rounded there, by
+ * about 2^-18 of that at most, and a row of q with an infinity or NaN gives NaN.
  * workspace: device, 256-byte aligned, at least
  * kda_kv_attend_workspace_bytes(cache, batch) bytes (the host fields of batch
  * set it; 0 on invalid input); its contents mean nothing between calls, and

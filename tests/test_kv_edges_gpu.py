@@ -225,6 +225,30 @@ def test_quantised_largest_and_smallest_values(act):
         assert torch.equal(got.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("fmt", ["act", "e4m3"])
+@pytest.mark.parametrize("act", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new,hq,hkv,d", [(1, 16, 2, 128), (9, 4, 2, 128), (150, 4, 2, 64), (40, 2, 1, 32), (1, 2, 1, 16)])
+def test_non_finite_queries_stay_in_their_row(new, hq, hkv, d, act, fmt):
+    """A query with a NaN or an infinity gives NaN (an infinity of keys of both signs is one of +inf scores) and leaves the
+    other heads and tokens alone."""
+    b = R.Batch([new, 1], [new + 90, 200], hq, hkv, d, 32, act, fmt, seed=101)
+    cache = fill_cache(b)
+    q = b.randn(b.rows, hq)
+    hit = [(0, 0, float("nan")), (new // 2, hq - 1, float("inf")), (new, 1, float("-inf"))]
+    clean = q.clone()
+    for t, h, x in hit:
+        q[t, h, d // 2] = x
+    out, want = (torch.empty_like(q, device="cuda") for _ in range(2))
+    for x, o in ((q, out), (clean, want)):
+        kda.kda_kv_attend(b.kv, kda.make_attn_io(x.cuda(), o), b.batch, b.workspace())
+        assert kda.kda_kv_poll_device_error(b.kv)[0] == kda.KDA_OK
+    check_attend(b, clean, want, cache, d ** -0.5)
+    for t, h, _ in hit:
+        assert torch.isnan(out[t, h]).all()
+        out[t, h] = want[t, h]
+    check_attend(b, clean, out, cache, d ** -0.5)
+
+
 # ---- tighter looks at attention ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", ["act", "e4m3"])
