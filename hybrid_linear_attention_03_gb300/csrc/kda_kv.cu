@@ -487,7 +487,7 @@ static uint64_t turn_of(double f) {
     constexpr double kInvTwoPi = 0x1.45f306dc9c883p-3, kInvTwoPiRest = -0x1.6b01ec5417056p-57;
     const double hi = f * kInvTwoPi, lo = std::fma(f, kInvTwoPi, -hi) + f * kInvTwoPiRest;
     auto units = [](double t) {
-        t = std::remainder(t, 1.0);  // exact, in [-1/2, 1/2]
+        t -= std::rint(t);  // exact, in [-1/2, 1/2] (std::remainder, the same, takes a microsecond for 64 pairs)
         const uint64_t u = uint64_t(std::rint(std::fabs(t) * 0x1p64));
         return t < 0 ? 0 - u : u;
     };
