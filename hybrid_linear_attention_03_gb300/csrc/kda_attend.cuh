@@ -88,7 +88,9 @@ struct Cursor {  // a place on the line: key `key` of item (n, h, tile)
 // The whole warp finds this CTA's piece [from, to) of the line; false if it
 // has none.  Lane i sums the sequences [i * per, (i + 1) * per), so the tables
 // are read twice: once for the sums, once inside the piece's sequence.
-__device__ __forceinline__ bool find_piece(const AttendParams &p, int cta, int n_cta, int lane, Cursor &from,
+// (P: the parameters of a kernel whose items are of this kind, with a batch view that load_seq reads.)
+template <typename P>
+__device__ __forceinline__ bool find_piece(const P &p, int cta, int n_cta, int lane, Cursor &from,
                                            Cursor &to) {
     const int N = p.b.n_seqs, per = (N + 31) / 32, tt = p.tile_tokens;
     const int n0 = min(lane * per, N), n1 = min(n0 + per, N);
@@ -187,7 +189,7 @@ struct ItemWalk {
     Seq sq;
     int tiles = -1;  // of sequence at.n; -1: not read yet
     __device__ __forceinline__ ItemWalk(const Cursor &a, const Cursor &z) : at(a), end(z) {}
-    __device__ __forceinline__ bool next(const AttendParams &p, Item &it) {
+    template <typename P> __device__ __forceinline__ bool next(const P &p, Item &it) {
         while (at.n < p.b.n_seqs && at.n <= end.n) {
             if (tiles < 0) tiles = load_seq(p.b, at.n, sq, false) ? (sq.T + p.tile_tokens - 1) / p.tile_tokens : 0;
             if (tiles == 0 || at.h >= p.hkv) {

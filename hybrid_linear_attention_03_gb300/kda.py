@@ -46,11 +46,13 @@ EXPORTS = ("kda_state_pool_bytes", "kda_state_pool_create", "kda_state_pool_dest
            "kda_prefix_cache_forget", "kda_prefix_cache_get_stats", "kda_prefix_cache_saved", "kda_stream_wait",
            "kda_state_pool_set_flags", "kda_profile_start", "kda_profile_stop", "kda_state_prefetch",
            "kda_kv_append", "kda_kv_read", "kda_kv_attend_workspace_bytes", "kda_kv_attend",
-           "kda_kv_poll_device_error")
+           "kda_kv_poll_device_error", "kda_latent_append", "kda_latent_read", "kda_latent_attend_workspace_bytes",
+           "kda_latent_attend", "kda_latent_prefill_workspace_bytes", "kda_latent_prefill", "kda_latent_poll_device_error")
 
 # kda_kernel_kind
 KERNEL_KINDS = ("step", "slot_copy", "prefill_meta", "prefill_intra", "prefill_chain", "prefill_out", "prefill_tails",
-                "state_prefetch", "prefill_intra_exact", "kv_append", "kv_read", "kv_attend", "kv_combine")
+                "state_prefetch", "prefill_intra_exact", "kv_append", "kv_read", "kv_attend", "kv_combine",
+                "latent_append", "latent_read", "latent_attend", "latent_prefill", "latent_combine")
 
 KDA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -123,6 +125,43 @@ class kda_kv_io(ctypes.Structure):
 class kda_attn_io(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
                 ("out_stride", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+class kda_latent_cache(ctypes.Structure):
+    _fields_ = [("c", ctypes.c_void_p), ("c_scale", ctypes.c_void_p), ("kr", ctypes.c_void_p), ("err", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
+class kda_latent_params(ctypes.Structure):
+    _fields_ = [("c_norm_w", ctypes.c_void_p), ("eps", ctypes.c_float), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class kda_latent_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("c", "kr", "q", "q_out")] + \
+               [(n, ctypes.c_int64) for n in ("c_stride", "kr_stride", "q_stride", "q_head_stride", "q_out_stride",
+                                              "q_out_head_stride")]
+
+
+class kda_latent_attn_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_c", "q_r", "out")] + \
+               [(n, ctypes.c_int64) for n in ("q_c_stride", "q_c_head_stride", "q_r_stride", "q_r_head_stride",
+                                              "out_stride", "out_head_stride")] + [("scale", ctypes.c_float)]
+
+
+class kda_latent_prefill_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_n", "q_r", "k", "kr", "v", "out")] + \
+               [(n, ctypes.c_int64) for n in ("q_n_stride", "q_n_head_stride", "q_r_stride", "q_r_head_stride", "k_stride",
+                                              "k_head_stride", "kr_stride", "v_stride", "v_head_stride", "out_stride",
+                                              "out_head_stride")] + \
+               [("nope_dim", ctypes.c_int32), ("value_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class kda_latent_prefill_batch(ctypes.Structure):
+    _fields_ = [("cu_seqlens", ctypes.c_void_p), ("cu_kv", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_kv_rows", ctypes.c_int32), ("max_new", ctypes.c_int32)]
 
 
 class KdaError(RuntimeError):
@@ -213,6 +252,21 @@ def lib() -> ctypes.CDLL:
         L.kda_kv_attend.restype = i32
         L.kda_kv_poll_device_error.argtypes = [P(kda_kv_cache), vp, P(ctypes.c_uint32)]
         L.kda_kv_poll_device_error.restype = i32
+        lc, lb = P(kda_latent_cache), P(kda_kv_batch)
+        L.kda_latent_append.argtypes = [lc, P(kda_latent_params), P(kda_latent_io), lb, vp]
+        L.kda_latent_append.restype = i32
+        L.kda_latent_read.argtypes = [lc, lb, vp, ctypes.c_int64, vp, ctypes.c_int64, vp]
+        L.kda_latent_read.restype = i32
+        L.kda_latent_attend_workspace_bytes.argtypes = [lc, lb]
+        L.kda_latent_attend_workspace_bytes.restype = sz
+        L.kda_latent_attend.argtypes = [lc, P(kda_latent_attn_io), lb, vp, sz, vp]
+        L.kda_latent_attend.restype = i32
+        L.kda_latent_prefill_workspace_bytes.argtypes = [lc, P(kda_latent_prefill_io), P(kda_latent_prefill_batch)]
+        L.kda_latent_prefill_workspace_bytes.restype = sz
+        L.kda_latent_prefill.argtypes = [lc, P(kda_latent_prefill_io), P(kda_latent_prefill_batch), vp, sz, vp]
+        L.kda_latent_prefill.restype = i32
+        L.kda_latent_poll_device_error.argtypes = [lc, vp, P(ctypes.c_uint32)]
+        L.kda_latent_poll_device_error.restype = i32
         L.kda_status_string.argtypes = [i32]
         L.kda_status_string.restype = ctypes.c_char_p
         _LIB = L
@@ -769,4 +823,217 @@ def kda_kv_poll_device_error(kv: PagedKV, stream=None) -> tuple[int, int]:
     flags = ctypes.c_uint32(0)
     st = int(lib().kda_kv_poll_device_error(kv.ref, _kv_stream(kv, None, stream, "kda_kv_poll_device_error"),
                                             ctypes.byref(flags)))
+    return st, int(flags.value)
+
+
+# ---- latent attention ---------------------------------------------------------------------
+
+
+class PagedLatent:
+    """A paged latent cache of one layer (a kda_latent_cache record and the tensors behind it).  c is [num_pages, page_size,
+    latent_dim] in ``act`` (kv_format "act") or float8_e4m3fn ("e4m3", with c_scale uint8 [num_pages, page_size]), kr
+    [num_pages, page_size, rope_dim] in ``act``; those not given are allocated, zero-filled, on ``device``."""
+
+    def __init__(self, num_pages, page_size, num_heads, latent_dim, rope_dim, act: torch.dtype = torch.bfloat16,
+                 kv_format: str = "act", c=None, kr=None, c_scale=None, device="cuda"):
+        if kv_format not in ("act", "e4m3"):
+            raise ValueError(f"kv_format must be \"act\" or \"e4m3\", not {kv_format!r}")
+        e4m3 = kv_format == "e4m3"
+        if not e4m3 and c_scale is not None:
+            raise ValueError("c_scale is for kv_format \"e4m3\"")
+        for t in (c, kr, c_scale):
+            if t is not None:
+                device = t.device
+                break
+
+        def made(t, name, dtype, *shape):
+            if t is not None:
+                return _kv_tensor(t, name, dtype, shape, device)
+            raw = torch.uint8 if dtype == torch.float8_e4m3fn else dtype
+            return torch.zeros(shape, dtype=raw, device=device).view(dtype)
+
+        self.c = made(c, "c", torch.float8_e4m3fn if e4m3 else act, num_pages, page_size, latent_dim)
+        self.c_scale = made(c_scale, "c_scale", torch.uint8, num_pages, page_size) if e4m3 else None
+        self.kr = made(kr, "kr", act, num_pages, page_size, rope_dim)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device, self.act, self.kv_format = self.c.device, act, kv_format
+        self.num_pages, self.page_size, self.num_heads = num_pages, page_size, num_heads
+        self.latent_dim, self.rope_dim = latent_dim, rope_dim
+        self.desc = kda_latent_cache(self.c.data_ptr(), _addr(self.c_scale), self.kr.data_ptr(), self.err.data_ptr(),
+                                     num_pages, page_size, num_heads, latent_dim, rope_dim, act_code(act),
+                                     KDA_KV_E4M3 if e4m3 else KDA_KV_ACT)
+        self.ref = ctypes.byref(self.desc)
+        # of row tensors, see _shape: a token's vectors, and the heads'
+        self.c_kind, self.kr_kind = (self.device, act, latent_dim), (self.device, act, rope_dim)
+        self.qc_kind, self.qr_kind = (self.device, act, num_heads, latent_dim), (self.device, act, num_heads, rope_dim)
+
+    def error_word(self) -> torch.Tensor:
+        return self.err
+
+
+def _strides(t, name, dims):
+    """Strides in elements of [rows, ..., channels] with the channels back to back (any that fits for an axis of one entry)."""
+    if t.dim() != dims or t.stride(-1) != 1:
+        raise ValueError(f"{name} must have {dims} axes, the last one contiguous")
+    return [t.stride(i) if t.shape[i] > 1 else t.shape[-1] for i in range(dims - 1)]
+
+
+def _shape(t):
+    """What a call checks of a row tensor: (device, type, sizes after the rows); None for no tensor."""
+    return None if t is None else (t.device, t.dtype, *t.shape[1:])
+
+
+def make_latent_params(c_norm_w: torch.Tensor | None = None, eps: float = 1e-5, inv_freq=(),
+                       interleaved: bool = False) -> kda_latent_params:
+    """The latents' norm weight (or None) and the rotation: inv_freq holds one frequency (radians per position) per rotated
+    pair, so 2 * len(inv_freq) channels of kr and q turn."""
+    freq = [float(f) for f in inv_freq]
+    arr = (ctypes.c_double * max(1, len(freq)))(*freq)
+    if c_norm_w is not None and (c_norm_w.dim() != 1 or not c_norm_w.is_contiguous()):
+        raise ValueError("c_norm_w must be a contiguous tensor [latent_dim]")
+    p = kda_latent_params(_addr(c_norm_w), float(eps), 2 * len(freq), int(bool(interleaved)),
+                          ctypes.cast(arr, ctypes.POINTER(ctypes.c_double)) if freq else None)
+    p._tensors = (c_norm_w, arr)
+    p._kind = None if c_norm_w is None else (c_norm_w.device, c_norm_w.dtype, c_norm_w.shape[0])
+    return p
+
+
+def make_latent_io(c: torch.Tensor, kr: torch.Tensor, q: torch.Tensor | None, q_out: torch.Tensor | None) -> kda_latent_io:
+    """c [rows, latent_dim], kr [rows, rope_dim], q and q_out [rows, heads, rope_dim] (or both None: cache only), any strides
+    over contiguous channels."""
+    heads = [_strides(t, n, 3) if t is not None else [0, 0] for n, t in (("q", q), ("q_out", q_out))]
+    io = kda_latent_io(c.data_ptr(), kr.data_ptr(), _addr(q), _addr(q_out), *_strides(c, "c", 2), *_strides(kr, "kr", 2),
+                       *heads[0], *heads[1])
+    io._tensors = (c, kr, q, q_out)
+    io._kinds = tuple(_shape(t) for t in io._tensors)
+    io._rows = min(t.shape[0] for t in io._tensors if t is not None)
+    return io
+
+
+def make_latent_attn_io(q_c: torch.Tensor, q_r: torch.Tensor, out: torch.Tensor, scale: float) -> kda_latent_attn_io:
+    """q_c and out [rows, heads, latent_dim], q_r [rows, heads, rope_dim], any strides over contiguous channels; scale is that
+    of the layer's scores, usually (nope_dim + rope_dim)^-0.5."""
+    io = kda_latent_attn_io(q_c.data_ptr(), q_r.data_ptr(), out.data_ptr(), *_strides(q_c, "q_c", 3), *_strides(q_r, "q_r", 3),
+                            *_strides(out, "out", 3), float(scale))
+    io._tensors = (q_c, q_r, out)
+    io._kinds = tuple(_shape(t) for t in io._tensors)
+    io._rows = min(t.shape[0] for t in io._tensors)
+    return io
+
+
+def make_latent_prefill_io(q_n: torch.Tensor, q_r: torch.Tensor, k: torch.Tensor, kr: torch.Tensor, v: torch.Tensor,
+                           out: torch.Tensor, scale: float | None = None) -> kda_latent_prefill_io:
+    """q_n [rows, heads, nope_dim], q_r [rows, heads, rope_dim], k [kv rows, heads, nope_dim], kr [kv rows, rope_dim], v [kv
+    rows, heads, value_dim], out [rows, heads, value_dim], any strides over contiguous channels; scale defaults to
+    (nope_dim + rope_dim)^-0.5."""
+    s = float(q_n.shape[-1] + q_r.shape[-1]) ** -0.5 if scale is None else float(scale)
+    io = kda_latent_prefill_io(q_n.data_ptr(), q_r.data_ptr(), k.data_ptr(), kr.data_ptr(), v.data_ptr(), out.data_ptr(),
+                               *_strides(q_n, "q_n", 3), *_strides(q_r, "q_r", 3), *_strides(k, "k", 3), *_strides(kr, "kr", 2),
+                               *_strides(v, "v", 3), *_strides(out, "out", 3), k.shape[-1], v.shape[-1], s)
+    io._tensors = (q_n, q_r, k, kr, v, out)
+    io._kinds = tuple(_shape(t) for t in io._tensors)
+    io._rows = min(t.shape[0] for t in (q_n, q_r, out))
+    io._kv_rows = min(t.shape[0] for t in (k, kr, v))
+    return io
+
+
+def make_latent_prefill_batch(cu_seqlens: torch.Tensor, cu_kv: torch.Tensor, max_rows: int, max_kv_rows: int,
+                              max_new: int) -> kda_latent_prefill_batch:
+    """The expanded form's device tables (int32 [n + 1] each) and host bounds; the record keeps the tensors alive."""
+    for name, t in (("cu_seqlens", cu_seqlens), ("cu_kv", cu_kv)):
+        if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or t.numel() < 1 or t.shape != cu_seqlens.shape \
+                or not t.is_contiguous() or t.device != cu_seqlens.device:
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor [n_seqs + 1], both on one device")
+    b = kda_latent_prefill_batch(cu_seqlens.data_ptr(), cu_kv.data_ptr(), cu_seqlens.numel() - 1, int(max_rows),
+                                 int(max_kv_rows), int(max_new))
+    b._tensors = (cu_seqlens, cu_kv)
+    b._device = cu_seqlens.device
+    return b
+
+
+def _check_kinds(where: str, names, kinds, want) -> None:
+    for name, kind, w in zip(names, kinds, want):
+        if kind is not None and kind != w:
+            raise ValueError(f"{where}: {name} must be (device, type, sizes after the rows) {w}, not {kind}")
+
+
+def _check_bound(where: str, what: str, bound: int, rows: int) -> None:
+    if rows < bound:
+        raise ValueError(f"{where}: the batch has up to {bound} {what}, the tensors {rows}")
+
+
+def _workspace(cache, workspace, where: str):
+    if workspace is None:
+        return None, 0
+    if workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"{where}: the workspace must be a contiguous tensor on {cache.device}")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def kda_latent_append(cache: PagedLatent, params: kda_latent_params | None, io: kda_latent_io, batch: kda_kv_batch,
+                      stream=None) -> None:
+    """Norm of c and rotation of kr and q; c and kr to their pages, q to q_out."""
+    where = "kda_latent_append"
+    _check_kinds(where, ("c", "kr", "q", "q_out"), io._kinds, (cache.c_kind, cache.kr_kind, cache.qr_kind, cache.qr_kind))
+    _check_bound(where, "rows", batch.max_rows, io._rows)
+    if params is not None:
+        _check_kinds(where, ("c_norm_w",), (params._kind,), (cache.c_kind,))
+        params = ctypes.byref(params)
+    st = lib().kda_latent_append(cache.ref, params, ctypes.byref(io), ctypes.byref(batch),
+                                 _kv_stream(cache, batch, stream, where))
+    if st != KDA_OK:
+        _check(st, "kda_latent_append")
+
+
+def kda_latent_read(cache: PagedLatent, batch: kda_kv_batch, c_out: torch.Tensor, kr_out: torch.Tensor, stream=None) -> None:
+    """The batch's tokens read back from their pages: c_out [rows, latent_dim], kr_out [rows, rope_dim]."""
+    where = "kda_latent_read"
+    _check_kinds(where, ("c_out", "kr_out"), (_shape(c_out), _shape(kr_out)), (cache.c_kind, cache.kr_kind))
+    _check_bound(where, "rows", batch.max_rows, min(c_out.shape[0], kr_out.shape[0]))
+    st = lib().kda_latent_read(cache.ref, ctypes.byref(batch), c_out.data_ptr(), *_strides(c_out, "c_out", 2),
+                               kr_out.data_ptr(), *_strides(kr_out, "kr_out", 2), _kv_stream(cache, batch, stream, where))
+    if st != KDA_OK:
+        _check(st, "kda_latent_read")
+
+
+def kda_latent_attend_workspace_bytes(cache: PagedLatent, batch: kda_kv_batch) -> int:
+    return int(lib().kda_latent_attend_workspace_bytes(cache.ref, ctypes.byref(batch)))
+
+
+def kda_latent_attend(cache: PagedLatent, io: kda_latent_attn_io, batch: kda_kv_batch, workspace: torch.Tensor,
+                      stream=None) -> None:
+    """The absorbed form, causal, of the batch's tokens over their sequences' pages."""
+    where = "kda_latent_attend"
+    _check_kinds(where, ("q_c", "q_r", "out"), io._kinds, (cache.qc_kind, cache.qr_kind, cache.qc_kind))
+    _check_bound(where, "rows", batch.max_rows, io._rows)
+    st = lib().kda_latent_attend(cache.ref, ctypes.byref(io), ctypes.byref(batch), *_workspace(cache, workspace, where),
+                                 _kv_stream(cache, batch, stream, where))
+    if st != KDA_OK:
+        _check(st, "kda_latent_attend")
+
+
+def kda_latent_prefill_workspace_bytes(cache: PagedLatent, io: kda_latent_prefill_io, batch: kda_latent_prefill_batch) -> int:
+    return int(lib().kda_latent_prefill_workspace_bytes(cache.ref, ctypes.byref(io), ctypes.byref(batch)))
+
+
+def kda_latent_prefill(cache: PagedLatent, io: kda_latent_prefill_io, batch: kda_latent_prefill_batch,
+                       workspace: torch.Tensor, stream=None) -> None:
+    """The expanded form, causal, over keys and values in rows; of the cache it takes heads, rope_dim, type and error word."""
+    where = "kda_latent_prefill"
+    d, a, h, n, v = cache.device, cache.act, cache.num_heads, io.nope_dim, io.value_dim
+    _check_kinds(where, ("q_n", "q_r", "k", "kr", "v", "out"), io._kinds,
+                 ((d, a, h, n), cache.qr_kind, (d, a, h, n), cache.kr_kind, (d, a, h, v), (d, a, h, v)))
+    _check_bound(where, "rows", batch.max_rows, io._rows)
+    _check_bound(where, "key rows", batch.max_kv_rows, io._kv_rows)
+    st = lib().kda_latent_prefill(cache.ref, ctypes.byref(io), ctypes.byref(batch), *_workspace(cache, workspace, where),
+                                  _kv_stream(cache, batch, stream, where))
+    if st != KDA_OK:
+        _check(st, "kda_latent_prefill")
+
+
+def kda_latent_poll_device_error(cache: PagedLatent, stream=None) -> tuple[int, int]:
+    """Returns (status, flags) of the cache's error word; reading clears it."""
+    flags = ctypes.c_uint32(0)
+    st = int(lib().kda_latent_poll_device_error(cache.ref, _kv_stream(cache, None, stream, "kda_latent_poll_device_error"),
+                                                ctypes.byref(flags)))
     return st, int(flags.value)

@@ -549,6 +549,144 @@ KDA_API kda_status kda_kv_attend(const kda_kv_cache *cache, const kda_attn_io *i
 /* kda_poll_device_error for a cache's error word. */
 KDA_API kda_status kda_kv_poll_device_error(const kda_kv_cache *cache, kda_stream_t stream, uint32_t *flags);
 
+/* ---- Latent attention: a paged cache of one latent vector a token -------
+ * Full-attention layers whose keys and values are products of one latent
+ * vector a token.  Source: "vLLM Kimi K3 지원", section "Prefill/Decode 분리
+ * (Disaggregation)" (the token-level MLA cache that moves beside the KDA
+ * states).  The pages print no formulas for them; these are, for the token at
+ * position p and all its heads together,
+ *   append   c <- c * w / sqrt(mean(c^2) + eps)
+ *            kr and each head's q_r rotated: (a, b) <- (a cos - b sin, a sin + b cos),
+ *            angle p * inv_freq[i], on pair i of the first rot_dim channels
+ *   absorbed o_h = sum_j softmax_j(scale * (q_c,h . c_j + q_r,h . kr_j)) c_j   over j <= p
+ *   expanded o_h = sum_j softmax_j(scale * (q_n,h . k_h,j + q_r,h . kr_j)) v_h,j over j <= p
+ * where a layer with up-projections U_k,h and U_v,h of the latent (k_h,j = U_k,h c_j,
+ * v_h,j = U_v,h c_j) has q_c,h = U_k,h^T q_n,h and applies U_v,h to the absorbed
+ * form's outputs.  Those products, like all projections, are the caller's.  The absorbed form
+ * reads a token's cache once for all heads (single tokens, drafts); the expanded one
+ * computes a fraction of it for each pair of tokens (prompts): its keys and values are
+ * products of what kda_latent_read brings back, or of the new tokens' own latents.
+ *
+ * The cache is plain device memory described by kda_latent_cache, one per layer:
+ *   c        [num_pages][page_size][latent_dim], in the activation dtype
+ *            (KDA_KV_ACT) or in e4m3 (KDA_KV_E4M3)
+ *   c_scale  KDA_KV_E4M3 only: [num_pages][page_size] bytes; a vector stands for
+ *            e4m3 * 2^(byte - 127), exponents and non-finite elements as in kda_kv_cache
+ *   kr       [num_pages][page_size][rope_dim], in the activation dtype
+ *   err      one device uint32, the cache's error word
+ * Pages, batches (kda_kv_batch), device errors and streams are as above; err is
+ * polled with kda_latent_poll_device_error. */
+typedef struct {
+    void *c;          /* 16-byte aligned */
+    uint8_t *c_scale; /* 16-byte aligned; NULL for KDA_KV_ACT */
+    void *kr;         /* 16-byte aligned */
+    uint32_t *err;
+    int32_t num_pages;  /* > 0 */
+    int32_t page_size;  /* 16, 32, 64 or 128 */
+    int32_t num_heads;  /* query heads, > 0 */
+    int32_t latent_dim; /* 128, 256 or 512 */
+    int32_t rope_dim;   /* 16, 32 or 64 */
+    int32_t act;        /* kda_dtype of rows, kr and norm weights */
+    int32_t format;     /* kda_kv_format of c */
+} kda_latent_cache;
+
+/* The norm and rotation of kda_latent_append. */
+typedef struct {
+    const void *c_norm_w; /* [latent_dim] act, 16-byte aligned; NULL: no norm */
+    float eps;
+    int32_t rot_dim;        /* 0 (no rotation) .. rope_dim, a multiple of 8 */
+    int32_t interleaved;    /* 0: pair i is channels (i, i + rot_dim/2); 1: (2i, 2i + 1) */
+    const double *inv_freq; /* HOST [rot_dim / 2]: radians per position (read during the call) */
+} kda_latent_params;
+
+/* Row tensors.  Every stride counts elements, is a multiple of 16 bytes, and is
+ * at least as long as what it steps over's innermost vector: rows of one projection, slices
+ * of them, and head-major tensors (a product's output) all fit. */
+typedef struct {
+    const void *c;  /* [rows][latent_dim] */
+    const void *kr; /* [rows][rope_dim] */
+    const void *q;  /* [rows][num_heads][rope_dim], or NULL with q_out: cache only */
+    void *q_out;    /* may be q itself (with the same strides) */
+    int64_t c_stride, kr_stride, q_stride, q_head_stride, q_out_stride, q_out_head_stride;
+} kda_latent_io;
+
+typedef struct {
+    const void *q_c; /* [rows][num_heads][latent_dim] */
+    const void *q_r; /* [rows][num_heads][rope_dim], rotated */
+    void *out;       /* [rows][num_heads][latent_dim]; must not overlap q_c or q_r */
+    int64_t q_c_stride, q_c_head_stride, q_r_stride, q_r_head_stride, out_stride, out_head_stride;
+    float scale; /* > 0, finite */
+} kda_latent_attn_io;
+
+typedef struct {
+    const void *q_n; /* [rows][num_heads][nope_dim] */
+    const void *q_r; /* [rows][num_heads][rope_dim], rotated */
+    const void *k;   /* [kv rows][num_heads][nope_dim] */
+    const void *kr;  /* [kv rows][rope_dim], rotated; one for all heads */
+    const void *v;   /* [kv rows][num_heads][value_dim] */
+    void *out;       /* [rows][num_heads][value_dim]; must not overlap the inputs */
+    int64_t q_n_stride, q_n_head_stride, q_r_stride, q_r_head_stride;
+    int64_t k_stride, k_head_stride, kr_stride, v_stride, v_head_stride, out_stride, out_head_stride;
+    int32_t nope_dim, value_dim; /* 64 or 128 each */
+    float scale;                 /* > 0, finite */
+} kda_latent_prefill_io;
+
+/* The expanded form's batch: sequence n owns the rows [cu_seqlens[n], cu_seqlens[n+1]),
+ * T_n of them, and the key and value rows [cu_kv[n], cu_kv[n+1]), L_n of them; its row t
+ * is the token at position L_n - T_n + t.  Both tables are DEVICE arrays, read when the
+ * call runs.  A sequence whose tables are inconsistent (either decreasing or past its
+ * bound, more than max_new tokens, L_n below T_n or past 2^31 - 1024) sets KDA_DEVERR_META
+ * and its rows are left as they were.  Rows past cu_seqlens[n_seqs] are neither read nor written. */
+typedef struct {
+    const int32_t *cu_seqlens; /* [n_seqs + 1], from 0 */
+    const int32_t *cu_kv;      /* [n_seqs + 1], from 0 */
+    int32_t n_seqs;
+    int32_t max_rows;    /* host bound on cu_seqlens[n_seqs] */
+    int32_t max_kv_rows; /* host bound on cu_kv[n_seqs]: k, kr and v have this many rows */
+    int32_t max_new;     /* host bound on the tokens of one sequence */
+} kda_latent_prefill_batch;
+
+/* Normalises the latents, rotates kr and q, writes c and kr to their pages (c quantised
+ * once, with the norm's roundings carried along) and q to q_out.  One launch.  p may be
+ * NULL: no norm, no rotation.  Angles as in kda_kv_append.
+ * Errors: KDA_ERR_INVALID_ARG (null or misaligned pointers, bad sizes or
+ * strides, only one of q and q_out), KDA_ERR_UNSUPPORTED (sizes outside the
+ * lists above), KDA_ERR_CUDA.  n_seqs = 0 or max_rows = 0 is a no-op. */
+KDA_API kda_status kda_latent_append(const kda_latent_cache *cache, const kda_latent_params *p, const kda_latent_io *io,
+                                     const kda_kv_batch *batch, kda_stream_t stream);
+
+/* Reads the batch's tokens back from their pages: c_out [max_rows][latent_dim] and kr_out
+ * [max_rows][rope_dim] act, rows c_stride and kr_stride elements apart (multiples of 16
+ * bytes), 16-byte aligned.  What comes back exactly stands at kda_kv_read; tokens of a page
+ * outside the cache come back as zeros.  Errors as kda_latent_append's. */
+KDA_API kda_status kda_latent_read(const kda_latent_cache *cache, const kda_kv_batch *batch, void *c_out, int64_t c_stride,
+                                   void *kr_out, int64_t kr_stride, kda_stream_t stream);
+
+/* The absorbed form, causal, of the batch's tokens over their sequences' pages (the tokens' own
+ * lines included).  Keys behind a row's position are never weighed, whatever they hold; a
+ * row whose keys are all absent or score -inf gets zeros.  Among the keys that a row sees, one with an
+ * infinity or NaN leaves what the formula gives, or, where its score is -inf, may add nothing at all.
+ * Precision: scores, the softmax's sums and the outputs before their rounding are in
+ * 32 bits; bf16 calls round each weight to bf16 (2^-8 of it) before it meets its value.
+ * workspace: device, 256-byte aligned, at least kda_latent_attend_workspace_bytes(cache,
+ * batch) bytes (the host fields set it; 0 on invalid input); its contents mean nothing
+ * between calls, and calls that share one must be ordered.  Results do not depend on it.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE, KDA_ERR_CUDA. */
+KDA_API size_t kda_latent_attend_workspace_bytes(const kda_latent_cache *cache, const kda_kv_batch *batch);
+KDA_API kda_status kda_latent_attend(const kda_latent_cache *cache, const kda_latent_attn_io *io, const kda_kv_batch *batch,
+                                     void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* The expanded form, causal, over keys and values in rows.  Of the cache it takes num_heads,
+ * rope_dim, act and err.  Masks, precision, workspace and errors as kda_latent_attend's. */
+KDA_API size_t kda_latent_prefill_workspace_bytes(const kda_latent_cache *cache, const kda_latent_prefill_io *io,
+                                                  const kda_latent_prefill_batch *batch);
+KDA_API kda_status kda_latent_prefill(const kda_latent_cache *cache, const kda_latent_prefill_io *io,
+                                      const kda_latent_prefill_batch *batch, void *workspace, size_t workspace_bytes,
+                                      kda_stream_t stream);
+
+/* kda_poll_device_error for a latent cache's error word. */
+KDA_API kda_status kda_latent_poll_device_error(const kda_latent_cache *cache, kda_stream_t stream, uint32_t *flags);
+
 /* Host watchdog: waits for the work enqueued on `stream` (NULL: the legacy
  * default stream) by polling it, for at most timeout_s seconds, instead of
  * blocking without limit.  KDA_OK once it has finished; KDA_ERR_TIMEOUT if it
@@ -591,6 +729,11 @@ typedef enum {
     KDA_KERNEL_KV_READ,        /* kda_kv_read */
     KDA_KERNEL_KV_ATTEND,      /* kda_kv_attend: scores, softmax and values over each CTA's share of the keys */
     KDA_KERNEL_KV_COMBINE,     /* kda_kv_attend: the shares of one row tile joined */
+    KDA_KERNEL_LATENT_APPEND,  /* kda_latent_append */
+    KDA_KERNEL_LATENT_READ,    /* kda_latent_read */
+    KDA_KERNEL_LATENT_ATTEND,  /* kda_latent_attend: as KDA_KERNEL_KV_ATTEND */
+    KDA_KERNEL_LATENT_PREFILL, /* kda_latent_prefill: as KDA_KERNEL_KV_ATTEND */
+    KDA_KERNEL_LATENT_COMBINE, /* either: the shares of one row tile joined */
     KDA_KERNEL_COUNT
 } kda_kernel_kind;
 typedef struct {
