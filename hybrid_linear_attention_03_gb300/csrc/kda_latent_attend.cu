@@ -131,21 +131,27 @@ void set_items(LatentRows &p, const AttendPlan &plan, int groups, int group, flo
 
 }  // namespace
 
-static AttendPlan choose(const kda_latent_cache *c, const kda_kv_batch *) {
+// The kernel of a call, from its sizes and types alone.
+struct LatentChoice {
     AttendPlan plan;
-    (void)c;
-    latent_generic_plan(&plan);
-    return plan;
+    kda_status (*launch)(const kda_latent_cache *, LatentParams &, const AttendPlan &, cudaStream_t);
+};
+static LatentChoice choose(const kda_latent_cache *c) {
+    LatentChoice ch;
+    if (latent_tile_plan(c, &ch.plan)) ch.launch = latent_tile_launch;
+    else latent_generic_plan(&ch.plan), ch.launch = latent_generic_launch;
+    return ch;
 }
 
-size_t latent_attend_workspace_bytes(const kda_latent_cache *c, const kda_kv_batch *b) {
-    const AttendPlan plan = choose(c, b);
+size_t latent_attend_workspace_bytes(const kda_latent_cache *c, const kda_kv_batch *) {
+    const AttendPlan plan = choose(c).plan;
     return share_bytes(plan.n_cta, plan.bm, c->latent_dim);
 }
 
 kda_status launch_latent_attend(const kda_latent_cache *c, const kda_latent_attn_io *io, const kda_kv_batch *b,
                                 void *workspace, cudaStream_t stream) {
-    const AttendPlan plan = choose(c, b);
+    const LatentChoice ch = choose(c);
+    const AttendPlan &plan = ch.plan;
     LatentParams p = {};
     p.b = make_view(c, b);
     p.q_a = io->q_c, p.q_r = io->q_r, p.out = io->out;
@@ -155,7 +161,7 @@ kda_status launch_latent_attend(const kda_latent_cache *c, const kda_latent_attn
     p.c = c->c, p.kr = c->kr, p.sc = c->c_scale, p.rope = c->rope_dim;
     const int groups = head_groups(c->num_heads, plan.bm);
     set_items(p, plan, groups, c->num_heads / groups, io->scale, workspace);
-    const kda_status st = latent_generic_launch(c, p, plan, stream);
+    const kda_status st = ch.launch(c, p, plan, stream);
     if (st != KDA_OK || p.b.max_len <= p.key_step) return st;  // sequences of one key step are never cut
     return combine(c->act, c->latent_dim, p, plan, b->max_new, stream);
 }

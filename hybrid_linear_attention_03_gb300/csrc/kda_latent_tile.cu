@@ -1,0 +1,470 @@
+// kda_latent_tile.cu -- kda_latent_attend for bf16 rows on the tensor cores.
+//
+// All heads share a key, and a key's first L channels are its value, so a tile of 64
+// keys lands in shared memory once and is read twice by the tensor cores: as it is for
+// the scores and, channels for rows, for the outputs,
+//   X = Q K^T  (64 rows x 64 keys, L + 64 channels),   O^T += C^T P^T  (L channels x rows).
+// Turned like that, O of 64 rows takes half of tensor memory (L / 128 times 64 columns);
+// the other way round 64 rows would take all of it and leave the scores no place.
+// Softmax in one pass as in kda_attend_tile.cu: a row's reference is its maximum at
+// the time it was last moved, and only moves when a score exceeds it by more than 8 (then the
+// four warps meet and scale O); until then a tile costs one vote.  The weights, bf16,
+// take the place of the tile's shared key part, which the scores have used by then.
+//
+// Warps: 0-3 softmax (two threads a row, later a thread a channel) and the rows of Q, 4
+// issues the products, 5 fetches pages by TMA.
+//
+// A latent behind a row's position weighs nothing, but 0 * NaN is NaN in the product.
+// So in the few tiles where some row does not see some key, the softmax warps zero the
+// latents of absent keys and the non-finite ones that not every row sees, once the scores
+// are there: a row that does see such a key has NaN for its weight, which is what
+// remains (or 0, for a score of -inf).
+#include "kda_attend_tc.cuh"
+#include "kda_latent.cuh"
+
+namespace kda {
+namespace kv {
+namespace {
+
+constexpr int KL = 64, BM = 64;       // keys of a tile, rows of an item
+constexpr int kBlock = 64 * 128;      // 64 rows of 64 channels, bf16, swizzled over 128 bytes
+constexpr int kThreads = 192;
+constexpr float kRefSlack = 8.f;
+
+template <int L> struct Cfg {
+    static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, matrix rows of O^T by 128
+    static constexpr int kQBytes = (NB + 1) * kBlock, kStage = (NB + 1) * kBlock;
+    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes;
+    static constexpr int kStages = kRoom / kStage < 6 ? kRoom / kStage : 6;
+    static constexpr int kMiscAt = kQBytes + kStages * kStage;
+    static constexpr int kColumns = L == 512 ? 512 : 256;  // tensor memory: scores by tile parity, O
+    static_assert(2 * KL + MT * BM <= kColumns && kStages >= 2, "room for two tiles");
+};
+
+struct alignas(16) Misc {
+    uint64_t full[6], empty[6];                  // by stage
+    uint64_t s_full[2], p_ready[2], o_done[2];   // by tile parity
+    uint64_t q_full, done;
+    uint32_t tmem;
+    int has;
+    Cursor piece[2];
+    alignas(16) float back[BM], inv[BM];  // what a move of the reference scales O by; an item's end: the rows' factors
+    long long out_at[BM];                 // element offsets of the rows in out
+};
+
+struct LatentMaps {
+    CUtensorMap c, kr;
+};
+
+// Lane l < 16 gets row l's columns [c, c + 32), lane l + 16 its columns [c + 32, c + 64), of the 16 rows a warp's
+// quarter of tensor memory holds of a product of 64.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], 32;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Barriers of the hardware's: 1 the votes, 2 the meetings of the 128 softmax threads.
+__device__ __forceinline__ bool any_of_128(bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(mine))
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ int tiles_of(const Item &it) { return (it.k1 - it.k0 + KL - 1) / KL; }
+// The table's entry for keys [kb + 16 lane, kb + 16 lane + 16) of the tile at kb (page 0 where there are none),
+// asked for a tile ahead.
+__device__ __forceinline__ int peek_page(const LatentParams &p, const Item &it, int kb, int lane) {
+    const int j = kb + lane * 16;
+    if (lane >= KL / 16 || j >= it.k1) return 0;
+    return p.b.table[size_t(it.n) * size_t(p.b.table_stride) + size_t(j >> p.b.page_shift)];
+}
+
+// Asks for the rows of Q (16-byte copies; rows past the item's, up to a warp's 16, are zeros).
+template <int L>
+__device__ __forceinline__ void ask_q(const LatentParams &p, const Item &it, unsigned char *q_img, int tid) {
+    const int c = tid & 7;
+#pragma unroll 1
+    for (int r = tid >> 3; r < ((it.rows + 15) & ~15); r += 16) {
+        long long row, head;
+        p.locate(it, min(r, it.rows - 1), row, head);
+        const bool there = r < it.rows;
+        const __nv_bfloat16 *a = static_cast<const __nv_bfloat16 *>(p.q_a) + row * p.qa_stride + head * p.qa_head + c * 8;
+        const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.q_r) + row * p.qr_stride + head * p.qr_head;
+        unsigned char *dst = q_img + sw128_chunk(r, c, 64);
+#pragma unroll
+        for (int k = 0; k < L / 64; ++k) cp_async16_or_zero(dst + k * kBlock, a + k * 64, there);
+        const bool in = c * 8 < p.rope;
+        cp_async16_or_zero(dst + (L / 64) * kBlock, b + (in ? c * 8 : 0), there && in);
+    }
+}
+
+// A tile in which some row does not see some key: zeroes the latents of absent keys and the non-finite ones that
+// not every row sees.  Two threads a key.
+template <int L>
+__device__ __noinline__ void look_over(const Item &it, int kb, uint32_t absent, unsigned char *tile, int tid) {
+    const int key = tid >> 1, j = kb + key, half = tid & 1;
+    const bool gone = j >= it.k1 || (absent >> (key / 16) & 1);
+    unsigned char *img = tile + key * 128;
+    auto piece = [&](int c) { return reinterpret_cast<uint4 *>(img + (c >> 3) * kBlock + (((c & 7) ^ (key & 7)) << 4)); };
+    bool bad = false;
+    if (!gone && j > it.ctx + it.tok0)
+        for (int c = half; c < L / 8; c += 2) bad |= odd_bf16(*piece(c));
+    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+    if (gone || bad)
+        for (int c = half; c < L / 8; c += 2) *piece(c) = make_uint4(0, 0, 0, 0);
+}
+
+template <int L>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_tile_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ LatentMaps maps) {
+    using C = Cfg<L>;
+    constexpr int NS = C::kStages, NB = C::NB, MT = C::MT;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc &ms = *reinterpret_cast<Misc *>(smem + C::kMiscAt);
+    unsigned char *ring = smem + C::kQBytes;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(&ms.full[i], 1), mbar_init(&ms.empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.o_done[i], 1);
+        mbar_init(&ms.q_full, 4), mbar_init(&ms.done, 1);
+        fence_mbar_init();
+    }
+    if (tid == 32) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.c) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.kr) : "memory");
+    }
+    if (warp == 4) tmem_alloc(&ms.tmem, C::kColumns);
+    wait_prior_kernel();
+    allow_next_kernel();
+    if (tid < 2) p.parts[2 * cta + tid].state = 0;
+    if (warp == 5) {
+        Cursor a, z;
+        const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
+        if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = ms.tmem, tm_o = tm + 2 * KL;
+    uint32_t *err = p.b.err;
+    bool ok = true;  // of this thread's waits
+
+    if (!ms.has) {
+    } else if (warp < 4) {
+        // ---- softmax: two threads a row, 32 keys each; for O: thread = channel of each 128 ----
+        const int row = 16 * warp + (lane & 15), key0 = (lane >> 4) * 32;
+        const uint32_t lanes = uint32_t(warp * 32) << 16;
+        ItemWalk walk(ms.piece[0], ms.piece[1]);
+        Item it = {};
+        uint32_t tile = 0;
+        auto put_q = [&] {
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&ms.q_full);
+        };
+        // O holds the product of tile t
+        auto wait_o = [&](uint32_t t) {
+            wait_for(ok, &ms.o_done[t & 1], (t >> 1) & 1, err);
+            __syncwarp();
+            tc_fence_after();
+        };
+        bool more = walk.next(p, it);
+        if (more) ask_q<L>(p, it, smem, tid), put_q();
+        while (more) {
+            const int nt = tiles_of(it), n_cols = (it.rows + 15) & ~15;
+            const bool live = 16 * warp < it.rows;  // this warp has rows of the item
+            const int lim = it.ctx + it.tok0 + p.token_of(min(row, it.rows - 1));  // last key the row sees
+            float ref = -INFINITY, l = 0.f;
+            int page = peek_page(p, it, it.k0, lane);
+            for (int v = 0; v < nt; ++v, ++tile) {
+                const int kb = it.k0 + v * KL;
+                const uint32_t absent = __ballot_sync(0xffffffffu, uint32_t(page) >= uint32_t(p.b.num_pages));
+                const bool check = absent != 0 || kb + KL - 1 > it.ctx + it.tok0;  // some row does not see some key
+                page = peek_page(p, it, kb + KL, lane);
+                unsigned char *stage = ring + tile % NS * C::kStage;
+                wait_for(ok, &ms.s_full[tile & 1], (tile >> 1) & 1, err);
+                __syncwarp();
+                tc_fence_after();
+                float x[32];
+                bool move = false;
+                float top = -INFINITY;
+                if (live) {
+                    tmem_ld_rows16(tm + lanes + (tile & 1) * KL, x);
+                    tmem_wait_ld();
+                    if (check) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int j = kb + key0 + i;
+                            if (j > lim || j >= it.k1 || (absent >> ((key0 + i) / 16) & 1)) x[i] = -INFINITY;
+                        }
+                    }
+                    float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int i = 4; i < 32; i += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[i + e]);
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    move = top > ref + kRefSlack;
+                }
+                if (any_of_128(move)) {
+                    const float f = move ? ex2(ref - top) : 1.f;
+                    if (live && lane < 16) ms.back[row] = f;
+                    if (move) ref = top, l *= f;
+                    named_sync<2, 128>();
+                    if (v > 0) {
+                        wait_o(tile - 1);
+#pragma unroll 1
+                        for (int c = 0; c < n_cols; c += 16) {
+                            float b[16];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 t = *reinterpret_cast<const float4 *>(&ms.back[c + i]);
+                                b[i] = t.x, b[i + 1] = t.y, b[i + 2] = t.z, b[i + 3] = t.w;
+                            }
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) {
+                                float o[16];
+                                tmem_ld16(tm_o + lanes + uint32_t(m * BM + c), o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= b[i];
+                                tmem_st16(tm_o + lanes + uint32_t(m * BM + c), o);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                if (live) {
+                    const float base = ref == -INFINITY ? 0.f : ref;
+                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), sh = make_float2(-base, -base);
+                    float2 sum = make_float2(0.f, 0.f);
+                    unsigned char *p_row = stage + NB * kBlock + row * 128;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float2 t = fma2(make_float2(x[i + 2 * e], x[i + 2 * e + 1]), sc, sh);
+                            t.x = ex2(t.x), t.y = ex2(t.y);
+                            sum = add2(sum, t);
+                            w[e] = pack_bf16(t.x, t.y);
+                        }
+                        *reinterpret_cast<uint4 *>(p_row + ((((key0 + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    l += sum.x + sum.y;
+                }
+                if (check) {
+                    const Item copy = it;
+                    look_over<L>(copy, kb, absent, stage, tid);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&ms.p_ready[tile & 1]);
+            }
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            // the item's scores are all there, so the rows of the next may take the place of its own
+            const Item was = it;
+            more = walk.next(p, it);
+            if (more) ask_q<L>(p, it, smem, tid);
+
+            // ---- output -----------------------------------------------------------------
+            const bool whole = was.whole();
+            float *data = p.part_data + (size_t(cta) * 2 + was.slot()) * size_t(BM) * (L + 2);
+            if (live && lane < 16) {
+                ms.inv[row] = !whole ? 1.f : l > 0.f || l != l ? 1.0f / l : 0.f;
+                if (row < was.rows) {
+                    long long token, head;
+                    p.locate(was, row, token, head);
+                    ms.out_at[row] = token * p.out_stride + head * p.out_head;
+                    if (!whole) data[BM * L + row] = ref, data[BM * L + BM + row] = l;
+                }
+            }
+            if (!whole && tid == 0) p.parts[2 * cta + was.slot()] = was.part();
+            wait_o(tile - 1);
+            named_sync<2, 128>();
+            if (more) put_q();
+#pragma unroll 1
+            for (int c = 0; c < n_cols; c += 16) {
+#pragma unroll 1
+                for (int m = 0; m < MT; ++m) {
+                    float o[16];
+                    tmem_ld16(tm_o + lanes + uint32_t(m * BM + c), o);
+                    tmem_wait_ld();
+                    const int ch = m * 128 + tid;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (c + i >= was.rows) break;
+                        if (whole)
+                            static_cast<__nv_bfloat16 *>(p.out)[ms.out_at[c + i] + ch] = __float2bfloat16_rn(o[i] * ms.inv[c + i]);
+                        else
+                            data[size_t(c + i) * L + ch] = o[i];
+                    }
+                }
+            }
+            tc_fence_before();  // the next item's products rewrite O
+            named_sync<2, 128>();  // and its end the rows' factors and places
+        }
+    } else if (warp == 4) {
+        // ---- products (converged warp, one lane issues; descriptors count 16-byte units) -------
+        const uint32_t id_s = idesc_bf16_f32(64, KL);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(ring));
+        const uint64_t v_desc = sdesc_sw128_mn(smem_u32(ring), kBlock);
+        const uint64_t p_desc = sdesc_sw128(smem_u32(ring + NB * kBlock));
+        ItemWalk walk(ms.piece[0], ms.piece[1]);
+        Item it = {};
+        uint32_t base = 0, n_q = 0;
+        auto scores = [&](uint32_t t) {
+            wait_for(ok, &ms.full[t % NS], (t / NS) & 1, err);
+            if (!(ok = __all_sync(0xffffffffu, ok))) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t kd = k_desc + uint64_t(t % NS * uint32_t(C::kStage >> 4));
+#pragma unroll
+                for (int k = 0; k < (NB + 1) * 4; ++k)
+                    mma_bf16(tm + (t & 1) * KL, q_desc + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2),
+                             kd + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), id_s, k > 0);
+                mma_commit(&ms.s_full[t & 1]);
+            }
+            __syncwarp();
+        };
+        while (ok && walk.next(p, it)) {
+            const int nt = tiles_of(it);
+            const uint32_t id_o = idesc_bf16_f32(128, (it.rows + 15) & ~15, true, false);
+            wait_for(ok, &ms.q_full, n_q++ & 1, err);
+            scores(base);
+            for (int v = 0; v < nt && ok; ++v) {
+                const uint32_t t = base + uint32_t(v);
+                if (v + 1 < nt) scores(t + 1);
+                wait_for(ok, &ms.p_ready[t & 1], (t >> 1) & 1, err);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t at = uint64_t(t % NS * uint32_t(C::kStage >> 4));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < KL / 16; ++k)
+                            mma_bf16(tm_o + uint32_t(m * BM), v_desc + at + uint64_t(m * 2 * (kBlock >> 4) + k * 128),
+                                     p_desc + at + uint64_t(k * 2), id_o, k > 0 || v > 0);
+                    mma_commit(&ms.o_done[t & 1]);
+                    mma_commit(&ms.empty[t % NS]);
+                }
+                __syncwarp();
+            }
+            base += uint32_t(nt);
+        }
+        // nothing of this CTA's is in flight when its tensor memory goes
+        if (elect_one()) mma_commit(&ms.done);
+        __syncwarp();
+        mbar_wait(&ms.done, 0, err);
+    } else {
+        // ---- page fetches ------------------------------------------------------------------
+        const int page_size = 1 << p.b.page_shift, box = min(page_size, KL);
+        ItemWalk walk(ms.piece[0], ms.piece[1]);
+        Item it = {};
+        uint32_t t = 0;
+        while (ok && walk.next(p, it)) {
+            auto page_at = [&](int kb) {
+                const int j = kb + lane * box;
+                return lane * box < KL && j < it.k1 ? load_page(p.b, it.n, j) : -1;
+            };
+            int next = page_at(it.k0);
+            for (int kb = it.k0; kb < it.k1 && ok; kb += KL, ++t) {
+                const int page = next, line = kb & (page_size - 1);  // a tile starts a box
+                next = page_at(kb + KL);
+                const uint32_t s = t % NS;
+                if (t >= NS) wait_for(ok, &ms.empty[s], (t / NS - 1) & 1, err);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+                if (lane == 0) mbar_arrive_expect_tx(&ms.full[s], uint32_t(__popc(there) * box * 128 * (NB + 1)));
+                __syncwarp();
+                unsigned char *dst = ring + s * C::kStage;
+                // lane = block of channels, the pages by turns
+                for (int i = 0; i < KL / box; ++i) {
+                    const int pg = __shfl_sync(0xffffffffu, page, i);
+                    if (pg < 0 || lane > NB) continue;
+                    if (lane < NB) tma_load_3d(dst + lane * kBlock + i * box * 128, &maps.c, &ms.full[s], lane * 64, line, pg);
+                    else tma_load_3d(dst + NB * kBlock + i * box * 128, &maps.kr, &ms.full[s], 0, line, pg);
+                }
+                __syncwarp();
+            }
+        }
+        // whichever role gives up, no copy is in flight when the CTA ends
+        for (uint32_t i = t - min(t, uint32_t(NS)); i < t; ++i) mbar_wait(&ms.full[i % NS], (i / NS) & 1, err);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc(tm, C::kColumns);
+}
+
+// [num_pages][page_size][channels]; a box is a tile's part of one page, 64 channels of it (zeros past the last
+// one: a shared key part of 16 or 32), swizzled over 128 bytes.
+inline bool latent_map(CUtensorMap *m, const void *base, const kda_latent_cache *c, int channels) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t D = cuuint64_t(channels), P = cuuint64_t(c->page_size);
+    const cuuint64_t dims[3] = {D, P, cuuint64_t(c->num_pages)};
+    const cuuint64_t strides[2] = {D * 2, D * P * 2};
+    const cuuint32_t box[3] = {64u, cuuint32_t(c->page_size < KL ? c->page_size : KL), 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int L> kda_status launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    using C = Cfg<L>;
+    LatentMaps maps;
+    if (!latent_map(&maps.c, c->c, c, L) || !latent_map(&maps.kr, c->kr, c, c->rope_dim)) return KDA_ERR_CUDA;
+    constexpr size_t smem = 1024 + C::kMiscAt + sizeof(Misc);
+    static_assert(smem <= 232448, "shared memory of a CTA");
+    if (!allow_smem<latent_tile_kernel<L>>(int(smem))) return KDA_ERR_CUDA;
+    p.key_step = KL;
+    p.item_cost = 2 * KL;
+    p.min_keys = 2 * KL;
+    const ProfScope prof(KDA_KERNEL_LATENT_ATTEND, stream);
+    return launch_overlapped(latent_tile_kernel<L>, dim3(unsigned(plan.n_cta)), kThreads, smem, stream, p, maps);
+}
+
+}  // namespace
+
+bool latent_tile_plan(const kda_latent_cache *c, AttendPlan *plan) {
+    if (c->act != KDA_BF16 || c->format != KDA_KV_ACT) return false;
+    plan->bm = BM;
+    plan->n_cta = sm_count();
+    return true;
+}
+
+kda_status latent_tile_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    switch (c->latent_dim) {
+        case 128: return launch<128>(c, p, plan, stream);
+        case 256: return launch<256>(c, p, plan, stream);
+        case 512: return launch<512>(c, p, plan, stream);
+    }
+    return KDA_ERR_UNSUPPORTED;
+}
+
+}  // namespace kv
+}  // namespace kda
