@@ -2,6 +2,7 @@
 // the workspace and the kernel that joins an item's parts (see kda_attend.cuh for the
 // sharing-out).
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_latent.cuh"
 
@@ -10,40 +11,73 @@ namespace kv {
 namespace {
 
 constexpr int kCombineThreads = 256;
-constexpr int kSlice = 128;  // channels that a warp joins of a row, four a lane (64 of values of 64)
+constexpr int kMaxCtas = 256;  // of an attention kernel's grid
 
-// Block (c, y): of the item whose first part CTA c left, eight (row, slice of channels)
-// pairs, one a warp: with M the largest of the parts' maxima,
+// A load that stays where it is written: the compiler moves plain ones to their uses, one after the other.
+__device__ __forceinline__ float2 load_now(const float *p) {
+    float2 v;
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
+// Block (x, y): of the x-th item that was cut, eight (row, slice of channels) pairs, one a
+// warp: with M the largest of the parts' maxima,
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// in the order of the parts.  The blocks of CTAs that cut no item return after one load; the others are a
-// chain of three round trips to L2, so the outputs of 16 parts are asked for at a time.
-template <typename Act, int D>
+// in the order of the parts.  A chain of three round trips to L2 (all CTAs' records, statistics,
+// outputs), so 16 loads of a lane are asked for at a time: of 16 parts where a slice is 64 channels, of
+// fewer where it is a whole row (many items: their blocks are then one wave).  Blocks go by items
+// that may be there and not by CTAs: empty ones took longer than the joining (one item: 14 us with them).
+template <typename Act, int D, int kSlice>
 __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const __grid_constant__ LatentRows p, int bm,
                                                                          int n_cta) {
-    constexpr int W = D < kSlice ? D : kSlice, kSlices = D / W, CPL = W / 32, kAhead = 16;
-    const int c = int(blockIdx.x), lane = int(threadIdx.x) & 31;
+    constexpr int kSlices = D / kSlice, kPieces = kSlice / 64, kMost = 16 / kPieces, kWords = kMaxCtas / 32;
+    const int lane = int(threadIdx.x) & 31;
     const int at = int(blockIdx.y) * (kCombineThreads / 32) + int(threadIdx.x >> 5);
-    const int r = at / kSlices, ch = at % kSlices * W + lane * CPL;
+    const int r = at / kSlices, ch = at % kSlices * kSlice + lane * 2;
     wait_prior_kernel();
     allow_next_kernel();
+    // bit i of word w: CTA 32 w + i left an item's first part, or one in its middle
+    uint32_t begins[kWords], goes_on[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        const int i = 32 * w + lane;
+        int first = 0, next = 0;
+        if (i < n_cta) first = p.parts[2 * i + 1].state, next = p.parts[2 * i].state;
+        begins[w] = __ballot_sync(0xffffffffu, first == 1);
+        goes_on[w] = __ballot_sync(0xffffffffu, next == 1);
+    }
+    int skip = int(blockIdx.x), c = -1;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        const int n = __popc(begins[w]);
+        if (c < 0 && skip < n) {
+            uint32_t left = begins[w];
+            for (; skip > 0; --skip) left &= left - 1;
+            c = 32 * w + __ffs(left) - 1;
+        }
+        skip -= n;
+    }
+    if (c < 0) return;
     const Part first = p.parts[2 * c + 1];
-    // the parts after CTA c's last one: the first parts of the CTAs behind it, up to the item's end
-    const int state = c + 1 + lane < n_cta ? p.parts[2 * (c + 1 + lane)].state : 2;
-    if (first.state != 1 || r >= first.rows) return;
-    unsigned ends = __ballot_sync(0xffffffffu, state != 1);
-    int n_parts = 1 + (ends ? __ffs(ends) : 32);
-    for (int base = c + 33; !ends && base < n_cta; base += 32) {
-        ends = __ballot_sync(0xffffffffu, base + lane >= n_cta || p.parts[2 * (base + lane)].state != 1);
-        n_parts += ends ? __ffs(ends) : 32;
+    if (r >= first.rows) return;
+    // its parts: CTA c's last one, then the first ones of the CTAs behind it up to one that ends the item
+    int n_parts = 2;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        const int from = c + n_parts - 1 - 32 * w;  // the next CTA to look at, in this word
+        if (from < 0 || from > 31) continue;
+        const uint32_t ends = ~goes_on[w] >> from;
+        n_parts += ends ? __ffs(ends) - 1 : 32 - from;
     }
     n_parts = min(n_parts, n_cta - c);
     const size_t stride = size_t(bm) * (D + 2);
     const float *data = p.part_data + size_t(2 * c) * stride;  // part i > 0 at 2 i strides, part 0 at one
-    float M = -INFINITY, l = 0.f, acc[CPL];
+    float M = -INFINITY, l = 0.f;
+    float2 acc[kPieces];
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) acc[e] = 0.f;
+    for (int e = 0; e < kPieces; ++e) acc[e] = make_float2(0.f, 0.f);
     for (int base = 0; base < n_parts; base += 32) {  // 32 parts a round, one statistics pair a lane
-        const int i = base + lane;
+        const int i = base + lane, cnt = min(32, n_parts - base);
         float m = -INFINITY, li = 0.f;
         if (i < n_parts) {
             const float *d = data + size_t(i == 0 ? 1 : 2 * i) * stride + size_t(bm) * D;
@@ -58,34 +92,32 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
         M = top;
         l = l * back + f * li;
 #pragma unroll
-        for (int e = 0; e < CPL; ++e) acc[e] *= back;
-        const int cnt = min(32, n_parts - base);
-        for (int i0 = 0; i0 < cnt; i0 += kAhead) {
-            float v[kAhead][CPL];
+        for (int e = 0; e < kPieces; ++e) acc[e].x *= back, acc[e].y *= back;
+        // outputs of N parts at a time, past the last one it again
+        auto add = [&](auto n, int k0) {
+            constexpr int N = decltype(n)::value;
+            float2 v[N][kPieces];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int ii = base + i0 + k;
+            for (int k = 0; k < N; ++k) {
+                const int ii = base + min(k0 + k, cnt - 1);
                 const float *d = data + size_t(ii == 0 ? 1 : 2 * ii) * stride + size_t(r) * D + ch;
 #pragma unroll
-                for (int e = 0; e < CPL; ++e) v[k][e] = 0.f;
-                if (i0 + k < cnt) {
-                    if constexpr (CPL == 4) {
-                        const float4 t = *reinterpret_cast<const float4 *>(d);
-                        v[k][0] = t.x, v[k][1] = t.y, v[k][2] = t.z, v[k][3] = t.w;
-                    } else {
-                        const float2 t = *reinterpret_cast<const float2 *>(d);
-                        v[k][0] = t.x, v[k][1] = t.y;
-                    }
-                }
+                for (int e = 0; e < kPieces; ++e) v[k][e] = load_now(d + e * 64);
             }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, (i0 + k) & 31);
-                if (i0 + k < cnt)
+            for (int k = 0; k < N; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                if (k0 + k < cnt)
 #pragma unroll
-                    for (int e = 0; e < CPL; ++e) acc[e] = fmaf(fk, v[k][e], acc[e]);
+                    for (int e = 0; e < kPieces; ++e)
+                        acc[e].x = fmaf(fk, v[k][e].x, acc[e].x), acc[e].y = fmaf(fk, v[k][e].y, acc[e].y);
             }
-        }
+        };
+        int k0 = 0;
+        if constexpr (kMost > 4)
+            for (; cnt - k0 > 4; k0 += kMost) add(std::integral_constant<int, kMost>(), k0);
+        constexpr int kRest = kMost < 4 ? kMost : 4;
+        for (; k0 < cnt; k0 += kRest) add(std::integral_constant<int, kRest>(), k0);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -94,30 +126,44 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
     Act *dst = static_cast<Act *>(p.out) + (static_cast<long long>(first.row) + t) * p.out_stride +
                (static_cast<long long>(first.h) * p.group + r - t * p.group) * p.out_head + ch;
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) dst[e] = from_f32<Act>(acc[e] * inv);
+    for (int e = 0; e < kPieces; ++e) {
+        if constexpr (sizeof(Act) == 2)
+            *reinterpret_cast<__nv_bfloat162 *>(dst + e * 64) = __floats2bfloat162_rn(acc[e].x * inv, acc[e].y * inv);
+        else
+            *reinterpret_cast<float2 *>(dst + e * 64) = make_float2(acc[e].x * inv, acc[e].y * inv);
+    }
 }
 
 template <typename Act, int D>
-kda_status combine_d(const LatentRows &p, const AttendPlan &plan, long long rows, cudaStream_t stream) {
-    const long long work = rows * (D < kSlice ? 1 : D / kSlice);
+kda_status combine_d(const LatentRows &p, const AttendPlan &plan, long long rows, long long items, cudaStream_t stream) {
+    const long long cut = std::min<long long>(items, plan.n_cta);
+    constexpr int kPer = kCombineThreads / 32;
+    // slices of 64 channels while their blocks are one wave of eight an SM
+    const bool wide = D > 64 && cut * rows * (D / 64) > 8LL * kPer * sm_count();
     const ProfScope prof(KDA_KERNEL_LATENT_COMBINE, stream);
-    return launch_overlapped(latent_combine_kernel<Act, D>,
-                             dim3(unsigned(plan.n_cta), unsigned((work + kCombineThreads / 32 - 1) / (kCombineThreads / 32))),
-                             kCombineThreads, 0, stream, p, plan.bm, plan.n_cta);
+    if constexpr (D > 64)
+        if (wide)
+            return launch_overlapped(latent_combine_kernel<Act, D, D>, dim3(unsigned(cut), unsigned((rows + kPer - 1) / kPer)),
+                                     kCombineThreads, 0, stream, p, plan.bm, plan.n_cta);
+    return launch_overlapped(latent_combine_kernel<Act, D, 64>,
+                             dim3(unsigned(cut), unsigned((rows * (D / 64) + kPer - 1) / kPer)), kCombineThreads, 0, stream, p,
+                             plan.bm, plan.n_cta);
 }
-template <typename Act> kda_status combine_t(int D, const LatentRows &p, const AttendPlan &plan, long long rows, cudaStream_t s) {
+template <typename Act>
+kda_status combine_t(int D, const LatentRows &p, const AttendPlan &plan, long long rows, long long items, cudaStream_t s) {
     switch (D) {
-        case 64: return combine_d<Act, 64>(p, plan, rows, s);
-        case 128: return combine_d<Act, 128>(p, plan, rows, s);
-        case 256: return combine_d<Act, 256>(p, plan, rows, s);
-        case 512: return combine_d<Act, 512>(p, plan, rows, s);
+        case 64: return combine_d<Act, 64>(p, plan, rows, items, s);
+        case 128: return combine_d<Act, 128>(p, plan, rows, items, s);
+        case 256: return combine_d<Act, 256>(p, plan, rows, items, s);
+        case 512: return combine_d<Act, 512>(p, plan, rows, items, s);
     }
     return KDA_ERR_UNSUPPORTED;
 }
-// rows: of a tile, at most
-kda_status combine(int act, int D, const LatentRows &p, const AttendPlan &plan, int max_new, cudaStream_t s) {
+// max_new and n_seqs bound the rows of a tile and the items there may be
+kda_status combine(int act, int D, const LatentRows &p, const AttendPlan &plan, int max_new, int n_seqs, cudaStream_t s) {
     const long long rows = std::min<long long>(p.tile_tokens, max_new) * p.group;
-    return act == KDA_BF16 ? combine_t<__nv_bfloat16>(D, p, plan, rows, s) : combine_t<float>(D, p, plan, rows, s);
+    const long long items = static_cast<long long>(n_seqs) * p.hkv * ((max_new - 1) / p.tile_tokens + 1);
+    return act == KDA_BF16 ? combine_t<__nv_bfloat16>(D, p, plan, rows, items, s) : combine_t<float>(D, p, plan, rows, items, s);
 }
 
 void set_items(LatentRows &p, const AttendPlan &plan, int groups, int group, float scale, void *workspace) {
@@ -140,6 +186,7 @@ static LatentChoice choose(const kda_latent_cache *c) {
     LatentChoice ch;
     if (latent_tile_plan(c, &ch.plan)) ch.launch = latent_tile_launch;
     else latent_generic_plan(&ch.plan), ch.launch = latent_generic_launch;
+    ch.plan.n_cta = std::min(ch.plan.n_cta, kMaxCtas);
     return ch;
 }
 
@@ -163,13 +210,14 @@ kda_status launch_latent_attend(const kda_latent_cache *c, const kda_latent_attn
     set_items(p, plan, groups, c->num_heads / groups, io->scale, workspace);
     const kda_status st = ch.launch(c, p, plan, stream);
     if (st != KDA_OK || p.b.max_len <= p.key_step) return st;  // sequences of one key step are never cut
-    return combine(c->act, c->latent_dim, p, plan, b->max_new, stream);
+    return combine(c->act, c->latent_dim, p, plan, b->max_new, b->n_seqs, stream);
 }
 
 static AttendPlan choose(const kda_latent_cache *c, const kda_latent_prefill_io *, const kda_latent_prefill_batch *) {
     AttendPlan plan;
     (void)c;
     latent_generic_plan(&plan);
+    plan.n_cta = std::min(plan.n_cta, kMaxCtas);
     return plan;
 }
 
@@ -194,7 +242,7 @@ kda_status launch_latent_prefill(const kda_latent_cache *c, const kda_latent_pre
     set_items(p, plan, c->num_heads, 1, io->scale, workspace);
     const kda_status st = prefill_generic_launch(c, io, p, plan, stream);
     if (st != KDA_OK || b->max_kv_rows <= p.key_step) return st;
-    return combine(c->act, io->value_dim, p, plan, b->max_new, stream);
+    return combine(c->act, io->value_dim, p, plan, b->max_new, b->n_seqs, stream);
 }
 
 }  // namespace kv

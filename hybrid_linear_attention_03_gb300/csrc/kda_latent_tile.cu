@@ -11,8 +11,13 @@
 // four warps meet and scale O); until then a tile costs one vote.  The weights, bf16,
 // take the place of the tile's shared key part, which the scores have used by then.
 //
+// A tile comes, is multiplied and leaves in parts of 128 channels, each with barriers of
+// its own: shared memory holds two tiles, and in whole ones the copies would wait
+// for the products and the products for the copies.
+//
 // Warps: 0-3 softmax (two threads a row, later a thread a channel) and the rows of Q, 4
-// issues the products, 5 fetches pages by TMA.
+// issues the scores, 5 fetches pages by TMA, 6 issues the outputs (a warp of its own, so that
+// neither product waits for what the other needs).
 //
 // A latent behind a row's position weighs nothing, but 0 * NaN is NaN in the product.
 // So in the few tiles where some row does not see some key, the softmax warps zero the
@@ -28,11 +33,11 @@ namespace {
 
 constexpr int KL = 64, BM = 64;       // keys of a tile, rows of an item
 constexpr int kBlock = 64 * 128;      // 64 rows of 64 channels, bf16, swizzled over 128 bytes
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr float kRefSlack = 8.f;
 
 template <int L> struct Cfg {
-    static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, matrix rows of O^T by 128
+    static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, its parts of 128 channels (matrix rows of O^T)
     static constexpr int kQBytes = (NB + 1) * kBlock, kStage = (NB + 1) * kBlock;
     static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes;
     static constexpr int kStages = kRoom / kStage < 6 ? kRoom / kStage : 6;
@@ -42,9 +47,9 @@ template <int L> struct Cfg {
 };
 
 struct alignas(16) Misc {
-    uint64_t full[6], empty[6];                  // by stage
+    uint64_t full[6][5], empty[6][5];            // by stage, the parts of the latents and the shared key parts
     uint64_t s_full[2], p_ready[2], o_done[2];   // by tile parity
-    uint64_t q_full, done;
+    uint64_t q_full, done[2];
     uint32_t tmem;
     int has;
     Cursor piece[2];
@@ -70,6 +75,16 @@ __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
         : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Four neighbouring lanes hold four values each: lane i of them gets everyone's i-th, in the order of the lanes.
+__device__ __forceinline__ void swap_4x4(float &a, float &b, float &c, float &d, int lane) {
+    auto swap = [&](float &x, float &y, int bit) {  // the lower lane's y for the upper one's x
+        const float t = __shfl_xor_sync(0xffffffffu, lane & bit ? x : y, bit);
+        if (lane & bit) x = t;
+        else y = t;
+    };
+    swap(a, b, 1), swap(c, d, 1), swap(a, c, 2), swap(b, d, 2);
 }
 
 // Barriers of the hardware's: 1 the votes, 2 the meetings of the 128 softmax threads.
@@ -142,9 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
 
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) mbar_init(&ms.full[i], 1), mbar_init(&ms.empty[i], 1);
+        for (int i = 0; i < NS; ++i)
+            for (int c = 0; c <= MT; ++c) mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.o_done[i], 1);
-        mbar_init(&ms.q_full, 4), mbar_init(&ms.done, 1);
+        mbar_init(&ms.q_full, 4), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
         fence_mbar_init();
     }
     if (tid == 32) {
@@ -304,86 +320,113 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_o(tile - 1);
             named_sync<2, 128>();
             if (more) put_q();
+            // a thread gets 16 rows of its channel; four neighbours swap them for four channels of a row each
+            const int ch0 = warp * 32 + (lane & ~3);
 #pragma unroll 1
             for (int c = 0; c < n_cols; c += 16) {
-#pragma unroll 1
-                for (int m = 0; m < MT; ++m) {
-                    float o[16];
-                    tmem_ld16(tm_o + lanes + uint32_t(m * BM + c), o);
-                    tmem_wait_ld();
-                    const int ch = m * 128 + tid;
+                float o[MT][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (c + i >= was.rows) break;
-                        if (whole)
-                            static_cast<__nv_bfloat16 *>(p.out)[ms.out_at[c + i] + ch] = __float2bfloat16_rn(o[i] * ms.inv[c + i]);
-                        else
-                            data[size_t(c + i) * L + ch] = o[i];
+                for (int m = 0; m < MT; ++m) tmem_ld16(tm_o + lanes + uint32_t(m * BM + c), o[m]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int g = 0; g < 16; g += 4) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) swap_4x4(o[m][g], o[m][g + 1], o[m][g + 2], o[m][g + 3], lane);
+                    const int r = c + g + (lane & 3);
+                    if (r < was.rows) {
+                        if (whole) {
+                            const float f = ms.inv[r];
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + ms.out_at[r] + ch0;
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+                                *reinterpret_cast<uint2 *>(dst + m * 128) = make_uint2(
+                                    pack_bf16(o[m][g] * f, o[m][g + 1] * f), pack_bf16(o[m][g + 2] * f, o[m][g + 3] * f));
+                        } else {
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+                                *reinterpret_cast<float4 *>(data + size_t(r) * L + ch0 + m * 128) =
+                                    make_float4(o[m][g], o[m][g + 1], o[m][g + 2], o[m][g + 3]);
+                        }
                     }
+                    __syncwarp();
                 }
             }
             tc_fence_before();  // the next item's products rewrite O
             named_sync<2, 128>();  // and its end the rows' factors and places
         }
     } else if (warp == 4) {
-        // ---- products (converged warp, one lane issues; descriptors count 16-byte units) -------
+        // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
         const uint32_t id_s = idesc_bf16_f32(64, KL);
         const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(ring));
+        ItemWalk walk(ms.piece[0], ms.piece[1]);
+        Item it = {};
+        uint32_t t = 0, n_q = 0;
+        while (ok && walk.next(p, it)) {
+            wait_for(ok, &ms.q_full, n_q++ & 1, err);
+            for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
+                const uint32_t s = t % NS;
+                if (t >= 2) wait_for(ok, &ms.p_ready[t & 1], ((t >> 1) - 1) & 1, err);  // the scores before have been read
+                const uint64_t kd = k_desc + uint64_t(s * uint32_t(C::kStage >> 4));
+                for (int c = 0; c <= MT && ok; ++c) {
+                    wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t at = uint64_t(c * 2 * (kBlock >> 4));
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (c < MT || k < 4)
+                                mma_bf16(tm + (t & 1) * KL, q_desc + at + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2),
+                                         kd + at + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), id_s, c > 0 || k > 0);
+                        if (c == MT) mma_commit(&ms.s_full[t & 1]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        // nothing of this CTA's is in flight when its tensor memory goes
+        if (elect_one()) mma_commit(&ms.done[0]);
+        __syncwarp();
+        mbar_wait(&ms.done[0], 0, err);
+    } else if (warp == 6) {
+        // ---- outputs, likewise ------------------------------------------------------------
         const uint64_t v_desc = sdesc_sw128_mn(smem_u32(ring), kBlock);
         const uint64_t p_desc = sdesc_sw128(smem_u32(ring + NB * kBlock));
         ItemWalk walk(ms.piece[0], ms.piece[1]);
         Item it = {};
-        uint32_t base = 0, n_q = 0;
-        auto scores = [&](uint32_t t) {
-            wait_for(ok, &ms.full[t % NS], (t / NS) & 1, err);
-            if (!(ok = __all_sync(0xffffffffu, ok))) return;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t kd = k_desc + uint64_t(t % NS * uint32_t(C::kStage >> 4));
-#pragma unroll
-                for (int k = 0; k < (NB + 1) * 4; ++k)
-                    mma_bf16(tm + (t & 1) * KL, q_desc + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2),
-                             kd + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), id_s, k > 0);
-                mma_commit(&ms.s_full[t & 1]);
-            }
-            __syncwarp();
-        };
+        uint32_t t = 0;
         while (ok && walk.next(p, it)) {
             const int nt = tiles_of(it);
             const uint32_t id_o = idesc_bf16_f32(128, (it.rows + 15) & ~15, true, false);
-            wait_for(ok, &ms.q_full, n_q++ & 1, err);
-            scores(base);
-            for (int v = 0; v < nt && ok; ++v) {
-                const uint32_t t = base + uint32_t(v);
-                if (v + 1 < nt) scores(t + 1);
+            for (int v = 0; v < nt && ok; ++v, ++t) {
                 wait_for(ok, &ms.p_ready[t & 1], (t >> 1) & 1, err);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t at = uint64_t(t % NS * uint32_t(C::kStage >> 4));
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                    for (int m = 0; m < MT; ++m) {
 #pragma unroll
                         for (int k = 0; k < KL / 16; ++k)
                             mma_bf16(tm_o + uint32_t(m * BM), v_desc + at + uint64_t(m * 2 * (kBlock >> 4) + k * 128),
                                      p_desc + at + uint64_t(k * 2), id_o, k > 0 || v > 0);
+                        mma_commit(&ms.empty[t % NS][m]);
+                    }
                     mma_commit(&ms.o_done[t & 1]);
-                    mma_commit(&ms.empty[t % NS]);
+                    mma_commit(&ms.empty[t % NS][MT]);
                 }
                 __syncwarp();
             }
-            base += uint32_t(nt);
         }
-        // nothing of this CTA's is in flight when its tensor memory goes
-        if (elect_one()) mma_commit(&ms.done);
+        if (elect_one()) mma_commit(&ms.done[1]);
         __syncwarp();
-        mbar_wait(&ms.done, 0, err);
-    } else {
+        mbar_wait(&ms.done[1], 0, err);
+    } else if (warp == 5) {
         // ---- page fetches ------------------------------------------------------------------
         const int page_size = 1 << p.b.page_shift, box = min(page_size, KL);
         ItemWalk walk(ms.piece[0], ms.piece[1]);
         Item it = {};
-        uint32_t t = 0;
+        uint32_t t = 0, asked = 0;  // tiles, and parts of them asked for
         while (ok && walk.next(p, it)) {
             auto page_at = [&](int kb) {
                 const int j = kb + lane * box;
@@ -394,24 +437,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int page = next, line = kb & (page_size - 1);  // a tile starts a box
                 next = page_at(kb + KL);
                 const uint32_t s = t % NS;
-                if (t >= NS) wait_for(ok, &ms.empty[s], (t / NS - 1) & 1, err);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-                if (lane == 0) mbar_arrive_expect_tx(&ms.full[s], uint32_t(__popc(there) * box * 128 * (NB + 1)));
-                __syncwarp();
+                const uint32_t there = __popc(__ballot_sync(0xffffffffu, page >= 0));
                 unsigned char *dst = ring + s * C::kStage;
-                // lane = block of channels, the pages by turns
-                for (int i = 0; i < KL / box; ++i) {
+                // a part at a time, as the outputs leave them: a lane a box
+                for (int c = 0; c <= MT; ++c) {
+                    const int blocks = c < MT ? 2 : 1, i = lane / blocks, b = 2 * c + lane % blocks;
                     const int pg = __shfl_sync(0xffffffffu, page, i);
-                    if (pg < 0 || lane > NB) continue;
-                    if (lane < NB) tma_load_3d(dst + lane * kBlock + i * box * 128, &maps.c, &ms.full[s], lane * 64, line, pg);
-                    else tma_load_3d(dst + NB * kBlock + i * box * 128, &maps.kr, &ms.full[s], 0, line, pg);
+                    if (t >= NS) wait_for(ok, &ms.empty[s][c], (t / NS - 1) & 1, err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&ms.full[s][c], there * uint32_t(box * 128 * blocks));
+                    ++asked;
+                    __syncwarp();
+                    if (i < KL / box && pg >= 0) {
+                        unsigned char *to = dst + b * kBlock + i * box * 128;
+                        if (c < MT) tma_load_3d(to, &maps.c, &ms.full[s][c], b * 64, line, pg);
+                        else tma_load_3d(to, &maps.kr, &ms.full[s][c], 0, line, pg);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
             }
         }
         // whichever role gives up, no copy is in flight when the CTA ends
-        for (uint32_t i = t - min(t, uint32_t(NS)); i < t; ++i) mbar_wait(&ms.full[i % NS], (i / NS) & 1, err);
+        for (uint32_t i = asked - min(asked, uint32_t(NS * (MT + 1))); i < asked; ++i) {
+            const uint32_t of = i / (MT + 1);
+            mbar_wait(&ms.full[of % NS][i % (MT + 1)], (of / NS) & 1, err);
+        }
     }
     tc_fence_before();
     __syncthreads();
