@@ -21,18 +21,22 @@ __device__ __forceinline__ float2 load_now(const float *p) {
 }
 
 // Block (x, y): of the x-th item that was cut, eight (row, slice of channels) pairs, one a
-// warp: with M the largest of the parts' maxima,
+// warp, or two, four warps sharing a pair's parts: with M the largest of the parts' maxima,
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// in the order of the parts.  A chain of three round trips to L2 (all CTAs' records, statistics,
+// in the order of the parts (of the four warps').  A chain of three round trips to L2 (all CTAs' records, statistics,
 // outputs), so 16 loads of a lane are asked for at a time: of 16 parts where a slice is 64 channels, of
 // fewer where it is a whole row (many items: their blocks are then one wave).  Blocks go by items
 // that may be there and not by CTAs: empty ones took longer than the joining (one item: 14 us with them).
-template <typename Act, int D, int kSlice>
+template <typename Act, int D, int kSlice, int kShare>
 __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const __grid_constant__ LatentRows p, int bm,
                                                                          int n_cta) {
     constexpr int kSlices = D / kSlice, kPieces = kSlice / 64, kMost = 16 / kPieces, kWords = kMaxCtas / 32;
-    const int lane = int(threadIdx.x) & 31;
-    const int at = int(blockIdx.y) * (kCombineThreads / 32) + int(threadIdx.x >> 5);
+    constexpr int kPairs = kCombineThreads / 32 / kShare;
+    static_assert(kShare == 1 || kPieces == 1, "shared sums of one piece a lane");
+    __shared__ float s_stat[kPairs][kShare][2];
+    __shared__ float2 s_acc[kPairs][kShare][32];
+    const int lane = int(threadIdx.x) & 31, pair = int(threadIdx.x >> 5) / kShare, share = int(threadIdx.x >> 5) % kShare;
+    const int at = int(blockIdx.y) * kPairs + pair;
     const int r = at / kSlices, ch = at % kSlices * kSlice + lane * 2;
     wait_prior_kernel();
     allow_next_kernel();
@@ -59,7 +63,7 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
     }
     if (c < 0) return;
     const Part first = p.parts[2 * c + 1];
-    if (r >= first.rows) return;
+    if (kShare == 1 && r >= first.rows) return;
     // its parts: CTA c's last one, then the first ones of the CTAs behind it up to one that ends the item
     int n_parts = 2;
 #pragma unroll
@@ -76,10 +80,11 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
     float2 acc[kPieces];
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) acc[e] = make_float2(0.f, 0.f);
-    for (int base = 0; base < n_parts; base += 32) {  // 32 parts a round, one statistics pair a lane
-        const int i = base + lane, cnt = min(32, n_parts - base);
+    const int per = (n_parts + kShare - 1) / kShare, begin = share * per, end = r < first.rows ? min(begin + per, n_parts) : begin;
+    for (int base = begin; base < end; base += 32) {  // 32 parts a round, one statistics pair a lane
+        const int i = base + lane, cnt = min(32, end - base);
         float m = -INFINITY, li = 0.f;
-        if (i < n_parts) {
+        if (i < end) {
             const float *d = data + size_t(i == 0 ? 1 : 2 * i) * stride + size_t(bm) * D;
             m = d[r], li = d[bm + r];
         }
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         top = fmaxf(top, M);
         const float ref = top == -INFINITY ? 0.f : top, back = exp2f(M - ref);
-        const float f = i < n_parts ? exp2f(m - ref) : 0.f;
+        const float f = i < end ? exp2f(m - ref) : 0.f;
         M = top;
         l = l * back + f * li;
 #pragma unroll
@@ -121,6 +126,23 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if constexpr (kShare > 1) {
+        if (lane == 0) s_stat[pair][share][0] = M, s_stat[pair][share][1] = l;
+        s_acc[pair][share][lane] = acc[0];
+        __syncthreads();
+        if (share != 0 || r >= first.rows) return;
+#pragma unroll
+        for (int g = 0; g < kShare; ++g) M = fmaxf(M, s_stat[pair][g][0]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        l = 0.f, acc[0] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < kShare; ++g) {
+            const float f = exp2f(s_stat[pair][g][0] - ref);
+            const float2 v = s_acc[pair][g][lane];
+            l = fmaf(f, s_stat[pair][g][1], l);
+            acc[0].x = fmaf(f, v.x, acc[0].x), acc[0].y = fmaf(f, v.y, acc[0].y);
+        }
+    }
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
     const int t = p.token_of(r);
     Act *dst = static_cast<Act *>(p.out) + (static_cast<long long>(first.row) + t) * p.out_stride +
@@ -134,20 +156,27 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
     }
 }
 
+template <typename Act, int D, int kSlice, int kShare>
+kda_status combine_as(const LatentRows &p, const AttendPlan &plan, long long rows, long long cut, cudaStream_t stream) {
+    constexpr int kPer = kCombineThreads / 32 / kShare;
+    const dim3 grid(unsigned(cut), unsigned((rows * (D / kSlice) + kPer - 1) / kPer));
+    // The blocks come as the attention's CTAs leave, and as many to an SM as it holds: shared memory that they do not
+    // use spreads them over the SMs (without it 64 of them met on 8 SMs: one sequence of 65536 tokens 84 us against 49).
+    const int per_sm = int((static_cast<long long>(grid.x) * grid.y + sm_count() - 1) / sm_count());
+    const size_t smem = per_sm >= 8 ? 0 : size_t(200 * 1024 / per_sm) & ~size_t(1023);
+    if (!allow_smem<latent_combine_kernel<Act, D, kSlice, kShare>>(200 * 1024)) return KDA_ERR_CUDA;
+    return launch_overlapped(latent_combine_kernel<Act, D, kSlice, kShare>, grid, kCombineThreads, smem, stream, p, plan.bm,
+                             plan.n_cta);
+}
 template <typename Act, int D>
 kda_status combine_d(const LatentRows &p, const AttendPlan &plan, long long rows, long long items, cudaStream_t stream) {
-    const long long cut = std::min<long long>(items, plan.n_cta);
-    constexpr int kPer = kCombineThreads / 32;
-    // slices of 64 channels while their blocks are one wave of eight an SM
-    const bool wide = D > 64 && cut * rows * (D / 64) > 8LL * kPer * sm_count();
+    const long long cut = std::min<long long>(items, plan.n_cta), one_wave = 8LL * 8 * sm_count();  // warps
     const ProfScope prof(KDA_KERNEL_LATENT_COMBINE, stream);
+    // few items, of many parts each: four warps share a slice's; many: a warp has a whole row
+    if (cut * rows * (D / 64) * 4 <= one_wave) return combine_as<Act, D, 64, 4>(p, plan, rows, cut, stream);
     if constexpr (D > 64)
-        if (wide)
-            return launch_overlapped(latent_combine_kernel<Act, D, D>, dim3(unsigned(cut), unsigned((rows + kPer - 1) / kPer)),
-                                     kCombineThreads, 0, stream, p, plan.bm, plan.n_cta);
-    return launch_overlapped(latent_combine_kernel<Act, D, 64>,
-                             dim3(unsigned(cut), unsigned((rows * (D / 64) + kPer - 1) / kPer)), kCombineThreads, 0, stream, p,
-                             plan.bm, plan.n_cta);
+        if (cut * rows * (D / 64) > one_wave) return combine_as<Act, D, D, 1>(p, plan, rows, cut, stream);
+    return combine_as<Act, D, 64, 1>(p, plan, rows, cut, stream);
 }
 template <typename Act>
 kda_status combine_t(int D, const LatentRows &p, const AttendPlan &plan, long long rows, long long items, cudaStream_t s) {

@@ -19,6 +19,9 @@
 // issues the scores, 5 fetches pages by TMA, 6 issues the outputs (a warp of its own, so that
 // neither product waits for what the other needs).
 //
+// e4m3 pages: eight more warps make one bf16 tile of the latents, scale included and
+// exact, a part at a time as the outputs of the tile before give its place back.
+//
 // A latent behind a row's position weighs nothing, but 0 * NaN is NaN in the product.
 // So in the few tiles where some row does not see some key, the softmax warps zero the
 // latents of absent keys and the non-finite ones that not every row sees, once the scores
@@ -33,21 +36,27 @@ namespace {
 
 constexpr int KL = 64, BM = 64;       // keys of a tile, rows of an item
 constexpr int kBlock = 64 * 128;      // 64 rows of 64 channels, bf16, swizzled over 128 bytes
-constexpr int kThreads = 224;
 constexpr float kRefSlack = 8.f;
 
-template <int L> struct Cfg {
+template <int L, bool kE4m3> struct Cfg {
     static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, its parts of 128 channels (matrix rows of O^T)
-    static constexpr int kQBytes = (NB + 1) * kBlock, kStage = (NB + 1) * kBlock;
-    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes;
+    // e4m3: eight warps that widen, and registers split by groups of four warps
+    static constexpr int kWiden = 8, kThreads = kE4m3 ? 512 : 224, kLaunch = 128, kSoftmax = 200, kOther = 104;
+    static_assert(kSoftmax + 3 * kOther <= 4 * kLaunch, "the split takes no more than the launch has");
+    static constexpr int kQBytes = (NB + 1) * kBlock;
+    static constexpr int kWide = kE4m3 ? NB * kBlock : 0;  // e4m3: one tile of latents as bf16
+    static constexpr int kPart = kE4m3 ? kBlock : 2 * kBlock;  // 128 channels of a tile as they come
+    static constexpr int kKrAt = MT * kPart, kStage = kKrAt + kBlock;  // the shared key part, later the weights
+    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes - kWide;
     static constexpr int kStages = kRoom / kStage < 6 ? kRoom / kStage : 6;
-    static constexpr int kMiscAt = kQBytes + kStages * kStage;
+    static constexpr int kWideAt = kQBytes, kRingAt = kWideAt + kWide, kMiscAt = kRingAt + kStages * kStage;
     static constexpr int kColumns = L == 512 ? 512 : 256;  // tensor memory: scores by tile parity, O
     static_assert(2 * KL + MT * BM <= kColumns && kStages >= 2, "room for two tiles");
 };
 
 struct alignas(16) Misc {
     uint64_t full[6][5], empty[6][5];            // by stage, the parts of the latents and the shared key parts
+    uint64_t wide_full[4], wide_free[4];         // e4m3, by part
     uint64_t s_full[2], p_ready[2], o_done[2];   // by tile parity
     uint64_t q_full, done[2];
     uint32_t tmem;
@@ -55,6 +64,7 @@ struct alignas(16) Misc {
     Cursor piece[2];
     alignas(16) float back[BM], inv[BM];  // what a move of the reference scales O by; an item's end: the rows' factors
     long long out_at[BM];                 // element offsets of the rows in out
+    alignas(16) uint8_t scale[6][KL];     // e4m3, by stage: the keys' scale exponents
 };
 
 struct LatentMaps {
@@ -114,6 +124,7 @@ __device__ __forceinline__ int peek_page(const LatentParams &p, const Item &it, 
 template <int L>
 __device__ __forceinline__ void ask_q(const LatentParams &p, const Item &it, unsigned char *q_img, int tid) {
     const int c = tid & 7;
+    const bool in = c * 8 < p.rope;
 #pragma unroll 1
     for (int r = tid >> 3; r < ((it.rows + 15) & ~15); r += 16) {
         long long row, head;
@@ -124,8 +135,25 @@ __device__ __forceinline__ void ask_q(const LatentParams &p, const Item &it, uns
         unsigned char *dst = q_img + sw128_chunk(r, c, 64);
 #pragma unroll
         for (int k = 0; k < L / 64; ++k) cp_async16_or_zero(dst + k * kBlock, a + k * 64, there);
-        const bool in = c * 8 < p.rope;
         cp_async16_or_zero(dst + (L / 64) * kBlock, b + (in ? c * 8 : 0), there && in);
+    }
+}
+
+// 16 e4m3 values times 2^(e - 127) as bf16, exactly.  Their sign, exponent and fraction in the places of a bf16's
+// are the value times 2^-120 (below e4m3's normal range too), so a packed product makes two.  NaN and factors past
+// bf16's range go by way of f16 and 32 bits.
+__device__ __forceinline__ void widen_bits(const uint4 &q, uint32_t e, uint32_t (&o)[8]) {
+    if (nan_codes(q) != 0 || e > 134) {
+        widen_e4m3(q, exp2_biased(int(e)), o);
+        return;
+    }
+    const uint32_t f = (e + 120) << 7 | (e + 120) << 23, in[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t t = __byte_perm(in[i / 2], 0, i & 1 ? 0x3424 : 0x1404);
+        const uint32_t v = (t >> 4 & 0x07f007f0u) | (t & 0x80008000u);
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&f));
+        o[i] = *reinterpret_cast<const uint32_t *>(&y);
     }
 }
 
@@ -145,20 +173,22 @@ __device__ __noinline__ void look_over(const Item &it, int kb, uint32_t absent, 
         for (int c = half; c < L / 8; c += 2) *piece(c) = make_uint4(0, 0, 0, 0);
 }
 
-template <int L>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int L, bool kE4m3>
+__global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     latent_tile_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ LatentMaps maps) {
-    using C = Cfg<L>;
-    constexpr int NS = C::kStages, NB = C::NB, MT = C::MT;
+    using C = Cfg<L, kE4m3>;
+    constexpr int NS = C::kStages, MT = C::MT;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc &ms = *reinterpret_cast<Misc *>(smem + C::kMiscAt);
-    unsigned char *ring = smem + C::kQBytes;
+    unsigned char *ring = smem + C::kRingAt, *wide = smem + C::kWideAt;
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i)
-            for (int c = 0; c <= MT; ++c) mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], 1);
+            for (int c = 0; c <= MT; ++c)
+                mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], kE4m3 && c < MT ? C::kWiden / MT : 1);
+        for (int c = 0; c < MT; ++c) mbar_init(&ms.wide_full[c], C::kWiden / MT), mbar_init(&ms.wide_free[c], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.o_done[i], 1);
         mbar_init(&ms.q_full, 4), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
         fence_mbar_init();
@@ -183,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *err = p.b.err;
     bool ok = true;  // of this thread's waits
 
-    if (!ms.has) {
-    } else if (warp < 4) {
+    if (warp < 4) {
+        if constexpr (kE4m3) set_regs<C::kSoftmax, C::kLaunch>();
         // ---- softmax: two threads a row, 32 keys each; for O: thread = channel of each 128 ----
         const int row = 16 * warp + (lane & 15), key0 = (lane >> 4) * 32;
         const uint32_t lanes = uint32_t(warp * 32) << 16;
@@ -203,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             tc_fence_after();
         };
-        bool more = walk.next(p, it);
+        bool more = ms.has && walk.next(p, it);
         if (more) ask_q<L>(p, it, smem, tid), put_q();
         while (more) {
             const int nt = tiles_of(it), n_cols = (it.rows + 15) & ~15;
@@ -274,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float base = ref == -INFINITY ? 0.f : ref;
                     const float2 sc = make_float2(p.scale_log2, p.scale_log2), sh = make_float2(-base, -base);
                     float2 sum = make_float2(0.f, 0.f);
-                    unsigned char *p_row = stage + NB * kBlock + row * 128;
+                    unsigned char *p_row = stage + C::kKrAt + row * 128;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         uint32_t w[4];
@@ -291,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (check) {
                     const Item copy = it;
-                    look_over<L>(copy, kb, absent, stage, tid);
+                    look_over<L>(copy, kb, absent, kE4m3 ? wide : stage, tid);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -354,114 +384,173 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();  // the next item's products rewrite O
             named_sync<2, 128>();  // and its end the rows' factors and places
         }
-    } else if (warp == 4) {
-        // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
-        const uint32_t id_s = idesc_bf16_f32(64, KL);
-        const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(ring));
-        ItemWalk walk(ms.piece[0], ms.piece[1]);
-        Item it = {};
-        uint32_t t = 0, n_q = 0;
-        while (ok && walk.next(p, it)) {
-            wait_for(ok, &ms.q_full, n_q++ & 1, err);
-            for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
-                const uint32_t s = t % NS;
-                if (t >= 2) wait_for(ok, &ms.p_ready[t & 1], ((t >> 1) - 1) & 1, err);  // the scores before have been read
-                const uint64_t kd = k_desc + uint64_t(s * uint32_t(C::kStage >> 4));
-                for (int c = 0; c <= MT && ok; ++c) {
-                    wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t at = uint64_t(c * 2 * (kBlock >> 4));
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (c < MT || k < 4)
-                                mma_bf16(tm + (t & 1) * KL, q_desc + at + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2),
-                                         kd + at + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), id_s, c > 0 || k > 0);
-                        if (c == MT) mma_commit(&ms.s_full[t & 1]);
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-        // nothing of this CTA's is in flight when its tensor memory goes
-        if (elect_one()) mma_commit(&ms.done[0]);
-        __syncwarp();
-        mbar_wait(&ms.done[0], 0, err);
-    } else if (warp == 6) {
-        // ---- outputs, likewise ------------------------------------------------------------
-        const uint64_t v_desc = sdesc_sw128_mn(smem_u32(ring), kBlock);
-        const uint64_t p_desc = sdesc_sw128(smem_u32(ring + NB * kBlock));
+    } else if (kE4m3 && warp >= 8) {
+        // ---- latents made bf16, scale included and exact: a warp has some keys of one part; 8 neighbouring lanes take
+        // the same 16-byte piece of 8 keys, which both tiles' swizzles put into different banks ------
+        if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
+        const int c = (warp - 8) % MT, key = (warp - 8) / MT * (8 * MT) + (lane & 7), pc = lane >> 3;
+        unsigned char *to = wide + 2 * c * kBlock + key * 128;
         ItemWalk walk(ms.piece[0], ms.piece[1]);
         Item it = {};
         uint32_t t = 0;
-        while (ok && walk.next(p, it)) {
-            const int nt = tiles_of(it);
-            const uint32_t id_o = idesc_bf16_f32(128, (it.rows + 15) & ~15, true, false);
-            for (int v = 0; v < nt && ok; ++v, ++t) {
-                wait_for(ok, &ms.p_ready[t & 1], (t >> 1) & 1, err);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t at = uint64_t(t % NS * uint32_t(C::kStage >> 4));
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                        for (int k = 0; k < KL / 16; ++k)
-                            mma_bf16(tm_o + uint32_t(m * BM), v_desc + at + uint64_t(m * 2 * (kBlock >> 4) + k * 128),
-                                     p_desc + at + uint64_t(k * 2), id_o, k > 0 || v > 0);
-                        mma_commit(&ms.empty[t % NS][m]);
-                    }
-                    mma_commit(&ms.o_done[t & 1]);
-                    mma_commit(&ms.empty[t % NS][MT]);
-                }
-                __syncwarp();
-            }
-        }
-        if (elect_one()) mma_commit(&ms.done[1]);
-        __syncwarp();
-        mbar_wait(&ms.done[1], 0, err);
-    } else if (warp == 5) {
-        // ---- page fetches ------------------------------------------------------------------
-        const int page_size = 1 << p.b.page_shift, box = min(page_size, KL);
-        ItemWalk walk(ms.piece[0], ms.piece[1]);
-        Item it = {};
-        uint32_t t = 0, asked = 0;  // tiles, and parts of them asked for
-        while (ok && walk.next(p, it)) {
-            auto page_at = [&](int kb) {
-                const int j = kb + lane * box;
-                return lane * box < KL && j < it.k1 ? load_page(p.b, it.n, j) : -1;
-            };
-            int next = page_at(it.k0);
-            for (int kb = it.k0; kb < it.k1 && ok; kb += KL, ++t) {
-                const int page = next, line = kb & (page_size - 1);  // a tile starts a box
-                next = page_at(kb + KL);
+        while (ok && ms.has && walk.next(p, it)) {
+            for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
                 const uint32_t s = t % NS;
-                const uint32_t there = __popc(__ballot_sync(0xffffffffu, page >= 0));
-                unsigned char *dst = ring + s * C::kStage;
-                // a part at a time, as the outputs leave them: a lane a box
-                for (int c = 0; c <= MT; ++c) {
-                    const int blocks = c < MT ? 2 : 1, i = lane / blocks, b = 2 * c + lane % blocks;
-                    const int pg = __shfl_sync(0xffffffffu, page, i);
-                    if (t >= NS) wait_for(ok, &ms.empty[s][c], (t / NS - 1) & 1, err);
+                if (c > 0) wait_for(ok, &ms.full[s][0], (t / NS) & 1, err);  // the scales
+                wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
+                __syncwarp();
+                const unsigned char *raw = ring + s * C::kStage + c * kBlock;
+                uint4 x[MT][2];
+                uint32_t e[MT];
+#pragma unroll
+                for (int g = 0; g < MT; ++g) {
+                    e[g] = ms.scale[s][key + 8 * g];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        x[g][u] = *reinterpret_cast<const uint4 *>(raw + row8_piece<128>(key + 8 * g, pc + 4 * u));
+                }
+                if (t > 0) wait_for(ok, &ms.wide_free[c], (t - 1) & 1, err);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+#pragma unroll
+                for (int g = 0; g < MT; ++g)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {  // pieces 0-3 are the first 64 channels
+                        uint32_t o[8];
+                        widen_bits(x[g][u], e[g], o);
+                        unsigned char *at = to + u * kBlock + g * 1024;
+                        *reinterpret_cast<uint4 *>(at + (((2 * pc) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(at + (((2 * pc + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.wide_full[c]), mbar_arrive(&ms.empty[s][c]);
+            }
+        }
+    } else {
+        if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
+        if (!ms.has) {
+        } else if (warp == 4) {
+            // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
+            const uint32_t id_s = idesc_bf16_f32(64, KL);
+            const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(kE4m3 ? wide : ring));
+            const uint64_t kr_desc = sdesc_sw128(smem_u32(ring + C::kKrAt));
+            ItemWalk walk(ms.piece[0], ms.piece[1]);
+            Item it = {};
+            uint32_t t = 0, n_q = 0;
+            while (ok && walk.next(p, it)) {
+                wait_for(ok, &ms.q_full, n_q++ & 1, err);
+                for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
+                    const uint32_t s = t % NS;
+                    // The scores before in this place have been read, and their product is done: so whoever sees
+                    // the scores of tile t knows that o_done is at most a tile behind.
+                    if (t >= 2) wait_for(ok, &ms.o_done[t & 1], ((t >> 1) - 1) & 1, err);
+                    const uint64_t stage = uint64_t(s * uint32_t(C::kStage >> 4));
+                    // (unrolled: a product whose descriptors are worked out as it goes takes twice as long)
+                    const uint64_t kd = k_desc + (kE4m3 ? 0 : stage), krd = kr_desc + stage;
+#pragma unroll
+                    for (int c = 0; c <= MT; ++c) {
+                        if (kE4m3 && c < MT) wait_for(ok, &ms.wide_full[c], t & 1, err);
+                        else wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        tc_fence_after();
+                        if (ok && elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < (c < MT ? 8 : 4); ++k) {
+                                const uint64_t at = uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2);
+                                mma_bf16(tm + (t & 1) * KL, q_desc + at + uint64_t(c * (2 * kBlock >> 4)),
+                                         c < MT ? kd + at + uint64_t(c * (2 * kBlock >> 4)) : krd + at, id_s, c > 0 || k > 0);
+                            }
+                            if (c == MT) mma_commit(&ms.s_full[t & 1]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            // nothing of this CTA's is in flight when its tensor memory goes
+            if (elect_one()) mma_commit(&ms.done[0]);
+            __syncwarp();
+            mbar_wait(&ms.done[0], 0, err);
+        } else if (warp == 6) {
+            // ---- outputs, likewise ------------------------------------------------------------
+            const uint64_t v_desc = sdesc_sw128_mn(smem_u32(kE4m3 ? wide : ring), kBlock);
+            const uint64_t p_desc = sdesc_sw128(smem_u32(ring + C::kKrAt));
+            ItemWalk walk(ms.piece[0], ms.piece[1]);
+            Item it = {};
+            uint32_t t = 0;
+            while (ok && walk.next(p, it)) {
+                const int nt = tiles_of(it);
+                const uint32_t id_o = idesc_bf16_f32(128, (it.rows + 15) & ~15, true, false);
+                for (int v = 0; v < nt && ok; ++v, ++t) {
+                    const uint32_t s = t % NS;
+                    wait_for(ok, &ms.p_ready[t & 1], (t >> 1) & 1, err);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&ms.full[s][c], there * uint32_t(box * 128 * blocks));
-                    ++asked;
-                    __syncwarp();
-                    if (i < KL / box && pg >= 0) {
-                        unsigned char *to = dst + b * kBlock + i * box * 128;
-                        if (c < MT) tma_load_3d(to, &maps.c, &ms.full[s][c], b * 64, line, pg);
-                        else tma_load_3d(to, &maps.kr, &ms.full[s][c], 0, line, pg);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t stage = uint64_t(s * uint32_t(C::kStage >> 4));
+                        const uint64_t vd = v_desc + (kE4m3 ? 0 : stage), pd = p_desc + stage;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                            for (int k = 0; k < KL / 16; ++k)
+                                mma_bf16(tm_o + uint32_t(m * BM), vd + uint64_t(m * 2 * (kBlock >> 4) + k * 128), pd + uint64_t(k * 2),
+                                         id_o, k > 0 || v > 0);
+                            mma_commit(kE4m3 ? &ms.wide_free[m] : &ms.empty[s][m]);
+                        }
+                        mma_commit(&ms.o_done[t & 1]);
+                        mma_commit(&ms.empty[s][MT]);
                     }
                     __syncwarp();
                 }
-                if (!ok) break;
             }
-        }
-        // whichever role gives up, no copy is in flight when the CTA ends
-        for (uint32_t i = asked - min(asked, uint32_t(NS * (MT + 1))); i < asked; ++i) {
-            const uint32_t of = i / (MT + 1);
-            mbar_wait(&ms.full[of % NS][i % (MT + 1)], (of / NS) & 1, err);
+            if (elect_one()) mma_commit(&ms.done[1]);
+            __syncwarp();
+            mbar_wait(&ms.done[1], 0, err);
+        } else if (warp == 5) {
+            // ---- page fetches ------------------------------------------------------------------
+            const int page_size = 1 << p.b.page_shift, box = min(page_size, KL);
+            ItemWalk walk(ms.piece[0], ms.piece[1]);
+            Item it = {};
+            uint32_t t = 0, asked = 0;  // tiles, and parts of them asked for
+            while (ok && walk.next(p, it)) {
+                auto page_at = [&](int kb) {
+                    const int j = kb + lane * box;
+                    return lane * box < KL && j < it.k1 ? load_page(p.b, it.n, j) : -1;
+                };
+                int next = page_at(it.k0);
+                for (int kb = it.k0; kb < it.k1 && ok; kb += KL, ++t) {
+                    const int page = next, line = kb & (page_size - 1);  // a tile starts a box
+                    next = page_at(kb + KL);
+                    const uint32_t s = t % NS;
+                    const uint32_t there = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                    unsigned char *dst = ring + s * C::kStage;
+                    // a part at a time, as the outputs leave them: a lane a box
+                    for (int c = 0; c <= MT; ++c) {
+                        const bool two = !kE4m3 && c < MT;  // bf16 latents: a box holds half of a part's channels
+                        const int i = two ? lane >> 1 : lane, b = two ? lane & 1 : 0;
+                        const int pg = __shfl_sync(0xffffffffu, page, i);
+                        if (t >= NS) wait_for(ok, &ms.empty[s][c], (t / NS - 1) & 1, err);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&ms.full[s][c], there * uint32_t(box * ((two ? 256 : 128) + (kE4m3 && c == 0 ? 1 : 0))));
+                        ++asked;
+                        __syncwarp();
+                        if (i < KL / box && pg >= 0) {
+                            unsigned char *to = dst + c * C::kPart + b * kBlock + i * box * 128;
+                            if (c < MT) tma_load_3d(to, &maps.c, &ms.full[s][c], c * 128 + b * 64, line, pg);
+                            else tma_load_3d(to, &maps.kr, &ms.full[s][c], 0, line, pg);
+                            if (kE4m3 && c == 0)
+                                bulk_load(&ms.scale[s][i * box], p.sc + (size_t(pg) << p.b.page_shift) + line, uint32_t(box), &ms.full[s][c]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+            }
+            // whichever role gives up, no copy is in flight when the CTA ends
+            for (uint32_t i = asked - min(asked, uint32_t(NS * (MT + 1))); i < asked; ++i) {
+                const uint32_t of = i / (MT + 1);
+                mbar_wait(&ms.full[of % NS][i % (MT + 1)], (of / NS) & 1, err);
+            }
         }
     }
     tc_fence_before();
@@ -472,49 +561,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // [num_pages][page_size][channels]; a box is a tile's part of one page, 64 channels of it (zeros past the last
 // one: a shared key part of 16 or 32), swizzled over 128 bytes.
-inline bool latent_map(CUtensorMap *m, const void *base, const kda_latent_cache *c, int channels) {
+inline bool latent_map(CUtensorMap *m, const void *base, const kda_latent_cache *c, int channels, bool e4m3) {
     auto fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t D = cuuint64_t(channels), P = cuuint64_t(c->page_size);
+    const cuuint64_t D = cuuint64_t(channels), P = cuuint64_t(c->page_size), esize = e4m3 ? 1 : 2;
     const cuuint64_t dims[3] = {D, P, cuuint64_t(c->num_pages)};
-    const cuuint64_t strides[2] = {D * 2, D * P * 2};
-    const cuuint32_t box[3] = {64u, cuuint32_t(c->page_size < KL ? c->page_size : KL), 1u};
+    const cuuint64_t strides[2] = {D * esize, D * P * esize};
+    const cuuint32_t box[3] = {e4m3 ? 128u : 64u, cuuint32_t(c->page_size < KL ? c->page_size : KL), 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+    return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int L> kda_status launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
-    using C = Cfg<L>;
+template <int L, bool kE4m3>
+kda_status launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    using C = Cfg<L, kE4m3>;
     LatentMaps maps;
-    if (!latent_map(&maps.c, c->c, c, L) || !latent_map(&maps.kr, c->kr, c, c->rope_dim)) return KDA_ERR_CUDA;
+    if (!latent_map(&maps.c, c->c, c, L, kE4m3) || !latent_map(&maps.kr, c->kr, c, c->rope_dim, false)) return KDA_ERR_CUDA;
     constexpr size_t smem = 1024 + C::kMiscAt + sizeof(Misc);
     static_assert(smem <= 232448, "shared memory of a CTA");
-    if (!allow_smem<latent_tile_kernel<L>>(int(smem))) return KDA_ERR_CUDA;
+    if (!allow_smem<latent_tile_kernel<L, kE4m3>>(int(smem))) return KDA_ERR_CUDA;
     p.key_step = KL;
     p.item_cost = 2 * KL;
     p.min_keys = 2 * KL;
     const ProfScope prof(KDA_KERNEL_LATENT_ATTEND, stream);
-    return launch_overlapped(latent_tile_kernel<L>, dim3(unsigned(plan.n_cta)), kThreads, smem, stream, p, maps);
+    return launch_overlapped(latent_tile_kernel<L, kE4m3>, dim3(unsigned(plan.n_cta)), C::kThreads, smem, stream, p, maps);
+}
+
+template <bool kE4m3>
+kda_status by_latent(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
+    switch (c->latent_dim) {
+        case 128: return launch<128, kE4m3>(c, p, plan, stream);
+        case 256: return launch<256, kE4m3>(c, p, plan, stream);
+        case 512: return launch<512, kE4m3>(c, p, plan, stream);
+    }
+    return KDA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 
 bool latent_tile_plan(const kda_latent_cache *c, AttendPlan *plan) {
-    if (c->act != KDA_BF16 || c->format != KDA_KV_ACT) return false;
+    if (c->act != KDA_BF16) return false;
     plan->bm = BM;
     plan->n_cta = sm_count();
     return true;
 }
 
 kda_status latent_tile_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
-    switch (c->latent_dim) {
-        case 128: return launch<128>(c, p, plan, stream);
-        case 256: return launch<256>(c, p, plan, stream);
-        case 512: return launch<512>(c, p, plan, stream);
-    }
-    return KDA_ERR_UNSUPPORTED;
+    return c->format == KDA_KV_E4M3 ? by_latent<true>(c, p, plan, stream) : by_latent<false>(c, p, plan, stream);
 }
 
 }  // namespace kv
