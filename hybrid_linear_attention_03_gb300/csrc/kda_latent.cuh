@@ -87,6 +87,9 @@ kda_status launch_latent_prefill(const kda_latent_cache *c, const kda_latent_pre
 // The kernels (see AttendPlan).
 bool latent_tile_plan(const kda_latent_cache *c, AttendPlan *plan);
 kda_status latent_tile_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream);
+bool prefill_tile_plan(const kda_latent_cache *c, const kda_latent_prefill_batch *b, AttendPlan *plan);
+kda_status prefill_tile_launch(const kda_latent_cache *c, const kda_latent_prefill_io *io, PrefillRowsParams &p,
+                               const AttendPlan &plan, cudaStream_t stream);
 void latent_generic_plan(AttendPlan *plan);
 kda_status latent_generic_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream);
 kda_status prefill_generic_launch(const kda_latent_cache *c, const kda_latent_prefill_io *io, PrefillRowsParams &p,

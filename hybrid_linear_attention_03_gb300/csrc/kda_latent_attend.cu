@@ -242,23 +242,29 @@ kda_status launch_latent_attend(const kda_latent_cache *c, const kda_latent_attn
     return combine(c->act, c->latent_dim, p, plan, b->max_new, b->n_seqs, stream);
 }
 
-static AttendPlan choose(const kda_latent_cache *c, const kda_latent_prefill_io *, const kda_latent_prefill_batch *) {
+struct PrefillChoice {
     AttendPlan plan;
-    (void)c;
-    latent_generic_plan(&plan);
-    plan.n_cta = std::min(plan.n_cta, kMaxCtas);
-    return plan;
+    kda_status (*launch)(const kda_latent_cache *, const kda_latent_prefill_io *, PrefillRowsParams &, const AttendPlan &,
+                         cudaStream_t);
+};
+static PrefillChoice choose(const kda_latent_cache *c, const kda_latent_prefill_batch *b) {
+    PrefillChoice ch;
+    if (prefill_tile_plan(c, b, &ch.plan)) ch.launch = prefill_tile_launch;
+    else latent_generic_plan(&ch.plan), ch.launch = prefill_generic_launch;
+    ch.plan.n_cta = std::min(ch.plan.n_cta, kMaxCtas);
+    return ch;
 }
 
 size_t latent_prefill_workspace_bytes(const kda_latent_cache *c, const kda_latent_prefill_io *io,
                                       const kda_latent_prefill_batch *b) {
-    const AttendPlan plan = choose(c, io, b);
+    const AttendPlan plan = choose(c, b).plan;
     return share_bytes(plan.n_cta, plan.bm, io->value_dim);
 }
 
 kda_status launch_latent_prefill(const kda_latent_cache *c, const kda_latent_prefill_io *io, const kda_latent_prefill_batch *b,
                                  void *workspace, cudaStream_t stream) {
-    const AttendPlan plan = choose(c, io, b);
+    const PrefillChoice ch = choose(c, b);
+    const AttendPlan &plan = ch.plan;
     PrefillRowsParams p = {};
     p.b = RowsView{b->cu_seqlens, b->cu_kv, c->err, b->n_seqs, b->max_rows, b->max_kv_rows, b->max_new};
     p.q_a = io->q_n, p.q_r = io->q_r, p.out = io->out;
@@ -269,7 +275,7 @@ kda_status launch_latent_prefill(const kda_latent_cache *c, const kda_latent_pre
     p.k_stride = io->k_stride, p.k_head = io->k_head_stride, p.kr_stride = io->kr_stride;
     p.v_stride = io->v_stride, p.v_head = io->v_head_stride;
     set_items(p, plan, c->num_heads, 1, io->scale, workspace);
-    const kda_status st = prefill_generic_launch(c, io, p, plan, stream);
+    const kda_status st = ch.launch(c, io, p, plan, stream);
     if (st != KDA_OK || b->max_kv_rows <= p.key_step) return st;
     return combine(c->act, io->value_dim, p, plan, b->max_new, b->n_seqs, stream);
 }
