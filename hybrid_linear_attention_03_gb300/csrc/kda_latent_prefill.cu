@@ -18,8 +18,7 @@
 // 10 and 11 fetch keys and values by TMA; 12-15 bring the rows of Q and look value tiles over:
 // where some row does not see some key, values past the item's keys (the next sequence's) are
 // zeroed and non-finite ones taken out; rows that do see those add them one by one.
-#include "kda_attend_tc.cuh"
-#include "kda_latent.cuh"
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 namespace kv {
@@ -28,7 +27,7 @@ namespace {
 constexpr int KP = 64;           // keys of a tile
 constexpr int kSideRows = 128;
 constexpr int kBlock = KP * 128;  // 64 keys of 64 channels
-constexpr int kThreads = 512, kLaunch = 128, kSoftmax = 200, kIssue = 56, kRows = 56;  // registers after the split
+constexpr int kThreads = 512, kLaunch = 128, kSoftmax = 184, kIssue = 72, kRows = 72;  // registers after the split
 static_assert(8 * kSoftmax + 4 * kIssue + 4 * kRows == 16 * kLaunch, "the split uses what the launch has");
 constexpr float kSumLimit = 65536.f;
 
@@ -356,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = warp - 8, qi = kByKeys ? 0 : s;  // the image of Q
             const uint32_t id_s = idesc_bf16_f32(128, KP), id_o = idesc_bf16_f32(128, DV, false, true);
             const uint32_t t_s = tm + uint32_t(s) * 128u, t_o = tm + 256u + uint32_t(s) * 128u;
-            const uint64_t q_desc = sdesc_sw128(smem_u32(smem) + uint32_t(qi) * C::kQBytes), k_desc = sdesc_sw128(smem_u32(k_ring));
-            const uint64_t v_desc = sdesc_sw128_mn(smem_u32(v_ring), kBlock);
+            const uint32_t q_desc = desc_k(smem_u32(smem) + uint32_t(qi) * C::kQBytes), k_desc = desc_k(smem_u32(k_ring));
+            const uint32_t v_desc = desc_mn(smem_u32(v_ring), kBlock);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t base = 0, n_q = 0, n = 0;
@@ -369,12 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = __all_sync(0xffffffffu, ok))) return;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t kd = k_desc + uint64_t(tg % NS * uint32_t(C::kKBytes >> 4));
-                    const uint32_t t_h = t_s + b * KP;
+                    const uint32_t kd = k_desc + tg % NS * uint32_t(C::kKBytes >> 4), t_h = t_s + b * KP;
 #pragma unroll
                     for (int k = 0; k < NK * 4; ++k)
-                        mma_bf16(t_h, q_desc + uint64_t((k >> 2) * (kSideRows * 8) + (k & 3) * 2),
-                                 kd + uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), id_s, k > 0);
+                        mma_lo(t_h, q_desc + uint32_t((k >> 2) * (kSideRows * 8) + (k & 3) * 2),
+                               kd + uint32_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), id_s, k > 0);
                     mma_commit(&ms.s_full[s][b]);
                     mma_commit(&ms.k_empty[tg % kBars]);
                     if (v + 1 == nv) mma_commit(&ms.q_free[qi]);
@@ -393,18 +391,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int v = 0; v < nv && ok; ++v, ++n) {
                     const uint32_t tg = base + uint32_t(side_tile<kByKeys>(s, v)), b = n & 1;
-                    wait_tile(ok, ms.v_full, tg, err);
-                    wait_tile(ok, ms.clean, tg, err);
-                    wait_for(ok, &ms.p_ready[s][b], (n >> 1) & 1, err);
+                    wait_all(ok, err, of_tile(ms.v_full, tg), of_tile(ms.clean, tg), Awaited{&ms.p_ready[s][b], (n >> 1) & 1});
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
                     // the first product starts O, unless value rows were added to it by hand
                     const uint32_t acc = v > 0 || any_odd(ms.odd[tg % kBars]);
                     if (elect_one()) {
-                        const uint64_t vd = v_desc + uint64_t(tg % NS * uint32_t(C::kVBytes >> 4));
+                        const uint32_t vd = v_desc + tg % NS * uint32_t(C::kVBytes >> 4);
 #pragma unroll
                         for (int k = 0; k < KP / 16; ++k)
-                            mma_bf16_ta(t_o, t_s + b * KP + uint32_t(k) * 8u, vd + uint64_t(k * 128), id_o, k > 0 || acc);
+                            mma_lo_ta(t_o, t_s + b * KP + uint32_t(k) * 8u, vd + uint32_t(k * 128), id_o, k > 0 || acc);
                         mma_commit(&ms.pv_done[s][b]);
                         mma_commit(&ms.v_empty[tg % kBars]);
                     }

@@ -27,8 +27,7 @@
 // latents of absent keys and the non-finite ones that not every row sees, once the scores
 // are there: a row that does see such a key has NaN for its weight, which is what
 // remains (or 0, for a score of -inf).
-#include "kda_attend_tc.cuh"
-#include "kda_latent.cuh"
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 namespace kv {
@@ -432,8 +431,8 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         } else if (warp == 4) {
             // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
             const uint32_t id_s = idesc_bf16_f32(64, KL);
-            const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(kE4m3 ? wide : ring));
-            const uint64_t kr_desc = sdesc_sw128(smem_u32(ring + C::kKrAt));
+            const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(kE4m3 ? wide : ring));
+            const uint32_t kr_desc = desc_k(smem_u32(ring + C::kKrAt));
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t t = 0, n_q = 0;
@@ -444,9 +443,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     // The scores before in this place have been read, and their product is done: so whoever sees
                     // the scores of tile t knows that o_done is at most a tile behind.
                     if (t >= 2) wait_for(ok, &ms.o_done[t & 1], ((t >> 1) - 1) & 1, err);
-                    const uint64_t stage = uint64_t(s * uint32_t(C::kStage >> 4));
-                    // (unrolled: a product whose descriptors are worked out as it goes takes twice as long)
-                    const uint64_t kd = k_desc + (kE4m3 ? 0 : stage), krd = kr_desc + stage;
+                    const uint32_t stage = s * uint32_t(C::kStage >> 4), kd = k_desc + (kE4m3 ? 0 : stage), krd = kr_desc + stage;
 #pragma unroll
                     for (int c = 0; c <= MT; ++c) {
                         if (kE4m3 && c < MT) wait_for(ok, &ms.wide_full[c], t & 1, err);
@@ -456,9 +453,8 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                         if (ok && elect_one()) {
 #pragma unroll
                             for (int k = 0; k < (c < MT ? 8 : 4); ++k) {
-                                const uint64_t at = uint64_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2);
-                                mma_bf16(tm + (t & 1) * KL, q_desc + at + uint64_t(c * (2 * kBlock >> 4)),
-                                         c < MT ? kd + at + uint64_t(c * (2 * kBlock >> 4)) : krd + at, id_s, c > 0 || k > 0);
+                                const uint32_t in = uint32_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), at = in + c * (2 * kBlock >> 4);
+                                mma_lo(tm + (t & 1) * KL, q_desc + at, c < MT ? kd + at : krd + in, id_s, c > 0 || k > 0);
                             }
                             if (c == MT) mma_commit(&ms.s_full[t & 1]);
                         }
@@ -472,8 +468,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             mbar_wait(&ms.done[0], 0, err);
         } else if (warp == 6) {
             // ---- outputs, likewise ------------------------------------------------------------
-            const uint64_t v_desc = sdesc_sw128_mn(smem_u32(kE4m3 ? wide : ring), kBlock);
-            const uint64_t p_desc = sdesc_sw128(smem_u32(ring + C::kKrAt));
+            const uint32_t v_desc = desc_mn(smem_u32(kE4m3 ? wide : ring), kBlock), p_desc = desc_k(smem_u32(ring + C::kKrAt));
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t t = 0;
@@ -486,14 +481,13 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t stage = uint64_t(s * uint32_t(C::kStage >> 4));
-                        const uint64_t vd = v_desc + (kE4m3 ? 0 : stage), pd = p_desc + stage;
+                        const uint32_t stage = s * uint32_t(C::kStage >> 4), vd = v_desc + (kE4m3 ? 0 : stage), pd = p_desc + stage;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
 #pragma unroll
                             for (int k = 0; k < KL / 16; ++k)
-                                mma_bf16(tm_o + uint32_t(m * BM), vd + uint64_t(m * 2 * (kBlock >> 4) + k * 128), pd + uint64_t(k * 2),
-                                         id_o, k > 0 || v > 0);
+                                mma_lo(tm_o + uint32_t(m * BM), vd + uint32_t(m * 2 * (kBlock >> 4) + k * 128), pd + uint32_t(k * 2),
+                                       id_o, k > 0 || v > 0);
                             mma_commit(kE4m3 ? &ms.wide_free[m] : &ms.empty[s][m]);
                         }
                         mma_commit(&ms.o_done[t & 1]);
