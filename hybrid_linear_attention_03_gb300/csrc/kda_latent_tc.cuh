@@ -38,19 +38,33 @@ __device__ __forceinline__ void mma_lo_ta(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// wait_for of several barriers: asked about together, which takes as long as one.
+// wait_for of two and three barriers, looked at one after the other without waiting in between, which takes little
+// longer than one look.  The first one is passed before the others are looked at for good: where its passing is what
+// makes a wait by parity for them sound, it stands first.
 struct Awaited {
     uint64_t *bar;
     uint32_t parity;
 };
-template <typename... W> __device__ __forceinline__ void wait_all(bool &ok, uint32_t *err, W... w) {
+__device__ __forceinline__ void wait_all(bool &ok, uint32_t *err, Awaited a, Awaited b, Awaited c) {
 #ifndef KDA_ATTEND_LOOKS
-    if ((int(mbar_try_wait(w.bar, w.parity)) & ...)) return;
+    const bool in_a = mbar_try_wait(a.bar, a.parity), in_b = mbar_try_wait(b.bar, b.parity), in_c = mbar_try_wait(c.bar, c.parity);
+    if (in_a && in_b && in_c) return;
 #endif
-    (wait_for(ok, w.bar, w.parity, err), ...);
+    wait_for(ok, a.bar, a.parity, err);
+    wait_for(ok, b.bar, b.parity, err);
+    wait_for(ok, c.bar, c.parity, err);
 }
 // Tile t's barrier of a ring.
 __device__ __forceinline__ Awaited of_tile(uint64_t *bars, uint32_t t) { return Awaited{&bars[t % kBars], (t / kBars) & 1}; }
+
+// The products of one warp in one piece: those of two warps that issue at the same time would go by turns, and both
+// be done when the later one is.  A place in shared memory that holds 1 while taken; whoever waits too long goes on, which
+// costs time and nothing else.  One lane.
+__device__ __forceinline__ void take_turn(uint32_t *place) {
+    for (int i = 0; i < 4096 && atomicCAS(place, 0u, 1u) != 0u; ++i) {
+    }
+}
+__device__ __forceinline__ void end_turn(uint32_t *place) { *reinterpret_cast<volatile uint32_t *>(place) = 0; }
 
 }  // namespace
 }  // namespace kv

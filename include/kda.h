@@ -636,7 +636,8 @@ typedef struct {
  * is the token at position L_n - T_n + t.  Both tables are DEVICE arrays, read when the
  * call runs.  A sequence whose tables are inconsistent (either decreasing or past its
  * bound, more than max_new tokens, L_n below T_n or past 2^31 - 1024) sets KDA_DEVERR_META
- * and its rows are left as they were.  Rows past cu_seqlens[n_seqs] are neither read nor written. */
+ * and its rows are left as they were.  Rows past cu_seqlens[n_seqs] are not written, and what
+ * they hold, like key and value rows past cu_kv[n_seqs], does not matter. */
 typedef struct {
     const int32_t *cu_seqlens; /* [n_seqs + 1], from 0 */
     const int32_t *cu_kv;      /* [n_seqs + 1], from 0 */
