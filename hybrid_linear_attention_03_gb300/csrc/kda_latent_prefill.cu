@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                             };
+                            if (!started) move_ref(true);
                             float sum_h = weigh();
                             // past the limit (or NaN), or a row without a reference yet
                             const bool need = r < it.rows && (!(sum_h <= kSumLimit) || ref == -INFINITY);
