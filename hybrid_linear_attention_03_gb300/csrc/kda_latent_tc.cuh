@@ -27,6 +27,16 @@ __device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a, uint32_t b, 
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
+// Likewise of e4m3 values, rows of 128 of them.
+__device__ __forceinline__ void mma_lo_e4m3(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem], A bf16 with two K values a column.
 __device__ __forceinline__ void mma_lo_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(

@@ -19,8 +19,13 @@
 // issues the scores, 5 fetches pages by TMA, 6 issues the outputs (a warp of its own, so that
 // neither product waits for what the other needs).
 //
-// e4m3 pages: eight more warps make one bf16 tile of the latents, scale included and
-// exact, a part at a time as the outputs of the tile before give its place back.
+// e4m3 pages: the scores take the latents as they are, against Q as the sum of two e4m3 terms
+// (exact to about 2^-18 of a row's largest value), beside those of the bf16 key parts.  Eight more
+// warps make one f16 tile of the latents for the outputs, a part at a time as those of the tile before
+// give its place back.  f16 holds an e4m3 value exactly and takes one conversion for two of
+// them, where bf16, which has room for the scales, takes three times as many instructions.  So the scales
+// (7 makes numbers of them) multiply the scores, and the weights on their way to f16, in
+// units that follow the largest scale a row has met.
 //
 // A latent behind a row's position weighs nothing, but 0 * NaN is NaN in the product.
 // So in the few tiles where some row does not see some key, the softmax warps zero the
@@ -36,39 +41,70 @@ namespace {
 constexpr int KL = 64, BM = 64;       // keys of a tile, rows of an item
 constexpr int kBlock = 64 * 128;      // 64 rows of 64 channels, bf16, swizzled over 128 bytes
 constexpr float kRefSlack = 8.f;
+// e4m3: weights (up to 2^8) times scales (up to p_unit) become f16 in units of p_unit / 2^7: no more than 2^15, and what an
+// f16 rounds off below its normal range is no more than 2^-32 of the largest scale's whole weight.
+constexpr float kPUnits = 128.f;
 
 template <int L, bool kE4m3> struct Cfg {
     static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, its parts of 128 channels (matrix rows of O^T)
-    // e4m3: eight warps that widen, and registers split by groups of four warps
-    static constexpr int kWiden = 8, kThreads = kE4m3 ? 512 : 224, kLaunch = 128, kSoftmax = 200, kOther = 104;
+    // e4m3: eight warps that bring the rows of Q, and registers split by groups of four warps
+    static constexpr int kRowWarps = 8, kThreads = kE4m3 ? 512 : 224, kLaunch = 128, kSoftmax = 200, kOther = 104;
     static_assert(kSoftmax + 3 * kOther <= 4 * kLaunch, "the split takes no more than the launch has");
     static constexpr int kQBytes = (NB + 1) * kBlock;
-    static constexpr int kWide = kE4m3 ? NB * kBlock : 0;  // e4m3: one tile of latents as bf16
+    static constexpr int kThird = kE4m3 ? kBlock : 0;  // e4m3: the weights' third terms, of two tiles
     static constexpr int kPart = kE4m3 ? kBlock : 2 * kBlock;  // 128 channels of a tile as they come
     static constexpr int kKrAt = MT * kPart, kStage = kKrAt + kBlock;  // the shared key part, later the weights
-    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes - kWide;
+    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBytes - kThird;
     static constexpr int kStages = kRoom / kStage < 6 ? kRoom / kStage : 6;
-    static constexpr int kWideAt = kQBytes, kRingAt = kWideAt + kWide, kMiscAt = kRingAt + kStages * kStage;
-    static constexpr int kColumns = L == 512 ? 512 : 256;  // tensor memory: scores by tile parity, O
-    static_assert(2 * KL + MT * BM <= kColumns && kStages >= 2, "room for two tiles");
+    static constexpr int kThirdAt = kQBytes, kRingAt = kThirdAt + kThird, kMiscAt = kRingAt + kStages * kStage;
+    // tensor memory: scores by tile parity (e4m3: of the latents, of the key parts), O
+    static constexpr int kScores = kE4m3 ? 2 * KL : KL, kOAt = 2 * kScores, kColumns = kOAt + MT * BM > 256 ? 512 : 256;
+    static_assert(kOAt + MT * BM <= kColumns && kStages >= 2, "room for two tiles");
 };
 
 struct alignas(16) Misc {
     uint64_t full[6][5], empty[6][5];            // by stage, the parts of the latents and the shared key parts
-    uint64_t wide_full[4], wide_free[4];         // e4m3, by part
+    uint64_t unit_full[2];                       // by tile parity: the scales are numbers
     uint64_t s_full[2], p_ready[2], o_done[2];   // by tile parity
-    uint64_t q_full, done[2];
+    uint64_t q_full, q_free, done[2];            // q_free (e4m3): an item's scores are there
     uint32_t tmem;
     int has;
     Cursor piece[2];
     alignas(16) float back[BM], inv[BM];  // what a move of the reference scales O by; an item's end: the rows' factors
     long long out_at[BM];                 // element offsets of the rows in out
     alignas(16) uint8_t scale[6][KL];     // e4m3, by stage: the keys' scale exponents
+    alignas(16) float unit[2][KL];        // by tile parity: the scales
+    float unit_top[2];                    // and the largest of them
+    float q_unit[4][BM];                  // by item: the rows' scales
+    uint64_t rows_full[4];                // and that they are there
 };
 
 struct LatentMaps {
     CUtensorMap c, kr;
 };
+
+// Any e4m3 NaN among sixteen.
+__device__ __forceinline__ bool odd_e4m3(const uint4 &w) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) odd |= ((x[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    return odd != 0;
+}
+// Instruction descriptor as idesc_e4m3_f32, of A e4m3 with its rows' values apart (a_mn of idesc_bf16_f32) and B e5m2.
+constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N) {
+    return (1u << 4) | (1u << 10) | (1u << 15) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+// Two numbers as the sums of three e5m2 terms each (the first of a pair in the low byte).
+__device__ __forceinline__ void split_e5m2(float lo, float hi, uint32_t (&o)[3]) {
+    __half2 r = __floats2half2_rn(lo, hi);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        o[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E5M2);
+        const uint32_t back = __byte_perm(o[i], 0, 0x1404);  // an e5m2 value is the upper byte of the same f16 value
+        if (i < 2) r = __hsub2(r, *reinterpret_cast<const __half2 *>(&back));
+    }
+}
 
 // Lane l < 16 gets row l's columns [c, c + 32), lane l + 16 its columns [c + 32, c + 64), of the 16 rows a warp's
 // quarter of tensor memory holds of a product of 64.
@@ -119,57 +155,95 @@ __device__ __forceinline__ int peek_page(const LatentParams &p, const Item &it, 
     return p.b.table[size_t(it.n) * size_t(p.b.table_stride) + size_t(j >> p.b.page_shift)];
 }
 
-// Asks for the rows of Q (16-byte copies; rows past the item's, up to a warp's 16, are zeros).
-template <int L>
+// Asks for the rows of Q that `threads` threads bring (16-byte copies; rows past the item's, up to a warp's 16, are
+// zeros): all of them, or only the part that meets kr.
+template <int L, bool kOnlyKr, int kThreads>
 __device__ __forceinline__ void ask_q(const LatentParams &p, const Item &it, unsigned char *q_img, int tid) {
     const int c = tid & 7;
     const bool in = c * 8 < p.rope;
 #pragma unroll 1
-    for (int r = tid >> 3; r < ((it.rows + 15) & ~15); r += 16) {
+    for (int r = tid >> 3; r < ((it.rows + 15) & ~15); r += kThreads / 8) {
         long long row, head;
         p.locate(it, min(r, it.rows - 1), row, head);
         const bool there = r < it.rows;
-        const __nv_bfloat16 *a = static_cast<const __nv_bfloat16 *>(p.q_a) + row * p.qa_stride + head * p.qa_head + c * 8;
         const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.q_r) + row * p.qr_stride + head * p.qr_head;
         unsigned char *dst = q_img + sw128_chunk(r, c, 64);
+        if constexpr (!kOnlyKr) {
+            const __nv_bfloat16 *a = static_cast<const __nv_bfloat16 *>(p.q_a) + row * p.qa_stride + head * p.qa_head + c * 8;
 #pragma unroll
-        for (int k = 0; k < L / 64; ++k) cp_async16_or_zero(dst + k * kBlock, a + k * 64, there);
+            for (int k = 0; k < L / 64; ++k) cp_async16_or_zero(dst + k * kBlock, a + k * 64, there);
+        }
         cp_async16_or_zero(dst + (L / 64) * kBlock, b + (in ? c * 8 : 0), there && in);
     }
 }
-
-// 16 e4m3 values times 2^(e - 127) as bf16, exactly.  Their sign, exponent and fraction in the places of a bf16's
-// are the value times 2^-120 (below e4m3's normal range too), so a packed product makes two.  NaN and factors past
-// bf16's range go by way of f16 and 32 bits.
-__device__ __forceinline__ void widen_bits(const uint4 &q, uint32_t e, uint32_t (&o)[8]) {
-    if (nan_codes(q) != 0 || e > 134) {
-        widen_e4m3(q, exp2_biased(int(e)), o);
-        return;
-    }
-    const uint32_t f = (e + 120) << 7 | (e + 120) << 23, in[4] = {q.x, q.y, q.z, q.w};
+// e4m3 pages: rows [r0, r0 + 8) of Q, one warp: those for the latents as 2^e (q1 + q2), two e4m3 terms, as in
+// kda_attend_tile.cu.
+template <int L>
+__device__ __forceinline__ void split_q(const LatentParams &p, const Item &it, unsigned char *q_img, float *q_unit, int r0, int lane) {
+    constexpr int kPieces = L / 8 > 32 ? L / 8 / 32 : 1, kB = 4;  // of 16 bytes, of a lane; rows at a time
+#pragma unroll 1
+    for (int g = 0; g < 8 && r0 + g < it.rows; g += kB) {
+        uint4 raw[kB][kPieces];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t t = __byte_perm(in[i / 2], 0, i & 1 ? 0x3424 : 0x1404);
-        const uint32_t v = (t >> 4 & 0x07f007f0u) | (t & 0x80008000u);
-        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&f));
-        o[i] = *reinterpret_cast<const uint32_t *>(&y);
+        for (int i = 0; i < kB; ++i) {
+            long long row, head;
+            p.locate(it, min(r0 + g + i, it.rows - 1), row, head);
+            const __nv_bfloat16 *a = static_cast<const __nv_bfloat16 *>(p.q_a) + row * p.qa_stride + head * p.qa_head;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int at = (lane + 32 * k) * 8;
+                raw[i][k] = r0 + g + i < it.rows && at < L ? *reinterpret_cast<const uint4 *>(a + at) : make_uint4(0, 0, 0, 0);
+            }
+        }
+        uint32_t m[kB];  // the largest magnitude as a bf16 pattern
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+            m[i] = 0;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const uint4 &w = raw[i][k];
+                const uint32_t t = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                            __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+                m[i] = max(m[i], max(t & 0xffffu, t >> 16));
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < kB; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+            const int e = m[i] >= 0x7f80u ? -1 : max(scale_exponent(__uint_as_float(m[i] << 16)), 1), r = r0 + g + i;
+            if (lane == 0) q_unit[r] = exp2_biased(e < 0 ? 127 : e);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int pc = lane + 32 * k;  // the row's piece of eight values
+                if (pc * 8 >= L) continue;
+                uint32_t w1[2], w2[2];
+                split_row(raw[i][k], e, w1, w2);
+                unsigned char *at = q_img + (pc >> 4) * kBlock + row8_piece<128>(r, (pc & 15) >> 1) + (pc & 1) * 8;
+                *reinterpret_cast<uint2 *>(at) = make_uint2(w1[0], w1[1]);
+                *reinterpret_cast<uint2 *>(at + (L / 128) * kBlock) = make_uint2(w2[0], w2[1]);
+            }
+        }
     }
 }
 
 // A tile in which some row does not see some key: zeroes the latents of absent keys and the non-finite ones that
 // not every row sees.  Two threads a key.
-template <int L>
+template <int L, bool kE4m3>
 __device__ __noinline__ void look_over(const Item &it, int kb, uint32_t absent, unsigned char *tile, int tid) {
+    constexpr int kPieces = kE4m3 ? L / 16 : L / 8;  // of 16 bytes, eight of them in a block's row
     const int key = tid >> 1, j = kb + key, half = tid & 1;
     const bool gone = j >= it.k1 || (absent >> (key / 16) & 1);
     unsigned char *img = tile + key * 128;
     auto piece = [&](int c) { return reinterpret_cast<uint4 *>(img + (c >> 3) * kBlock + (((c & 7) ^ (key & 7)) << 4)); };
     bool bad = false;
     if (!gone && j > it.ctx + it.tok0)
-        for (int c = half; c < L / 8; c += 2) bad |= odd_bf16(*piece(c));
+        for (int c = half; c < kPieces; c += 2) bad |= kE4m3 ? odd_e4m3(*piece(c)) : odd_bf16(*piece(c));
     bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
     if (gone || bad)
-        for (int c = half; c < L / 8; c += 2) *piece(c) = make_uint4(0, 0, 0, 0);
+        for (int c = half; c < kPieces; c += 2) *piece(c) = make_uint4(0, 0, 0, 0);
 }
 
 template <int L, bool kE4m3>
@@ -180,16 +254,16 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc &ms = *reinterpret_cast<Misc *>(smem + C::kMiscAt);
-    unsigned char *ring = smem + C::kRingAt, *wide = smem + C::kWideAt;
+    unsigned char *ring = smem + C::kRingAt, *third = smem + C::kThirdAt;
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5, cta = int(blockIdx.x);
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i)
             for (int c = 0; c <= MT; ++c)
-                mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], kE4m3 && c < MT ? C::kWiden / MT : 1);
-        for (int c = 0; c < MT; ++c) mbar_init(&ms.wide_full[c], C::kWiden / MT), mbar_init(&ms.wide_free[c], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.o_done[i], 1);
-        mbar_init(&ms.q_full, 4), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
+                mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.o_done[i], 1), mbar_init(&ms.unit_full[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&ms.rows_full[i], C::kRowWarps);
+        mbar_init(&ms.q_full, kE4m3 ? C::kRowWarps : 4), mbar_init(&ms.q_free, 1), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
         fence_mbar_init();
     }
     if (tid == 32) {
@@ -208,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = ms.tmem, tm_o = tm + 2 * KL;
+    const uint32_t tm = ms.tmem, tm_o = tm + C::kOAt;
     uint32_t *err = p.b.err;
     bool ok = true;  // of this thread's waits
 
@@ -220,7 +294,9 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         ItemWalk walk(ms.piece[0], ms.piece[1]);
         Item it = {};
         uint32_t tile = 0;
+        uint32_t n_it = 0;  // items so far
         auto put_q = [&] {
+            if (kE4m3) return;  // others bring them
             cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
@@ -233,12 +309,22 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             tc_fence_after();
         };
         bool more = ms.has && walk.next(p, it);
-        if (more) ask_q<L>(p, it, smem, tid), put_q();
-        while (more) {
+        auto ask = [&] {
+            if constexpr (!kE4m3) ask_q<L, false, 128>(p, it, smem, tid);
+        };
+        if (more) ask(), put_q();
+        for (; more; ++n_it) {
             const int nt = tiles_of(it), n_cols = (it.rows + 15) & ~15;
             const bool live = 16 * warp < it.rows;  // this warp has rows of the item
             const int lim = it.ctx + it.tok0 + p.token_of(min(row, it.rows - 1));  // last key the row sees
             float ref = -INFINITY, l = 0.f;
+            // e4m3: what weights times their keys' scales are in units of, before they become f16 (a power of two)
+            float p_unit = 0x1p-100f, q_unit = 0.f;
+            if constexpr (kE4m3) {
+                wait_for(ok, &ms.rows_full[n_it & 3], (n_it >> 2) & 1, err);
+                __syncwarp();
+                q_unit = fmaxf(p.scale_log2 * ms.q_unit[n_it & 3][row], 0x1p-149f);
+            }
             int page = peek_page(p, it, it.k0, lane);
             for (int v = 0; v < nt; ++v, ++tile) {
                 const int kb = it.k0 + v * KL;
@@ -247,19 +333,42 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 page = peek_page(p, it, kb + KL, lane);
                 unsigned char *stage = ring + tile % NS * C::kStage;
                 wait_for(ok, &ms.s_full[tile & 1], (tile >> 1) & 1, err);
+                // (in order, so that no later wait for these barriers is two phases ahead)
+                if (tile >= 2) wait_for(ok, &ms.o_done[tile & 1], ((tile >> 1) - 1) & 1, err);
                 __syncwarp();
                 tc_fence_after();
                 float x[32];
                 bool move = false;
-                float top = -INFINITY;
+                float top = -INFINITY, unit_top = 0.f;
+                if constexpr (kE4m3) wait_for(ok, &ms.unit_full[tile & 1], (tile >> 1) & 1, err), __syncwarp();
+                const float *unit = ms.unit[tile & 1] + key0;
                 if (live) {
-                    tmem_ld_rows16(tm + lanes + (tile & 1) * KL, x);
-                    tmem_wait_ld();
+                    tmem_ld_rows16(tm + lanes + (tile & 1) * C::kScores, x);
+                    if constexpr (kE4m3) {
+                        // scores in powers of two: the latents' times their scales, and the key parts'
+                        float y[32];
+                        tmem_ld_rows16(tm + lanes + (tile & 1) * C::kScores + KL, y);
+                        const float2 f2 = make_float2(q_unit, q_unit), sc = make_float2(p.scale_log2, p.scale_log2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 u = *reinterpret_cast<const float4 *>(unit + i);
+                            const float2 a = fma2(mul2(make_float2(u.x, u.y), f2), make_float2(x[i], x[i + 1]),
+                                                  mul2(make_float2(y[i], y[i + 1]), sc));
+                            const float2 b = fma2(mul2(make_float2(u.z, u.w), f2), make_float2(x[i + 2], x[i + 3]),
+                                                  mul2(make_float2(y[i + 2], y[i + 3]), sc));
+                            x[i] = a.x, x[i + 1] = a.y, x[i + 2] = b.x, x[i + 3] = b.y;
+                        }
+                        if (!check) unit_top = ms.unit_top[tile & 1];
+                    } else {
+                        tmem_wait_ld();
+                    }
                     if (check) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const int j = kb + key0 + i;
                             if (j > lim || j >= it.k1 || (absent >> ((key0 + i) / 16) & 1)) x[i] = -INFINITY;
+                            else if (kE4m3) unit_top = fmaxf(unit_top, unit[i]);
                         }
                     }
                     float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -267,14 +376,24 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     for (int i = 4; i < 32; i += 4)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[i + e]);
-                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kE4m3 ? 1.f : p.scale_log2);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     move = top > ref + kRefSlack;
+                    if constexpr (kE4m3) {
+                        unit_top = fmaxf(unit_top, __shfl_xor_sync(0xffffffffu, unit_top, 16));
+                        move = move || unit_top > p_unit;
+                    }
                 }
                 if (any_of_128(move)) {
-                    const float f = move ? ex2(ref - top) : 1.f;
+                    const float to = top > ref + kRefSlack ? top : ref;
+                    float f = to != ref ? ex2(ref - to) : 1.f;
+                    l *= f, ref = to;
+                    if constexpr (kE4m3) {
+                        // (with room for scales four times as large)
+                        const float unit_to = unit_top > p_unit ? fminf(4.f * unit_top, 0x1p127f) : p_unit;
+                        f = f * (p_unit / unit_to), p_unit = unit_to;
+                    }
                     if (live && lane < 16) ms.back[row] = f;
-                    if (move) ref = top, l *= f;
                     named_sync<2, 128>();
                     if (v > 0) {
                         wait_o(tile - 1);
@@ -301,26 +420,45 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 }
                 if (live) {
                     const float base = ref == -INFINITY ? 0.f : ref;
-                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), sh = make_float2(-base, -base);
+                    const float one = kE4m3 ? 1.f : p.scale_log2, per = kE4m3 ? kPUnits / p_unit : 1.f;
+                    const float2 sc = make_float2(one, one), sh = make_float2(-base, -base), per2 = make_float2(per, per);
                     float2 sum = make_float2(0.f, 0.f);
                     unsigned char *p_row = stage + C::kKrAt + row * 128;
+                    constexpr int kStep = kE4m3 ? 16 : 8;  // keys whose weights, or terms of them, fill 16 bytes
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4];
+                    for (int i = 0; i < 32; i += kStep) {
+                        uint32_t w[kE4m3 ? 3 : 1][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < kStep / 2; ++e) {
                             float2 t = fma2(make_float2(x[i + 2 * e], x[i + 2 * e + 1]), sc, sh);
                             t.x = ex2(t.x), t.y = ex2(t.y);
                             sum = add2(sum, t);
-                            w[e] = pack_bf16(t.x, t.y);
+                            if constexpr (kE4m3) {
+                                const float2 u = *reinterpret_cast<const float2 *>(unit + i + 2 * e);
+                                const float2 z = mul2(t, mul2(u, per2));
+                                // the scale of a key that the row does not see may be anything
+                                t = check ? make_float2(t.x == 0.f ? 0.f : z.x, t.y == 0.f ? 0.f : z.y) : z;
+                                uint32_t h[3];
+                                split_e5m2(t.x, t.y, h);
+#pragma unroll
+                                for (int k = 0; k < 3; ++k) w[k][e >> 1] = e & 1 ? w[k][e >> 1] | h[k] << 16 : h[k];
+                            } else {
+                                w[0][e] = pack_bf16(t.x, t.y);
+                            }
                         }
-                        *reinterpret_cast<uint4 *>(p_row + ((((key0 + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        const int c = (key0 + i) / kStep;  // the piece of 16 bytes
+                        auto put = [&](unsigned char *to, int c, const uint32_t (&v)[4]) {
+                            *reinterpret_cast<uint4 *>(to + ((c ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        };
+                        put(p_row, c, w[0]);
+                        if constexpr (kE4m3)
+                            put(p_row, 4 + c, w[1]), put(third + row * 128, int(tile & 1) * 4 + c, w[2]);
                     }
                     l += sum.x + sum.y;
                 }
                 if (check) {
                     const Item copy = it;
-                    look_over<L>(copy, kb, absent, kE4m3 ? wide : stage, tid);
+                    look_over<L, kE4m3>(copy, kb, absent, stage, tid);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -331,13 +469,14 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             // the item's scores are all there, so the rows of the next may take the place of its own
             const Item was = it;
             more = walk.next(p, it);
-            if (more) ask_q<L>(p, it, smem, tid);
+            if (more) ask();
 
             // ---- output -----------------------------------------------------------------
             const bool whole = was.whole();
             float *data = p.part_data + (size_t(cta) * 2 + was.slot()) * size_t(BM) * (L + 2);
             if (live && lane < 16) {
-                ms.inv[row] = !whole ? 1.f : l > 0.f || l != l ? 1.0f / l : 0.f;
+                const float up = kE4m3 ? p_unit / kPUnits : 1.f;
+                ms.inv[row] = !whole ? up : l > 0.f || l != l ? up / l : 0.f;
                 if (row < was.rows) {
                     long long token, head;
                     p.locate(was, row, token, head);
@@ -372,9 +511,11 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                                     pack_bf16(o[m][g] * f, o[m][g + 1] * f), pack_bf16(o[m][g + 2] * f, o[m][g + 3] * f));
                         } else {
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
+                            for (int m = 0; m < MT; ++m) {
+                                const float f = kE4m3 ? ms.inv[r] : 1.f;
                                 *reinterpret_cast<float4 *>(data + size_t(r) * L + ch0 + m * 128) =
-                                    make_float4(o[m][g], o[m][g + 1], o[m][g + 2], o[m][g + 3]);
+                                    make_float4(o[m][g] * f, o[m][g + 1] * f, o[m][g + 2] * f, o[m][g + 3] * f);
+                            }
                         }
                     }
                     __syncwarp();
@@ -384,79 +525,60 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             named_sync<2, 128>();  // and its end the rows' factors and places
         }
     } else if (kE4m3 && warp >= 8) {
-        // ---- latents made bf16, scale included and exact: a warp has some keys of one part; 8 neighbouring lanes take
-        // the same 16-byte piece of 8 keys, which both tiles' swizzles put into different banks ------
+        // ---- rows of Q (e4m3), once the last item's scores are there.  Those are at most two tiles
+        // ahead of the outputs, so nobody reads the scales of four items before ------------------
         if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
-        const int c = (warp - 8) % MT, key = (warp - 8) / MT * (8 * MT) + (lane & 7), pc = lane >> 3;
-        unsigned char *to = wide + 2 * c * kBlock + key * 128;
         ItemWalk walk(ms.piece[0], ms.piece[1]);
         Item it = {};
-        uint32_t t = 0;
-        while (ok && ms.has && walk.next(p, it)) {
-            for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
-                const uint32_t s = t % NS;
-                if (c > 0) wait_for(ok, &ms.full[s][0], (t / NS) & 1, err);  // the scales
-                wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
-                __syncwarp();
-                const unsigned char *raw = ring + s * C::kStage + c * kBlock;
-                uint4 x[MT][2];
-                uint32_t e[MT];
-#pragma unroll
-                for (int g = 0; g < MT; ++g) {
-                    e[g] = ms.scale[s][key + 8 * g];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        x[g][u] = *reinterpret_cast<const uint4 *>(raw + row8_piece<128>(key + 8 * g, pc + 4 * u));
-                }
-                if (t > 0) wait_for(ok, &ms.wide_free[c], (t - 1) & 1, err);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-#pragma unroll
-                for (int g = 0; g < MT; ++g)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {  // pieces 0-3 are the first 64 channels
-                        uint32_t o[8];
-                        widen_bits(x[g][u], e[g], o);
-                        unsigned char *at = to + u * kBlock + g * 1024;
-                        *reinterpret_cast<uint4 *>(at + (((2 * pc) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(at + (((2 * pc + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.wide_full[c]), mbar_arrive(&ms.empty[s][c]);
-            }
+        for (uint32_t n_it = 0; ms.has && walk.next(p, it); ++n_it) {
+            if (n_it > 0) wait_for(ok, &ms.q_free, (n_it - 1) & 1, err);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            ask_q<L, true, 32 * C::kRowWarps>(p, it, smem, tid - 256);
+            split_q<L>(p, it, smem, ms.q_unit[n_it & 3], (warp - 8) * 8, lane);
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_full), mbar_arrive(&ms.rows_full[n_it & 3]);
         }
     } else {
         if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
         if (!ms.has) {
         } else if (warp == 4) {
             // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
-            const uint32_t id_s = idesc_bf16_f32(64, KL);
-            const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(kE4m3 ? wide : ring));
-            const uint32_t kr_desc = desc_k(smem_u32(ring + C::kKrAt));
+            const uint32_t id_s = idesc_bf16_f32(64, KL), id_8 = idesc_e4m3_f32(64, KL);
+            const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring));
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t t = 0, n_q = 0;
             while (ok && walk.next(p, it)) {
                 wait_for(ok, &ms.q_full, n_q++ & 1, err);
                 for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
-                    const uint32_t s = t % NS;
-                    // The scores before in this place have been read, and their product is done: so whoever sees
-                    // the scores of tile t knows that o_done is at most a tile behind.
-                    if (t >= 2) wait_for(ok, &ms.o_done[t & 1], ((t >> 1) - 1) & 1, err);
-                    const uint32_t stage = s * uint32_t(C::kStage >> 4), kd = k_desc + (kE4m3 ? 0 : stage), krd = kr_desc + stage;
+                    const uint32_t s = t % NS, t_s = tm + (t & 1) * C::kScores;
+                    if (t >= 2) wait_for(ok, &ms.p_ready[t & 1], ((t >> 1) - 1) & 1, err);  // those before have been read
+                    const uint32_t kd = k_desc + s * uint32_t(C::kStage >> 4);
 #pragma unroll
                     for (int c = 0; c <= MT; ++c) {
-                        if (kE4m3 && c < MT) wait_for(ok, &ms.wide_full[c], t & 1, err);
-                        else wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
+                        wait_for(ok, &ms.full[s][c], (t / NS) & 1, err);
                         ok = __all_sync(0xffffffffu, ok);
                         tc_fence_after();
                         if (ok && elect_one()) {
+                            if (kE4m3 && c < MT) {
 #pragma unroll
-                            for (int k = 0; k < (c < MT ? 8 : 4); ++k) {
-                                const uint32_t in = uint32_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2), at = in + c * (2 * kBlock >> 4);
-                                mma_lo(tm + (t & 1) * KL, q_desc + at, c < MT ? kd + at : krd + in, id_s, c > 0 || k > 0);
+                                for (int k = 0; k < 8; ++k)  // both terms of Q against the same keys
+                                    mma_lo_e4m3(t_s, q_desc + uint32_t((c + k / 4 * MT) * (kBlock >> 4) + (k & 3) * 2),
+                                                kd + uint32_t(c * (C::kPart >> 4) + (k & 3) * 2), id_8, c > 0 || k > 0);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < (c < MT ? 8 : 4); ++k) {
+                                    const uint32_t in = uint32_t((k >> 2) * (kBlock >> 4) + (k & 3) * 2);
+                                    mma_lo(t_s + (kE4m3 ? KL : 0), q_desc + in + uint32_t(c * (2 * kBlock >> 4)),
+                                           kd + in + uint32_t(c * (C::kPart >> 4)), id_s, (!kE4m3 && c > 0) || k > 0);
+                                }
                             }
-                            if (c == MT) mma_commit(&ms.s_full[t & 1]);
+                            if (c == MT) {
+                                mma_commit(&ms.s_full[t & 1]);
+                                if (kE4m3 && v == 1) mma_commit(&ms.q_free);
+                            }
                         }
                         __syncwarp();
                     }
@@ -468,32 +590,40 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             mbar_wait(&ms.done[0], 0, err);
         } else if (warp == 6) {
             // ---- outputs, likewise ------------------------------------------------------------
-            const uint32_t v_desc = desc_mn(smem_u32(kE4m3 ? wide : ring), kBlock), p_desc = desc_k(smem_u32(ring + C::kKrAt));
+            const uint32_t v_desc = desc_mn(smem_u32(ring), kBlock), p_desc = desc_k(smem_u32(ring + C::kKrAt)), p3_desc = desc_k(smem_u32(third));
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
             uint32_t t = 0;
             while (ok && walk.next(p, it)) {
                 const int nt = tiles_of(it);
-                const uint32_t id_o = idesc_bf16_f32(128, (it.rows + 15) & ~15, true, false);
+                const int cols = (it.rows + 15) & ~15;
+                const uint32_t id_o = kE4m3 ? idesc_e4m3_e5m2_f32(128, cols) : idesc_bf16_f32(128, cols, true, false);
                 for (int v = 0; v < nt && ok; ++v, ++t) {
                     const uint32_t s = t % NS;
                     wait_for(ok, &ms.p_ready[t & 1], (t >> 1) & 1, err);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t stage = s * uint32_t(C::kStage >> 4), vd = v_desc + (kE4m3 ? 0 : stage), pd = p_desc + stage;
+                    const uint32_t stage = s * uint32_t(C::kStage >> 4), vd = v_desc + stage, pd = p_desc + stage;
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
+                    for (int m = 0; m < MT; ++m) {
+                        if (ok && elect_one()) {
+                            if constexpr (kE4m3) {
 #pragma unroll
-                            for (int k = 0; k < KL / 16; ++k)
-                                mma_lo(tm_o + uint32_t(m * BM), vd + uint32_t(m * 2 * (kBlock >> 4) + k * 128), pd + uint32_t(k * 2),
-                                       id_o, k > 0 || v > 0);
-                            mma_commit(kE4m3 ? &ms.wide_free[m] : &ms.empty[s][m]);
+                                for (int k = 0; k < 6; ++k)  // 32 keys, a term of their weights
+                                    mma_lo_e4m3(tm_o + uint32_t(m * BM), vd + uint32_t(m * (kBlock >> 4) + (k & 1) * 256),
+                                                (k < 4 ? pd + uint32_t(k * 2) : p3_desc + (t & 1) * 4 + uint32_t((k & 1) * 2)), id_o,
+                                                k > 0 || v > 0);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < KL / 16; ++k)
+                                    mma_lo(tm_o + uint32_t(m * BM), vd + uint32_t(m * 2 * (kBlock >> 4) + k * 128), pd + uint32_t(k * 2),
+                                           id_o, k > 0 || v > 0);
+                            }
+                            mma_commit(&ms.empty[s][m]);
+                            if (m + 1 == MT) mma_commit(&ms.o_done[t & 1]), mma_commit(&ms.empty[s][MT]);
                         }
-                        mma_commit(&ms.o_done[t & 1]);
-                        mma_commit(&ms.empty[s][MT]);
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             if (elect_one()) mma_commit(&ms.done[1]);
@@ -525,14 +655,14 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                         if (t >= NS) wait_for(ok, &ms.empty[s][c], (t / NS - 1) & 1, err);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
                         if (lane == 0)
-                            mbar_arrive_expect_tx(&ms.full[s][c], there * uint32_t(box * ((two ? 256 : 128) + (kE4m3 && c == 0 ? 1 : 0))));
+                            mbar_arrive_expect_tx(&ms.full[s][c], there * uint32_t(box * ((two ? 256 : 128) + (kE4m3 && c == MT ? 1 : 0))));
                         ++asked;
                         __syncwarp();
                         if (i < KL / box && pg >= 0) {
                             unsigned char *to = dst + c * C::kPart + b * kBlock + i * box * 128;
                             if (c < MT) tma_load_3d(to, &maps.c, &ms.full[s][c], c * 128 + b * 64, line, pg);
                             else tma_load_3d(to, &maps.kr, &ms.full[s][c], 0, line, pg);
-                            if (kE4m3 && c == 0)
+                            if (kE4m3 && c == MT)
                                 bulk_load(&ms.scale[s][i * box], p.sc + (size_t(pg) << p.b.page_shift) + line, uint32_t(box), &ms.full[s][c]);
                         }
                         __syncwarp();
@@ -544,6 +674,27 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             for (uint32_t i = asked - min(asked, uint32_t(NS * (MT + 1))); i < asked; ++i) {
                 const uint32_t of = i / (MT + 1);
                 mbar_wait(&ms.full[of % NS][i % (MT + 1)], (of / NS) & 1, err);
+            }
+        } else if (kE4m3 && warp == 7) {
+            // ---- scales as numbers, and the largest --------------------------------------------
+            ItemWalk walk(ms.piece[0], ms.piece[1]);
+            Item it = {};
+            uint32_t t = 0;
+            while (ok && walk.next(p, it)) {
+                for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
+                    const uint32_t s = t % NS;
+                    if (t >= 2) wait_for(ok, &ms.p_ready[t & 1], ((t >> 1) - 1) & 1, err);  // those before have been used
+                    wait_for(ok, &ms.full[s][MT], (t / NS) & 1, err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    const float a = exp2_biased(ms.scale[s][lane]), b = exp2_biased(ms.scale[s][lane + 32]);
+                    ms.unit[t & 1][lane] = a, ms.unit[t & 1][lane + 32] = b;
+                    float top = fmaxf(a, b);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    if (lane == 0) ms.unit_top[t & 1] = top;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.unit_full[t & 1]);
+                }
             }
         }
     }
@@ -577,7 +728,7 @@ kda_status launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &
     static_assert(smem <= 232448, "shared memory of a CTA");
     if (!allow_smem<latent_tile_kernel<L, kE4m3>>(int(smem))) return KDA_ERR_CUDA;
     p.key_step = KL;
-    p.item_cost = 2 * KL;
+    p.item_cost = 8 * KL;
     p.min_keys = 2 * KL;
     const ProfScope prof(KDA_KERNEL_LATENT_ATTEND, stream);
     return launch_overlapped(latent_tile_kernel<L, kE4m3>, dim3(unsigned(plan.n_cta)), C::kThreads, smem, stream, p, maps);
