@@ -47,9 +47,10 @@ constexpr float kPUnits = 128.f;
 
 template <int L, bool kE4m3> struct Cfg {
     static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, its parts of 128 channels (matrix rows of O^T)
-    // e4m3: eight warps that bring the rows of Q, and registers split by groups of four warps
-    static constexpr int kRowWarps = 8, kThreads = kE4m3 ? 512 : 224, kLaunch = 128, kSoftmax = 200, kOther = 104;
-    static_assert(kSoftmax + 3 * kOther <= 4 * kLaunch, "the split takes no more than the launch has");
+    // softmax warps in groups of four; e4m3: eight warps that bring the rows of Q, and registers split by four warps
+    static constexpr int kGroups = kE4m3 ? 2 : 1, kSoftThreads = 128 * kGroups, kFirst = 4 * kGroups, kRowWarps = 8;
+    static constexpr int kThreads = kSoftThreads + (kE4m3 ? 128 + 32 * kRowWarps : 96), kLaunch = 96, kSoftmax = 144, kOther = 64;
+    static_assert(2 * kSoftmax + 3 * kOther <= 5 * kLaunch, "the split takes no more than the launch has");
     static constexpr int kQBytes = (NB + 1) * kBlock;
     static constexpr int kThird = kE4m3 ? kBlock : 0;  // e4m3: the weights' third terms, of two tiles
     static constexpr int kPart = kE4m3 ? kBlock : 2 * kBlock;  // 128 channels of a tile as they come
@@ -76,6 +77,7 @@ struct alignas(16) Misc {
     alignas(16) float unit[2][KL];        // by tile parity: the scales
     float unit_top[2];                    // and the largest of them
     float q_unit[4][BM];                  // by item: the rows' scales
+    float top[2][BM], scale_top[2][BM], sum[BM];  // what the two groups of softmax warps tell one another of a row
     uint64_t rows_full[4];                // and that they are there
 };
 
@@ -106,7 +108,7 @@ __device__ __forceinline__ void split_e5m2(float lo, float hi, uint32_t (&o)[3])
     }
 }
 
-// Lane l < 16 gets row l's columns [c, c + 32), lane l + 16 its columns [c + 32, c + 64), of the 16 rows a warp's
+// Lane l < 16 gets row l's columns [c, c + N), lane l + 16 its columns [c + 32, c + 32 + N), of the 16 rows a warp's
 // quarter of tensor memory holds of a product of 64.
 __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
     uint32_t r[32];
@@ -121,6 +123,17 @@ __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16], 32;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 // Four neighbouring lanes hold four values each: lane i of them gets everyone's i-th, in the order of the lanes.
 __device__ __forceinline__ void swap_4x4(float &a, float &b, float &c, float &d, int lane) {
@@ -132,16 +145,17 @@ __device__ __forceinline__ void swap_4x4(float &a, float &b, float &c, float &d,
     swap(a, b, 1), swap(c, d, 1), swap(a, c, 2), swap(b, d, 2);
 }
 
-// Barriers of the hardware's: 1 the votes, 2 the meetings of the 128 softmax threads.
-__device__ __forceinline__ bool any_of_128(bool mine) {
+// Barriers of the hardware's: 1 the votes, 2 the meetings of the softmax threads.
+template <int kThreads>
+__device__ __forceinline__ bool any_of(bool mine) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(uint32_t(mine))
+        : "r"(uint32_t(mine)), "n"(kThreads)
         : "memory");
     return r != 0;
 }
@@ -180,7 +194,7 @@ __device__ __forceinline__ void ask_q(const LatentParams &p, const Item &it, uns
 // kda_attend_tile.cu.
 template <int L>
 __device__ __forceinline__ void split_q(const LatentParams &p, const Item &it, unsigned char *q_img, float *q_unit, int r0, int lane) {
-    constexpr int kPieces = L / 8 > 32 ? L / 8 / 32 : 1, kB = 4;  // of 16 bytes, of a lane; rows at a time
+    constexpr int kPieces = L / 8 > 32 ? L / 8 / 32 : 1, kB = 2;  // of 16 bytes, of a lane; rows at a time
 #pragma unroll 1
     for (int g = 0; g < 8 && r0 + g < it.rows; g += kB) {
         uint4 raw[kB][kPieces];
@@ -230,20 +244,22 @@ __device__ __forceinline__ void split_q(const LatentParams &p, const Item &it, u
 }
 
 // A tile in which some row does not see some key: zeroes the latents of absent keys and the non-finite ones that
-// not every row sees.  Two threads a key.
+// not every row sees.  Two threads a key, or four.
 template <int L, bool kE4m3>
 __device__ __noinline__ void look_over(const Item &it, int kb, uint32_t absent, unsigned char *tile, int tid) {
     constexpr int kPieces = kE4m3 ? L / 16 : L / 8;  // of 16 bytes, eight of them in a block's row
-    const int key = tid >> 1, j = kb + key, half = tid & 1;
+    constexpr int kEach = Cfg<L, kE4m3>::kSoftThreads / KL;
+    const int key = tid / kEach, j = kb + key, first = tid % kEach;
     const bool gone = j >= it.k1 || (absent >> (key / 16) & 1);
     unsigned char *img = tile + key * 128;
     auto piece = [&](int c) { return reinterpret_cast<uint4 *>(img + (c >> 3) * kBlock + (((c & 7) ^ (key & 7)) << 4)); };
     bool bad = false;
     if (!gone && j > it.ctx + it.tok0)
-        for (int c = half; c < kPieces; c += 2) bad |= kE4m3 ? odd_e4m3(*piece(c)) : odd_bf16(*piece(c));
-    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+        for (int c = first; c < kPieces; c += kEach) bad |= kE4m3 ? odd_e4m3(*piece(c)) : odd_bf16(*piece(c));
+#pragma unroll
+    for (int o = 1; o < kEach; o *= 2) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
     if (gone || bad)
-        for (int c = half; c < kPieces; c += 2) *piece(c) = make_uint4(0, 0, 0, 0);
+        for (int c = first; c < kPieces; c += kEach) *piece(c) = make_uint4(0, 0, 0, 0);
 }
 
 template <int L, bool kE4m3>
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         for (int i = 0; i < NS; ++i)
             for (int c = 0; c <= MT; ++c)
                 mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], 4), mbar_init(&ms.o_done[i], 1), mbar_init(&ms.unit_full[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], C::kFirst), mbar_init(&ms.o_done[i], 1), mbar_init(&ms.unit_full[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&ms.rows_full[i], C::kRowWarps);
         mbar_init(&ms.q_full, kE4m3 ? C::kRowWarps : 4), mbar_init(&ms.q_free, 1), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
         fence_mbar_init();
@@ -270,11 +286,11 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.c) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.kr) : "memory");
     }
-    if (warp == 4) tmem_alloc(&ms.tmem, C::kColumns);
+    if (warp == C::kFirst) tmem_alloc(&ms.tmem, C::kColumns);
     wait_prior_kernel();
     allow_next_kernel();
     if (tid < 2) p.parts[2 * cta + tid].state = 0;
-    if (warp == 5) {
+    if (warp == C::kFirst + 1) {
         Cursor a, z;
         const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
         if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has;
@@ -286,11 +302,14 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     uint32_t *err = p.b.err;
     bool ok = true;  // of this thread's waits
 
-    if (warp < 4) {
+    if (warp < C::kFirst) {
         if constexpr (kE4m3) set_regs<C::kSoftmax, C::kLaunch>();
-        // ---- softmax: two threads a row, 32 keys each; for O: thread = channel of each 128 ----
-        const int row = 16 * warp + (lane & 15), key0 = (lane >> 4) * 32;
-        const uint32_t lanes = uint32_t(warp * 32) << 16;
+        // ---- softmax: two threads a row, 32 keys each, or four of 16; for O: thread = channel of each 128,
+        // groups take 16 rows in turn ----
+        constexpr int G = C::kGroups, kKeys = 32 / G;
+        const int quarter = warp & 3, group = G > 1 ? warp >> 2 : 0;
+        const int row = 16 * quarter + (lane & 15), key0 = (lane >> 4) * 32 + group * kKeys;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
         ItemWalk walk(ms.piece[0], ms.piece[1]);
         Item it = {};
         uint32_t tile = 0;
@@ -315,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         if (more) ask(), put_q();
         for (; more; ++n_it) {
             const int nt = tiles_of(it), n_cols = (it.rows + 15) & ~15;
-            const bool live = 16 * warp < it.rows;  // this warp has rows of the item
+            const bool live = 16 * quarter < it.rows;  // this warp has rows of the item
             const int lim = it.ctx + it.tok0 + p.token_of(min(row, it.rows - 1));  // last key the row sees
             float ref = -INFINITY, l = 0.f;
             // e4m3: what weights times their keys' scales are in units of, before they become f16 (a power of two)
@@ -337,21 +356,21 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 if (tile >= 2) wait_for(ok, &ms.o_done[tile & 1], ((tile >> 1) - 1) & 1, err);
                 __syncwarp();
                 tc_fence_after();
-                float x[32];
+                float x[kKeys];
                 bool move = false;
                 float top = -INFINITY, unit_top = 0.f;
                 if constexpr (kE4m3) wait_for(ok, &ms.unit_full[tile & 1], (tile >> 1) & 1, err), __syncwarp();
                 const float *unit = ms.unit[tile & 1] + key0;
                 if (live) {
-                    tmem_ld_rows16(tm + lanes + (tile & 1) * C::kScores, x);
+                    tmem_ld_rows16(tm + lanes + (tile & 1) * C::kScores + group * kKeys, x);
                     if constexpr (kE4m3) {
                         // scores in powers of two: the latents' times their scales, and the key parts'
-                        float y[32];
-                        tmem_ld_rows16(tm + lanes + (tile & 1) * C::kScores + KL, y);
+                        float y[kKeys];
+                        tmem_ld_rows16(tm + lanes + (tile & 1) * C::kScores + KL + group * kKeys, y);
                         const float2 f2 = make_float2(q_unit, q_unit), sc = make_float2(p.scale_log2, p.scale_log2);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
+                        for (int i = 0; i < kKeys; i += 4) {
                             const float4 u = *reinterpret_cast<const float4 *>(unit + i);
                             const float2 a = fma2(mul2(make_float2(u.x, u.y), f2), make_float2(x[i], x[i + 1]),
                                                   mul2(make_float2(y[i], y[i + 1]), sc));
@@ -365,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     }
                     if (check) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < kKeys; ++i) {
                             const int j = kb + key0 + i;
                             if (j > lim || j >= it.k1 || (absent >> ((key0 + i) / 16) & 1)) x[i] = -INFINITY;
                             else if (kE4m3) unit_top = fmaxf(unit_top, unit[i]);
@@ -373,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     }
                     float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int i = 4; i < 32; i += 4)
+                    for (int i = 4; i < kKeys; i += 4)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[i + e]);
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kE4m3 ? 1.f : p.scale_log2);
@@ -384,7 +403,12 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                         move = move || unit_top > p_unit;
                     }
                 }
-                if (any_of_128(move)) {
+                if (any_of<C::kSoftThreads>(move)) {
+                    if constexpr (G > 1) {  // the row's maxima over both groups' keys
+                        if (lane < 16) ms.top[group][row] = top, ms.scale_top[group][row] = unit_top;
+                        named_sync<2, C::kSoftThreads>();
+                        top = fmaxf(top, ms.top[group ^ 1][row]), unit_top = fmaxf(unit_top, ms.scale_top[group ^ 1][row]);
+                    }
                     const float to = top > ref + kRefSlack ? top : ref;
                     float f = to != ref ? ex2(ref - to) : 1.f;
                     l *= f, ref = to;
@@ -393,12 +417,12 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                         const float unit_to = unit_top > p_unit ? fminf(4.f * unit_top, 0x1p127f) : p_unit;
                         f = f * (p_unit / unit_to), p_unit = unit_to;
                     }
-                    if (live && lane < 16) ms.back[row] = f;
-                    named_sync<2, 128>();
+                    if (live && lane < 16) ms.back[row] = f;  // (the same number from both groups)
+                    named_sync<2, C::kSoftThreads>();
                     if (v > 0) {
                         wait_o(tile - 1);
 #pragma unroll 1
-                        for (int c = 0; c < n_cols; c += 16) {
+                        for (int c = 16 * group; c < n_cols; c += 16 * G) {
                             float b[16];
 #pragma unroll
                             for (int i = 0; i < 16; i += 4) {
@@ -426,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     unsigned char *p_row = stage + C::kKrAt + row * 128;
                     constexpr int kStep = kE4m3 ? 16 : 8;  // keys whose weights, or terms of them, fill 16 bytes
 #pragma unroll
-                    for (int i = 0; i < 32; i += kStep) {
+                    for (int i = 0; i < kKeys; i += kStep) {
                         uint32_t w[kE4m3 ? 3 : 1][4];
 #pragma unroll
                         for (int e = 0; e < kStep / 2; ++e) {
@@ -466,6 +490,11 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 if (ok && lane == 0) mbar_arrive(&ms.p_ready[tile & 1]);
             }
             l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if constexpr (G > 1) {
+                if (group == 1 && lane < 16) ms.sum[row] = l;
+                named_sync<2, C::kSoftThreads>();
+                l += ms.sum[row];  // (of use to the first group)
+            }
             // the item's scores are all there, so the rows of the next may take the place of its own
             const Item was = it;
             more = walk.next(p, it);
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             // ---- output -----------------------------------------------------------------
             const bool whole = was.whole();
             float *data = p.part_data + (size_t(cta) * 2 + was.slot()) * size_t(BM) * (L + 2);
-            if (live && lane < 16) {
+            if (live && group == 0 && lane < 16) {
                 const float up = kE4m3 ? p_unit / kPUnits : 1.f;
                 ms.inv[row] = !whole ? up : l > 0.f || l != l ? up / l : 0.f;
                 if (row < was.rows) {
@@ -486,12 +515,12 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             }
             if (!whole && tid == 0) p.parts[2 * cta + was.slot()] = was.part();
             wait_o(tile - 1);
-            named_sync<2, 128>();
+            named_sync<2, C::kSoftThreads>();
             if (more) put_q();
             // a thread gets 16 rows of its channel; four neighbours swap them for four channels of a row each
-            const int ch0 = warp * 32 + (lane & ~3);
+            const int ch0 = quarter * 32 + (lane & ~3);
 #pragma unroll 1
-            for (int c = 0; c < n_cols; c += 16) {
+            for (int c = 16 * group; c < n_cols; c += 16 * G) {
                 float o[MT][16];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) tmem_ld16(tm_o + lanes + uint32_t(m * BM + c), o[m]);
@@ -522,9 +551,9 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 }
             }
             tc_fence_before();  // the next item's products rewrite O
-            named_sync<2, 128>();  // and its end the rows' factors and places
+            named_sync<2, C::kSoftThreads>();  // and its end the rows' factors and places
         }
-    } else if (kE4m3 && warp >= 8) {
+    } else if (kE4m3 && warp >= C::kFirst + 4) {
         // ---- rows of Q (e4m3), once the last item's scores are there.  Those are at most two tiles
         // ahead of the outputs, so nobody reads the scales of four items before ------------------
         if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
@@ -533,8 +562,8 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         for (uint32_t n_it = 0; ms.has && walk.next(p, it); ++n_it) {
             if (n_it > 0) wait_for(ok, &ms.q_free, (n_it - 1) & 1, err);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            ask_q<L, true, 32 * C::kRowWarps>(p, it, smem, tid - 256);
-            split_q<L>(p, it, smem, ms.q_unit[n_it & 3], (warp - 8) * 8, lane);
+            ask_q<L, true, 32 * C::kRowWarps>(p, it, smem, tid - 32 * (C::kFirst + 4));
+            split_q<L>(p, it, smem, ms.q_unit[n_it & 3], (warp - C::kFirst - 4) * 8, lane);
             cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
@@ -543,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     } else {
         if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
         if (!ms.has) {
-        } else if (warp == 4) {
+        } else if (warp == C::kFirst) {
             // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
             const uint32_t id_s = idesc_bf16_f32(64, KL), id_8 = idesc_e4m3_f32(64, KL);
             const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring));
@@ -588,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             if (elect_one()) mma_commit(&ms.done[0]);
             __syncwarp();
             mbar_wait(&ms.done[0], 0, err);
-        } else if (warp == 6) {
+        } else if (warp == C::kFirst + 2) {
             // ---- outputs, likewise ------------------------------------------------------------
             const uint32_t v_desc = desc_mn(smem_u32(ring), kBlock), p_desc = desc_k(smem_u32(ring + C::kKrAt)), p3_desc = desc_k(smem_u32(third));
             ItemWalk walk(ms.piece[0], ms.piece[1]);
@@ -629,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             if (elect_one()) mma_commit(&ms.done[1]);
             __syncwarp();
             mbar_wait(&ms.done[1], 0, err);
-        } else if (warp == 5) {
+        } else if (warp == C::kFirst + 1) {
             // ---- page fetches ------------------------------------------------------------------
             const int page_size = 1 << p.b.page_shift, box = min(page_size, KL);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
@@ -675,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 const uint32_t of = i / (MT + 1);
                 mbar_wait(&ms.full[of % NS][i % (MT + 1)], (of / NS) & 1, err);
             }
-        } else if (kE4m3 && warp == 7) {
+        } else if (kE4m3 && warp == C::kFirst + 3) {
             // ---- scales as numbers, and the largest --------------------------------------------
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
@@ -701,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) tmem_dealloc(tm, C::kColumns);
+    if (warp == C::kFirst) tmem_dealloc(tm, C::kColumns);
 }
 
 // [num_pages][page_size][channels]; a box is a tile's part of one page, 64 channels of it (zeros past the last
