@@ -5,7 +5,8 @@
 // kda_attend_generic.cu.  A CTA holds 32 rows and walks 32 keys a step through shared
 // memory: 16 threads side by side share two rows of the scores with two keys each; then
 // 64 threads share 8 rows of the outputs, DV / 64 channels each, in registers.  In the
-// absorbed form a key's first channels are its value, so the tile is read once for both.
+// absorbed form a key's first channels are its value, so the tile is read once for both.  Bound by the
+// reads of shared memory behind its multiplications: 8 of them for 48 bytes of scores, 8 for 16 of outputs.
 #include <type_traits>
 
 #include "kda_latent.cuh"
@@ -17,11 +18,6 @@ namespace {
 constexpr int BM = 32, KS = 32, kThreads = 256;
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 r = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                       __uint_as_float(r.y & 0xffff0000u));
-}
 __device__ __forceinline__ float4 load4(const uint8_t *p) {
     const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
     const float2 a = unpack_e4m3(uint16_t(r)), b = unpack_e4m3(uint16_t(r >> 16));
@@ -48,7 +44,7 @@ template <int DA, int DV, bool kExpanded> struct Smem {
     int has;
 };
 
-template <typename P, typename Act, typename Kv, int DA, int DV>
+template <typename P, typename Kv, int DA, int DV>
 __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_constant__ P p) {
     constexpr bool kExpanded = std::is_same_v<P, PrefillRowsParams>;
     using S = Smem<DA, DV, kExpanded>;
@@ -78,8 +74,8 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
             if (r < it.rows) {
                 long long row, head;
                 p.locate(it, r, row, head);
-                x = c < DA ? load4(static_cast<const Act *>(p.q_a) + row * p.qa_stride + head * p.qa_head + c)
-                           : load4(static_cast<const Act *>(p.q_r) + row * p.qr_stride + head * p.qr_head + (c - DA));
+                x = c < DA ? load4(static_cast<const float *>(p.q_a) + row * p.qa_stride + head * p.qa_head + c)
+                           : load4(static_cast<const float *>(p.q_r) + row * p.qr_stride + head * p.qr_head + (c - DA));
             }
             *reinterpret_cast<float4 *>(&s.q[r][c]) =
                 make_float4(x.x * p.scale_log2, x.y * p.scale_log2, x.z * p.scale_log2, x.w * p.scale_log2);
@@ -123,13 +119,13 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (at.line >= 0) {
                     if constexpr (kExpanded) {
-                        x = c < DA ? load4(static_cast<const Act *>(p.k) + at.line * p.k_stride + it.h * p.k_head + c)
-                                   : load4(static_cast<const Act *>(p.kr) + at.line * p.kr_stride + (c - DA));
+                        x = c < DA ? load4(static_cast<const float *>(p.k) + at.line * p.k_stride + it.h * p.k_head + c)
+                                   : load4(static_cast<const float *>(p.kr) + at.line * p.kr_stride + (c - DA));
                     } else if (c < DA) {
                         x = load4(static_cast<const Kv *>(p.c) + at.line * DA + c);
                         x = make_float4(x.x * at.unit, x.y * at.unit, x.z * at.unit, x.w * at.unit);
                     } else {
-                        x = load4(static_cast<const Act *>(p.kr) + at.line * p.rope + (c - DA));
+                        x = load4(static_cast<const float *>(p.kr) + at.line * p.rope + (c - DA));
                     }
                 }
                 *reinterpret_cast<float4 *>(&s.k[j][c]) = x;
@@ -140,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
                     const int j = i / (DV / 4), c = i % (DV / 4) * 4;
                     const long long line = s.at[j].line;
                     *reinterpret_cast<float4 *>(&s.v[j][c]) =
-                        line >= 0 ? load4(static_cast<const Act *>(p.v) + line * p.v_stride + it.h * p.v_head + c)
+                        line >= 0 ? load4(static_cast<const float *>(p.v) + line * p.v_stride + it.h * p.v_head + c)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
@@ -229,24 +225,24 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
             if (r >= it.rows) continue;
             long long row, head;
             p.locate(it, r, row, head);
-            Act *dst = static_cast<Act *>(p.out) + row * p.out_stride + head * p.out_head;
+            float *dst = static_cast<float *>(p.out) + row * p.out_stride + head * p.out_head;
             const float f = s.f[r];
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
                 const int ch = c / CV * 64 * CV + cx * CV + c % CV;
-                if (whole) dst[ch] = from_f32<Act>(o[a][c] * f);
+                if (whole) dst[ch] = o[a][c] * f;
                 else data[size_t(r) * DV + ch] = o[a][c];
             }
         }
     }
 }
 
-template <typename P, typename Act, typename Kv, int DA, int DV>
+template <typename P, typename Kv, int DA, int DV>
 kda_status launch(P &p, const AttendPlan &plan, cudaStream_t stream) {
-    auto kern = latent_generic_kernel<P, Act, Kv, DA, DV>;
+    auto kern = latent_generic_kernel<P, Kv, DA, DV>;
     constexpr int smem = int(sizeof(Smem<DA, DV, std::is_same_v<P, PrefillRowsParams>>));
     static_assert(smem <= 232448, "shared memory of a CTA");
-    if (!allow_smem<latent_generic_kernel<P, Act, Kv, DA, DV>>(smem)) return KDA_ERR_CUDA;
+    if (!allow_smem<latent_generic_kernel<P, Kv, DA, DV>>(smem)) return KDA_ERR_CUDA;
     p.key_step = KS;
     p.item_cost = KS;
     p.min_keys = 2 * KS;
@@ -254,22 +250,21 @@ kda_status launch(P &p, const AttendPlan &plan, cudaStream_t stream) {
     return launch_overlapped(kern, dim3(unsigned(plan.n_cta)), kThreads, size_t(smem), stream, p);
 }
 
-template <typename Act, typename Kv>
+template <typename Kv>
 kda_status by_latent(int L, LatentParams &p, const AttendPlan &plan, cudaStream_t s) {
     switch (L) {
-        case 128: return launch<LatentParams, Act, Kv, 128, 128>(p, plan, s);
-        case 256: return launch<LatentParams, Act, Kv, 256, 256>(p, plan, s);
-        case 512: return launch<LatentParams, Act, Kv, 512, 512>(p, plan, s);
+        case 128: return launch<LatentParams, Kv, 128, 128>(p, plan, s);
+        case 256: return launch<LatentParams, Kv, 256, 256>(p, plan, s);
+        case 512: return launch<LatentParams, Kv, 512, 512>(p, plan, s);
     }
     return KDA_ERR_UNSUPPORTED;
 }
 
-template <typename Act>
 kda_status by_heads(int dn, int dv, PrefillRowsParams &p, const AttendPlan &plan, cudaStream_t s) {
-    if (dn == 64 && dv == 64) return launch<PrefillRowsParams, Act, Act, 64, 64>(p, plan, s);
-    if (dn == 64 && dv == 128) return launch<PrefillRowsParams, Act, Act, 64, 128>(p, plan, s);
-    if (dn == 128 && dv == 64) return launch<PrefillRowsParams, Act, Act, 128, 64>(p, plan, s);
-    if (dn == 128 && dv == 128) return launch<PrefillRowsParams, Act, Act, 128, 128>(p, plan, s);
+    if (dn == 64 && dv == 64) return launch<PrefillRowsParams, float, 64, 64>(p, plan, s);
+    if (dn == 64 && dv == 128) return launch<PrefillRowsParams, float, 64, 128>(p, plan, s);
+    if (dn == 128 && dv == 64) return launch<PrefillRowsParams, float, 128, 64>(p, plan, s);
+    if (dn == 128 && dv == 128) return launch<PrefillRowsParams, float, 128, 128>(p, plan, s);
     return KDA_ERR_UNSUPPORTED;
 }
 
@@ -281,17 +276,13 @@ void latent_generic_plan(AttendPlan *plan) {
 }
 
 kda_status latent_generic_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
-    if (c->act == KDA_BF16)
-        return c->format == KDA_KV_E4M3 ? by_latent<__nv_bfloat16, uint8_t>(c->latent_dim, p, plan, stream)
-                                        : by_latent<__nv_bfloat16, __nv_bfloat16>(c->latent_dim, p, plan, stream);
-    return c->format == KDA_KV_E4M3 ? by_latent<float, uint8_t>(c->latent_dim, p, plan, stream)
-                                    : by_latent<float, float>(c->latent_dim, p, plan, stream);
+    return c->format == KDA_KV_E4M3 ? by_latent<uint8_t>(c->latent_dim, p, plan, stream)
+                                    : by_latent<float>(c->latent_dim, p, plan, stream);
 }
 
-kda_status prefill_generic_launch(const kda_latent_cache *c, const kda_latent_prefill_io *io, PrefillRowsParams &p,
+kda_status prefill_generic_launch(const kda_latent_cache *, const kda_latent_prefill_io *io, PrefillRowsParams &p,
                                   const AttendPlan &plan, cudaStream_t stream) {
-    return c->act == KDA_BF16 ? by_heads<__nv_bfloat16>(io->nope_dim, io->value_dim, p, plan, stream)
-                              : by_heads<float>(io->nope_dim, io->value_dim, p, plan, stream);
+    return by_heads(io->nope_dim, io->value_dim, p, plan, stream);
 }
 
 }  // namespace kv

@@ -12,20 +12,27 @@
 // take the place of the tile's shared key part, which the scores have used by then.
 //
 // A tile comes, is multiplied and leaves in parts of 128 channels, each with barriers of
-// its own: shared memory holds two tiles, and in whole ones the copies would wait
+// its own: shared memory holds two tiles of 512 channels, and in whole ones the copies would wait
 // for the products and the products for the copies.
 //
-// Warps: 0-3 softmax (two threads a row, later a thread a channel) and the rows of Q, 4
-// issues the scores, 5 fetches pages by TMA, 6 issues the outputs (a warp of its own, so that
-// neither product waits for what the other needs).
+// Warps: softmax (4; e4m3: 8), then one that issues the scores, one that fetches pages by TMA, and
+// one that issues the outputs (so that neither product waits for what the other needs).  In
+// the softmax two threads share a row, four in e4m3; for O a thread is a channel.
 //
-// e4m3 pages: the scores take the latents as they are, against Q as the sum of two e4m3 terms
-// (exact to about 2^-18 of a row's largest value), beside those of the bf16 key parts.  Eight more
-// warps make one f16 tile of the latents for the outputs, a part at a time as those of the tile before
-// give its place back.  f16 holds an e4m3 value exactly and takes one conversion for two of
-// them, where bf16, which has room for the scales, takes three times as many instructions.  So the scales
-// (7 makes numbers of them) multiply the scores, and the weights on their way to f16, in
-// units that follow the largest scale a row has met.
+// e4m3 pages go to both products as they are.  The scores take them against Q as the sum of two e4m3 terms,
+// 2^e (q1 + q2) (exact to about 2^-18 of a row's largest value), beside those of the bf16 key parts; the outputs
+// against the weights as three e5m2 terms, p1 + p2 + p3, each what the ones before leave: off by
+// (1/9)^3 after the 2^-11 of the f16 they are split from, together less than the 2^-8 of bf16 weights, and
+// e5m2 reaches down to 2^-22 of the largest weight where e4m3 would end at 2^-18.  The
+// keys' scales (one more warp makes numbers of them) multiply the scores, and the weights before they are split,
+// in units that follow the largest scale a row has met.  Eight more warps bring and split the rows of
+// Q.  (Latents widened to f16 for the outputs: 64 verifies of 8 tokens 715 us against 432; to bf16, 835:
+// two tiles and a wide one fill shared memory, and one tile's widening, products and copies wait in turn.)
+//
+// What bounds it (latents of 512, pages of 64): single tokens, the cache's bytes: 64 sequences of up
+// to 32768 tokens at 64 heads take 142 us, 5.4 TB/s.  Verifies in e4m3, the reads of shared memory:
+// a product of 64 x 64 scores reads 4 KB in its 32.5 cycles and one of 128 channels 6 KB in 48.5 (measured), 2330 cycles
+// a tile and 320 for its copy; a tile takes 2900.  One sequence of 4096 tokens: 17 us, of them 7 before the first tile is there.
 //
 // A latent behind a row's position weighs nothing, but 0 * NaN is NaN in the product.
 // So in the few tiles where some row does not see some key, the softmax warps zero the
@@ -41,8 +48,9 @@ namespace {
 constexpr int KL = 64, BM = 64;       // keys of a tile, rows of an item
 constexpr int kBlock = 64 * 128;      // 64 rows of 64 channels, bf16, swizzled over 128 bytes
 constexpr float kRefSlack = 8.f;
-// e4m3: weights (up to 2^8) times scales (up to p_unit) become f16 in units of p_unit / 2^7: no more than 2^15, and what an
-// f16 rounds off below its normal range is no more than 2^-32 of the largest scale's whole weight.
+// e4m3: weights (up to 2^8) times scales (up to p_unit) are split in units of p_unit / 2^7: no more than 2^15, and what the
+// last term leaves below its normal range, 2^-17, no more than 2^-22 of the largest scale's whole weight (p_unit is up to four
+// times that scale).
 constexpr float kPUnits = 128.f;
 
 template <int L, bool kE4m3> struct Cfg {
@@ -85,14 +93,6 @@ struct LatentMaps {
     CUtensorMap c, kr;
 };
 
-// Any e4m3 NaN among sixteen.
-__device__ __forceinline__ bool odd_e4m3(const uint4 &w) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    uint32_t odd = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) odd |= ((x[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    return odd != 0;
-}
 // Instruction descriptor as idesc_e4m3_f32, of A e4m3 with its rows' values apart (a_mn of idesc_bf16_f32) and B e5m2.
 constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N) {
     return (1u << 4) | (1u << 10) | (1u << 15) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
@@ -255,7 +255,7 @@ __device__ __noinline__ void look_over(const Item &it, int kb, uint32_t absent, 
     auto piece = [&](int c) { return reinterpret_cast<uint4 *>(img + (c >> 3) * kBlock + (((c & 7) ^ (key & 7)) << 4)); };
     bool bad = false;
     if (!gone && j > it.ctx + it.tok0)
-        for (int c = first; c < kPieces; c += kEach) bad |= kE4m3 ? odd_e4m3(*piece(c)) : odd_bf16(*piece(c));
+        for (int c = first; c < kPieces; c += kEach) bad |= kE4m3 ? nan_codes(*piece(c)) != 0 : odd_bf16(*piece(c));
 #pragma unroll
     for (int o = 1; o < kEach; o *= 2) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
     if (gone || bad)
@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             uint32_t t = 0, n_q = 0;
             while (ok && walk.next(p, it)) {
                 wait_for(ok, &ms.q_full, n_q++ & 1, err);
+                ok = __all_sync(0xffffffffu, ok);
                 for (int v = tiles_of(it); v > 0 && ok; --v, ++t) {
                     const uint32_t s = t % NS, t_s = tm + (t & 1) * C::kScores;
                     if (t >= 2) wait_for(ok, &ms.p_ready[t & 1], ((t >> 1) - 1) & 1, err);  // those before have been read

@@ -642,7 +642,7 @@ typedef struct {
     const int32_t *cu_seqlens; /* [n_seqs + 1], from 0 */
     const int32_t *cu_kv;      /* [n_seqs + 1], from 0 */
     int32_t n_seqs;
-    int32_t max_rows;    /* host bound on cu_seqlens[n_seqs] */
+    int32_t max_rows;    /* host bound on cu_seqlens[n_seqs]: q_n, q_r and out have this many rows */
     int32_t max_kv_rows; /* host bound on cu_kv[n_seqs]: k, kr and v have this many rows */
     int32_t max_new;     /* host bound on the tokens of one sequence */
 } kda_latent_prefill_batch;
@@ -668,7 +668,11 @@ KDA_API kda_status kda_latent_read(const kda_latent_cache *cache, const kda_kv_b
  * row whose keys are all absent or score -inf gets zeros.  Among the keys that a row sees, one with an
  * infinity or NaN leaves what the formula gives, or, where its score is -inf, may add nothing at all.
  * Precision: scores, the softmax's sums and the outputs before their rounding are in
- * 32 bits; bf16 calls round each weight to bf16 (2^-8 of it) before it meets its value.
+ * 32 bits; bf16 calls round each weight by at most 2^-8 of it before it meets its value.
+ * Over e4m3 pages they also take q_c as two e4m3 terms times a power of two a row, which
+ * rounds elements below 2^-10 of the row's largest by 2^-18 of that, and a row of q_c with an
+ * infinity or NaN gets NaN; and a weight times its key's scale may be rounded by 2^-22 of the largest
+ * weight times the largest scale that the row sees, where that is more.
  * workspace: device, 256-byte aligned, at least kda_latent_attend_workspace_bytes(cache,
  * batch) bytes (the host fields set it; 0 on invalid input); its contents mean nothing
  * between calls, and calls that share one must be ordered.  Results do not depend on it.
