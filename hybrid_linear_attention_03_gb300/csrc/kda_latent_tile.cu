@@ -15,9 +15,9 @@
 // its own: shared memory holds two tiles of 512 channels, and in whole ones the copies would wait
 // for the products and the products for the copies.
 //
-// Warps: softmax (4; e4m3: 8), then one that issues the scores, one that fetches pages by TMA, and
+// Warps: eight for the softmax, then one that issues the scores, one that fetches pages by TMA, and
 // one that issues the outputs (so that neither product waits for what the other needs).  In
-// the softmax two threads share a row, four in e4m3; for O a thread is a channel.
+// the softmax four threads share a row; for O a thread is a channel.
 //
 // e4m3 pages go to both products as they are.  The scores take them against Q as the sum of two e4m3 terms,
 // 2^e (q1 + q2) (exact to about 2^-18 of a row's largest value), beside those of the bf16 key parts; the outputs
@@ -46,6 +46,7 @@ namespace kv {
 namespace {
 
 constexpr int KL = 64, BM = 64;       // keys of a tile, rows of an item
+constexpr int kSoftThreads = 256, kFirst = kSoftThreads / 32;  // two groups of four softmax warps; the first warp behind them
 constexpr int kBlock = 64 * 128;      // 64 rows of 64 channels, bf16, swizzled over 128 bytes
 constexpr float kRefSlack = 8.f;
 // e4m3: weights (up to 2^8) times scales (up to p_unit) are split in units of p_unit / 2^7: no more than 2^15, and what the
@@ -55,8 +56,8 @@ constexpr float kPUnits = 128.f;
 
 template <int L, bool kE4m3> struct Cfg {
     static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, its parts of 128 channels (matrix rows of O^T)
-    // softmax warps in groups of four; e4m3: eight warps that bring the rows of Q, and registers split by four warps
-    static constexpr int kGroups = kE4m3 ? 2 : 1, kSoftThreads = 128 * kGroups, kFirst = 4 * kGroups, kRowWarps = 8;
+    // e4m3: eight more warps, that bring the rows of Q, and registers split by four warps
+    static constexpr int kRowWarps = 8;
     static constexpr int kThreads = kSoftThreads + (kE4m3 ? 128 + 32 * kRowWarps : 96), kLaunch = 96, kSoftmax = 144, kOther = 64;
     static_assert(2 * kSoftmax + 3 * kOther <= 5 * kLaunch, "the split takes no more than the launch has");
     static constexpr int kQBytes = (NB + 1) * kBlock;
@@ -108,21 +109,8 @@ __device__ __forceinline__ void split_e5m2(float lo, float hi, uint32_t (&o)[3])
     }
 }
 
-// Lane l < 16 gets row l's columns [c, c + N), lane l + 16 its columns [c + 32, c + 32 + N), of the 16 rows a warp's
+// Lane l < 16 gets row l's columns [c, c + 16), lane l + 16 its columns [c + 32, c + 48), of the 16 rows a warp's
 // quarter of tensor memory holds of a product of 64.
-__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], 32;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
@@ -244,11 +232,11 @@ __device__ __forceinline__ void split_q(const LatentParams &p, const Item &it, u
 }
 
 // A tile in which some row does not see some key: zeroes the latents of absent keys and the non-finite ones that
-// not every row sees.  Two threads a key, or four.
+// not every row sees.  Four threads a key.
 template <int L, bool kE4m3>
 __device__ __noinline__ void look_over(const Item &it, int kb, uint32_t absent, unsigned char *tile, int tid) {
     constexpr int kPieces = kE4m3 ? L / 16 : L / 8;  // of 16 bytes, eight of them in a block's row
-    constexpr int kEach = Cfg<L, kE4m3>::kSoftThreads / KL;
+    constexpr int kEach = kSoftThreads / KL;
     const int key = tid / kEach, j = kb + key, first = tid % kEach;
     const bool gone = j >= it.k1 || (absent >> (key / 16) & 1);
     unsigned char *img = tile + key * 128;
@@ -277,20 +265,20 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         for (int i = 0; i < NS; ++i)
             for (int c = 0; c <= MT; ++c)
                 mbar_init(&ms.full[i][c], 1), mbar_init(&ms.empty[i][c], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], C::kFirst), mbar_init(&ms.o_done[i], 1), mbar_init(&ms.unit_full[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ms.s_full[i], 1), mbar_init(&ms.p_ready[i], kFirst), mbar_init(&ms.o_done[i], 1), mbar_init(&ms.unit_full[i], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&ms.rows_full[i], C::kRowWarps);
-        mbar_init(&ms.q_full, kE4m3 ? C::kRowWarps : 4), mbar_init(&ms.q_free, 1), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
+        mbar_init(&ms.q_full, kE4m3 ? C::kRowWarps : kFirst), mbar_init(&ms.q_free, 1), mbar_init(&ms.done[0], 1), mbar_init(&ms.done[1], 1);
         fence_mbar_init();
     }
     if (tid == 32) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.c) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.kr) : "memory");
     }
-    if (warp == C::kFirst) tmem_alloc(&ms.tmem, C::kColumns);
+    if (warp == kFirst) tmem_alloc(&ms.tmem, C::kColumns);
     wait_prior_kernel();
     allow_next_kernel();
     if (tid < 2) p.parts[2 * cta + tid].state = 0;
-    if (warp == C::kFirst + 1) {
+    if (warp == kFirst + 1) {
         Cursor a, z;
         const bool has = find_piece(p, cta, int(gridDim.x), lane, a, z);
         if (lane == 0) ms.piece[0] = a, ms.piece[1] = z, ms.has = has;
@@ -302,12 +290,12 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     uint32_t *err = p.b.err;
     bool ok = true;  // of this thread's waits
 
-    if (warp < C::kFirst) {
+    if (warp < kFirst) {
         if constexpr (kE4m3) set_regs<C::kSoftmax, C::kLaunch>();
-        // ---- softmax: two threads a row, 32 keys each, or four of 16; for O: thread = channel of each 128,
-        // groups take 16 rows in turn ----
-        constexpr int G = C::kGroups, kKeys = 32 / G;
-        const int quarter = warp & 3, group = G > 1 ? warp >> 2 : 0;
+        // ---- softmax: four threads a row, 16 keys each; for O: thread = channel of each 128, the groups take 16 rows
+        // in turn ----
+        constexpr int kKeys = 16;
+        const int quarter = warp & 3, group = warp >> 2;
         const int row = 16 * quarter + (lane & 15), key0 = (lane >> 4) * 32 + group * kKeys;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         ItemWalk walk(ms.piece[0], ms.piece[1]);
@@ -329,7 +317,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         };
         bool more = ms.has && walk.next(p, it);
         auto ask = [&] {
-            if constexpr (!kE4m3) ask_q<L, false, 128>(p, it, smem, tid);
+            if constexpr (!kE4m3) ask_q<L, false, kSoftThreads>(p, it, smem, tid);
         };
         if (more) ask(), put_q();
         for (; more; ++n_it) {
@@ -403,12 +391,11 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                         move = move || unit_top > p_unit;
                     }
                 }
-                if (any_of<C::kSoftThreads>(move)) {
-                    if constexpr (G > 1) {  // the row's maxima over both groups' keys
-                        if (lane < 16) ms.top[group][row] = top, ms.scale_top[group][row] = unit_top;
-                        named_sync<2, C::kSoftThreads>();
-                        top = fmaxf(top, ms.top[group ^ 1][row]), unit_top = fmaxf(unit_top, ms.scale_top[group ^ 1][row]);
-                    }
+                if (any_of<kSoftThreads>(move)) {
+                    // the row's maxima over both groups' keys
+                    if (lane < 16) ms.top[group][row] = top, ms.scale_top[group][row] = unit_top;
+                    named_sync<2, kSoftThreads>();
+                    top = fmaxf(top, ms.top[group ^ 1][row]), unit_top = fmaxf(unit_top, ms.scale_top[group ^ 1][row]);
                     const float to = top > ref + kRefSlack ? top : ref;
                     float f = to != ref ? ex2(ref - to) : 1.f;
                     l *= f, ref = to;
@@ -418,11 +405,11 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                         f = f * (p_unit / unit_to), p_unit = unit_to;
                     }
                     if (live && lane < 16) ms.back[row] = f;  // (the same number from both groups)
-                    named_sync<2, C::kSoftThreads>();
+                    named_sync<2, kSoftThreads>();
                     if (v > 0) {
                         wait_o(tile - 1);
 #pragma unroll 1
-                        for (int c = 16 * group; c < n_cols; c += 16 * G) {
+                        for (int c = 16 * group; c < n_cols; c += 32) {
                             float b[16];
 #pragma unroll
                             for (int i = 0; i < 16; i += 4) {
@@ -490,11 +477,9 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 if (ok && lane == 0) mbar_arrive(&ms.p_ready[tile & 1]);
             }
             l += __shfl_xor_sync(0xffffffffu, l, 16);
-            if constexpr (G > 1) {
-                if (group == 1 && lane < 16) ms.sum[row] = l;
-                named_sync<2, C::kSoftThreads>();
-                l += ms.sum[row];  // (of use to the first group)
-            }
+            if (group == 1 && lane < 16) ms.sum[row] = l;
+            named_sync<2, kSoftThreads>();
+            l += ms.sum[row];  // (of use to the first group)
             // the item's scores are all there, so the rows of the next may take the place of its own
             const Item was = it;
             more = walk.next(p, it);
@@ -515,12 +500,12 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             }
             if (!whole && tid == 0) p.parts[2 * cta + was.slot()] = was.part();
             wait_o(tile - 1);
-            named_sync<2, C::kSoftThreads>();
+            named_sync<2, kSoftThreads>();
             if (more) put_q();
             // a thread gets 16 rows of its channel; four neighbours swap them for four channels of a row each
             const int ch0 = quarter * 32 + (lane & ~3);
 #pragma unroll 1
-            for (int c = 16 * group; c < n_cols; c += 16 * G) {
+            for (int c = 16 * group; c < n_cols; c += 32) {
                 float o[MT][16];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) tmem_ld16(tm_o + lanes + uint32_t(m * BM + c), o[m]);
@@ -551,9 +536,9 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 }
             }
             tc_fence_before();  // the next item's products rewrite O
-            named_sync<2, C::kSoftThreads>();  // and its end the rows' factors and places
+            named_sync<2, kSoftThreads>();  // and its end the rows' factors and places
         }
-    } else if (kE4m3 && warp >= C::kFirst + 4) {
+    } else if (kE4m3 && warp >= kFirst + 4) {
         // ---- rows of Q (e4m3), once the last item's scores are there.  Those are at most two tiles
         // ahead of the outputs, so nobody reads the scales of four items before ------------------
         if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
@@ -562,8 +547,8 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
         for (uint32_t n_it = 0; ms.has && walk.next(p, it); ++n_it) {
             if (n_it > 0) wait_for(ok, &ms.q_free, (n_it - 1) & 1, err);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            ask_q<L, true, 32 * C::kRowWarps>(p, it, smem, tid - 32 * (C::kFirst + 4));
-            split_q<L>(p, it, smem, ms.q_unit[n_it & 3], (warp - C::kFirst - 4) * 8, lane);
+            ask_q<L, true, 32 * C::kRowWarps>(p, it, smem, tid - 32 * (kFirst + 4));
+            split_q<L>(p, it, smem, ms.q_unit[n_it & 3], (warp - kFirst - 4) * 8, lane);
             cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
@@ -572,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     } else {
         if constexpr (kE4m3) set_regs<C::kOther, C::kLaunch>();
         if (!ms.has) {
-        } else if (warp == C::kFirst) {
+        } else if (warp == kFirst) {
             // ---- scores (converged warp, one lane issues; descriptors count 16-byte units) -------
             const uint32_t id_s = idesc_bf16_f32(64, KL), id_8 = idesc_e4m3_f32(64, KL);
             const uint32_t q_desc = desc_k(smem_u32(smem)), k_desc = desc_k(smem_u32(ring));
@@ -618,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             if (elect_one()) mma_commit(&ms.done[0]);
             __syncwarp();
             mbar_wait(&ms.done[0], 0, err);
-        } else if (warp == C::kFirst + 2) {
+        } else if (warp == kFirst + 2) {
             // ---- outputs, likewise ------------------------------------------------------------
             const uint32_t v_desc = desc_mn(smem_u32(ring), kBlock), p_desc = desc_k(smem_u32(ring + C::kKrAt)), p3_desc = desc_k(smem_u32(third));
             ItemWalk walk(ms.piece[0], ms.piece[1]);
@@ -659,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             if (elect_one()) mma_commit(&ms.done[1]);
             __syncwarp();
             mbar_wait(&ms.done[1], 0, err);
-        } else if (warp == C::kFirst + 1) {
+        } else if (warp == kFirst + 1) {
             // ---- page fetches ------------------------------------------------------------------
             const int page_size = 1 << p.b.page_shift, box = min(page_size, KL);
             ItemWalk walk(ms.piece[0], ms.piece[1]);
@@ -705,7 +690,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 const uint32_t of = i / (MT + 1);
                 mbar_wait(&ms.full[of % NS][i % (MT + 1)], (of / NS) & 1, err);
             }
-        } else if (kE4m3 && warp == C::kFirst + 3) {
+        } else if (kE4m3 && warp == kFirst + 3) {
             // ---- scales as numbers, and the largest --------------------------------------------
             ItemWalk walk(ms.piece[0], ms.piece[1]);
             Item it = {};
@@ -731,7 +716,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == C::kFirst) tmem_dealloc(tm, C::kColumns);
+    if (warp == kFirst) tmem_dealloc(tm, C::kColumns);
 }
 
 // [num_pages][page_size][channels]; a box is a tile's part of one page, 64 channels of it (zeros past the last
