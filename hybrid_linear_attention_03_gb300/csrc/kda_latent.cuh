@@ -90,7 +90,7 @@ kda_status latent_tile_launch(const kda_latent_cache *c, LatentParams &p, const 
 bool prefill_tile_plan(const kda_latent_cache *c, const kda_latent_prefill_batch *b, AttendPlan *plan);
 kda_status prefill_tile_launch(const kda_latent_cache *c, const kda_latent_prefill_io *io, PrefillRowsParams &p,
                                const AttendPlan &plan, cudaStream_t stream);
-void latent_generic_plan(AttendPlan *plan);
+void latent_generic_plan(int latent, AttendPlan *plan);  // 0: the expanded form
 kda_status latent_generic_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream);
 kda_status prefill_generic_launch(const kda_latent_cache *c, const kda_latent_prefill_io *io, PrefillRowsParams &p,
                                   const AttendPlan &plan, cudaStream_t stream);

@@ -11,7 +11,7 @@ namespace kv {
 namespace {
 
 constexpr int kCombineThreads = 256;
-constexpr int kMaxCtas = 256;  // of an attention kernel's grid
+constexpr int kMaxCtas = 320;  // of an attention kernel's grid
 
 // A load that stays where it is written: the compiler moves plain ones to their uses, one after the other.
 __device__ __forceinline__ float2 load_now(const float *p) {
@@ -214,7 +214,7 @@ struct LatentChoice {
 static LatentChoice choose(const kda_latent_cache *c) {
     LatentChoice ch;
     if (latent_tile_plan(c, &ch.plan)) ch.launch = latent_tile_launch;
-    else latent_generic_plan(&ch.plan), ch.launch = latent_generic_launch;
+    else latent_generic_plan(c->latent_dim, &ch.plan), ch.launch = latent_generic_launch;
     ch.plan.n_cta = std::min(ch.plan.n_cta, kMaxCtas);
     return ch;
 }
@@ -250,7 +250,7 @@ struct PrefillChoice {
 static PrefillChoice choose(const kda_latent_cache *c, const kda_latent_prefill_batch *b) {
     PrefillChoice ch;
     if (prefill_tile_plan(c, b, &ch.plan)) ch.launch = prefill_tile_launch;
-    else latent_generic_plan(&ch.plan), ch.launch = prefill_generic_launch;
+    else latent_generic_plan(0, &ch.plan), ch.launch = prefill_generic_launch;
     ch.plan.n_cta = std::min(ch.plan.n_cta, kMaxCtas);
     return ch;
 }

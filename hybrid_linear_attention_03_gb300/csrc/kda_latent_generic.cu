@@ -7,6 +7,7 @@
 // 64 threads share 8 rows of the outputs, DV / 64 channels each, in registers.  In the
 // absorbed form a key's first channels are its value, so the tile is read once for both.  Bound by the
 // reads of shared memory behind its multiplications: 8 of them for 48 bytes of scores, 8 for 16 of outputs.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_latent.cuh"
@@ -237,10 +238,20 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
     }
 }
 
+// CTAs of an SM by the latent's channels (0: the expanded form): two where shared memory holds two, as eight warps
+// leave the SM waiting at their barriers (five sequences of 800 tokens at most, 12 heads: 54 us with one, 47 with
+// two; three prompts of 700 at most 219 and 163).
+constexpr int ctas_of_sm(int latent) { return latent == 512 ? 1 : 2; }
+
 template <typename P, typename Kv, int DA, int DV>
 kda_status launch(P &p, const AttendPlan &plan, cudaStream_t stream) {
     auto kern = latent_generic_kernel<P, Kv, DA, DV>;
-    constexpr int smem = int(sizeof(Smem<DA, DV, std::is_same_v<P, PrefillRowsParams>>));
+    // As much that the CTAs of an SM are kCtas: launched while the kernel before still holds some SMs, a grid that leaves
+    // room would crowd the others (three prompts of 700 tokens at most: 456 us for what takes 233).
+    constexpr bool kExpanded = std::is_same_v<P, PrefillRowsParams>;
+    constexpr int kNeeds = int(sizeof(Smem<DA, DV, kExpanded>)), kCtas = ctas_of_sm(kExpanded ? 0 : DA);
+    constexpr int smem = std::max(kNeeds, (kCtas == 1 ? 120 : 80) * 1024);
+    static_assert(kCtas * (smem + 1024) <= 228 * 1024, "they fit");
     static_assert(smem <= 232448, "shared memory of a CTA");
     if (!allow_smem<latent_generic_kernel<P, Kv, DA, DV>>(smem)) return KDA_ERR_CUDA;
     p.key_step = KS;
@@ -270,9 +281,9 @@ kda_status by_heads(int dn, int dv, PrefillRowsParams &p, const AttendPlan &plan
 
 }  // namespace
 
-void latent_generic_plan(AttendPlan *plan) {
+void latent_generic_plan(int latent, AttendPlan *plan) {
     plan->bm = BM;
-    plan->n_cta = sm_count();
+    plan->n_cta = ctas_of_sm(latent) * sm_count();
 }
 
 kda_status latent_generic_launch(const kda_latent_cache *c, LatentParams &p, const AttendPlan &plan, cudaStream_t stream) {
