@@ -52,7 +52,7 @@ constexpr float kRefSlack = 8.f;
 // e4m3: weights (up to 2^8) times scales (up to p_unit) are split in units of p_unit / 2^7: no more than 2^15, and what the
 // last term leaves below its normal range, 2^-17, no more than 2^-22 of the largest scale's whole weight (p_unit is up to four
 // times that scale).
-constexpr float kPUnits = 128.f;
+constexpr float kPUnits = 128.f, kLeastUnit = 0x1p-120f;  // kPUnits / p_unit stays finite
 
 template <int L, bool kE4m3> struct Cfg {
     static constexpr int NB = L / 64, MT = L / 128;  // blocks of a latent, its parts of 128 channels (matrix rows of O^T)
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
             const int lim = it.ctx + it.tok0 + p.token_of(min(row, it.rows - 1));  // last key the row sees
             float ref = -INFINITY, l = 0.f;
             // e4m3: what weights times their keys' scales are in units of, before they become f16 (a power of two)
-            float p_unit = 0x1p-100f, q_unit = 0.f;
+            float p_unit = kLeastUnit, q_unit = 0.f;
             if constexpr (kE4m3) {
                 wait_for(ok, &ms.rows_full[n_it & 3], (n_it >> 2) & 1, err);
                 __syncwarp();

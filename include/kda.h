@@ -672,7 +672,7 @@ KDA_API kda_status kda_latent_read(const kda_latent_cache *cache, const kda_kv_b
  * Over e4m3 pages they also take q_c as two e4m3 terms times a power of two a row, which
  * rounds elements below 2^-10 of the row's largest by 2^-18 of that, and a row of q_c with an
  * infinity or NaN gets NaN; and a weight times its key's scale may be rounded by 2^-22 of the largest
- * weight times the largest scale that the row sees, where that is more.
+ * weight times the largest scale that the row sees (taken as at least 2^-122), where that is more.
  * workspace: device, 256-byte aligned, at least kda_latent_attend_workspace_bytes(cache,
  * batch) bytes (the host fields set it; 0 on invalid input); its contents mean nothing
  * between calls, and calls that share one must be ordered.  Results do not depend on it.

@@ -435,6 +435,29 @@ def test_small_scales_and_zero_queries(scale, fmt):
     b.check_attend(q, out, held, scale)
 
 
+@FMTS
+@pytest.mark.parametrize("power", [-117, -100, 100])
+def test_latents_of_extreme_sizes(power, fmt):
+    """Scales next to the ends of their range.  (In units of the latents, so that the tolerance's floor of 1e-30 means nothing;
+    weights times scales are off by 2^-22 of the largest, of scales as of 2^-122 at least: with 70 keys and codes of up to 448
+    less than 70 * 448 * 2^-144, where a 2^-7 of sum p |v| is above 2^-126.)"""
+    b = R.Batch([2], [70], 9, 512, 64, 16, BF, fmt, seed=97)
+    w = b.whole()
+    c, kr = w.randn(w.rows, 512, gain=2.0 ** power), w.randn(w.rows, 64)
+    kda.kda_latent_append(b.kv, None, kda.make_latent_io(c.cuda(), kr.cuda(), None, None), w.batch)
+    held, kr = b.held()[0]
+    q = b.queries()
+    q[0].mul_(2.0 ** -power if power < 0 and power > -110 else 2.0 ** -100 if power > 0 else 1.0)
+    out = torch.empty_like(q[0])
+    kda.kda_latent_attend(b.kv, kda.make_latent_attn_io(*q, out, 0.05), b.batch, b.workspace())
+    b.no_error()
+    qc, qr = q[0].double().cpu(), q[1].double().cpu()
+    s = (torch.einsum("thl,jl->thj", qc, held) + torch.einsum("thr,jr->thj", qr, kr)) * 0.05
+    ref, mag = R.attend(s, held[:, None] * 2.0 ** -power, 68)
+    qk = (qc.norm(dim=-1) * held.norm(dim=-1).max() + qr.norm(dim=-1) * kr.norm(dim=-1).max()) * 0.05
+    R.check(out.double().cpu() * 2.0 ** -power, ref, mag, qk, 576, BF)
+
+
 def test_bad_pages_and_tables_on_the_device():
     """A page outside the cache: its tokens are absent; inconsistent tables: the sequence's rows are left alone."""
     for act, new, total, heads in ((BF, [1, 1], [100, 90], 16), (BF, [20, 30], [100, 90], 4), (F32, [2, 3], [100, 90], 4)):
