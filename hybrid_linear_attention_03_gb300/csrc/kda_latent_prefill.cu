@@ -14,6 +14,9 @@
 // weights, the product of the other and the other side's are under way.  So that two tiles of keys fit beside 256
 // rows of Q of 192 channels, values come in half tiles.  ref moves, and O and the sums with it, when the
 // weights of a half sum to more than 2^16.
+// A prompt of 8192 tokens at 64 heads of 128 + 64 / 128 takes 1100 us (1250 TFLOP/s), 512 tokens behind 32256 530 us: 4050 cycles for
+// 128 keys of both sides, where their products' multiplications and reads take 2660 and a thread's softmax about 3000, the two
+// waiting for each other by turns.
 //
 // Warps: 0-3 side 0, 4-7 side 1 (a thread a row); 8 and 9 issue a side's products each;
 // 10 and 11 fetch the rows of Q, keys and values by TMA; 12-15 look values over:
