@@ -781,6 +781,57 @@ def test_prefill_bad_tables():
 
 
 @ACTS
+def test_prefill_replayed_with_other_lengths(act):
+    """Captured once, replayed with tables that move work between CTAs, sequences that drop out and one past the bound."""
+    r = R.Rows([300, 129, 40], [700, 400, 333], 3, 128, 64, 128, act, seed=83)
+    ws, st = r.workspace(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        r.call(ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            r.call(ws)
+    torch.cuda.synchronize()
+    for new, total in (([300, 129, 40], [700, 400, 333]), ([1, 0, 256], [1433, 0, 256]), ([0, 128, 0], [5, 1400, 9]),
+                       ([7, 8, 9], [7, 8, 9]), ([255, 1, 128], [255, 1000, 129])):
+        r.new, r.total, r.rows, r.keys = new, total, sum(new), sum(total)
+        for host, dev, n in ((r.cu, r.dev[0], new), (r.cu_kv, r.dev[1], total)):
+            host.copy_(torch.tensor([0, n[0], n[0] + n[1], sum(n)], dtype=torch.int32))
+            dev.copy_(host)
+        r.out.fill_(9.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            g.replay()
+        torch.cuda.synchronize()
+        good = [i for i in range(3) if sum(total[:i + 1]) <= r.max_keys]
+        if len(good) == 3:
+            r.no_error()
+        else:  # the last sequence's keys go past the bound: its rows are left alone
+            assert kda.kda_latent_poll_device_error(r.cache)[1] == kda.KDA_DEVERR_META
+            assert (r.out[int(r.cu[2]):] == 9.0).all()
+        r.check(only=good)
+
+
+def test_two_prefills_at_once():
+    """Two streams, each with its own workspace, at the same time: what each gives alone."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = [R.Rows([n] * 3, [n + 300, n, n + 77], 4, 128, 64, 128, BF, seed=n) for n in (90, 300)]
+    work = [(r, r.workspace()) for r in work]
+    for r, ws in work:
+        r.call(ws)
+    torch.cuda.synchronize()
+    alone = [r.out.clone() for r, _ in work]
+    for _ in range(20):
+        for st, (r, ws) in zip(streams, work):
+            r.call(ws, stream=st)
+    torch.cuda.synchronize()
+    for (r, _), out in zip(work, alone):
+        r.no_error()
+        assert torch.equal(r.out, out)
+        r.check()
+
+
+@ACTS
 def test_prefill_layouts(act):
     """Head-major tensors, rows 16 bytes apart from any wider border, loose bounds, and replay from a graph."""
     new, total, heads = [70, 9], [130, 9], 3
