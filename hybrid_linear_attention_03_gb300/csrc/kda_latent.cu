@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_co
     __shared__ float2 cs[kWarps][kMaxHalf];
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int per_row = kWarps / p.rows_per_cta, part = warp % per_row;  // warps of a row
-    const int row = int(blockIdx.x) * p.rows_per_cta + warp / per_row;
+    const long long at_row = static_cast<long long>(blockIdx.x) * p.rows_per_cta + warp / per_row;
+    const int row = int(min(at_row, static_cast<long long>(p.b.max_rows)));
     wait_prior_kernel();
     allow_next_kernel();
     if (warp == 0) report_seqs(p.b, lane);
@@ -269,75 +270,74 @@ struct LatentReadParams {
     const uint8_t *sc;
     void *c_out, *kr_out;
     long long c_stride, kr_stride;
-    int32_t latent, rope, rows_per_warp;
+    int32_t latent, rope;
 };
 
-// A warp a row, up to four of them in flight.
+// A warp a row (four one after the other took as long or longer).
 template <typename Act, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadParams p) {
     using V = Vec<Act>;
     constexpr int N = V::N, NC = kE4m3 ? 16 : N, kPieces = 512 / NC / 32;  // channels of a loaded piece of c
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    const long long row_base = static_cast<long long>(blockIdx.x) * kWarps * p.rows_per_warp + warp;
+    const long long at_row = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const int row = int(min(at_row, static_cast<long long>(p.b.max_rows)));
     const int n = p.latent / NC, nr = p.rope / N;
     wait_prior_kernel();
     allow_next_kernel();
     if (warp == kWarps - 1) report_seqs(p.b, lane);
-    for (int i = 0; i < p.rows_per_warp; ++i) {
-        const long long row = row_base + i * kWarps;
-        if (row >= p.b.max_rows) return;
-        int pos, page;
-        find_row(p.b, int(row), lane, pos, page);
-        pos = __shfl_sync(0xffffffffu, pos, 0), page = __shfl_sync(0xffffffffu, page, 0);
-        if (pos < 0) continue;
-        const size_t vec = (size_t(max(page, 0)) << p.b.page_shift) + size_t(pos & ((1 << p.b.page_shift) - 1));
-        uint4 raw[kPieces], rr = make_uint4(0, 0, 0, 0);
-        int ex = 0;
+    if (row >= p.b.max_rows) return;
+    int pos, page;
+    find_row(p.b, row, lane, pos, page);
+    pos = __shfl_sync(0xffffffffu, pos, 0), page = __shfl_sync(0xffffffffu, page, 0);
+    if (pos < 0) return;
+    const size_t vec = (size_t(max(page, 0)) << p.b.page_shift) + size_t(pos & ((1 << p.b.page_shift) - 1));
+    uint4 raw[kPieces], rr = make_uint4(0, 0, 0, 0);
+    int ex = 0;
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            raw[k] = make_uint4(0, 0, 0, 0);
-            if (page >= 0 && lane + 32 * k < n)
-                raw[k] = *reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p.pc) +
-                                                          (vec * size_t(p.latent) + size_t(lane + 32 * k) * NC) *
-                                                              (kE4m3 ? 1 : sizeof(Act)));
-        }
-        if (page >= 0) {
-            if (lane < nr)
-                rr = *reinterpret_cast<const uint4 *>(static_cast<const Act *>(p.pkr) + vec * size_t(p.rope) + lane * N);
-            if constexpr (kE4m3) ex = p.sc[vec];
-        }
-        Act *dst = static_cast<Act *>(p.c_out) + size_t(row) * size_t(p.c_stride);
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int at = lane + 32 * k;
-            if (at >= n) continue;
-            if constexpr (kE4m3) {
-                const float f = exp2_biased(ex);
-                const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-                for (int j = 0; j < NC / N; ++j) {
-                    float x[N];
-#pragma unroll
-                    for (int e = 0; e < N; e += 2) {
-                        const int c = j * N + e;
-                        const float2 t = unpack_e4m3(uint16_t(w[c / 4] >> ((c & 2) * 8)));
-                        x[e] = t.x * f, x[e + 1] = t.y * f;
-                    }
-                    *reinterpret_cast<uint4 *>(dst + at * NC + j * N) = V::pack(x);
-                }
-            } else {
-                *reinterpret_cast<uint4 *>(dst + at * N) = raw[k];
-            }
-        }
-        if (lane < nr)
-            *reinterpret_cast<uint4 *>(static_cast<Act *>(p.kr_out) + size_t(row) * size_t(p.kr_stride) + lane * N) = rr;
+    for (int k = 0; k < kPieces; ++k) {
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (page >= 0 && lane + 32 * k < n)
+            raw[k] = *reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p.pc) +
+                                                      (vec * size_t(p.latent) + size_t(lane + 32 * k) * NC) *
+                                                          (kE4m3 ? 1 : sizeof(Act)));
     }
+    if (page >= 0) {
+        if (lane < nr)
+            rr = *reinterpret_cast<const uint4 *>(static_cast<const Act *>(p.pkr) + vec * size_t(p.rope) + lane * N);
+        if constexpr (kE4m3) ex = p.sc[vec];
+    }
+    Act *dst = static_cast<Act *>(p.c_out) + size_t(row) * size_t(p.c_stride);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int at = lane + 32 * k;
+        if (at >= n) continue;
+        if constexpr (kE4m3) {
+            const float f = exp2_biased(ex);
+            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+            for (int j = 0; j < NC / N; ++j) {
+                float x[N];
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    const int c = j * N + e;
+                    const float2 t = unpack_e4m3(uint16_t(w[c / 4] >> ((c & 2) * 8)));
+                    x[e] = t.x * f, x[e + 1] = t.y * f;
+                }
+                *reinterpret_cast<uint4 *>(dst + at * NC + j * N) = V::pack(x);
+            }
+        } else {
+            *reinterpret_cast<uint4 *>(dst + at * N) = raw[k];
+        }
+    }
+    if (lane < nr)
+        *reinterpret_cast<uint4 *>(static_cast<Act *>(p.kr_out) + size_t(row) * size_t(p.kr_stride) + lane * N) = rr;
 }
 
 template <typename Act, bool kE4m3> kda_status append_t(LatentAppendParams &p, int rows, cudaStream_t stream) {
-    // Few rows: one a CTA (latency).  Many: a warp each.
-    p.rows_per_cta = rows <= 4 * sm_count() ? 1 : rows <= 16 * sm_count() ? 2 : kWarps;
-    const dim3 grid(unsigned((rows + p.rows_per_cta - 1) / p.rows_per_cta));
+    // Few rows: one a CTA (latency).  Many: a warp each.  64 heads, us with one, two and four rows a CTA: 608 rows 4.6,
+    // 4.6, 4.8; 1216 7.1, 6.7, 6.8; 2432 10.2, 10.7, 11.1; 4864 18.2, 16.2, 18.6; 9728 38, 34, 31.
+    p.rows_per_cta = rows <= 4 * sm_count() ? 1 : rows <= 32 * sm_count() ? 2 : kWarps;
+    const dim3 grid(unsigned((rows - 1) / p.rows_per_cta + 1));
     constexpr int N = Vec<Act>::N;
     const bool wide = p.half_rot % N == 0;
     const int places = p.rope / (2 * (wide ? N : 4));
@@ -349,10 +349,8 @@ template <typename Act, bool kE4m3> kda_status append_t(LatentAppendParams &p, i
 }
 
 template <typename Act, bool kE4m3> kda_status read_t(LatentReadParams &p, int rows, cudaStream_t stream) {
-    p.rows_per_warp = rows <= 8 * kWarps * sm_count() ? 1 : 4;
-    const int per_cta = kWarps * p.rows_per_warp;
     const ProfScope prof(KDA_KERNEL_LATENT_READ, stream);
-    return launch_overlapped(latent_read_kernel<Act, kE4m3>, dim3(unsigned((rows + per_cta - 1) / per_cta)), kThreads, 0, stream,
+    return launch_overlapped(latent_read_kernel<Act, kE4m3>, dim3(unsigned((rows - 1) / kWarps + 1)), kThreads, 0, stream,
                              p);
 }
 
