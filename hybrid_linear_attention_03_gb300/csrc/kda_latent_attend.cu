@@ -172,10 +172,12 @@ template <typename Act, int D>
 kda_status combine_d(const LatentRows &p, const AttendPlan &plan, long long rows, long long items, cudaStream_t stream) {
     const long long cut = std::min<long long>(items, plan.n_cta), one_wave = 8LL * 8 * sm_count();  // warps
     const ProfScope prof(KDA_KERNEL_LATENT_COMBINE, stream);
-    // few items, of many parts each: four warps share a slice's; many: a warp has a whole row
-    if (cut * rows * (D / 64) * 4 <= one_wave) return combine_as<Act, D, 64, 4>(p, plan, rows, cut, stream);
+    // Few items, of many parts each: four warps share a slice's; many: a warp has a whole row.  The joining alone (L2 cold),
+    // us, shared, by slices and by rows (64 rows of 512 channels): 1 item 12, 18, 65; 4 items 15.9, 11.8, 26; 12 items 26, 11.8, 13.9;
+    // 16 items 32, 13.9, 12.0; 64 items 112, 26, 13.
+    if (cut * rows * (D / 64) * 8 <= one_wave) return combine_as<Act, D, 64, 4>(p, plan, rows, cut, stream);
     if constexpr (D > 64)
-        if (cut * rows * (D / 64) > one_wave) return combine_as<Act, D, D, 1>(p, plan, rows, cut, stream);
+        if (cut * rows * (D / 64) * 4 > one_wave * 3) return combine_as<Act, D, D, 1>(p, plan, rows, cut, stream);
     return combine_as<Act, D, 64, 1>(p, plan, rows, cut, stream);
 }
 template <typename Act>
