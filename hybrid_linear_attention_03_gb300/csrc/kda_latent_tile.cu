@@ -29,10 +29,11 @@
 // Q.  (Latents widened to f16 for the outputs: 64 verifies of 8 tokens 715 us against 432; to bf16, 835:
 // two tiles and a wide one fill shared memory, and one tile's widening, products and copies wait in turn.)
 //
-// What bounds it (latents of 512, pages of 64): single tokens, the cache's bytes: 64 sequences of up
-// to 32768 tokens at 64 heads take 142 us, 5.4 TB/s.  Verifies in e4m3, the reads of shared memory:
+// What bounds it (latents of 512, pages of 64): single tokens, the cache's bytes: 64 sequences of 4001
+// to 16384 tokens at 64 heads take 142 us, 5.4 TB/s.  Verifies in e4m3, the reads of shared memory:
 // a product of 64 x 64 scores reads 4 KB in its 32.5 cycles and one of 128 channels 6 KB in 48.5 (measured), 2330 cycles
-// a tile and 320 for its copy; a tile takes 2900.  One sequence of 4096 tokens: 17 us, of them 7 before the first tile is there.
+// a tile and 320 for its copy; a tile takes 2900.  One sequence of 4096 tokens: 16 us, of them
+// 3.5 before the first page is asked for and 3.5 for writing the parts.
 //
 // A latent behind a row's position weighs nothing, but 0 * NaN is NaN in the product.
 // So in the few tiles where some row does not see some key, the softmax warps zero the
