@@ -92,7 +92,7 @@ __device__ __noinline__ void add_odd_rows(const PrefillRowsParams &p, const Item
                 float o[16];
                 tmem_ld16(t_o + uint32_t(ch), o);
                 tmem_wait_ld();
-                if (j <= lim && w != 0.f) {
+                if (j <= lim) {  // (also where it weighs 0: as in a tile that every row sees, 0 * infinity is NaN)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = fmaf(w, __bfloat162float(val[ch + i]), o[i]);
                 }

@@ -666,7 +666,9 @@ KDA_API kda_status kda_latent_read(const kda_latent_cache *cache, const kda_kv_b
 /* The absorbed form, causal, of the batch's tokens over their sequences' pages (the tokens' own
  * lines included).  Keys behind a row's position are never weighed, whatever they hold; a
  * row whose keys are all absent or score -inf gets zeros.  Among the keys that a row sees, one with an
- * infinity or NaN leaves what the formula gives, or, where its score is -inf, may add nothing at all.
+ * infinity or NaN leaves what the formula gives with weights in 32 bits: one that is 2^-126 of the largest or
+ * less may be 0 there, and 0 times an infinity is NaN.  (So a key whose score is -inf may make its value's
+ * infinities NaN, among zeros if all do; a latent with such a score may also add nothing at all.)
  * Precision: scores, the softmax's sums and the outputs before their rounding are in
  * 32 bits; bf16 calls round each weight by at most 2^-8 of it before it meets its value.
  * Over e4m3 pages they also take q_c as two e4m3 terms times a power of two a row, which
