@@ -1,7 +1,9 @@
 """Latent attention at its corners on a GPU, against the plain float64 statements of latent_ref.py: values that are not finite
-under weights too small for 32 bits."""
+under weights too small for 32 bits, values next to the end of the type's range."""
 
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -9,6 +11,7 @@ import torch
 from hybrid_linear_attention_03_gb300 import build as kbuild
 from hybrid_linear_attention_03_gb300 import kda
 
+import latent_precision as P
 import latent_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -73,3 +76,48 @@ def test_rows_without_weights_beside_values_that_are_not_finite(act, new):
     assert (r.out[..., :3] == 0).all() and (r.out[..., 4:] == 0).all() and (r.out[:first, :, 3] == 0).all()
     seen = r.out[first:, :, 3]
     assert (torch.isnan(seen) | (seen == 0)).all()
+
+
+@ACTS
+@pytest.mark.parametrize("new", [4, 300])
+def test_large_values_under_rising_scores(act, new):
+    """The first 64 keys score 2^9 below the others, which together stay below where the reference would move: 64 values of
+    2^105 (up to 2^107) weigh 2^15 there, 8 times over, and their weighted mean is as finite as they are."""
+    total, gain = 500, 2.0 ** 105
+    r = R.Rows([new], [total], 2, 128, 64, 128, act, seed=new)
+    for t in (r.qn, r.qr, r.k, r.kr):
+        t.zero_()
+    r.qn[..., 0] = 1.0
+    r.k[64:, :, 0] = 9 * math.log(2.0) / r.scale
+    r.v.mul_(gain)
+    assert float(r.v.float().abs().max()) * 2.0 ** 16 * -(-total // 64) < 2.0 ** 127
+    r.call()
+    r.no_error()
+    s = (torch.einsum("thn,jhn->thj", r.qn.double().cpu(), r.k.double().cpu())) * r.scale
+    ref, mag = R.attend(s, r.v.double().cpu() / gain, total - new)
+    P.within_contract(r.out.double().cpu() / gain, ref, mag, 2.0 ** -14, act)
+
+
+@pytest.mark.parametrize("act,fmt", [(BF, "act"), (BF, "e4m3"), (F32, "act"), (F32, "e4m3")])
+@pytest.mark.parametrize("new,heads", [(1, 16), (40, 3)])
+def test_large_latents_under_rising_scores(act, fmt, new, heads):
+    """As above for the absorbed form, whose reference moves when a score leads it by 8."""
+    total, gain, scale = 300, 2.0 ** 105, 0.05
+    b = R.Batch([new], [total], heads, 512, 64, 64, act, fmt, seed=new)
+    w = b.whole()
+    kr = torch.zeros(total, 64)
+    kr[64:, 0] = 7.5 * math.log(2.0) / scale
+    kda.kda_latent_append(b.kv, None, kda.make_latent_io(w.randn(total, 512, gain=gain).cuda(), kr.to(act).cuda(), None, None), w.batch)
+    c, kr = b.held()[0]
+    assert float(c.abs().max()) * 2.0 ** 8 * total < 2.0 ** 127
+    q = b.queries()
+    q[0].mul_(2.0 ** -105 / 64), q[1].zero_()
+    q[1][..., 0] = 1.0
+    out = torch.empty_like(q[0])
+    kda.kda_latent_attend(b.kv, kda.make_latent_attn_io(*q, out, scale), b.batch, b.workspace())
+    b.no_error()
+    s = (torch.einsum("thl,jl->thj", q[0].double().cpu(), c) + torch.einsum("thr,jr->thj", q[1].double().cpu(), kr)) * scale
+    ref, mag = R.attend(s, c[:, None] / gain, total - new)
+    # scores of at most 6: 576 products and 4 more, in 32 bits; over e4m3 pages q_c's small elements and the smallest weights
+    extra = 2.0 ** -22 * total * float(c.abs().max()) / gain if fmt == "e4m3" and act == BF else 0.0
+    P.within_contract(out.double().cpu() / gain, ref, mag, 2.0 ** -10 if fmt == "e4m3" and act == BF else 2.0 ** -11, act, extra)
