@@ -17,8 +17,8 @@ namespace kv {
 namespace {
 
 constexpr int BM = 32, KS = 32, kThreads = 256;
-// In place of the weight of a key that the row does not see, whose value may be anything.  (Not 0: a key that the row
-// does see may weigh that little, and 0 * infinity is NaN in every tile.)
+// In place of the weight of a key that the row does not see (or that scores -inf), whose value may be anything.  Not 0: a key
+// that the row does see may weigh that little, and 0 * infinity is NaN in every tile.
 constexpr float kUnseen = -1.f;
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -164,12 +164,10 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 float x[2];
-                bool unseen[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     x[e] = x2[a][e].x + x2[a][e].y;
-                    unseen[e] = masked && (s.at[tx + 16 * e].line < 0 || kb + tx + 16 * e > lim[a]);
-                    if (unseen[e]) x[e] = -INFINITY;
+                    if (masked && (s.at[tx + 16 * e].line < 0 || kb + tx + 16 * e > lim[a])) x[e] = -INFINITY;
                 }
                 float mx = fmaxf(x[0], x[1]);
 #pragma unroll
@@ -178,9 +176,9 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[e] = exp2f(x[e] - ref);
-                    sum += x[e];
-                    s.p[tx + 16 * e][2 * ty + a] = unseen[e] ? kUnseen : x[e];
+                    const float w = exp2f(x[e] - ref);
+                    sum += w;
+                    s.p[tx + 16 * e][2 * ty + a] = masked && x[e] == -INFINITY ? kUnseen : w;
                 }
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
