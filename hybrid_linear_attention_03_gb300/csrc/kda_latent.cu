@@ -7,10 +7,10 @@
 // which the queries' are most of the bytes (64 heads of 64 channels: 16 KB read and
 // written, beside 2 KB for the cache).  A thread takes two places of 4 or 8 channels of
 // such a vector that turn together, so no partner has to be fetched from another lane.
-// Bound by memory: 32768 tokens at 64 heads with e4m3 pages 111 us, 5.2 TB/s; reading as many back 18 us.
-// One token: 5.5 us, the chain from the tables to a row's place and angles.
-#include <atomic>
-
+// Bound by memory: 32768 tokens at 64 heads with e4m3 pages 99 us, 6.0 TB/s, reading as many back 12.9 us, 4.6 TB/s
+// (in a graph, one after another over tensors that do not fit L2; a call alone behind an emptied L2, launch included, 106 and
+// 20 us).  One token: 3.5 us like that, called one after another from the host 5.6: the chain from the tables to a
+// row's place and angles.
 #include "kda_latent.cuh"
 #include "kda_rows.cuh"
 
@@ -170,7 +170,8 @@ __device__ __forceinline__ void latent_to_page(const LatentAppendParams &p, size
 // A row is one warp's, or two or all four warps of a CTA share its vectors (few rows: latency); the last of them
 // has the latent.  A thread's places are the same in all its vectors, so it keeps their cosines and sines in
 // registers (from shared memory for each vector, a CTA's warps sharing all its rows: 119 us for 32768 tokens and
-// 53 for eight prompts of 500 to 2000, against 111 and 43; with four vectors in flight instead of three 135 and 53).
+// 53 for eight prompts of 500 to 2000, against 111 and 43; with four vectors in flight instead of three 135 and 53; between
+// events around single calls behind an emptied L2, which is longer than the kernel).
 // W: channels of a place, 8 (bf16, 16 bytes) where half the channels that turn are a multiple of it, else 4.
 template <typename Act, bool kE4m3, int W>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(const __grid_constant__ LatentAppendParams p) {
@@ -273,7 +274,8 @@ struct LatentReadParams {
     int32_t latent, rope;
 };
 
-// A warp a row (four one after the other took as long or longer).
+// A warp a row.  64 heads' cache, bf16 / e4m3 pages, in a graph one after another: 1 row 1.7 / 1.6 us, 1216 2.8 / 2.5, 4864 4.2 /
+// 4.1, 9728 5.9 / 5.8, 32768 13.9 / 12.9 (floors 11.1 and 8.6).
 template <typename Act, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadParams p) {
     using V = Vec<Act>;
@@ -334,9 +336,13 @@ __global__ void __launch_bounds__(kThreads) latent_read_kernel(const LatentReadP
 }
 
 template <typename Act, bool kE4m3> kda_status append_t(LatentAppendParams &p, int rows, cudaStream_t stream) {
-    // Few rows: one a CTA (latency).  Many: a warp each.  64 heads, us with one, two and four rows a CTA: 608 rows 4.6,
-    // 4.6, 4.8; 1216 7.1, 6.7, 6.8; 2432 10.2, 10.7, 11.1; 4864 18.2, 16.2, 18.6; 9728 38, 34, 31.
-    p.rows_per_cta = rows <= 4 * sm_count() ? 1 : rows <= 32 * sm_count() ? 2 : kWarps;
+    // The fewest rows a CTA that leave one wave (an SM holds six CTAs), else a warp each.  With norm and rotation, latents of
+    // 512 to pages in bf16 / e4m3, in a graph one after another, us with one, two and four rows a CTA:
+    //   64 heads  912 rows 6.0 / 6.4, 6.6 / 7.0, 7.6 / 8.0; 1064 8.5 / 9.4, 7.4 / 8.0, 7.9 / 8.2;
+    //             1824 10.4 / 11.1, 8.6 / 9.1, 9.4 / 9.9; 2128 12.5 / 13.5, 11.8 / 12.8, 10.6 / 11.9; 9728 40 / 44, 35 / 38, 31 / 34
+    //   8 heads   912 rows 4.5 / 4.9, 4.6 / 5.0, 4.6 / 5.0; 1064 6.6 / 7.4, 4.9 / 5.5, 4.6 / 5.0;
+    //             1824 7.9 / 8.6, 5.2 / 5.8, 4.9 / 5.6; 2128 9.5 / 10.6, 7.8 / 8.8, 5.6 / 7.0; 9728 30 / 34, 21 / 24, 14 / 17
+    p.rows_per_cta = rows <= 6 * sm_count() ? 1 : rows <= 12 * sm_count() ? 2 : kWarps;
     const dim3 grid(unsigned((rows - 1) / p.rows_per_cta + 1));
     constexpr int N = Vec<Act>::N;
     const bool wide = p.half_rot % N == 0;
