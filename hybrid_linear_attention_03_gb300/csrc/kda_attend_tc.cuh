@@ -22,7 +22,8 @@ constexpr int KT = 128;  // keys of a tile
 // while the barrier is in t's phase or just past it.
 //   Not before: the phase of tile t - kBars has passed.  Inside an item that holds for
 // every role that takes all tiles or every second one, which has waited for that tile
-// itself (kBars is even).  From item to item it rests on the order of the items: an odd
+// itself (kBars is even).  From item to item, in the kernels over pages of keys and values
+// (that of kda_latent_prefill.cu has reasons of its own, given there), it rests on the order of the items: an odd
 // number of tiles makes the sides swap barriers, a side may sit an item out, and the
 // softmax waits for values only where it checks them.  But nobody waits for an item's
 // tiles before its rows of Q (q_full, row_unit) or the scores that need them, and the

@@ -126,6 +126,21 @@ __device__ __forceinline__ void look_over(const Item &it, int kb, unsigned char 
     __syncwarp();
 }
 
+// Why the waits by parity are sound (see kBars: when someone waits for tile t, tile t - 8 is past, and t + 8 is not).
+// Here the warp that fetches keys brings Q too, once q_free says that the last item's scores are done, while that item's
+// values may still be on their way.
+//   Not two past: t + 8 takes a stage that is free after t's, which all who wait for t have to say first.
+//   Keys.  A tile is asked for when the one kStagesK (at most 3) before it is free, so if tile i was asked for, those up to
+// i - 3 are past.  By rows both issuing warps wait for every tile, also of items that a side sits out.  By keys a side waits
+// for its own: inside an item t - 2 was asked for before; at its start, q_full: Q is asked for behind all keys of the items before.
+//   Values (half tiles 2 t and 2 t + 1).  The warps that look them over wait for each in turn: the one before was asked for, so
+// those up to 7 before are free.  So `clean` completes in order, and whoever has seen it of one knows all before it past, of
+// v_full and of clean.  By rows a side's issuing warp waits for clean of every one, and issues an item's scores
+// after that, which are what its softmax waits for first.  By keys, inside an item, a side has seen clean of both halves of
+// t - 2 before it issues the scores of t.  At its start, b being its first tile, side 0 goes on to wait for 2 b and side 1
+// for 2 b + 2, so those up to 2 b - 5 (1 + 2 (b - 3), the latest for 2 b + 3) have to be past.  q_full is behind q_free of the item
+// before, which both sides give, and tile b - 3 is either in that item, where its side also has the last tile, b - 1, whose scores
+// (and q_free) it issues after it has seen b - 3 clean; or in one before that, which its side was through with before.
 template <int DN, int DV, bool kByKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ PrefillRowsParams p, const __grid_constant__ PrefillMaps maps) {

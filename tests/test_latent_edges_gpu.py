@@ -1,8 +1,9 @@
 """Latent attention at its corners on a GPU, against the plain float64 statements of latent_ref.py: values that are not finite
-under weights too small for 32 bits, values next to the end of the type's range."""
+under weights too small for 32 bits, values next to the end of the type's range, and many short items in a CTA."""
 
 from __future__ import annotations
 
+import itertools
 import math
 
 import pytest
@@ -121,3 +122,57 @@ def test_large_latents_under_rising_scores(act, fmt, new, heads):
     # scores of at most 6: 576 products and 4 more, in 32 bits; over e4m3 pages q_c's small elements and the smallest weights
     extra = 2.0 ** -22 * total * float(c.abs().max()) / gain if fmt == "e4m3" and act == BF else 0.0
     P.within_contract(out.double().cpu() / gain, ref, mag, 2.0 ** -10 if fmt == "e4m3" and act == BF else 2.0 ** -11, act, extra)
+
+
+ORDERS = [k for t in itertools.product(range(1, 5), repeat=3) for k in t]  # every order of three items of one to four tiles
+
+
+@ACTS
+@pytest.mark.parametrize("n,heads,news,max_new", [
+    (100, 64, [1, 2], 2),              # sides by keys, a sequence's heads in a row
+    (1500, 1, [1, 3, 2], 3),           # by keys, other numbers of tiles from item to item
+    (1500, 1, [1, 130, 7, 2], 200),    # by rows: the second side sits most items out
+    (600, 2, [130, 1, 129, 128, 5], 130),
+])
+def test_short_items_in_every_order(act, n, heads, news, max_new):
+    """A CTA's items of one to four tiles of 128 keys one after the other: what one leaves in rings, barriers and tensor memory is
+    the next one's beginning."""
+    total = [128 * ORDERS[i % len(ORDERS)] - (37 * i) % 128 for i in range(n)]
+    new = [min(news[i % len(news)], t) for i, t in enumerate(total)]
+    if act == F32:
+        n = n // 4
+        total, new = total[:n], new[:n]
+    gen = torch.Generator(device="cuda").manual_seed(n + heads)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(act)
+
+    rows, keys, N, Rr, V = sum(new), sum(total), 64, 64, 64
+    qn, qr, k, kr, v = randn(rows, heads, N), randn(rows, heads, Rr), randn(keys, heads, N), randn(keys, Rr), randn(keys, heads, V)
+    out = torch.full((rows + 1, heads, V), 9.0, dtype=act, device="cuda")
+    cache = kda.PagedLatent(1, 16, heads, 128, Rr, act)
+    cu, cu_kv = (torch.tensor([0, *itertools.accumulate(x)], dtype=torch.int32, device="cuda") for x in (new, total))
+    batch = kda.make_latent_prefill_batch(cu, cu_kv, rows, keys, max_new)
+    io = kda.make_latent_prefill_io(qn, qr, k, kr, v, out)
+    ws = torch.empty(kda.kda_latent_prefill_workspace_bytes(cache, io, batch), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        kda.kda_latent_prefill(cache, io, batch, ws)
+    assert kda.kda_latent_poll_device_error(cache) == (kda.KDA_OK, 0)
+    assert (out[rows:] == 9.0).all()
+    scale = (N + Rr) ** -0.5
+    j = torch.arange(512, device="cuda")
+    for a in range(0, n, 50):  # 50 sequences at a time, padded, in float64 on the device
+        ids = torch.arange(a, min(a + 50, n), device="cuda")
+        T, L = (cu[ids + 1] - cu[ids]).long(), (cu_kv[ids + 1] - cu_kv[ids]).long()
+        t = torch.arange(int(T.max()), device="cuda")
+        row, key = (cu[ids].long()[:, None] + t).clamp(max=rows - 1), (cu_kv[ids].long()[:, None] + j).clamp(max=keys - 1)
+        s = torch.einsum("nthc,njhc->nthj", qn[row].double(), k[key].double())
+        s = (s + torch.einsum("nthc,njc->nthj", qr[row].double(), kr[key].double())) * scale
+        seen = j <= (L - T)[:, None, None] + t[:, None]
+        p = torch.softmax(s.masked_fill(~seen[:, :, None], -torch.inf), -1)
+        ref, mag = (torch.einsum("nthj,njhc->nthc", p, x) for x in (v[key].double(), v[key].double().abs()))
+        real = t < T[:, None]
+        top = torch.cat((k[key].double(), kr[key].double()[:, :, None].expand(-1, -1, heads, -1)), -1).norm(dim=-1).max()
+        qk = torch.cat((qn[row], qr[row]), -1).double().norm(dim=-1) * top * scale
+        rel = (N + Rr + 4) * 2.0 ** -24 * qk[..., None] * 2 + 2.0 ** -20
+        P.within_contract(out[row][real], ref[real].cpu(), mag[real].cpu(), rel[real].cpu(), act, what=f"sequences from {a}")
