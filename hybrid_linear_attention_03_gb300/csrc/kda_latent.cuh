@@ -2,7 +2,8 @@
 // their host entry points.  How the keys of a call are shared out over the CTAs, the
 // records of the shares and the walk over items are those of kda_attend.cuh:
 //   absorbed  an item is (sequence, group of heads, run of tokens); all heads share a key,
-//             so the cache's "heads" are groups of as many as a row tile holds;
+//             so the cache's "heads" are groups of as many as a row tile holds (the last group
+//             may have fewer: rows for heads past the last one are worked on as that one's, and not written);
 //   expanded  an item is (sequence, head, run of tokens).
 #pragma once
 
@@ -34,7 +35,7 @@ struct LatentRows {
     const void *q_a, *q_r;  // the heads' own part (latent_dim or nope_dim channels), the part that meets kr
     void *out;
     long long qa_stride, qa_head, qr_stride, qr_head, out_stride, out_head;
-    int32_t hkv, group;                               // groups of heads, heads of one
+    int32_t hkv, group, heads;                        // groups of heads, rows of one for a token, heads of them all
     int32_t tile_tokens, key_step, item_cost, min_keys;  // as in AttendParams
     int32_t rope;
     float scale_log2;
@@ -42,10 +43,11 @@ struct LatentRows {
     float *part_data;
     uint32_t group_inv;
     __device__ __forceinline__ int token_of(int r) const { return int(uint32_t(r) * group_inv >> 16); }
-    // token and head of row r of an item
-    __device__ __forceinline__ void locate(const Item &it, int r, long long &row, long long &head) const {
-        const int t = token_of(r);
-        row = it.row0 + it.tok0 + t, head = it.h * group + r - t * group;
+    // token and head of row r of an item; false, and the last head, where the group has no such one
+    __device__ __forceinline__ bool locate(const Item &it, int r, long long &row, long long &head) const {
+        const int t = token_of(r), h = it.h * group + r - t * group;
+        row = it.row0 + it.tok0 + t, head = min(h, heads - 1);
+        return h < heads;
     }
 };
 struct LatentParams : LatentRows {
@@ -65,11 +67,14 @@ inline BatchView make_view(const kda_latent_cache *c, const kda_kv_batch *b) {
     return make_view(&pages, b);
 }
 
-// Equal groups of heads: the fewest that leave each at most `most` of them.
-inline int head_groups(int heads, int most) {
-    int n = (heads + most - 1) / most;
-    while (heads % n) ++n;
-    return n;
+// Heads of a group, and groups: the fewest that leave each at most `most` heads, and those as even as that allows.
+// (Equal groups only: 67 heads would be 67 groups of one and read the cache as often, 64 single tokens over 4001 to 16384 7010 us.)
+struct HeadGroups {
+    int each, groups;
+};
+inline HeadGroups head_groups(int heads, int most) {
+    const int n = (heads - 1) / most + 1, each = (heads - 1) / n + 1;
+    return {each, (heads - 1) / each + 1};
 }
 
 kda_status launch_latent_append(const kda_latent_cache *c, const kda_latent_params *p, const kda_latent_io *io,

@@ -144,9 +144,10 @@ __global__ void __launch_bounds__(kCombineThreads) latent_combine_kernel(const _
         }
     }
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-    const int t = p.token_of(r);
+    const int t = p.token_of(r), head = first.h * p.group + r - t * p.group;
+    if (head >= p.heads) return;
     Act *dst = static_cast<Act *>(p.out) + (static_cast<long long>(first.row) + t) * p.out_stride +
-               (static_cast<long long>(first.h) * p.group + r - t * p.group) * p.out_head + ch;
+               static_cast<long long>(head) * p.out_head + ch;
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
         if constexpr (sizeof(Act) == 2)
@@ -197,10 +198,10 @@ kda_status combine(int act, int D, const LatentRows &p, const AttendPlan &plan, 
     return act == KDA_BF16 ? combine_t<__nv_bfloat16>(D, p, plan, rows, items, s) : combine_t<float>(D, p, plan, rows, items, s);
 }
 
-void set_items(LatentRows &p, const AttendPlan &plan, int groups, int group, float scale, void *workspace) {
-    p.hkv = groups, p.group = group;
-    p.group_inv = (65536u + uint32_t(group) - 1) / uint32_t(group);
-    p.tile_tokens = plan.bm / group;
+void set_items(LatentRows &p, const AttendPlan &plan, int heads, HeadGroups g, float scale, void *workspace) {
+    p.hkv = g.groups, p.group = g.each, p.heads = heads;
+    p.group_inv = (65536u + uint32_t(g.each) - 1) / uint32_t(g.each);
+    p.tile_tokens = plan.bm / g.each;
     p.scale_log2 = scale * kLog2e;
     p.parts = static_cast<Part *>(workspace);
     p.part_data = reinterpret_cast<float *>(static_cast<char *>(workspace) + parts_bytes(plan.n_cta));
@@ -237,8 +238,7 @@ kda_status launch_latent_attend(const kda_latent_cache *c, const kda_latent_attn
     p.qr_stride = io->q_r_stride, p.qr_head = io->q_r_head_stride;
     p.out_stride = io->out_stride, p.out_head = io->out_head_stride;
     p.c = c->c, p.kr = c->kr, p.sc = c->c_scale, p.rope = c->rope_dim;
-    const int groups = head_groups(c->num_heads, plan.bm);
-    set_items(p, plan, groups, c->num_heads / groups, io->scale, workspace);
+    set_items(p, plan, c->num_heads, head_groups(c->num_heads, plan.bm), io->scale, workspace);
     const kda_status st = ch.launch(c, p, plan, stream);
     if (st != KDA_OK || p.b.max_len <= p.key_step) return st;  // sequences of one key step are never cut
     return combine(c->act, c->latent_dim, p, plan, b->max_new, b->n_seqs, stream);
@@ -276,7 +276,7 @@ kda_status launch_latent_prefill(const kda_latent_cache *c, const kda_latent_pre
     p.k = io->k, p.kr = io->kr, p.v = io->v, p.rope = c->rope_dim;
     p.k_stride = io->k_stride, p.k_head = io->k_head_stride, p.kr_stride = io->kr_stride;
     p.v_stride = io->v_stride, p.v_head = io->v_head_stride;
-    set_items(p, plan, c->num_heads, 1, io->scale, workspace);
+    set_items(p, plan, c->num_heads, HeadGroups{1, c->num_heads}, io->scale, workspace);
     const kda_status st = ch.launch(c, io, p, plan, stream);
     if (st != KDA_OK || b->max_kv_rows <= p.key_step) return st;
     return combine(c->act, io->value_dim, p, plan, b->max_new, b->n_seqs, stream);

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
             const int r = r0 + a;
             if (r >= it.rows) continue;
             long long row, head;
-            p.locate(it, r, row, head);
+            if (!p.locate(it, r, row, head)) continue;
             float *dst = static_cast<float *>(p.out) + row * p.out_stride + head * p.out_head;
             const float f = s.f[r];
 #pragma unroll

@@ -82,7 +82,7 @@ struct alignas(16) Misc {
     int has;
     Cursor piece[2];
     alignas(16) float back[BM], inv[BM];  // what a move of the reference scales O by; an item's end: the rows' factors
-    long long out_at[BM];                 // element offsets of the rows in out
+    long long out_at[BM];                 // element offsets of the rows in out, -1 for one of no head
     alignas(16) uint8_t scale[6][KL];     // e4m3, by stage: the keys' scale exponents
     alignas(16) float unit[2][KL];        // by tile parity: the scales
     float unit_top[2];                    // and the largest of them
@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 ms.inv[row] = !whole ? up : l > 0.f || l != l ? up / l : 0.f;
                 if (row < was.rows) {
                     long long token, head;
-                    p.locate(was, row, token, head);
-                    ms.out_at[row] = token * p.out_stride + head * p.out_head;
+                    const bool there = p.locate(was, row, token, head);
+                    ms.out_at[row] = there ? token * p.out_stride + head * p.out_head : -1;
                     if (!whole) data[BM * L + row] = ref, data[BM * L + BM + row] = l;
                 }
             }
@@ -517,9 +517,11 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                     for (int m = 0; m < MT; ++m) swap_4x4(o[m][g], o[m][g + 1], o[m][g + 2], o[m][g + 3], lane);
                     const int r = c + g + (lane & 3);
                     if (r < was.rows) {
-                        if (whole) {
+                        const long long at = ms.out_at[r];
+                        if (at < 0) {  // a row of no head
+                        } else if (whole) {
                             const float f = ms.inv[r];
-                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + ms.out_at[r] + ch0;
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at + ch0;
 #pragma unroll
                             for (int m = 0; m < MT; ++m)
                                 *reinterpret_cast<uint2 *>(dst + m * 128) = make_uint2(

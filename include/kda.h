@@ -678,6 +678,7 @@ KDA_API kda_status kda_latent_read(const kda_latent_cache *cache, const kda_kv_b
  * Range: outputs are summed before they are divided by the weights' sum, with weights of up to 1 (32-bit calls),
  * 2^8 (bf16), or 2^16 for 64 keys together (bf16, expanded form): they are finite where the largest of the
  * latents or values, times that, times the row's keys (for the last, its keys / 64), is below 2^127.
+ * The pages are read once for every 64 heads (32-bit calls: 32), the last of which may be fewer.
  * workspace: device, 256-byte aligned, at least kda_latent_attend_workspace_bytes(cache,
  * batch) bytes (the host fields set it; 0 on invalid input); its contents mean nothing
  * between calls, and calls that share one must be ordered.  Results do not depend on it.

@@ -1,5 +1,6 @@
 """Latent attention at its corners on a GPU, against the plain float64 statements of latent_ref.py: values that are not finite
-under weights too small for 32 bits, values next to the end of the type's range, and many short items in a CTA."""
+under weights too small for 32 bits, values next to the end of the type's range, many short items in a CTA, and heads
+that do not fill their groups."""
 
 from __future__ import annotations
 
@@ -176,3 +177,45 @@ def test_short_items_in_every_order(act, n, heads, news, max_new):
         qk = torch.cat((qn[row], qr[row]), -1).double().norm(dim=-1) * top * scale
         rel = (N + Rr + 4) * 2.0 ** -24 * qk[..., None] * 2 + 2.0 ** -20
         P.within_contract(out[row][real], ref[real].cpu(), mag[real].cpu(), rel[real].cpu(), act, what=f"sequences from {a}")
+
+
+@pytest.mark.parametrize("act,fmt", [(BF, "act"), (BF, "e4m3"), (F32, "act"), (F32, "e4m3")])
+@pytest.mark.parametrize("heads,new,total,latent", [
+    (65, [1, 1], [300, 64], 512), (67, [1] * 40, [1 + 29 * i % 400 for i in range(40)], 512), (71, [2, 1], [2000, 65], 256),
+    (127, [1, 3], [129, 700], 128), (129, [1], [900], 512), (131, [5, 0, 1], [5, 9, 190], 128), (33, [1, 2], [300, 80], 512),
+    (37, [7, 1], [90, 1500], 256), (193, [1], [333], 128)])
+def test_heads_that_do_not_fill_their_groups(act, fmt, heads, new, total, latent):
+    """Rows past the last head are nobody's: what stands behind and between the heads of out stays, whole items and parts."""
+    b = R.Batch(new, total, heads, latent, 64, 64, act, fmt, seed=heads, fill=NAN, extra_rows=1)
+    held, q = b.fill_cache(), b.queries()
+    guard = torch.full((b.max_rows, heads + 3, latent + 8), 9.0, dtype=act, device="cuda")
+    out = guard[:, 1:1 + heads, 8:]
+    # queries whose next rows hold NaN, so that one read for a head that is not there would show
+    wide = [torch.full((b.max_rows, heads + 2, t.shape[2]), NAN, dtype=act, device="cuda") for t in q]
+    for w, t in zip(wide, q):
+        w[:, :heads] = t
+    io = kda.make_latent_attn_io(*(w[:, :heads] for w in wide), out, 0.07)
+    kda.kda_latent_attend(b.kv, io, b.batch, b.workspace())
+    b.no_error()
+    b.check_attend(q, out, held, 0.07)
+    assert (out[b.rows:] == 9.0).all() and (guard[:, 0] == 9.0).all() and (guard[:, heads + 1:] == 9.0).all() and (guard[..., :8] == 9.0).all()
+
+
+@ACTS
+def test_time_follows_the_groups_of_heads(act):
+    """A head or three past a full group cost another pass over the pages, not one a head (67 times where that was so)."""
+    us = {}
+    per = 64 if act == BF else 32
+    for heads in (per, per + 3, 2 * per):
+        b = R.Batch([1] * 8, [4000 + 300 * i for i in range(8)], heads, 512, 64, 64, act, "act", seed=1)
+        q = b.queries()
+        io, ws = kda.make_latent_attn_io(*q, torch.empty_like(q[0]), 0.05), b.workspace()
+        for _ in range(3):
+            kda.kda_latent_attend(b.kv, io, b.batch, ws)
+        torch.cuda.synchronize()
+        kda.kda_profile_start(64)
+        for _ in range(10):
+            kda.kda_latent_attend(b.kv, io, b.batch, ws)
+        torch.cuda.synchronize()
+        us[heads] = kda.kda_profile_stop()["latent_attend"][1]
+    assert us[per + 3] < 4 * us[per] and us[2 * per] < 4 * us[per], us
