@@ -35,16 +35,22 @@ struct LatentRows {
     const void *q_a, *q_r;  // the heads' own part (latent_dim or nope_dim channels), the part that meets kr
     void *out;
     long long qa_stride, qa_head, qr_stride, qr_head, out_stride, out_head;
-    int32_t hkv, group, heads;                        // groups of heads, rows of one for a token, heads of them all
+    int32_t hkv, group;                               // groups of heads, heads of one (the last may have fewer)
     int32_t tile_tokens, key_step, item_cost, min_keys;  // as in AttendParams
     int32_t rope;
     float scale_log2;
     Part *parts;
     float *part_data;
     uint32_t group_inv;
+    int32_t heads;  // of all groups
     __device__ __forceinline__ int token_of(int r) const { return int(uint32_t(r) * group_inv >> 16); }
-    // token and head of row r of an item; false, and the last head, where the group has no such one
-    __device__ __forceinline__ bool locate(const Item &it, int r, long long &row, long long &head) const {
+    // token and head of row r of an item (absorbed: one from `heads` on is none)
+    __device__ __forceinline__ void locate(const Item &it, int r, long long &row, long long &head) const {
+        const int t = token_of(r);
+        row = it.row0 + it.tok0 + t, head = it.h * group + r - t * group;
+    }
+    // likewise; false, and the last head, where the group has no such one
+    __device__ __forceinline__ bool locate_head(const Item &it, int r, long long &row, long long &head) const {
         const int t = token_of(r), h = it.h * group + r - t * group;
         row = it.row0 + it.tok0 + t, head = min(h, heads - 1);
         return h < heads;

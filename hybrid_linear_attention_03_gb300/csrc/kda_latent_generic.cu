@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
             if (r < it.rows) {
                 long long row, head;
                 p.locate(it, r, row, head);
+                if constexpr (!kExpanded) head = min(int(head), p.heads - 1);
                 x = c < DA ? load4(static_cast<const float *>(p.q_a) + row * p.qa_stride + head * p.qa_head + c)
                            : load4(static_cast<const float *>(p.q_r) + row * p.qr_stride + head * p.qr_head + (c - DA));
             }
@@ -228,7 +229,9 @@ __global__ void __launch_bounds__(kThreads) latent_generic_kernel(const __grid_c
             const int r = r0 + a;
             if (r >= it.rows) continue;
             long long row, head;
-            if (!p.locate(it, r, row, head)) continue;
+            p.locate(it, r, row, head);
+            if constexpr (!kExpanded)
+                if (head >= p.heads) continue;
             float *dst = static_cast<float *>(p.out) + row * p.out_stride + head * p.out_head;
             const float f = s.f[r];
 #pragma unroll

@@ -167,7 +167,7 @@ __device__ __forceinline__ void ask_q(const LatentParams &p, const Item &it, uns
 #pragma unroll 1
     for (int r = tid >> 3; r < ((it.rows + 15) & ~15); r += kThreads / 8) {
         long long row, head;
-        p.locate(it, min(r, it.rows - 1), row, head);
+        p.locate_head(it, min(r, it.rows - 1), row, head);
         const bool there = r < it.rows;
         const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.q_r) + row * p.qr_stride + head * p.qr_head;
         unsigned char *dst = q_img + sw128_chunk(r, c, 64);
@@ -190,7 +190,7 @@ __device__ __forceinline__ void split_q(const LatentParams &p, const Item &it, u
 #pragma unroll
         for (int i = 0; i < kB; ++i) {
             long long row, head;
-            p.locate(it, min(r0 + g + i, it.rows - 1), row, head);
+            p.locate_head(it, min(r0 + g + i, it.rows - 1), row, head);
             const __nv_bfloat16 *a = static_cast<const __nv_bfloat16 *>(p.q_a) + row * p.qa_stride + head * p.qa_head;
 #pragma unroll
             for (int k = 0; k < kPieces; ++k) {
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<L, kE4m3>::kThreads, 1)
                 ms.inv[row] = !whole ? up : l > 0.f || l != l ? up / l : 0.f;
                 if (row < was.rows) {
                     long long token, head;
-                    const bool there = p.locate(was, row, token, head);
+                    const bool there = p.locate_head(was, row, token, head);
                     ms.out_at[row] = there ? token * p.out_stride + head * p.out_head : -1;
                     if (!whole) data[BM * L + row] = ref, data[BM * L + BM + row] = l;
                 }
