@@ -1,7 +1,7 @@
 // kda_latent_prefill.cu -- kda_latent_prefill for bf16 rows on the tensor cores.
 //
 // Per head, scores X = Q K^T over nope_dim channels of its own and up to 64 shared by all
-// heads (128 rows x 64 keys at a time), one thread a row turns them into weights
+// heads (128 rows x 128 keys a product), one thread a row turns them, 64 at a time, into weights
 // P = 2^(scale log2e X - ref) and leaves them as bf16 where the scores were, and
 // O += P V reads them from there: the softmax and the sides of kda_attend_tile.cu,
 //   sides by rows  (more than 128 tokens a sequence): side s has rows [128 s, 128 s + 128) of a
@@ -14,9 +14,11 @@
 // weights, the product of the other and the other side's are under way.  So that two tiles of keys fit beside 256
 // rows of Q of 192 channels, values come in half tiles.  ref moves, and O and the sums with it, when the
 // weights of a half sum to more than 2^16.
-// A prompt of 8192 tokens at 64 heads of 128 + 64 / 128 takes 1100 us (1250 TFLOP/s), 512 tokens behind 32256 530 us: 4050 cycles for
+// A prompt of 8192 tokens at 64 heads of 128 + 64 / 128 takes 1090 to 1130 us from box to box (1210 to 1260 TFLOP/s), 512 tokens
+// behind 32256 540 to 553 us: 4050 cycles for
 // 128 keys of both sides, where their products' multiplications and reads take 2660 and a thread's softmax about 3000, the two
-// waiting for each other by turns.
+// waiting for each other by turns.  Five of the eight forms spill 4 to 12 bytes at the registers of the split (12 to 156 read back,
+// most where the heads' own channels are 64 and the sides go by keys).
 //
 // Warps: 0-3 side 0, 4-7 side 1 (a thread a row); 8 and 9 issue a side's products each;
 // 10 and 11 fetch the rows of Q, keys and values by TMA; 12-15 look values over:

@@ -8,7 +8,7 @@
 // the other way round 64 rows would take all of it and leave the scores no place.
 // Softmax in one pass as in kda_attend_tile.cu: a row's reference is its maximum at
 // the time it was last moved, and only moves when a score exceeds it by more than 8 (then the
-// four warps meet and scale O); until then a tile costs one vote.  The weights, bf16,
+// eight warps meet and scale O); until then a tile costs one vote.  The weights, bf16,
 // take the place of the tile's shared key part, which the scores have used by then.
 //
 // A tile comes, is multiplied and leaves in parts of 128 channels, each with barriers of
@@ -26,11 +26,12 @@
 // e5m2 reaches down to 2^-22 of the largest weight where e4m3 would end at 2^-18.  The
 // keys' scales (one more warp makes numbers of them) multiply the scores, and the weights before they are split,
 // in units that follow the largest scale a row has met.  Eight more warps bring and split the rows of
-// Q.  (Latents widened to f16 for the outputs: 64 verifies of 8 tokens 715 us against 432; to bf16, 835:
+// Q.  (Latents widened to f16 for the outputs: 64 verifies of 8 tokens 715 us against 434; to bf16, 835:
 // two tiles and a wide one fill shared memory, and one tile's widening, products and copies wait in turn.)
+// For latents of 512 over e4m3 pages, 144 registers of a softmax thread are 48 bytes too few (spilled, 88 read back).
 //
 // What bounds it (latents of 512, pages of 64): single tokens, the cache's bytes: 64 sequences of 4001
-// to 16384 tokens at 64 heads take 142 us, 5.4 TB/s.  Verifies in e4m3, the reads of shared memory:
+// to 16384 tokens at 64 heads take 144 us, 5.3 TB/s.  Verifies in e4m3, the reads of shared memory:
 // a product of 64 x 64 scores reads 4 KB in its 32.5 cycles and one of 128 channels 6 KB in 48.5 (measured), 2330 cycles
 // a tile and 320 for its copy; a tile takes 2900.  One sequence of 4096 tokens: 16 us, of them
 // 3.5 before the first page is asked for and 3.5 for writing the parts.

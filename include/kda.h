@@ -688,7 +688,8 @@ KDA_API kda_status kda_latent_attend(const kda_latent_cache *cache, const kda_la
                                      void *workspace, size_t workspace_bytes, kda_stream_t stream);
 
 /* The expanded form, causal, over keys and values in rows.  Of the cache it takes num_heads,
- * rope_dim, act and err.  Masks, precision, workspace and errors as kda_latent_attend's. */
+ * rope_dim, act and err.  Masks, precision, range, workspace and errors as kda_latent_attend's.  The kernel is chosen
+ * by max_new (up to 128, or more) and the types, so a bound far above what the sequences bring costs time. */
 KDA_API size_t kda_latent_prefill_workspace_bytes(const kda_latent_cache *cache, const kda_latent_prefill_io *io,
                                                   const kda_latent_prefill_batch *batch);
 KDA_API kda_status kda_latent_prefill(const kda_latent_cache *cache, const kda_latent_prefill_io *io,
