@@ -15,7 +15,7 @@
 // rows of Q of 192 channels, values come in half tiles.  ref moves, and O and the sums with it, when the
 // weights of a half sum to more than 2^16.
 // A prompt of 8192 tokens at 64 heads of 128 + 64 / 128 takes 1090 to 1130 us from one GB300 to another (1210 to 1260 TFLOP/s), 512 tokens
-// behind 32256 540 to 553 us: 4050 cycles for
+// behind 32256 537 to 553 us: 4050 cycles for
 // 128 keys of both sides, where their products' multiplications and reads take 2660 and a thread's softmax about 3000, the two
 // waiting for each other by turns.  Five of the eight forms spill 4 to 12 bytes at the registers of the split (12 to 156 read back,
 // most where the heads' own channels are 64 and the sides go by keys).
